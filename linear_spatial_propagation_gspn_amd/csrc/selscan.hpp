@@ -1,0 +1,141 @@
+// selscan.hpp -- what the selective scan's forward and backward share: the
+// launch parameters, the softplus, the wave-uniform loads of B_t and C_t.
+#pragma once
+
+#include "sequence.hpp"
+
+namespace gspn {
+
+constexpr float kLog2E = 1.44269504088896340736f;
+
+struct SelK {
+    SeqK seq;
+    int32_t channels, groups, n, per;  // per: channels a group
+    int32_t softplus, shift, blocks;   // blocks: 64-channel blocks a group
+    const void* x;
+    const void* dt;
+    const void* z;
+    const void* B;
+    const void* C;
+    void* out;
+    int64_t ldx, lddt, ldz, ldb, ldc, ldo;
+    const float* A;
+    const float* D;
+    const float* bias;
+    float* state;   // pool
+    float* check;   // kept states [id][n][channels], or null
+    float* carry;   // [chunk][n][channels]: last states, then first states
+    float* sums;    // [chunk][channels]: sum of d
+    // backward
+    const void* gy;
+    void* dx;
+    void* ddt;
+    void* dz;
+    int64_t ldgy, lddx, ldddt, lddz;
+    float* part;    // [chunk][n + 2][channels]: sums for dA, dD, ddt_bias
+    float* partbc;  // [channel block][row][2][groups][n]: sums for dB, dC
+};
+
+// log(1 + e^v).  With e = e^{-|v|} it is max(v, 0) + log(1 + e); the sum 1 + e
+// drops the low bits of a small e, which are added back to first order (the
+// whole error of u = 1 + e is e - (u - 1), and log(1 + e) changes by it over u,
+// with u between 1 and 2 wherever it matters).
+__device__ __forceinline__ float softplus_f(float v) {
+    const float e = __builtin_amdgcn_exp2f(-__builtin_fabsf(v) * kLog2E);
+    const float u = 1.0f + e;
+    const float l = __builtin_amdgcn_logf(u) * 0.693147180559945309417f + (e - (u - 1.0f));
+    return (v > 0.0f ? v : 0.0f) + l;
+}
+
+// A wave's B_t and C_t: N values each, the same for every lane.
+//  kScalar: N values at a 4-byte aligned address, loaded as dwords by scalar
+//    loads (N == NP, even for 16-bit types).
+//  otherwise lane i < NP holds B_t[i], lane NP + i C_t[i], and each value is
+//    broadcast by a lane read (any N, any alignment).
+template <typename T, int NP>
+struct Words {
+    static constexpr int kCount = NP * static_cast<int>(sizeof(T)) / 4 > 0 ? NP * static_cast<int>(sizeof(T)) / 4 : 1;
+    uint32_t w[kCount];
+};
+
+typedef const __attribute__((address_space(4))) uint32_t* const_words;
+
+template <typename T, int NP>
+__device__ __forceinline__ Words<T, NP> ld_words(const T* p) {
+    Words<T, NP> r;
+    const const_words q = (const_words)(reinterpret_cast<uintptr_t>(p));
+#pragma unroll
+    for (int i = 0; i < Words<T, NP>::kCount; ++i) r.w[i] = q[i];
+    return r;
+}
+
+template <typename T, int NP>
+__device__ __forceinline__ float word_value(const Words<T, NP>& r, int i) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(r.w[i]);
+    const uint32_t w = r.w[i >> 1];
+    return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
+}
+
+__device__ __forceinline__ float lane_value(float v, int lane) {
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
+}
+
+inline SelK selscan_params(const gspn_selscan_args& a) {
+    SelK k{};
+    k.seq = make_seq(a.seq);
+    k.channels = static_cast<int32_t>(a.channels);
+    k.groups = static_cast<int32_t>(a.groups);
+    k.n = static_cast<int32_t>(a.n);
+    k.per = static_cast<int32_t>(a.channels / a.groups);
+    k.softplus = a.softplus != 0;
+    k.blocks = (k.per + 63) / 64;
+    k.x = a.x;
+    k.dt = a.dt;
+    k.z = a.z;
+    k.B = a.B;
+    k.C = a.C;
+    k.out = a.out;
+    k.ldx = a.ldx;
+    k.lddt = a.lddt;
+    k.ldz = a.ldz;
+    k.ldb = a.ldb;
+    k.ldc = a.ldc;
+    k.ldo = a.ldo;
+    k.A = a.A;
+    k.D = a.D;
+    k.bias = a.dt_bias;
+    k.state = a.state;
+    k.check = a.checkpoints;
+    k.gy = a.gy;
+    k.dx = a.dx;
+    k.ddt = a.ddt;
+    k.dz = a.dz;
+    k.ldgy = a.ldgy;
+    k.lddx = a.lddx;
+    k.ldddt = a.ldddt;
+    k.lddz = a.lddz;
+    return k;
+}
+
+#ifdef GSPN_CHECK_LAUNCHES
+inline void replay_selscan(const char* kn, const gspn_selscan_args& a, const SelK& k, int64_t ids, int es) {
+    GSPN_REPLAY_ROWS(kn, "x", a.x, a.seq.rows, a.ldx, a.channels, es);
+    GSPN_REPLAY_ROWS(kn, "dt", a.dt, a.seq.rows, a.lddt, a.channels, es);
+    GSPN_REPLAY_ROWS(kn, "z", a.z, a.seq.rows, a.ldz, a.channels, es);
+    GSPN_REPLAY_ROWS(kn, "B", a.B, a.seq.rows, a.ldb, a.groups * a.n, es);
+    GSPN_REPLAY_ROWS(kn, "C", a.C, a.seq.rows, a.ldc, a.groups * a.n, es);
+    GSPN_REPLAY_ROWS(kn, "out", a.out, a.seq.rows, a.ldo, a.channels, es);
+    GSPN_REPLAY_ROWS(kn, "A", a.A, a.channels, a.n, a.n, 4);
+    GSPN_REPLAY_ROWS(kn, "state", a.state, a.seq.nslots, a.channels * a.n, a.channels * a.n, 4);
+    if (k.carry) {
+        GSPN_REPLAY_ROWS(kn, "carry", k.carry, ids * a.n, a.channels, a.channels, 4);
+        GSPN_REPLAY_ROWS(kn, "sums", k.sums, ids, a.channels, a.channels, 4);
+    }
+    if (a.checkpoints) {
+        const int64_t kept = chunk_ids(a.seq.cu != nullptr, a.seq.rows, a.seq.nseq, kCheckShift);
+        GSPN_REPLAY_ROWS(kn, "checkpoints", a.checkpoints, kept * a.n, a.channels, a.channels, 4);
+    }
+}
+#endif
+
+}  // namespace gspn

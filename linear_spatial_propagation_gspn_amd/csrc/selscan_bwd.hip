@@ -1,0 +1,588 @@
+// selscan_bwd.hip -- gradients of the selective scan.
+//
+// With gy' = gy silu(z) and g = dL/dh: g_t = C_t gy'_t + a_{t+1} g_{t+1}, run
+// against the row order, and
+//   dC_t[n] = sum_c gy' h_t       dB_t[n] = sum_c g_t d x
+//   dx = d sum_n g B + D gy'      dd = sum_n g (A a h_{t-1} + x B)
+//   dA = sum_t g d a h_{t-1}      ddt = dd softplus'(dt + bias)
+// The states come back from the forward's checkpoints, one every 16 rows: a
+// wave reruns 16 rows forward, keeping a_t and a_t h_{t-1} in registers, and
+// walks back over them.  Four lanes share a channel (SPL states each), which
+// keeps those 16 rows within 128 registers.  Each of the four takes a quarter
+// of the rows for what is per row and channel (softplus, gate, the outputs);
+// the row's values reach the others as DPP operands.
+//
+// dB and dC are sums over channels: inside a wave by lane swaps (four values
+// a swap pair, so that each half, then quarter, of the wave carries another
+// value), over a block's four waves in LDS, over blocks by a second pass in a
+// fixed order.  The sums over rows (dA, dD, ddt_bias) stay in registers per
+// chunk and are joined the same way.
+//
+// Bound by the vector ALU: about 20 instructions an element and state.
+#include "selscan.hpp"
+
+#include <type_traits>
+
+namespace gspn {
+namespace {
+
+constexpr float kLn2 = 0.693147180559945309417f;
+constexpr int kTile = 1 << kCheckShift;  // rows rerun together
+
+template <int kCtrl>
+__device__ __forceinline__ float dpp(float v) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), kCtrl, 0xf, 0xf, true));
+}
+
+// Lane J of each quad to all four (SPLIT 4), or the lane's own value.
+template <int SPLIT, int J>
+__device__ __forceinline__ float quad_of(float v) {
+    if constexpr (SPLIT == 1) return v;
+    return dpp<J * 0x55>(v);
+}
+
+template <int SPLIT>
+__device__ __forceinline__ float quad_sum(float v) {
+    if constexpr (SPLIT == 1) return v;
+    v += dpp<0xB1>(v);  // lanes 1 0 3 2
+    v += dpp<0x4E>(v);  // lanes 2 3 0 1
+    return v;
+}
+
+__device__ __forceinline__ float swap_add32(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+__device__ __forceinline__ float swap_add16(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Four values summed over the wave's channels (lanes equal modulo SPLIT): the
+// 16-lane row r of the wave receives the sum of v[r == 1 ? 2 : r == 2 ? 1 : r].
+template <int SPLIT>
+__device__ __forceinline__ float channel_sum(const float (&v)[4]) {
+    float s = swap_add16(swap_add32(v[0], v[1]), swap_add32(v[2], v[3]));
+    s += dpp<0x128>(s);  // row rotate by 8
+    s += dpp<0x124>(s);  // by 4
+    if constexpr (SPLIT == 1) {
+        s += dpp<0x122>(s);
+        s += dpp<0x121>(s);
+    }
+    return s;
+}
+
+// The chunk's own part of dL/dh before its first row, and its sum of d: what
+// the join over chunks needs.  One lane a channel, as in the forward.
+template <typename T, int NP, bool kScalar>
+__global__ __launch_bounds__(64) void selscan_bwd_local_kernel(const SelK p) {
+    const Chunk ck = find_chunk(p.seq, blockIdx.x, p.shift);
+    if (ck.seq < 0 || ck.k == 0) return;  // nothing before it
+    const int g = blockIdx.y / p.blocks;
+    const int local = (blockIdx.y - g * p.blocks) * 64 + static_cast<int>(threadIdx.x);
+    const bool live = local < p.per;
+    const int c = g * p.per + (live ? local : p.per - 1);
+    float A2[NP], ag[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        A2[i] = i < p.n ? p.A[static_cast<int64_t>(c) * p.n + i] * kLog2E : 0.0f;
+        ag[i] = 0.0f;
+    }
+    const float bias = p.bias ? p.bias[c] : 0.0f;
+    const T* const dt = static_cast<const T*>(p.dt);
+    const T* const z = static_cast<const T*>(p.z);
+    const T* const gy = static_cast<const T*>(p.gy);
+    const T* const C = static_cast<const T*>(p.C) + static_cast<int64_t>(g) * p.n;
+    const int lane = threadIdx.x;
+    float sum = 0.0f;
+    constexpr int U = 4;
+    float nd[U], ng[U], nz[U], nc[U];
+    auto load = [&](int t0) {  // rows t0, t0 - 1, ..
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int64_t t = t0 - i >= ck.r0 ? t0 - i : ck.r0;
+            nd[i] = Store<T>::ld(dt + t * p.lddt + c);
+            ng[i] = Store<T>::ld(gy + t * p.ldgy + c);
+            nz[i] = z ? Store<T>::ld(z + t * p.ldz + c) : 0.0f;
+            if constexpr (!kScalar) nc[i] = lane < p.n ? Store<T>::ld(C + t * p.ldc + lane) : 0.0f;
+        }
+    };
+    load(ck.r1 - 1);
+    for (int t0 = ck.r1 - 1; t0 >= ck.r0; t0 -= U) {
+        float dv[U], gv[U], zv[U], cv[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            dv[i] = nd[i];
+            gv[i] = ng[i];
+            zv[i] = nz[i];
+            if constexpr (!kScalar) cv[i] = nc[i];
+        }
+        if (t0 - U >= ck.r0) load(t0 - U);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int t = t0 - i;
+            if (t < ck.r0) break;
+            Words<T, NP> cw;
+            if constexpr (kScalar) cw = ld_words<T, NP>(C + t * p.ldc);
+            float d = dv[i] + bias;
+            if (p.softplus) d = softplus_f(d);
+            sum += d;
+            float gp = gv[i];
+            if (z) gp *= zv[i] * gate_sigmoid<T>(zv[i]);
+#pragma unroll
+            for (int n = 0; n < NP; ++n) {
+                const float cc = kScalar ? word_value<T, NP>(cw, n) : lane_value(cv[i], n);
+                ag[n] = __builtin_amdgcn_exp2f(d * A2[n]) * __builtin_fmaf(cc, gp, ag[n]);
+            }
+        }
+    }
+    if (!live) return;
+    const int64_t id = chunk_base(p.seq, ck.seq, ck.begin, p.shift) + ck.k;
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+        if (i < p.n) p.carry[(id * p.n + i) * p.channels + c] = ag[i];
+    p.sums[id * p.channels + c] = sum;
+}
+
+// The join against the row order: carry[k] := dL/dh after chunk k's last row.
+__global__ __launch_bounds__(256) void selscan_bwd_join_kernel(const SelK p) {
+    const int s = blockIdx.x;
+    const int begin = seq_begin(p.seq, s);
+    const int end = seq_end(p.seq, s, begin);
+    const int count = static_cast<int>(chunks_each(end - begin, p.shift));
+    if (count < 2) return;
+    const int64_t e = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x;  // n * channels + c
+    if (e >= static_cast<int64_t>(p.channels) * p.n) return;
+    const int i = static_cast<int>(e / p.channels);
+    const int c = static_cast<int>(e - static_cast<int64_t>(i) * p.channels);
+    const float A2 = p.A[static_cast<int64_t>(c) * p.n + i] * kLog2E;
+    const int64_t base = chunk_base(p.seq, s, begin, p.shift);
+    const int64_t step = static_cast<int64_t>(p.channels) * p.n;
+    float* const q = p.carry + base * step + e;
+    const float* const sd = p.sums + base * p.channels + c;
+    float g = 0.0f;
+    constexpr int U = 8;
+    for (int k0 = count - 1; k0 >= 0; k0 -= U) {
+        float own[U], d[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const bool in = k0 - j > 0;  // the first chunk left nothing
+            own[j] = in ? q[(k0 - j) * step] : 0.0f;
+            d[j] = in ? sd[static_cast<int64_t>(k0 - j) * p.channels] : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            if (k0 - j >= 0) {
+                q[(k0 - j) * step] = g;
+                g = __builtin_fmaf(__builtin_amdgcn_exp2f(d[j] * A2), g, own[j]);
+            }
+        }
+    }
+}
+
+template <int NP>
+struct Split {
+    static constexpr int kLanes = NP >= 4 ? 4 : 1;      // lanes sharing a channel
+    static constexpr int kStates = NP / kLanes;         // states a lane
+    static constexpr int kRows = kTile / kLanes;        // rows of a tile a lane has to itself
+    static constexpr int kWaveCh = 64 / kLanes;         // channels a wave
+    static constexpr int kBlockCh = 4 * kWaveCh;        // channels a block
+};
+
+template <typename T, int NP, bool kGate>
+__global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
+    typedef Split<NP> S;
+    constexpr int SPLIT = S::kLanes, SPL = S::kStates, R = S::kRows;
+    __shared__ __attribute__((aligned(16))) float bc[2][kTile][2 * NP];
+    __shared__ float red[2][4][kTile][2 * NP];
+    const Chunk ck = find_chunk(p.seq, blockIdx.x, p.shift);
+    const int g = blockIdx.y / p.blocks;
+    const int cb = blockIdx.y - g * p.blocks;
+    const int tid = threadIdx.x;
+    const int wave = tid >> 6;
+    const int lane = tid & 63;
+    const int sub = lane % SPLIT;
+    const int local = cb * S::kBlockCh + wave * S::kWaveCh + lane / SPLIT;
+    const bool live = local < p.per;
+    const int c = g * p.per + (live ? local : p.per - 1);
+    const int n0 = sub * SPL;
+    float dA[SPL], dD = 0.0f, db = 0.0f;
+#pragma unroll
+    for (int s = 0; s < SPL; ++s) dA[s] = 0.0f;
+
+    if (ck.seq >= 0 && ck.r1 > ck.r0) {
+        float A2[SPL], ag[SPL];
+#pragma unroll
+        for (int s = 0; s < SPL; ++s) {
+            const bool in = n0 + s < p.n;
+            A2[s] = in ? p.A[static_cast<int64_t>(c) * p.n + n0 + s] * kLog2E : 0.0f;
+            ag[s] = 0.0f;
+            if (ck.count > 1 && in) {
+                const int64_t id = chunk_base(p.seq, ck.seq, ck.begin, p.shift) + ck.k;
+                ag[s] = p.carry[(id * p.n + n0 + s) * p.channels + c];
+            }
+        }
+        const float bias = p.bias ? p.bias[c] : 0.0f;
+        const float skip = p.D ? p.D[c] : 0.0f;
+        const T* const x = static_cast<const T*>(p.x) + c;
+        const T* const dt = static_cast<const T*>(p.dt) + c;
+        const T* const z = static_cast<const T*>(p.z) + (kGate ? c : 0);
+        const T* const gy = static_cast<const T*>(p.gy) + c;
+        const T* const B = static_cast<const T*>(p.B) + static_cast<int64_t>(g) * p.n;
+        const T* const C = static_cast<const T*>(p.C) + static_cast<int64_t>(g) * p.n;
+        const int64_t check0 =
+            chunk_base(p.seq, ck.seq, ck.begin, kCheckShift) + ((ck.r0 - ck.begin) >> kCheckShift);
+
+        constexpr int kBC = (kTile * 2 * NP + 255) / 256;  // values of B and C a lane stages
+        T nx[R], nd[R], ng[R], nz[R];
+        float nbc[kBC], nh[SPL];
+        auto load = [&](int tile) {
+            const int base = ck.r0 + tile * kTile;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int r = base + i * SPLIT + sub;
+                const int64_t t = r < ck.r1 ? r : ck.r1 - 1;
+                nx[i] = x[t * p.ldx];
+                nd[i] = dt[t * p.lddt];
+                ng[i] = gy[t * p.ldgy];
+                if constexpr (kGate) nz[i] = z[t * p.ldz];
+            }
+#pragma unroll
+            for (int i = 0; i < kBC; ++i) {
+                const int v = tid + i * 256;
+                const int r = base + v / (2 * NP);
+                const int n = v % NP;
+                nbc[i] = 0.0f;
+                if (v < kTile * 2 * NP && n < p.n && r < ck.r1)
+                    nbc[i] = (v / NP) % 2 == 0 ? Store<T>::ld(B + r * p.ldb + n) : Store<T>::ld(C + r * p.ldc + n);
+            }
+#pragma unroll
+            for (int s = 0; s < SPL; ++s)
+                nh[s] = n0 + s < p.n ? p.check[((check0 + tile) * p.n + n0 + s) * p.channels + c] : 0.0f;
+        };
+        // the block's sums of dB and dC of a finished tile
+        auto flush = [&](int tile, int buf) {
+#pragma unroll
+            for (int i = 0; i < kBC; ++i) {
+                const int v = tid + i * 256;
+                const int row = v / (2 * NP);
+                const int n = v % NP;
+                const int r = ck.r0 + tile * kTile + row;
+                if (v < kTile * 2 * NP && n < p.n && r < ck.r1) {
+                    const int m = v % (2 * NP);
+                    const float s = (red[buf][0][row][m] + red[buf][1][row][m]) +
+                                    (red[buf][2][row][m] + red[buf][3][row][m]);
+                    const int64_t o = ((static_cast<int64_t>(cb) * p.seq.rows + r) * 2 + (v / NP) % 2) * p.groups + g;
+                    p.partbc[o * p.n + n] = s;
+                }
+            }
+        };
+
+        const int tiles = (ck.r1 - ck.r0 + kTile - 1) / kTile;
+        load(tiles - 1);
+        int buf = 0;
+        for (int tile = tiles - 1; tile >= 0; --tile, buf ^= 1) {
+            const int base = ck.r0 + tile * kTile;
+#pragma unroll
+            for (int i = 0; i < kBC; ++i) {
+                const int v = tid + i * 256;
+                if (v < kTile * 2 * NP) (&bc[buf][0][0])[v] = nbc[i];
+            }
+            float xv[R], dv[R], uv[R], gp[R], sg[R], gz[R], yv[R], h[SPL];
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const bool in = live && base + i * SPLIT + sub < ck.r1;
+                const float v = Store<T>::ld(&nd[i]) + bias;
+                dv[i] = p.softplus ? softplus_f(v) : v;
+                sg[i] = p.softplus ? sigmoid(v) : 1.0f;
+                dv[i] = in ? dv[i] : 0.0f;
+                xv[i] = in ? Store<T>::ld(&nx[i]) : 0.0f;
+                gp[i] = in ? Store<T>::ld(&ng[i]) : 0.0f;
+                gz[i] = yv[i] = 0.0f;
+                if constexpr (kGate) {
+                    const float zv = Store<T>::ld(&nz[i]);
+                    const float s = gate_sigmoid<T>(zv);
+                    gz[i] = gp[i] * silu_grad(zv, s);
+                    gp[i] *= zv * s;
+                    gp[i] = in ? gp[i] : 0.0f;
+                }
+                uv[i] = dv[i] * xv[i];
+            }
+#pragma unroll
+            for (int s = 0; s < SPL; ++s) h[s] = nh[s];
+            __syncthreads();
+            if (tile + 1 < tiles) flush(tile + 1, buf ^ 1);
+            if (tile > 0) load(tile - 1);
+
+            float a[kTile][SPL], q[kTile][SPL];  // q = a_t h_{t-1}
+            auto forward = [&](auto jc, int i) {
+                constexpr int J = decltype(jc)::value;
+                const int t = i * SPLIT + J;
+                float b[SPL];
+                widen(ld_pack<float, SPL>(&bc[buf][t][n0]), b);
+                const float d = quad_of<SPLIT, J>(dv[i]);
+                const float u = quad_of<SPLIT, J>(uv[i]);
+#pragma unroll
+                for (int s = 0; s < SPL; ++s) {
+                    a[t][s] = __builtin_amdgcn_exp2f(d * A2[s]);
+                    q[t][s] = a[t][s] * h[s];
+                    h[s] = __builtin_fmaf(u, b[s], q[t][s]);
+                }
+                if constexpr (kGate) {
+                    float cv[SPL], y = 0.0f;
+                    widen(ld_pack<float, SPL>(&bc[buf][t][NP + n0]), cv);
+#pragma unroll
+                    for (int s = 0; s < SPL; ++s) y = __builtin_fmaf(cv[s], h[s], y);
+                    y = quad_sum<SPLIT>(y);
+                    yv[i] = SPLIT == 1 || sub == J ? y : yv[i];
+                }
+            };
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                forward(std::integral_constant<int, 0>{}, i);
+                if constexpr (SPLIT == 4) {
+                    forward(std::integral_constant<int, 1>{}, i);
+                    forward(std::integral_constant<int, 2>{}, i);
+                    forward(std::integral_constant<int, 3>{}, i);
+                }
+            }
+
+            float gb[R], ga[R], vB[4], vC[4];
+            auto back = [&](auto jc, int i) {
+                constexpr int J = decltype(jc)::value;
+                const int t = i * SPLIT + J;
+                float b[SPL], cv[SPL];
+                widen(ld_pack<float, SPL>(&bc[buf][t][n0]), b);
+                widen(ld_pack<float, SPL>(&bc[buf][t][NP + n0]), cv);
+                const float d = quad_of<SPLIT, J>(dv[i]);
+                const float u = quad_of<SPLIT, J>(uv[i]);
+                const float y = quad_of<SPLIT, J>(gp[i]);
+                float sb = 0.0f, sa = 0.0f;
+#pragma unroll
+                for (int s = 0; s < SPL; ++s) {
+                    const float gt = __builtin_fmaf(cv[s], y, ag[s]);
+                    const int m = ((kTile - 1 - t) * SPL + s) % 4;
+                    vC[m] = y * __builtin_fmaf(u, b[s], q[t][s]);
+                    vB[m] = gt * u;
+                    sb = __builtin_fmaf(gt, b[s], sb);
+                    const float gq = gt * q[t][s];
+                    sa = __builtin_fmaf(gq, A2[s], sa);
+                    dA[s] = __builtin_fmaf(gq, d, dA[s]);
+                    ag[s] = a[t][s] * gt;
+                }
+                sb = quad_sum<SPLIT>(sb);
+                sa = quad_sum<SPLIT>(sa);
+                if (SPLIT == 1 || sub == J) {
+                    gb[i] = sb;
+                    ga[i] = sa;
+                }
+                if (((kTile - 1 - t) * SPL + SPL) % 4 == 0) {
+                    // row r of the wave holds value m(r): row t + 4 / SPL - 1 - m / SPL, state m % SPL
+                    const float rb = channel_sum<SPLIT>(vB);
+                    const float rc = channel_sum<SPLIT>(vC);
+                    const int r = lane >> 4;
+                    const int m = r == 1 ? 2 : r == 2 ? 1 : r;
+                    if ((lane & 15) < SPLIT) {
+                        float* const o = &red[buf][wave][t + 4 / SPL - 1 - m / SPL][n0 + m % SPL];
+                        o[0] = rb;
+                        o[NP] = rc;
+                    }
+                }
+            };
+#pragma unroll
+            for (int i = R - 1; i >= 0; --i) {
+                if constexpr (SPLIT == 4) {
+                    back(std::integral_constant<int, 3>{}, i);
+                    back(std::integral_constant<int, 2>{}, i);
+                    back(std::integral_constant<int, 1>{}, i);
+                }
+                back(std::integral_constant<int, 0>{}, i);
+            }
+
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int r = base + i * SPLIT + sub;
+                if (live && r < ck.r1) {
+                    const int64_t t = r;
+                    const float ddt = __builtin_fmaf(xv[i], gb[i], ga[i] * kLn2) * sg[i];
+                    Store<T>::st(static_cast<T*>(p.dx) + t * p.lddx + c, __builtin_fmaf(skip, gp[i], dv[i] * gb[i]));
+                    Store<T>::st(static_cast<T*>(p.ddt) + t * p.ldddt + c, ddt);
+                    dD = __builtin_fmaf(gp[i], xv[i], dD);
+                    db += ddt;
+                    if constexpr (kGate)
+                        Store<T>::st(static_cast<T*>(p.dz) + t * p.lddz + c, gz[i] * __builtin_fmaf(skip, xv[i], yv[i]));
+                }
+            }
+        }
+        __syncthreads();
+        flush(0, buf ^ 1);
+    }
+
+    float* const part = p.part + static_cast<int64_t>(blockIdx.x) * (p.n + 2) * p.channels + c;
+    dD = quad_sum<SPLIT>(dD);
+    db = quad_sum<SPLIT>(db);
+    if (!live) return;
+#pragma unroll
+    for (int s = 0; s < SPL; ++s)
+        if (n0 + s < p.n) part[static_cast<int64_t>(n0 + s) * p.channels] = dA[s];
+    if (sub == 0) {
+        part[static_cast<int64_t>(p.n) * p.channels] = dD;
+        part[static_cast<int64_t>(p.n + 1) * p.channels] = db;
+    }
+}
+
+// dB and dC from the channel blocks' sums [block][row][2][groups * n], in the
+// blocks' order; rows outside the sequences have no sums and stay as they are.
+template <typename T>
+__global__ __launch_bounds__(256) void selscan_bc_kernel(const SelK p, T* __restrict__ dB, T* __restrict__ dC) {
+    const int64_t gn = static_cast<int64_t>(p.groups) * p.n;
+    const int64_t per = static_cast<int64_t>(p.seq.rows) * 2 * gn;
+    const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (e >= per) return;
+    const int64_t row = e / (2 * gn);
+    const int64_t m = e - row * 2 * gn;
+    const int lo = seq_begin(p.seq, 0);
+    const int hi = seq_end(p.seq, p.seq.nseq - 1, seq_begin(p.seq, p.seq.nseq - 1));
+    if (row < lo || row >= hi) return;
+    float s = 0.0f;
+    int b = 0;
+    for (; b + 8 <= p.blocks; b += 8) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = p.partbc[(b + j) * per + e];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s += v[j];
+    }
+    for (; b < p.blocks; ++b) s += p.partbc[b * per + e];
+    if (m < gn) Store<T>::st(dB + row * gn + m, s);
+    else Store<T>::st(dC + row * gn + (m - gn), s);
+}
+
+template <typename T, int NP>
+void run_bwd(const SelK& k, dim3 grid, hipStream_t stream) {
+    if (k.z) hipLaunchKernelGGL((selscan_bwd_kernel<T, NP, true>), grid, dim3(256), 0, stream, k);
+    else hipLaunchKernelGGL((selscan_bwd_kernel<T, NP, false>), grid, dim3(256), 0, stream, k);
+}
+
+template <typename T>
+void run_bwd_n(const SelK& k, dim3 grid, hipStream_t stream) {
+    if (k.n <= 1) run_bwd<T, 1>(k, grid, stream);
+    else if (k.n <= 4) run_bwd<T, 4>(k, grid, stream);
+    else if (k.n <= 8) run_bwd<T, 8>(k, grid, stream);
+    else run_bwd<T, 16>(k, grid, stream);
+}
+
+template <typename T, int NP>
+void run_local(bool scalar, const SelK& k, dim3 grid, hipStream_t stream) {
+    if (scalar) hipLaunchKernelGGL((selscan_bwd_local_kernel<T, NP, true>), grid, dim3(64), 0, stream, k);
+    else hipLaunchKernelGGL((selscan_bwd_local_kernel<T, NP, false>), grid, dim3(64), 0, stream, k);
+}
+
+template <typename T>
+void run_local_n(const SelK& k, dim3 grid, hipStream_t stream) {
+    const int es = sizeof(T);
+    auto scalar = [&](int np) { return k.n == np && np * es % 4 == 0 && aligned_rows(k.C, k.ldc, es, 4); };
+    if (k.n <= 1) run_local<T, 1>(sizeof(T) == 4 && scalar(1), k, grid, stream);
+    else if (k.n <= 4) run_local<T, 4>(scalar(4), k, grid, stream);
+    else if (k.n <= 8) run_local<T, 8>(scalar(8), k, grid, stream);
+    else run_local<T, 16>(scalar(16), k, grid, stream);
+}
+
+int64_t block_channels(int64_t n) { return n <= 1 ? Split<1>::kBlockCh : Split<4>::kBlockCh; }
+
+}  // namespace
+
+int64_t selscan_bwd_blocks(int64_t channels, int64_t groups, int64_t n) {
+    const int64_t bch = block_channels(n);
+    return (channels / groups + bch - 1) / bch;
+}
+
+// Rows per chunk of the backward: equal sequences stay whole where they give
+// two waves a SIMD, otherwise chunks as long as two waves a SIMD allow (the
+// kernel's registers leave room for two).
+int selscan_bwd_shift(int64_t rows, int64_t nseq, int64_t channels, int64_t groups, int64_t n, bool ragged) {
+    const int64_t waves = 4 * groups * selscan_bwd_blocks(channels, groups, n);
+    int64_t longest = rows;
+    if (!ragged && nseq > 0) longest = rows / nseq;
+    int whole = kCheckShift;
+    while ((int64_t{1} << whole) < longest) ++whole;
+    if (!ragged && nseq * waves >= 2048) return whole;
+    int shift = whole;
+    while (shift > kCheckShift && (rows >> shift) * waves < 2048) --shift;
+    return shift;
+}
+
+hipError_t launch_selscan_bwd(const gspn_selscan_args& a, int dtype, hipStream_t stream) {
+    SelK k = selscan_params(a);
+    const bool ragged = a.seq.cu != nullptr;
+    k.shift = selscan_bwd_shift(a.seq.rows, a.seq.nseq, a.channels, a.groups, a.n, ragged);
+    const int64_t ids = chunk_ids(ragged, a.seq.rows, a.seq.nseq, k.shift);
+    const bool cut = (int64_t{1} << k.shift) < (ragged ? a.seq.rows : a.seq.rows / a.seq.nseq);
+    const int64_t bcb = selscan_bwd_blocks(a.channels, a.groups, a.n);
+    // workspace: [dB/dC sums][dA, dD, ddt_bias sums][carries][sums of d]
+    k.partbc = static_cast<float*>(a.workspace);
+    k.part = k.partbc + bcb * a.seq.rows * 2 * a.groups * a.n;
+    k.carry = k.part + ids * (a.n + 2) * a.channels;
+    k.sums = k.carry + ids * a.n * a.channels;
+    const int es = dtype == kF32 ? 4 : 2;
+    (void)es;
+    hipError_t e;
+    if (cut) {
+        const dim3 lg(static_cast<unsigned>(ids), static_cast<unsigned>(k.groups * k.blocks));
+#ifdef GSPN_CHECK_LAUNCHES
+        replay_selscan("selscan_bwd_local_kernel", a, k, ids, es);
+#endif
+        GSPN_REPLAYED("selscan_bwd_local_kernel", 64, 0);
+        if (dtype == kF32) run_local_n<float>(k, lg, stream);
+        else run_local_n<bf16_t>(k, lg, stream);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        const dim3 jg(static_cast<unsigned>(a.seq.nseq), static_cast<unsigned>((a.channels * a.n + 255) / 256));
+        GSPN_REPLAYED("selscan_bwd_join_kernel", 256, 0);
+        hipLaunchKernelGGL(selscan_bwd_join_kernel, jg, dim3(256), 0, stream, k);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    k.blocks = static_cast<int32_t>(bcb);
+    const dim3 grid(static_cast<unsigned>(ids), static_cast<unsigned>(k.groups * bcb));
+#ifdef GSPN_CHECK_LAUNCHES
+    if (!cut) k.carry = nullptr;
+    replay_selscan("selscan_bwd_kernel", a, k, ids, es);
+    GSPN_REPLAY_ROWS("selscan_bwd_kernel", "gy", a.gy, a.seq.rows, a.ldgy, a.channels, es);
+    GSPN_REPLAY_ROWS("selscan_bwd_kernel", "dx", a.dx, a.seq.rows, a.lddx, a.channels, es);
+    GSPN_REPLAY_ROWS("selscan_bwd_kernel", "ddt", a.ddt, a.seq.rows, a.ldddt, a.channels, es);
+    GSPN_REPLAY_ROWS("selscan_bwd_kernel", "dz", a.dz, a.seq.rows, a.lddz, a.channels, es);
+    GSPN_REPLAY_ROWS("selscan_bwd_kernel", "row sums", k.part, ids * (a.n + 2), a.channels, a.channels, 4);
+    GSPN_REPLAY_ROWS("selscan_bwd_kernel", "channel sums", k.partbc, bcb * a.seq.rows, 2 * a.groups * a.n,
+                     2 * a.groups * a.n, 4);
+#endif
+    GSPN_REPLAYED("selscan_bwd_kernel", 256, 2 * kTile * 32 * 4 * 5);
+    if (dtype == kF32) run_bwd_n<float>(k, grid, stream);
+    else run_bwd_n<bf16_t>(k, grid, stream);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+
+    const int64_t values = a.seq.rows * 2 * a.groups * a.n;
+    if (values > 0) {
+        const dim3 bg(static_cast<unsigned>((values + 255) / 256));
+        GSPN_REPLAY_ROWS("selscan_bc_kernel", "dB", a.dB, a.seq.rows, a.groups * a.n, a.groups * a.n, es);
+        GSPN_REPLAY_ROWS("selscan_bc_kernel", "dC", a.dC, a.seq.rows, a.groups * a.n, a.groups * a.n, es);
+        GSPN_REPLAYED("selscan_bc_kernel", 256, 0);
+        if (dtype == kF32)
+            hipLaunchKernelGGL(selscan_bc_kernel<float>, bg, dim3(256), 0, stream, k, static_cast<float*>(a.dB),
+                               static_cast<float*>(a.dC));
+        else
+            hipLaunchKernelGGL(selscan_bc_kernel<bf16_t>, bg, dim3(256), 0, stream, k, static_cast<bf16_t*>(a.dB),
+                               static_cast<bf16_t*>(a.dC));
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    ReduceK r{};
+    r.part = k.part;
+    r.parts = ids;
+    r.c = a.channels;
+    r.ld = r.cols = (a.n + 2) * a.channels;
+    r.o[0] = {a.dA, static_cast<int32_t>(a.n), a.n, 1};
+    r.o[1] = {a.dD, 1, 1, 0};
+    r.o[2] = {a.ddt_bias, 1, 1, 0};
+    return launch_reduce_parts(r, stream);
+}
+
+}  // namespace gspn
