@@ -42,10 +42,10 @@
  *    entry, zero starts from zeros; NULL: every sequence starts from zeros.
  *  - Empty calls (no rows and no sequence, or no channel) return GSPN_OK and
  *    queue nothing.
- *  - Aliasing: an output, a state pool, a workspace may overlap nothing else.
- *    (Row-strided tensors may interleave, as the halves of one matrix do:
- *    inputs are not compared with each other, and an output only by the
- *    bytes from its first to its last element.)
+ *  - Aliasing: an output, a state pool, a workspace may overlap nothing else
+ *    (inputs may overlap inputs).  Row tensors of the same row stride in
+ *    bytes may be column slices of one matrix; of different strides they are
+ *    compared by the bytes from their first to their last element.
  *  - Sums over rows (gradients of parameters) are formed in fixed order:
  *    repeated calls give the same bits.
  */

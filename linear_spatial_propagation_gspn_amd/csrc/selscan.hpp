@@ -40,10 +40,12 @@ struct SelK {
 // drops the low bits of a small e, which are added back to first order (the
 // whole error of u = 1 + e is e - (u - 1), and log(1 + e) changes by it over u,
 // with u between 1 and 2 wherever it matters).
-__device__ __forceinline__ float softplus_f(float v) {
+// slope: its derivative 1 / (1 + e^{-v}), from the same e.
+__device__ __forceinline__ float softplus_f(float v, float* slope = nullptr) {
     const float e = __builtin_amdgcn_exp2f(-__builtin_fabsf(v) * kLog2E);
     const float u = 1.0f + e;
     const float l = __builtin_amdgcn_logf(u) * 0.693147180559945309417f + (e - (u - 1.0f));
+    if (slope) *slope = (v > 0.0f ? 1.0f : e) * __builtin_amdgcn_rcpf(u);
     return (v > 0.0f ? v : 0.0f) + l;
 }
 

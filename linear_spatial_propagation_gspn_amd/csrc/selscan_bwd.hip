@@ -294,8 +294,8 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
             for (int i = 0; i < R; ++i) {
                 const bool in = live && base + i * SPLIT + sub < ck.r1;
                 const float v = Store<T>::ld(&nd[i]) + bias;
-                dv[i] = p.softplus ? softplus_f(v) : v;
-                sg[i] = p.softplus ? sigmoid(v) : 1.0f;
+                sg[i] = 1.0f;
+                dv[i] = p.softplus ? softplus_f(v, &sg[i]) : v;
                 dv[i] = in ? dv[i] : 0.0f;
                 xv[i] = in ? Store<T>::ld(&nx[i]) : 0.0f;
                 gp[i] = in ? Store<T>::ld(&ng[i]) : 0.0f;

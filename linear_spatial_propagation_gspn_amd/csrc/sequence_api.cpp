@@ -29,7 +29,7 @@ class Buffers {
     // [rows][c] elements of es bytes, rows ld apart.
     void rows(const void* p, int64_t n, int64_t ld, int64_t c, int64_t es, bool out, bool optional = false) {
         if (ld < c || ld > kMaxStride) fail(GSPN_ERR_BAD_SHAPE);
-        add(p, n < 1 || c < 1 ? 0 : ((n - 1) * ld + c) * es, es, out, optional);
+        add(p, n < 1 || c < 1 ? 0 : ((n - 1) * ld + c) * es, es, out, optional, ld * es, c * es);
     }
     void flat(const void* p, int64_t bytes, int64_t align, bool out, bool optional = false) {
         add(p, bytes, align, out, optional);
@@ -40,9 +40,7 @@ class Buffers {
             if (!b_[i].out) continue;
             for (int j = 0; j < count_; ++j) {
                 if (i == j || (b_[j].out && j < i)) continue;
-                const uintptr_t a0 = reinterpret_cast<uintptr_t>(b_[i].p), b0 = reinterpret_cast<uintptr_t>(b_[j].p);
-                if (a0 < b0 + static_cast<uintptr_t>(b_[j].bytes) && b0 < a0 + static_cast<uintptr_t>(b_[i].bytes))
-                    return GSPN_ERR_ALIASING;
+                if (overlap(b_[i], b_[j])) return GSPN_ERR_ALIASING;
             }
         }
         return GSPN_OK;
@@ -52,6 +50,7 @@ class Buffers {
     struct One {
         const void* p;
         int64_t bytes;
+        int64_t pitch, width;  // bytes from row to row and of a row; 0: one run
         bool out;
     };
     static constexpr int kMax = 32;
@@ -59,17 +58,28 @@ class Buffers {
     int count_ = 0;
     gspn_status st_ = GSPN_OK;
 
+    // Whether two tensors share a byte.  Row tensors of one pitch may lie in
+    // one another's gaps, as column slices of one matrix do.
+    static bool overlap(const One& a, const One& b) {
+        const int64_t a0 = reinterpret_cast<int64_t>(a.p), b0 = reinterpret_cast<int64_t>(b.p);
+        if (a0 >= b0 + b.bytes || b0 >= a0 + a.bytes) return false;
+        if (a.pitch == 0 || a.pitch != b.pitch) return true;
+        const int64_t d = ((b0 - a0) % a.pitch + a.pitch) % a.pitch;  // b's columns after a's
+        return d < a.width || d + b.width > a.pitch;
+    }
+
     void fail(gspn_status s) {
         if (st_ == GSPN_OK) st_ = s;
     }
-    void add(const void* p, int64_t bytes, int64_t align, bool out, bool optional) {
+    void add(const void* p, int64_t bytes, int64_t align, bool out, bool optional, int64_t pitch = 0,
+             int64_t width = 0) {
         if (bytes == 0) return;  // nothing of it is touched
         if (!p) {
             if (!optional) fail(GSPN_ERR_NULL_POINTER);
             return;
         }
         if (reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(align) != 0) fail(GSPN_ERR_MISALIGNED);
-        if (count_ < kMax) b_[count_++] = {p, bytes, out};
+        if (count_ < kMax) b_[count_++] = {p, bytes, pitch, width, out};
     }
 };
 
