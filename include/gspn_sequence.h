@@ -15,7 +15,7 @@
  * Conventions shared by every call here
  * -------------------------------------
  *  - Rows.  A tensor [rows][c] has unit column stride and a row stride `ld`
- *    in elements (ld >= c), so that the halves or slices of a projection's
+ *    in elements (c <= ld <= 2^27), so that the halves or slices of a projection's
  *    rows are taken as they are.  Alignment: the element size.  Row strides
  *    and offsets may pass 32 bits; rows < 2^31, c <= 2^19.
  *  - Storage type: x, dt, z, B, C, h, gate and their gradients and outputs
@@ -63,7 +63,7 @@ extern "C" {
 #define GSPN_SCAN_MAX_STATE 16
 #define GSPN_JOIN_MAX_CHANNELS 16384
 /* Rows between two kept states of a scan (gspn_selective_scan_fwd). */
-#define GSPN_SCAN_CHECKPOINT_ROWS 16
+#define GSPN_SCAN_CHECKPOINT_ROWS 8
 
 /* The sequences of one call (see "Sequences" and "Slots" above). */
 typedef struct {
@@ -132,7 +132,7 @@ gspn_status gspn_causal_conv_bwd(const gspn_conv_args* args, int dtype, void* st
  *   state          pool [nslots][channels][n] fp32 or NULL: receives h after
  *                  the last row (an empty sequence as in the convolution)
  *   checkpoints    NULL, or gspn_selective_scan_checkpoint_bytes() bytes: the
- *                  fp32 states before every 16th row of each sequence, for
+ *                  fp32 states before every 8th row of each sequence, for
  *                  the backward
  *   workspace      gspn_selective_scan_workspace_bytes() bytes, 4-byte aligned
  * gspn_selective_scan_step: one row per sequence (rows == nseq; cu and resume

@@ -19,7 +19,9 @@
 namespace gspn {
 namespace {
 
-constexpr int kSelRows = 4;  // rows whose loads are in flight together
+#ifndef GSPN_SELSCAN_WAVES
+#define GSPN_SELSCAN_WAVES 8192
+#endif
 
 // One wave: one chunk of one sequence, 64 channels of one group.
 // kOut false: the chunk from zero; its last state and sum of d to carry/sums.
@@ -35,8 +37,13 @@ __global__ __launch_bounds__(64) void selscan_kernel(const SelK p) {
     const bool live = local < p.per;
     const int c = g * p.per + (live ? local : p.per - 1);
 
+    // Only the first chunk starts from the pool entry.  The chunk sums take
+    // it in (what they leave for the next chunk includes it) and keep a copy
+    // in the last chunk's place, which nothing else uses: the second pass
+    // overwrites the entry while its first chunk starts.
     int slot = kNoSlot;
-    if (kOut && p.state) slot = slot_of(p.seq, ck.seq);
+    if (p.state && (kOut || ck.k == 0)) slot = slot_of(p.seq, ck.seq);
+    const bool resumed = slot >= 0 && p.seq.resume && p.seq.resume[ck.seq] != 0;
 
     float A2[NP], h[NP];
 #pragma unroll
@@ -44,91 +51,156 @@ __global__ __launch_bounds__(64) void selscan_kernel(const SelK p) {
         A2[i] = i < p.n ? p.A[static_cast<int64_t>(c) * p.n + i] * kLog2E : 0.0f;
         h[i] = 0.0f;
     }
-    const int64_t id = chunk_base(p.seq, ck.seq, ck.begin, p.shift) + ck.k;
     const int64_t plane = static_cast<int64_t>(p.channels);
-    if (kOut) {
-        if (ck.count > 1) {
-#pragma unroll
-            for (int i = 0; i < NP; ++i)
-                if (i < p.n) h[i] = p.carry[(id * p.n + i) * plane + c];
-        } else if (slot >= 0 && p.seq.resume && p.seq.resume[ck.seq] != 0) {
+    const int64_t id = chunk_base(p.seq, ck.seq, ck.begin, p.shift) + ck.k;
+    float* const carry = p.carry + id * p.n * plane;  // null for whole sequences, and then unused
+    if (ck.k == 0) {
+        if (resumed && (!kOut || ck.count == 1)) {
 #pragma unroll
             for (int i = 0; i < NP; ++i)
                 if (i < p.n) h[i] = p.state[(static_cast<int64_t>(slot) * plane + c) * p.n + i];
+            if (!kOut && live) {
+#pragma unroll
+                for (int i = 0; i < NP; ++i)
+                    if (i < p.n) carry[((ck.count - 1) * static_cast<int64_t>(p.n) + i) * plane + c] = h[i];
+            }
+        } else if (resumed || (kOut && ck.count > kDirectChunks)) {
+            const int64_t from = ck.count > kDirectChunks ? 0 : ck.count - 1;  // the join has put it in its place
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+                if (i < p.n) h[i] = carry[(from * p.n + i) * plane + c];
+        }
+    } else if (kOut && ck.count > kDirectChunks) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+            if (i < p.n) h[i] = carry[i * plane + c];
+    } else if (kOut) {
+        for (int k = -ck.k; k < 0; ++k) {
+            const float d = p.sums[(id + k) * plane + c];
+            float last[NP];
+#pragma unroll
+            for (int i = 0; i < NP; ++i) last[i] = i < p.n ? carry[(k * static_cast<int64_t>(p.n) + i) * plane + c] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < NP; ++i) h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * A2[i]), h[i], last[i]);
         }
     }
     const float bias = p.bias ? p.bias[c] : 0.0f;
     const float skip = p.D ? p.D[c] : 0.0f;
-    const bool gated = p.z != nullptr;
-    const T* const x = static_cast<const T*>(p.x);
-    const T* const dt = static_cast<const T*>(p.dt);
-    const T* const z = static_cast<const T*>(p.z);
-    const T* const B = static_cast<const T*>(p.B) + static_cast<int64_t>(g) * p.n;
-    const T* const C = static_cast<const T*>(p.C) + static_cast<int64_t>(g) * p.n;
-    T* const out = static_cast<T*>(p.out);
+    const bool gated = kOut && p.z != nullptr;
+    // Row pointers are uniform (scalar registers) and step row by row; the
+    // lane's column is a 32-bit offset.  Past the chunk they stay on its last
+    // row.
+    const unsigned col = static_cast<unsigned>(c);
+    const int64_t first = ck.r0;
+    const T* xr = static_cast<const T*>(p.x) + first * p.ldx;
+    const T* dr = static_cast<const T*>(p.dt) + first * p.lddt;
+    const T* zr = gated ? static_cast<const T*>(p.z) + first * p.ldz : nullptr;
+    const T* Br = static_cast<const T*>(p.B) + first * p.ldb + static_cast<int64_t>(g) * p.n;
+    const T* Cr = static_cast<const T*>(p.C) + first * p.ldc + static_cast<int64_t>(g) * p.n;
+    T* outr = kOut ? static_cast<T*>(p.out) + first * p.ldo : nullptr;
     const int lane = threadIdx.x;
     const bool mine = lane < 2 * NP && (lane & (NP - 1)) < p.n;
-    const T* const bc = (lane < NP ? B : C) + (lane & (NP - 1));
-    const int64_t ldbc = lane < NP ? p.ldb : p.ldc;
+    const unsigned bcol = static_cast<unsigned>(lane & (NP - 1));
 
+    constexpr int kSelRows = NP == 1 ? 8 : 4;  // rows whose loads are in flight together
     float sum = 0.0f;
-    float nx[kSelRows], nd[kSelRows], nz[kSelRows], nb[kSelRows];
-    auto load = [&](int t0) {
+    T nx[kSelRows], nd[kSelRows], nz[kSelRows];
+    float nb[kSelRows];
+    int loaded = ck.r0;  // the row that the pointers are on
+    auto load = [&]() {
 #pragma unroll
         for (int i = 0; i < kSelRows; ++i) {
-            const int64_t t = t0 + i < ck.r1 ? t0 + i : ck.r1 - 1;
-            nx[i] = Store<T>::ld(x + t * p.ldx + c);
-            nd[i] = Store<T>::ld(dt + t * p.lddt + c);
-            nz[i] = kOut && gated ? Store<T>::ld(z + t * p.ldz + c) : 0.0f;
-            if constexpr (!kScalar) nb[i] = mine ? Store<T>::ld(bc + t * ldbc) : 0.0f;
+            nx[i] = xr[col];
+            nd[i] = dr[col];
+            if (gated) nz[i] = zr[col];
+            if constexpr (!kScalar) nb[i] = mine ? Store<T>::ld((lane < NP ? Br : Cr) + bcol) : 0.0f;
+            if (++loaded < ck.r1) {
+                xr += p.ldx;
+                dr += p.lddt;
+                if (gated) zr += p.ldz;
+                if constexpr (!kScalar) {
+                    Br += p.ldb;
+                    Cr += p.ldc;
+                }
+            }
         }
     };
-    if (ck.r0 < ck.r1) load(ck.r0);
+    Words<T, NP> bw, cw, bw1, cw1;
+    int words = ck.r0;
+    if (ck.r0 < ck.r1) {
+        load();
+        if constexpr (kScalar) {
+            bw1 = ld_words<T, NP>(Br);
+            if (kOut) cw1 = ld_words<T, NP>(Cr);
+        }
+    }
     for (int t0 = ck.r0; t0 < ck.r1; t0 += kSelRows) {
         if (kOut && p.check && ((t0 - ck.begin) & ((1 << kCheckShift) - 1)) == 0) {
             const int64_t kid = chunk_base(p.seq, ck.seq, ck.begin, kCheckShift) + ((t0 - ck.begin) >> kCheckShift);
+            float* const q = p.check + kid * p.n * plane;
 #pragma unroll
             for (int i = 0; i < NP; ++i)
-                if (i < p.n && live) p.check[(kid * p.n + i) * plane + c] = h[i];
+                if (i < p.n && live) q[i * plane + col] = h[i];
         }
-        float xv[kSelRows], dv[kSelRows], zv[kSelRows], bv[kSelRows];
+        // what is per row and channel, four rows at once; a row past the
+        // chunk gets a step of zero, which leaves the state as it is
+        float xv[kSelRows], d[kSelRows], f[kSelRows], bv[kSelRows];
 #pragma unroll
         for (int i = 0; i < kSelRows; ++i) {
-            xv[i] = nx[i];
-            dv[i] = nd[i];
-            zv[i] = nz[i];
+            xv[i] = Store<T>::ld(&nx[i]);
+            d[i] = Store<T>::ld(&nd[i]) + bias;
+            f[i] = 1.0f;
             if constexpr (!kScalar) bv[i] = nb[i];
         }
-        if (t0 + kSelRows < ck.r1) load(t0 + kSelRows);
+        if (p.softplus) {
+#pragma unroll
+            for (int i = 0; i < kSelRows; ++i) d[i] = softplus_f(d[i]);
+        }
+        if (gated) {
+#pragma unroll
+            for (int i = 0; i < kSelRows; ++i) {
+                const float zv = Store<T>::ld(&nz[i]);
+                f[i] = zv * gate_sigmoid<T>(zv);
+            }
+        }
+        if (t0 + kSelRows > ck.r1) {
+#pragma unroll
+            for (int i = 0; i < kSelRows; ++i) {
+                if (t0 + i >= ck.r1) d[i] = xv[i] = 0.0f;
+            }
+        } else if (t0 + kSelRows < ck.r1) {
+            load();
+        }
 #pragma unroll
         for (int i = 0; i < kSelRows; ++i) {
-            const int t = t0 + i;
-            if (t >= ck.r1) break;
-            Words<T, NP> bw, cw;
             if constexpr (kScalar) {
-                bw = ld_words<T, NP>(B + t * p.ldb);
-                if (kOut) cw = ld_words<T, NP>(C + t * p.ldc);
+                bw = bw1;
+                cw = cw1;
+                if (++words < ck.r1) {  // the next row's words come while this one is computed
+                    Br += p.ldb;
+                    Cr += p.ldc;
+                }
+                bw1 = ld_words<T, NP>(Br);
+                if (kOut) cw1 = ld_words<T, NP>(Cr);
             }
-            float d = dv[i] + bias;
-            if (p.softplus) d = softplus_f(d);
-            const float u = d * xv[i];
-            sum += d;
-            float y = 0.0f;
+            const float u = d[i] * xv[i];
+            float y = kOut ? skip * xv[i] : 0.0f;
+            sum += d[i];
 #pragma unroll
             for (int n = 0; n < NP; ++n) {
                 const float b = kScalar ? word_value<T, NP>(bw, n) : lane_value(bv[i], n);
-                const float a = __builtin_amdgcn_exp2f(d * A2[n]);
+                const float a = __builtin_amdgcn_exp2f(d[i] * A2[n]);
                 h[n] = __builtin_fmaf(a, h[n], u * b);
                 if (kOut) {
                     const float cc = kScalar ? word_value<T, NP>(cw, n) : lane_value(bv[i], NP + n);
                     y = __builtin_fmaf(cc, h[n], y);
                 }
             }
-            if (kOut) {
-                y = __builtin_fmaf(skip, xv[i], y);
-                if (gated) y *= zv[i] * gate_sigmoid<T>(zv[i]);
+            if (kOut && t0 + i < ck.r1) {
+                y *= f[i];
                 if (slot == kBadSlot) y = __builtin_nanf("");
-                if (live && p.out) Store<T>::st(out + t * p.ldo + c, y);
+                if (live) Store<T>::st(outr + col, y);
+                outr += p.ldo;
             }
         }
     }
@@ -145,29 +217,28 @@ __global__ __launch_bounds__(64) void selscan_kernel(const SelK p) {
     }
 }
 
-// The join over a sequence's chunks: carry[k] := the state before chunk k.
-// A lane per (state, channel); the chunks' values are loaded eight at a time
-// ahead of the serial products.
+// The join over the chunks of a long sequence: carry[k] := the state before
+// chunk k.  A lane per (state, channel); the chunks' values are loaded 16 at a
+// time ahead of the serial products.
 __global__ __launch_bounds__(256) void selscan_join_kernel(const SelK p) {
     const int s = blockIdx.x;
     const int begin = seq_begin(p.seq, s);
     const int end = seq_end(p.seq, s, begin);
     const int count = static_cast<int>(chunks_each(end - begin, p.shift));
-    if (count < 2) return;
+    if (count <= kDirectChunks) return;
     const int slot = p.state ? slot_of(p.seq, s) : kNoSlot;
-    const int64_t e = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x;  // n * channels + c
-    if (e >= static_cast<int64_t>(p.channels) * p.n) return;
-    const int i = static_cast<int>(e / p.channels);
-    const int c = static_cast<int>(e - static_cast<int64_t>(i) * p.channels);
+    const int e = static_cast<int>(blockIdx.y * 256 + threadIdx.x);  // n * channels + c
+    if (e >= p.channels * p.n) return;
+    const int i = e / p.channels;
+    const int c = e - i * p.channels;
     const float A2 = p.A[static_cast<int64_t>(c) * p.n + i] * kLog2E;
-    float h = 0.0f;
-    if (slot >= 0 && p.seq.resume && p.seq.resume[s] != 0)
-        h = p.state[(static_cast<int64_t>(slot) * p.channels + c) * p.n + i];
     const int64_t base = chunk_base(p.seq, s, begin, p.shift);
     const int64_t step = static_cast<int64_t>(p.channels) * p.n;
     float* const q = p.carry + base * step + e;
     const float* const sd = p.sums + base * p.channels + c;
-    constexpr int U = 8;
+    float h = 0.0f;
+    if (slot >= 0 && p.seq.resume && p.seq.resume[s] != 0) h = q[(count - 1) * step];
+    constexpr int U = 16;
     for (int k0 = 0; k0 < count; k0 += U) {
         float last[U], d[U];
 #pragma unroll
@@ -180,7 +251,9 @@ __global__ __launch_bounds__(256) void selscan_join_kernel(const SelK p) {
         for (int j = 0; j < U; ++j) {
             if (k0 + j < count) {
                 q[(k0 + j) * step] = h;
-                h = __builtin_fmaf(__builtin_amdgcn_exp2f(d[j] * A2), h, last[j]);
+                // the first chunk's last state includes the one it began with
+                const float a = k0 + j > 0 ? __builtin_amdgcn_exp2f(d[j] * A2) : 0.0f;
+                h = __builtin_fmaf(a, h, last[j]);
             }
         }
     }
@@ -304,11 +377,11 @@ int selscan_shift(int64_t rows, int64_t nseq, int64_t channels, int64_t groups, 
     const int64_t waves = groups * ((channels / groups + 63) / 64);
     int64_t longest = rows;
     if (!ragged && nseq > 0) longest = rows / nseq;
-    int whole = kCheckShift;
+    int whole = kMinChunkShift;
     while ((int64_t{1} << whole) < longest) ++whole;
     if (!ragged && nseq * waves >= 1536) return whole;
     int shift = whole;
-    while (shift > kCheckShift && (rows >> shift) * waves < 4096) --shift;
+    while (shift > kMinChunkShift && (rows >> shift) * waves < GSPN_SELSCAN_WAVES) --shift;
     return shift;
 }
 
@@ -334,11 +407,13 @@ hipError_t launch_selscan_fwd(const gspn_selscan_args& a, int dtype, hipStream_t
         else run_selscan_n<bf16_t>(false, k, grid, stream);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        const dim3 jg(static_cast<unsigned>(a.seq.nseq), static_cast<unsigned>((a.channels * a.n + 255) / 256));
-        GSPN_REPLAYED("selscan_join_kernel", 256, 0);
-        hipLaunchKernelGGL(selscan_join_kernel, jg, dim3(256), 0, stream, k);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
+        if (needs_join(a, k.shift)) {
+            const dim3 jg(static_cast<unsigned>(a.seq.nseq), static_cast<unsigned>((a.channels * a.n + 255) / 256));
+            GSPN_REPLAYED("selscan_join_kernel", 256, 0);
+            hipLaunchKernelGGL(selscan_join_kernel, jg, dim3(256), 0, stream, k);
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
     }
 #ifdef GSPN_CHECK_LAUNCHES
     replay_selscan("selscan_kernel", a, k, ids, es);

@@ -82,6 +82,15 @@ __device__ __forceinline__ float lane_value(float v, int lane) {
     return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
 }
 
+// Sequences of up to this many chunks need no launch to join them: a chunk
+// walks over those before it (or behind it, in the backward) by itself, at
+// about one row's work each.
+constexpr int kDirectChunks = 16;
+
+inline bool needs_join(const gspn_selscan_args& a, int shift) {
+    return (a.seq.cu ? (a.seq.rows >> shift) + 1 : chunks_each(a.seq.rows / a.seq.nseq, shift)) > kDirectChunks;
+}
+
 inline SelK selscan_params(const gspn_selscan_args& a) {
     SelK k{};
     k.seq = make_seq(a.seq);

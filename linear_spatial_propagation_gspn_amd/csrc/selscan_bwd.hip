@@ -5,10 +5,10 @@
 //   dC_t[n] = sum_c gy' h_t       dB_t[n] = sum_c g_t d x
 //   dx = d sum_n g B + D gy'      dd = sum_n g (A a h_{t-1} + x B)
 //   dA = sum_t g d a h_{t-1}      ddt = dd softplus'(dt + bias)
-// The states come back from the forward's checkpoints, one every 16 rows: a
-// wave reruns 16 rows forward, keeping a_t and a_t h_{t-1} in registers, and
+// The states come back from the forward's checkpoints, one every 8 rows: a
+// wave reruns 8 rows forward, keeping a_t and a_t h_{t-1} in registers, and
 // walks back over them.  Four lanes share a channel (SPL states each), which
-// keeps those 16 rows within 128 registers.  Each of the four takes a quarter
+// keeps those 8 rows within 64 registers.  Each of the four takes a quarter
 // of the rows for what is per row and channel (softplus, gate, the outputs);
 // the row's values reach the others as DPP operands.
 //
@@ -26,12 +26,25 @@
 namespace gspn {
 namespace {
 
+#ifndef GSPN_SELSCAN_BWD_WAVES
+#define GSPN_SELSCAN_BWD_WAVES 16384
+#endif
 constexpr float kLn2 = 0.693147180559945309417f;
 constexpr int kTile = 1 << kCheckShift;  // rows rerun together
 
 template <int kCtrl>
 __device__ __forceinline__ float dpp(float v) {
     return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), kCtrl, 0xf, 0xf, true));
+}
+
+// A uniform pointer to `row` of a tensor, kept in scalar registers: without
+// this the compiler carries a 64-bit vector address for every tensor and row of
+// a tile over the loop, and spills.
+template <typename T>
+__device__ __forceinline__ T* row_at(const void* p, int64_t row, int64_t ld) {
+    uintptr_t a = reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(row * ld) * sizeof(T);
+    asm volatile("" : "+s"(a));
+    return reinterpret_cast<T*>(a);
 }
 
 // Lane J of each quad to all four (SPLIT 4), or the lane's own value.
@@ -90,50 +103,76 @@ __global__ __launch_bounds__(64) void selscan_bwd_local_kernel(const SelK p) {
         ag[i] = 0.0f;
     }
     const float bias = p.bias ? p.bias[c] : 0.0f;
-    const T* const dt = static_cast<const T*>(p.dt);
-    const T* const z = static_cast<const T*>(p.z);
-    const T* const gy = static_cast<const T*>(p.gy);
-    const T* const C = static_cast<const T*>(p.C) + static_cast<int64_t>(g) * p.n;
+    const unsigned col = static_cast<unsigned>(c);
+    const int64_t last = ck.r1 - 1;
+    const T* dr = static_cast<const T*>(p.dt) + last * p.lddt;
+    const T* gr = static_cast<const T*>(p.gy) + last * p.ldgy;
+    const T* zr = p.z ? static_cast<const T*>(p.z) + last * p.ldz : nullptr;
+    const T* Cr = static_cast<const T*>(p.C) + last * p.ldc + static_cast<int64_t>(g) * p.n;
     const int lane = threadIdx.x;
     float sum = 0.0f;
-    constexpr int U = 4;
-    float nd[U], ng[U], nz[U], nc[U];
-    auto load = [&](int t0) {  // rows t0, t0 - 1, ..
+    constexpr int U = NP == 1 ? 8 : 4;
+    T nd[U], ng[U], nz[U];
+    float nc[U];
+    int loaded = ck.r1 - 1;  // the row that the pointers are on
+    auto load = [&]() {      // the next U rows against the row order; past the chunk, its first row again
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const int64_t t = t0 - i >= ck.r0 ? t0 - i : ck.r0;
-            nd[i] = Store<T>::ld(dt + t * p.lddt + c);
-            ng[i] = Store<T>::ld(gy + t * p.ldgy + c);
-            nz[i] = z ? Store<T>::ld(z + t * p.ldz + c) : 0.0f;
-            if constexpr (!kScalar) nc[i] = lane < p.n ? Store<T>::ld(C + t * p.ldc + lane) : 0.0f;
+            nd[i] = dr[col];
+            ng[i] = gr[col];
+            if (zr) nz[i] = zr[col];
+            if constexpr (!kScalar) nc[i] = lane < p.n ? Store<T>::ld(Cr + lane) : 0.0f;
+            if (loaded-- > ck.r0) {
+                dr -= p.lddt;
+                gr -= p.ldgy;
+                if (zr) zr -= p.ldz;
+                if constexpr (!kScalar) Cr -= p.ldc;
+            }
         }
     };
-    load(ck.r1 - 1);
+    Words<T, NP> cw, cw1;
+    int words = ck.r1 - 1;
+    load();
+    if constexpr (kScalar) cw1 = ld_words<T, NP>(Cr);
     for (int t0 = ck.r1 - 1; t0 >= ck.r0; t0 -= U) {
-        float dv[U], gv[U], zv[U], cv[U];
+        float d[U], gp[U], cv[U];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            dv[i] = nd[i];
-            gv[i] = ng[i];
-            zv[i] = nz[i];
+            d[i] = Store<T>::ld(&nd[i]) + bias;
+            gp[i] = Store<T>::ld(&ng[i]);
             if constexpr (!kScalar) cv[i] = nc[i];
         }
-        if (t0 - U >= ck.r0) load(t0 - U);
+        if (p.softplus) {
+#pragma unroll
+            for (int i = 0; i < U; ++i) d[i] = softplus_f(d[i]);
+        }
+        if (p.z) {
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const float zv = Store<T>::ld(&nz[i]);
+                gp[i] *= zv * gate_sigmoid<T>(zv);
+            }
+        }
+        if (t0 - U + 1 < ck.r0) {  // rows before the chunk: no decay, no gradient
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                if (t0 - i < ck.r0) d[i] = gp[i] = 0.0f;
+            }
+        } else if (t0 - U >= ck.r0) {
+            load();
+        }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const int t = t0 - i;
-            if (t < ck.r0) break;
-            Words<T, NP> cw;
-            if constexpr (kScalar) cw = ld_words<T, NP>(C + t * p.ldc);
-            float d = dv[i] + bias;
-            if (p.softplus) d = softplus_f(d);
-            sum += d;
-            float gp = gv[i];
-            if (z) gp *= zv[i] * gate_sigmoid<T>(zv[i]);
+            if constexpr (kScalar) {
+                cw = cw1;
+                if (words-- > ck.r0) Cr -= p.ldc;
+                cw1 = ld_words<T, NP>(Cr);
+            }
+            sum += d[i];
 #pragma unroll
             for (int n = 0; n < NP; ++n) {
                 const float cc = kScalar ? word_value<T, NP>(cw, n) : lane_value(cv[i], n);
-                ag[n] = __builtin_amdgcn_exp2f(d * A2[n]) * __builtin_fmaf(cc, gp, ag[n]);
+                ag[n] = __builtin_amdgcn_exp2f(d[i] * A2[n]) * __builtin_fmaf(cc, gp[i], ag[n]);
             }
         }
     }
@@ -145,24 +184,25 @@ __global__ __launch_bounds__(64) void selscan_bwd_local_kernel(const SelK p) {
     p.sums[id * p.channels + c] = sum;
 }
 
-// The join against the row order: carry[k] := dL/dh after chunk k's last row.
+// The join of long sequences, against the row order: carry[k] := dL/dh after
+// chunk k's last row.
 __global__ __launch_bounds__(256) void selscan_bwd_join_kernel(const SelK p) {
     const int s = blockIdx.x;
     const int begin = seq_begin(p.seq, s);
     const int end = seq_end(p.seq, s, begin);
     const int count = static_cast<int>(chunks_each(end - begin, p.shift));
-    if (count < 2) return;
-    const int64_t e = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x;  // n * channels + c
-    if (e >= static_cast<int64_t>(p.channels) * p.n) return;
-    const int i = static_cast<int>(e / p.channels);
-    const int c = static_cast<int>(e - static_cast<int64_t>(i) * p.channels);
+    if (count <= kDirectChunks) return;
+    const int e = static_cast<int>(blockIdx.y * 256 + threadIdx.x);  // n * channels + c
+    if (e >= p.channels * p.n) return;
+    const int i = e / p.channels;
+    const int c = e - i * p.channels;
     const float A2 = p.A[static_cast<int64_t>(c) * p.n + i] * kLog2E;
     const int64_t base = chunk_base(p.seq, s, begin, p.shift);
     const int64_t step = static_cast<int64_t>(p.channels) * p.n;
     float* const q = p.carry + base * step + e;
     const float* const sd = p.sums + base * p.channels + c;
     float g = 0.0f;
-    constexpr int U = 8;
+    constexpr int U = 16;
     for (int k0 = count - 1; k0 >= 0; k0 -= U) {
         float own[U], d[U];
 #pragma unroll
@@ -218,35 +258,46 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
             const bool in = n0 + s < p.n;
             A2[s] = in ? p.A[static_cast<int64_t>(c) * p.n + n0 + s] * kLog2E : 0.0f;
             ag[s] = 0.0f;
-            if (ck.count > 1 && in) {
-                const int64_t id = chunk_base(p.seq, ck.seq, ck.begin, p.shift) + ck.k;
-                ag[s] = p.carry[(id * p.n + n0 + s) * p.channels + c];
+        }
+        const int64_t id = chunk_base(p.seq, ck.seq, ck.begin, p.shift) + ck.k;
+        // dL/dh after the chunk: the join's, or the chunks behind it here
+        const bool joined = ck.count > kDirectChunks;
+        for (int k = joined ? 0 : ck.count - 1 - ck.k; k >= (joined ? 0 : 1); --k) {
+            const float d = joined ? 0.0f : p.sums[(id + k) * p.channels + c];
+#pragma unroll
+            for (int s = 0; s < SPL; ++s) {
+                const float own = n0 + s < p.n ? p.carry[((id + k) * p.n + n0 + s) * p.channels + c] : 0.0f;
+                ag[s] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * A2[s]), ag[s], own);
             }
         }
         const float bias = p.bias ? p.bias[c] : 0.0f;
         const float skip = p.D ? p.D[c] : 0.0f;
-        const T* const x = static_cast<const T*>(p.x) + c;
-        const T* const dt = static_cast<const T*>(p.dt) + c;
-        const T* const z = static_cast<const T*>(p.z) + (kGate ? c : 0);
-        const T* const gy = static_cast<const T*>(p.gy) + c;
         const T* const B = static_cast<const T*>(p.B) + static_cast<int64_t>(g) * p.n;
         const T* const C = static_cast<const T*>(p.C) + static_cast<int64_t>(g) * p.n;
         const int64_t check0 =
             chunk_base(p.seq, ck.seq, ck.begin, kCheckShift) + ((ck.r0 - ck.begin) >> kCheckShift);
+        // A lane's place in a group of SPLIT rows, from the group's uniform
+        // first row: four row strides fit 32 bits.
+        auto place = [&](int64_t ld) { return static_cast<unsigned>(sub * static_cast<int>(ld) + c); };
+        const unsigned ox = place(p.ldx), od = place(p.lddt), og = place(p.ldgy), oz = kGate ? place(p.ldz) : 0;
+        const unsigned qx = place(p.lddx), qd = place(p.ldddt), qz = kGate ? place(p.lddz) : 0;
 
         constexpr int kBC = (kTile * 2 * NP + 255) / 256;  // values of B and C a lane stages
         T nx[R], nd[R], ng[R], nz[R];
         float nbc[kBC], nh[SPL];
         auto load = [&](int tile) {
             const int base = ck.r0 + tile * kTile;
+            const int left = ck.r1 - base - sub;
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const int r = base + i * SPLIT + sub;
-                const int64_t t = r < ck.r1 ? r : ck.r1 - 1;
-                nx[i] = x[t * p.ldx];
-                nd[i] = dt[t * p.lddt];
-                ng[i] = gy[t * p.ldgy];
-                if constexpr (kGate) nz[i] = z[t * p.ldz];
+                const int64_t t = base + i * SPLIT;
+                nx[i] = nd[i] = ng[i] = nz[i] = T{};
+                if (i * SPLIT < left) {
+                    nx[i] = row_at<const T>(p.x, t, p.ldx)[ox];
+                    nd[i] = row_at<const T>(p.dt, t, p.lddt)[od];
+                    ng[i] = row_at<const T>(p.gy, t, p.ldgy)[og];
+                    if constexpr (kGate) nz[i] = row_at<const T>(p.z, t, p.ldz)[oz];
+                }
             }
 #pragma unroll
             for (int i = 0; i < kBC; ++i) {
@@ -257,9 +308,10 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
                 if (v < kTile * 2 * NP && n < p.n && r < ck.r1)
                     nbc[i] = (v / NP) % 2 == 0 ? Store<T>::ld(B + r * p.ldb + n) : Store<T>::ld(C + r * p.ldc + n);
             }
+            const float* const q = row_at<const float>(p.check, (check0 + tile) * p.n, p.channels);
 #pragma unroll
             for (int s = 0; s < SPL; ++s)
-                nh[s] = n0 + s < p.n ? p.check[((check0 + tile) * p.n + n0 + s) * p.channels + c] : 0.0f;
+                nh[s] = n0 + s < p.n ? q[static_cast<unsigned>((n0 + s) * p.channels + c)] : 0.0f;
         };
         // the block's sums of dB and dC of a finished tile
         auto flush = [&](int tile, int buf) {
@@ -402,16 +454,17 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
 
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const int r = base + i * SPLIT + sub;
-                if (live && r < ck.r1) {
-                    const int64_t t = r;
+                const int64_t t = base + i * SPLIT;
+                if (live && i * SPLIT < ck.r1 - base - sub) {
                     const float ddt = __builtin_fmaf(xv[i], gb[i], ga[i] * kLn2) * sg[i];
-                    Store<T>::st(static_cast<T*>(p.dx) + t * p.lddx + c, __builtin_fmaf(skip, gp[i], dv[i] * gb[i]));
-                    Store<T>::st(static_cast<T*>(p.ddt) + t * p.ldddt + c, ddt);
+                    Store<T>::st(row_at<T>(p.dx, t, p.lddx) + qx,
+                                 __builtin_fmaf(skip, gp[i], dv[i] * gb[i]));
+                    Store<T>::st(row_at<T>(p.ddt, t, p.ldddt) + qd, ddt);
                     dD = __builtin_fmaf(gp[i], xv[i], dD);
                     db += ddt;
                     if constexpr (kGate)
-                        Store<T>::st(static_cast<T*>(p.dz) + t * p.lddz + c, gz[i] * __builtin_fmaf(skip, xv[i], yv[i]));
+                        Store<T>::st(row_at<T>(p.dz, t, p.lddz) + qz,
+                                     gz[i] * __builtin_fmaf(skip, xv[i], yv[i]));
                 }
             }
         }
@@ -505,11 +558,11 @@ int selscan_bwd_shift(int64_t rows, int64_t nseq, int64_t channels, int64_t grou
     const int64_t waves = 4 * groups * selscan_bwd_blocks(channels, groups, n);
     int64_t longest = rows;
     if (!ragged && nseq > 0) longest = rows / nseq;
-    int whole = kCheckShift;
+    int whole = kMinChunkShift;
     while ((int64_t{1} << whole) < longest) ++whole;
     if (!ragged && nseq * waves >= 2048) return whole;
     int shift = whole;
-    while (shift > kCheckShift && (rows >> shift) * waves < 2048) --shift;
+    while (shift > kMinChunkShift && (rows >> shift) * waves < GSPN_SELSCAN_BWD_WAVES) --shift;
     return shift;
 }
 
@@ -537,10 +590,12 @@ hipError_t launch_selscan_bwd(const gspn_selscan_args& a, int dtype, hipStream_t
         if (dtype == kF32) run_local_n<float>(k, lg, stream);
         else run_local_n<bf16_t>(k, lg, stream);
         if ((e = hipGetLastError()) != hipSuccess) return e;
-        const dim3 jg(static_cast<unsigned>(a.seq.nseq), static_cast<unsigned>((a.channels * a.n + 255) / 256));
-        GSPN_REPLAYED("selscan_bwd_join_kernel", 256, 0);
-        hipLaunchKernelGGL(selscan_bwd_join_kernel, jg, dim3(256), 0, stream, k);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
+        if (needs_join(a, k.shift)) {
+            const dim3 jg(static_cast<unsigned>(a.seq.nseq), static_cast<unsigned>((a.channels * a.n + 255) / 256));
+            GSPN_REPLAYED("selscan_bwd_join_kernel", 256, 0);
+            hipLaunchKernelGGL(selscan_bwd_join_kernel, jg, dim3(256), 0, stream, k);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        }
     }
     k.blocks = static_cast<int32_t>(bcb);
     const dim3 grid(static_cast<unsigned>(ids), static_cast<unsigned>(k.groups * bcb));

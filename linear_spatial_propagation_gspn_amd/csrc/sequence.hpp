@@ -208,7 +208,8 @@ int64_t conv_bwd_parts(int64_t rows, int64_t nseq, int64_t c);
 int selscan_shift(int64_t rows, int64_t nseq, int64_t channels, int64_t groups, bool ragged);
 int selscan_bwd_shift(int64_t rows, int64_t nseq, int64_t channels, int64_t groups, int64_t n, bool ragged);
 int64_t selscan_bwd_blocks(int64_t channels, int64_t groups, int64_t n);  // channel blocks of the backward
-constexpr int kCheckShift = 4;  // GSPN_SCAN_CHECKPOINT_ROWS
+constexpr int kCheckShift = 3;  // GSPN_SCAN_CHECKPOINT_ROWS
+constexpr int kMinChunkShift = 4;
 
 hipError_t launch_selscan_fwd(const gspn_selscan_args& a, int dtype, hipStream_t stream);
 hipError_t launch_selscan_step(const gspn_selscan_args& a, int dtype, hipStream_t stream);

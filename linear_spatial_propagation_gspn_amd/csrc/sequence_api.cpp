@@ -15,7 +15,7 @@ namespace {
 
 constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxChannels = int64_t{1} << 19;
-constexpr int64_t kMaxStride = int64_t{1} << 40;
+constexpr int64_t kMaxStride = int64_t{1} << 27;
 
 bool valid_dtype(int64_t dt) { return dt == GSPN_F32 || dt == GSPN_BF16; }
 int64_t elem_size(int64_t dt) { return dt == GSPN_F32 ? 4 : 2; }
@@ -28,7 +28,8 @@ class Buffers {
   public:
     // [rows][c] elements of es bytes, rows ld apart.
     void rows(const void* p, int64_t n, int64_t ld, int64_t c, int64_t es, bool out, bool optional = false) {
-        if (ld < c || ld > kMaxStride) fail(GSPN_ERR_BAD_SHAPE);
+        if (ld < c) fail(GSPN_ERR_BAD_SHAPE);
+        if (ld > kMaxStride) fail(GSPN_ERR_UNSUPPORTED);
         add(p, n < 1 || c < 1 ? 0 : ((n - 1) * ld + c) * es, es, out, optional, ld * es, c * es);
     }
     void flat(const void* p, int64_t bytes, int64_t align, bool out, bool optional = false) {

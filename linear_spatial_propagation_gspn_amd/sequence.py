@@ -35,7 +35,7 @@ from . import gspn as G
 GSPN_CONV_MIN_WIDTH, GSPN_CONV_MAX_WIDTH = 2, 4
 GSPN_SCAN_MAX_STATE = 16
 GSPN_JOIN_MAX_CHANNELS = 16384
-GSPN_SCAN_CHECKPOINT_ROWS = 16
+GSPN_SCAN_CHECKPOINT_ROWS = 8
 
 # Symbols declared in include/gspn_sequence.h.
 EXPORTS = ("gspn_causal_conv_fwd", "gspn_causal_conv_step", "gspn_causal_conv_bwd_workspace_bytes",
@@ -342,7 +342,7 @@ def gspn_selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, softpl
     1 to 16; D, dt_bias fp32 [channels].  ``state`` (fp32 [slots, channels,
     n]): continued where ``resume`` says so, left holding the last states.
     ``checkpoints`` (True, or a buffer a former call returned): also keeps the
-    states before every 16th row for gspn_selective_scan_bwd; the call then
+    states before every 8th row for gspn_selective_scan_bwd; the call then
     returns (out, checkpoints).  Rows outside the sequences of ``cu`` are left
     as they are in ``out``."""
     code = _need_rows(x, "x")
@@ -569,7 +569,7 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus: bool 
                    nseq=None) -> torch.Tensor:
     """The selective scan as a differentiable op (no state); rows outside the
     sequences of ``cu`` are zero.  The forward keeps its states before every
-    16th row (n / 4 bytes an element of x) until the backward."""
+    8th row (n / 2 bytes an element of x) until the backward."""
     return _SelectiveScan.apply(bool(softplus), cu, nseq, x, dt, A, B, C, D, z, dt_bias)
 
 

@@ -513,24 +513,31 @@ def test_empty_calls():
 
 
 def test_rows_beyond_32_bits():
-    """Row strides of 2^30 elements: the third row lies 2^32 bytes in."""
-    ld, c = 1 << 30, 16
-    big = torch.empty(3 * ld, dtype=BF16, device=DEV)
+    """The widest row stride, 2^27 elements: the last of 34 rows lies 8.25 GiB in, past 2^32 elements."""
+    ld, c, rows = 1 << 27, 16, 34
+    big = torch.empty((rows - 1) * ld + 1024, dtype=BF16, device=DEV)
     g = gen(6)
-    far = lambda at: torch.as_strided(big, (3, c), (ld, 1), at)  # noqa: E731
-    k = scan_case(g, 3, c, 1, 8, BF16)
+    far = lambda at: torch.as_strided(big, (rows, c), (ld, 1), at)  # noqa: E731
+    k = scan_case(g, rows, c, 1, 8, BF16)
     w = dev(rnd(g, c, 4))
     x, dt, z = far(0), far(64), far(128)
     for t, v in ((x, k["x"]), (dt, k["dt"]), (z, k["z"])):
         t.copy_(v)
     near = on_gpu(k)
     assert torch.equal(S.gspn_causal_conv_fwd(x, w, out=far(256)), S.gspn_causal_conv_fwd(near["x"], w))
+    for a, b in zip(S.gspn_causal_conv_bwd(x, w, None, z)[:2], S.gspn_causal_conv_bwd(near["x"], w, None, near["z"])):
+        assert torch.equal(a, b)
     o = dict(near, x=x, dt=dt, z=z)
     out, kept = run_fwd(o, checkpoints=True, out=far(512))
     assert torch.equal(out, run_fwd(near))
     for a, b in zip(run_bwd(o, x, checkpoints=kept).values(), run_bwd(near, near["x"]).values()):
         assert torch.equal(a, b)
-    assert torch.equal(S.gspn_block_join_fwd(x, z, dt)[0], S.gspn_block_join_fwd(near["x"], near["z"], near["dt"])[0])
+    pre = dev(rnd(g, c))
+    far_join, near_join = (S.gspn_block_join_fwd(a, b, d, pre=pre) for a, b, d in
+                           ((x, z, dt), (near["x"], near["z"], near["dt"])))
+    assert all(torch.equal(a, b) for a, b in zip(far_join, near_join))
+    with pytest.raises(G.GspnError):
+        S.gspn_causal_conv_fwd(torch.as_strided(big, (2, c), (ld + 1, 1)), w)
 
 
 # ------------------------------------------------------------------------------------- autograd, streams, graphs

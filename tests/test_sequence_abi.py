@@ -257,7 +257,7 @@ def test_scan_validation(lib):
         refuse(lib, "scan", kind, SHAPE, seq_nseq=7)
         refuse(lib, "scan", kind, SHAPE, lddt=23)
         refuse(lib, "scan", kind, SHAPE, ldb=31)
-        refuse(lib, "scan", kind, SHAPE, ldc=1 << 41)
+        refuse(lib, "scan", kind, UNSUP, ldc=(1 << 27) + 1)
         for f in ("x", "dt", "B", "C", "A"):
             refuse(lib, "scan", kind, NULLP, **{f: None})
             refuse(lib, "scan", kind, MISAL, **{f: lambda a, f=f: getattr(a, f) + 2})
@@ -280,9 +280,9 @@ def test_scan_validation(lib):
     refuse(lib, "scan", "fwd", OK, seq_rows=0, seq_nseq=0, x=None, A=None)
     assert lib.gspn_selective_scan_workspace_bytes(40, 2, 24, 5, 16, 0) == -1
     assert lib.gspn_selective_scan_workspace_bytes(16, 1, 24, 1, 16, 1) == 0  # one chunk
-    # states before rows 0, 16, 32 of each sequence; packed: room for any offsets
-    assert lib.gspn_selective_scan_checkpoint_bytes(80, 2, 24, 16, 0) == 2 * 3 * 16 * 24 * 4
-    assert lib.gspn_selective_scan_checkpoint_bytes(80, 2, 24, 16, 1) == (80 // 16 + 2) * 16 * 24 * 4
+    # states before rows 0, 8, .. 32 of each sequence; packed: room for any offsets
+    assert lib.gspn_selective_scan_checkpoint_bytes(80, 2, 24, 16, 0) == 2 * 5 * 16 * 24 * 4
+    assert lib.gspn_selective_scan_checkpoint_bytes(80, 2, 24, 16, 1) == (80 // 8 + 2) * 16 * 24 * 4
 
 
 def test_join_validation(lib):
