@@ -19,9 +19,6 @@
 namespace gspn {
 namespace {
 
-#ifndef GSPN_SELSCAN_WAVES
-#define GSPN_SELSCAN_WAVES 8192
-#endif
 
 // One wave: one chunk of one sequence, 64 channels of one group.
 // kOut false: the chunk from zero; its last state and sum of d to carry/sums.
@@ -32,6 +29,7 @@ __global__ __launch_bounds__(64) void selscan_kernel(const SelK p) {
     const Chunk ck = find_chunk(p.seq, blockIdx.x, p.shift);
     if (ck.seq < 0) return;
     if (!kOut && ck.k + 1 == ck.count) return;  // nothing follows
+    const int N = kScalar ? NP : p.n;
     const int g = blockIdx.y / p.blocks;
     const int local = (blockIdx.y - g * p.blocks) * 64 + static_cast<int>(threadIdx.x);
     const bool live = local < p.per;
@@ -43,45 +41,51 @@ __global__ __launch_bounds__(64) void selscan_kernel(const SelK p) {
     // overwrites the entry while its first chunk starts.
     int slot = kNoSlot;
     if (p.state && (kOut || ck.k == 0)) slot = slot_of(p.seq, ck.seq);
-    const bool resumed = slot >= 0 && p.seq.resume && p.seq.resume[ck.seq] != 0;
 
     float A2[NP], h[NP];
+    ld_states<NP, kScalar>(p.A + static_cast<int64_t>(c) * N, N, A2);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-        A2[i] = i < p.n ? p.A[static_cast<int64_t>(c) * p.n + i] * kLog2E : 0.0f;
+        A2[i] *= kLog2E;
         h[i] = 0.0f;
     }
     const int64_t plane = static_cast<int64_t>(p.channels);
     const int64_t id = chunk_base(p.seq, ck.seq, ck.begin, p.shift) + ck.k;
-    float* const carry = p.carry + id * p.n * plane;  // null for whole sequences, and then unused
-    if (ck.k == 0) {
-        if (resumed && (!kOut || ck.count == 1)) {
+    float* const carry = p.carry + id * N * plane;  // null for whole sequences, and then unused
+    if (ck.k == 0 && (!kOut || ck.count == 1)) {
+        if (slot >= 0 && p.seq.resume && p.seq.resume[ck.seq] != 0)
+            ld_states<NP, kScalar>(p.state + (static_cast<int64_t>(slot) * plane + c) * N, N, h);
+        if (!kOut && live) {
 #pragma unroll
             for (int i = 0; i < NP; ++i)
-                if (i < p.n) h[i] = p.state[(static_cast<int64_t>(slot) * plane + c) * p.n + i];
-            if (!kOut && live) {
-#pragma unroll
-                for (int i = 0; i < NP; ++i)
-                    if (i < p.n) carry[((ck.count - 1) * static_cast<int64_t>(p.n) + i) * plane + c] = h[i];
-            }
-        } else if (resumed || (kOut && ck.count > kDirectChunks)) {
-            const int64_t from = ck.count > kDirectChunks ? 0 : ck.count - 1;  // the join has put it in its place
-#pragma unroll
-            for (int i = 0; i < NP; ++i)
-                if (i < p.n) h[i] = carry[(from * p.n + i) * plane + c];
+                if (i < N) carry[((ck.count - 1) * static_cast<int64_t>(N) + i) * plane + c] = h[i];
         }
+    } else if (kOut && ck.k == 0) {
+        const int64_t from = ck.count > kDirectChunks ? 0 : ck.count - 1;  // the join has put it in its place
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+            if (i < N) h[i] = carry[(from * N + i) * plane + c];
     } else if (kOut && ck.count > kDirectChunks) {
 #pragma unroll
         for (int i = 0; i < NP; ++i)
-            if (i < p.n) h[i] = carry[i * plane + c];
+            if (i < N) h[i] = carry[i * plane + c];
     } else if (kOut) {
-        for (int k = -ck.k; k < 0; ++k) {
-            const float d = p.sums[(id + k) * plane + c];
-            float last[NP];
+        constexpr int U = 1;
+        for (int k = -ck.k; k < 0; k += U) {
+            float d[U], last[U][NP];
 #pragma unroll
-            for (int i = 0; i < NP; ++i) last[i] = i < p.n ? carry[(k * static_cast<int64_t>(p.n) + i) * plane + c] : 0.0f;
+            for (int j = 0; j < U; ++j) {
+                const bool in = k + j < 0;
+                d[j] = in ? p.sums[(id + k + j) * plane + c] : 0.0f;
 #pragma unroll
-            for (int i = 0; i < NP; ++i) h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * A2[i]), h[i], last[i]);
+                for (int i = 0; i < NP; ++i)
+                    last[j][i] = in && i < N ? carry[((k + j) * static_cast<int64_t>(N) + i) * plane + c] : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < U; ++j)  // past the last: a decay of 1 and nothing added
+#pragma unroll
+                for (int i = 0; i < NP; ++i)
+                    h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(d[j] * A2[i]), h[i], last[j][i]);
         }
     }
     const float bias = p.bias ? p.bias[c] : 0.0f;
@@ -95,11 +99,11 @@ __global__ __launch_bounds__(64) void selscan_kernel(const SelK p) {
     const T* xr = static_cast<const T*>(p.x) + first * p.ldx;
     const T* dr = static_cast<const T*>(p.dt) + first * p.lddt;
     const T* zr = gated ? static_cast<const T*>(p.z) + first * p.ldz : nullptr;
-    const T* Br = static_cast<const T*>(p.B) + first * p.ldb + static_cast<int64_t>(g) * p.n;
-    const T* Cr = static_cast<const T*>(p.C) + first * p.ldc + static_cast<int64_t>(g) * p.n;
+    const T* Br = static_cast<const T*>(p.B) + first * p.ldb + static_cast<int64_t>(g) * N;
+    const T* Cr = static_cast<const T*>(p.C) + first * p.ldc + static_cast<int64_t>(g) * N;
     T* outr = kOut ? static_cast<T*>(p.out) + first * p.ldo : nullptr;
     const int lane = threadIdx.x;
-    const bool mine = lane < 2 * NP && (lane & (NP - 1)) < p.n;
+    const bool mine = lane < 2 * NP && (lane & (NP - 1)) < N;
     const unsigned bcol = static_cast<unsigned>(lane & (NP - 1));
 
     constexpr int kSelRows = NP == 1 ? 8 : 4;  // rows whose loads are in flight together
@@ -137,10 +141,10 @@ __global__ __launch_bounds__(64) void selscan_kernel(const SelK p) {
     for (int t0 = ck.r0; t0 < ck.r1; t0 += kSelRows) {
         if (kOut && p.check && ((t0 - ck.begin) & ((1 << kCheckShift) - 1)) == 0) {
             const int64_t kid = chunk_base(p.seq, ck.seq, ck.begin, kCheckShift) + ((t0 - ck.begin) >> kCheckShift);
-            float* const q = p.check + kid * p.n * plane;
+            float* const q = p.check + kid * N * plane;
 #pragma unroll
             for (int i = 0; i < NP; ++i)
-                if (i < p.n && live) q[i * plane + col] = h[i];
+                if (i < N && live) q[i * plane + col] = h[i];
         }
         // what is per row and channel, four rows at once; a row past the
         // chunk gets a step of zero, which leaves the state as it is
@@ -208,52 +212,64 @@ __global__ __launch_bounds__(64) void selscan_kernel(const SelK p) {
     if (!kOut) {
 #pragma unroll
         for (int i = 0; i < NP; ++i)
-            if (i < p.n) p.carry[(id * p.n + i) * plane + c] = h[i];
+            if (i < N) p.carry[(id * N + i) * plane + c] = h[i];
         p.sums[id * plane + c] = sum;
     } else if (slot >= 0 && ck.k + 1 == ck.count) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
-            if (i < p.n) p.state[(static_cast<int64_t>(slot) * plane + c) * p.n + i] = h[i];
+        for (int i = 0; i < NP; ++i) {
+            float* const q = p.state + (static_cast<int64_t>(slot) * plane + c) * N + i;
+            if constexpr (kScalar && NP % 4 == 0) {
+                const float four[4] = {h[i & ~3], h[(i & ~3) + 1], h[(i & ~3) + 2], h[(i & ~3) + 3]};
+                if (i % 4 == 0) st_pack<float, 4>(q, four);
+            } else if (i < N) {
+                *q = h[i];
+            }
+        }
     }
 }
 
 // The join over the chunks of a long sequence: carry[k] := the state before
-// chunk k.  A lane per (state, channel); the chunks' values are loaded 16 at a
-// time ahead of the serial products.
+// chunk k.  A lane takes V channels of one state; the chunks' values are loaded
+// 32 / V at a time ahead of the serial products.
+template <int V>
 __global__ __launch_bounds__(256) void selscan_join_kernel(const SelK p) {
     const int s = blockIdx.x;
     const int begin = seq_begin(p.seq, s);
     const int end = seq_end(p.seq, s, begin);
     const int count = static_cast<int>(chunks_each(end - begin, p.shift));
     if (count <= kDirectChunks) return;
-    const int slot = p.state ? slot_of(p.seq, s) : kNoSlot;
-    const int e = static_cast<int>(blockIdx.y * 256 + threadIdx.x);  // n * channels + c
+    const int e = static_cast<int>(blockIdx.y * 256 + threadIdx.x) * V;  // n * channels + c
     if (e >= p.channels * p.n) return;
     const int i = e / p.channels;
     const int c = e - i * p.channels;
-    const float A2 = p.A[static_cast<int64_t>(c) * p.n + i] * kLog2E;
     const int64_t base = chunk_base(p.seq, s, begin, p.shift);
     const int64_t step = static_cast<int64_t>(p.channels) * p.n;
     float* const q = p.carry + base * step + e;
     const float* const sd = p.sums + base * p.channels + c;
-    float h = 0.0f;
-    if (slot >= 0 && p.seq.resume && p.seq.resume[s] != 0) h = q[(count - 1) * step];
-    constexpr int U = 16;
+    float A2[V], h[V];
+    widen(ld_pack<float, V>(q + (count - 1) * step), h);  // the state before the sequence
+#pragma unroll
+    for (int v = 0; v < V; ++v) A2[v] = p.A[static_cast<int64_t>(c + v) * p.n + i] * kLog2E;
+    constexpr int U = V == 1 ? 16 : 8;
     for (int k0 = 0; k0 < count; k0 += U) {
-        float last[U], d[U];
+        float last[U][V], d[U][V];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            const bool in = k0 + j + 1 < count;  // the last chunk left nothing
-            last[j] = in ? q[(k0 + j) * step] : 0.0f;
-            d[j] = in ? sd[static_cast<int64_t>(k0 + j) * p.channels] : 0.0f;
+            // from the last chunk on the values are of no use: what follows is not stored
+            const int64_t k = k0 + j < count ? k0 + j : count - 1;
+            widen(ld_pack<float, V>(q + k * step), last[j]);
+            widen(ld_pack<float, V>(sd + k * p.channels), d[j]);
         }
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             if (k0 + j < count) {
-                q[(k0 + j) * step] = h;
-                // the first chunk's last state includes the one it began with
-                const float a = k0 + j > 0 ? __builtin_amdgcn_exp2f(d[j] * A2) : 0.0f;
-                h = __builtin_fmaf(a, h, last[j]);
+                st_pack<float, V>(q + (k0 + j) * step, h);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    // the first chunk's last state includes the one it began with
+                    const float a = k0 + j > 0 ? __builtin_amdgcn_exp2f(d[j][v] * A2[v]) : 0.0f;
+                    h[v] = __builtin_fmaf(a, h[v], last[j][v]);
+                }
             }
         }
     }
@@ -347,7 +363,8 @@ template <typename T>
 void run_selscan_n(bool out, const SelK& k, dim3 grid, hipStream_t stream) {
     const int es = sizeof(T);
     auto scalar = [&](int np) {
-        return k.n == np && np * es % 4 == 0 && aligned_rows(k.B, k.ldb, es, 4) && aligned_rows(k.C, k.ldc, es, 4);
+        return k.n == np && np * es % 4 == 0 && aligned_rows(k.B, k.ldb, es, 4) && aligned_rows(k.C, k.ldc, es, 4) &&
+               (np < 4 || (aligned_rows(k.A, k.n, 4, 16) && aligned_rows(k.state, k.n, 4, 16)));
     };
     if (k.n <= 1) run_selscan<T, 1>(out, sizeof(T) == 4 && scalar(1), k, grid, stream);
     else if (k.n <= 4) run_selscan<T, 4>(out, scalar(4), k, grid, stream);
@@ -371,9 +388,13 @@ void run_step(const SelK& k, bool vec, hipStream_t stream) {
 
 // Rows per chunk.  Cutting a sequence costs a second pass over all but its
 // last chunk, so equal sequences stay whole where they fill the GPU by
-// themselves (a wave and a half a SIMD); otherwise the chunks are as long as
-// four waves a SIMD allow, 16 rows at least.
-int selscan_shift(int64_t rows, int64_t nseq, int64_t channels, int64_t groups, bool ragged) {
+// themselves (a wave and a half a SIMD).  Otherwise the chunks, of 16 rows at
+// least, are as long as eight waves a SIMD allow (four for up to 4 states,
+// whose rows are short work against the join): one sequence of 65536 rows and
+// 2048 channels with 16 states took 1027 us at 4 waves, 923 at 8, 902 at 16,
+// 16 ragged prompts of 4096 channels 344, 300 and 301, four of 3136 rows with
+// one state (768 channels, fp32) 52 at 4 against 59 at 8.
+int selscan_shift(int64_t rows, int64_t nseq, int64_t channels, int64_t groups, int64_t n, bool ragged) {
     const int64_t waves = groups * ((channels / groups + 63) / 64);
     int64_t longest = rows;
     if (!ragged && nseq > 0) longest = rows / nseq;
@@ -381,14 +402,14 @@ int selscan_shift(int64_t rows, int64_t nseq, int64_t channels, int64_t groups, 
     while ((int64_t{1} << whole) < longest) ++whole;
     if (!ragged && nseq * waves >= 1536) return whole;
     int shift = whole;
-    while (shift > kMinChunkShift && (rows >> shift) * waves < GSPN_SELSCAN_WAVES) --shift;
+    while (shift > kMinChunkShift && (rows >> shift) * waves < (n > 4 ? 8192 : 4096)) --shift;
     return shift;
 }
 
 hipError_t launch_selscan_fwd(const gspn_selscan_args& a, int dtype, hipStream_t stream) {
     SelK k = selscan_params(a);
     const bool ragged = a.seq.cu != nullptr;
-    k.shift = selscan_shift(a.seq.rows, a.seq.nseq, a.channels, a.groups, ragged);
+    k.shift = selscan_shift(a.seq.rows, a.seq.nseq, a.channels, a.groups, a.n, ragged);
     const int64_t ids = chunk_ids(ragged, a.seq.rows, a.seq.nseq, k.shift);
     const bool cut = (int64_t{1} << k.shift) < (ragged ? a.seq.rows : a.seq.rows / a.seq.nseq);
     if (cut) {
@@ -408,9 +429,12 @@ hipError_t launch_selscan_fwd(const gspn_selscan_args& a, int dtype, hipStream_t
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         if (needs_join(a, k.shift)) {
-            const dim3 jg(static_cast<unsigned>(a.seq.nseq), static_cast<unsigned>((a.channels * a.n + 255) / 256));
+            const int v = join_lane(a);
+            const dim3 jg(static_cast<unsigned>(a.seq.nseq),
+                          static_cast<unsigned>((a.channels * a.n + 256 * v - 1) / (256 * v)));
             GSPN_REPLAYED("selscan_join_kernel", 256, 0);
-            hipLaunchKernelGGL(selscan_join_kernel, jg, dim3(256), 0, stream, k);
+            if (v == 4) hipLaunchKernelGGL(selscan_join_kernel<4>, jg, dim3(256), 0, stream, k);
+            else hipLaunchKernelGGL(selscan_join_kernel<1>, jg, dim3(256), 0, stream, k);
             e = hipGetLastError();
             if (e != hipSuccess) return e;
         }

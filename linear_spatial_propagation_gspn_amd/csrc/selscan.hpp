@@ -78,6 +78,24 @@ __device__ __forceinline__ float word_value(const Words<T, NP>& r, int i) {
     return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
 }
 
+// The n (<= NP) values of a channel's row of A or of a pool entry.  kWhole: n is
+// NP and the rows are 16-byte aligned (NP a multiple of 4): one cache line a
+// lane in four accesses instead of 16.
+template <int NP, bool kWhole>
+__device__ __forceinline__ void ld_states(const float* p, int n, float (&v)[NP]) {
+    if constexpr (kWhole && NP % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < NP; i += 4) {
+            const Pack<float, 4> q = ld_pack<float, 4>(p + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[i + j] = q.e[j];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) v[i] = i < n ? p[i] : 0.0f;
+    }
+}
+
 __device__ __forceinline__ float lane_value(float v, int lane) {
     return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
 }
@@ -85,10 +103,21 @@ __device__ __forceinline__ float lane_value(float v, int lane) {
 // Sequences of up to this many chunks need no launch to join them: a chunk
 // walks over those before it (or behind it, in the backward) by itself, at
 // about one row's work each.
-constexpr int kDirectChunks = 16;
+// (Longer walks cost more than the launch: 16 prompts in 8192 rows of 4096
+// channels took 343 us at 16 chunks against 320.)
+constexpr int kDirectChunks = 4;
 
 inline bool needs_join(const gspn_selscan_args& a, int shift) {
     return (a.seq.cu ? (a.seq.rows >> shift) + 1 : chunks_each(a.seq.rows / a.seq.nseq, shift)) > kDirectChunks;
+}
+
+// Channels a lane of the joins takes: four where that still leaves a wave a
+// SIMD (16 prompts of 4096 channels: GSPN_JOIN_A us against GSPN_JOIN_B at one),
+// else one, whose longer loads ahead suit few lanes.
+inline int join_lane(const gspn_selscan_args& a) {
+    return a.channels % 4 == 0 && aligned_rows(a.workspace, a.channels, 4, 16) &&
+                   a.seq.nseq * a.channels * a.n >= 4 * 65536
+               ? 4 : 1;
 }
 
 inline SelK selscan_params(const gspn_selscan_args& a) {

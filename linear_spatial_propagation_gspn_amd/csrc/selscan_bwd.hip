@@ -26,9 +26,6 @@
 namespace gspn {
 namespace {
 
-#ifndef GSPN_SELSCAN_BWD_WAVES
-#define GSPN_SELSCAN_BWD_WAVES 16384
-#endif
 constexpr float kLn2 = 0.693147180559945309417f;
 constexpr int kTile = 1 << kCheckShift;  // rows rerun together
 
@@ -41,11 +38,14 @@ __device__ __forceinline__ float dpp(float v) {
 // this the compiler carries a 64-bit vector address for every tensor and row of
 // a tile over the loop, and spills.
 template <typename T>
-__device__ __forceinline__ T* row_at(const void* p, int64_t row, int64_t ld) {
+__device__ __forceinline__ __attribute__((address_space(1))) T* row_at(const void* p, int64_t row, int64_t ld) {
     uintptr_t a = reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(row * ld) * sizeof(T);
     asm volatile("" : "+s"(a));
-    return reinterpret_cast<T*>(a);
+    return (__attribute__((address_space(1))) T*)a;
 }
+
+__device__ __forceinline__ void st_at(__attribute__((address_space(1))) float* p, float v) { *p = v; }
+__device__ __forceinline__ void st_at(__attribute__((address_space(1))) bf16_t* p, float v) { *p = f32_to_bf16(v); }
 
 // Lane J of each quad to all four (SPLIT 4), or the lane's own value.
 template <int SPLIT, int J>
@@ -92,14 +92,16 @@ template <typename T, int NP, bool kScalar>
 __global__ __launch_bounds__(64) void selscan_bwd_local_kernel(const SelK p) {
     const Chunk ck = find_chunk(p.seq, blockIdx.x, p.shift);
     if (ck.seq < 0 || ck.k == 0) return;  // nothing before it
+    const int N = kScalar ? NP : p.n;
     const int g = blockIdx.y / p.blocks;
     const int local = (blockIdx.y - g * p.blocks) * 64 + static_cast<int>(threadIdx.x);
     const bool live = local < p.per;
     const int c = g * p.per + (live ? local : p.per - 1);
     float A2[NP], ag[NP];
+    ld_states<NP, kScalar>(p.A + static_cast<int64_t>(c) * N, N, A2);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-        A2[i] = i < p.n ? p.A[static_cast<int64_t>(c) * p.n + i] * kLog2E : 0.0f;
+        A2[i] *= kLog2E;
         ag[i] = 0.0f;
     }
     const float bias = p.bias ? p.bias[c] : 0.0f;
@@ -108,7 +110,7 @@ __global__ __launch_bounds__(64) void selscan_bwd_local_kernel(const SelK p) {
     const T* dr = static_cast<const T*>(p.dt) + last * p.lddt;
     const T* gr = static_cast<const T*>(p.gy) + last * p.ldgy;
     const T* zr = p.z ? static_cast<const T*>(p.z) + last * p.ldz : nullptr;
-    const T* Cr = static_cast<const T*>(p.C) + last * p.ldc + static_cast<int64_t>(g) * p.n;
+    const T* Cr = static_cast<const T*>(p.C) + last * p.ldc + static_cast<int64_t>(g) * N;
     const int lane = threadIdx.x;
     float sum = 0.0f;
     constexpr int U = NP == 1 ? 8 : 4;
@@ -121,7 +123,7 @@ __global__ __launch_bounds__(64) void selscan_bwd_local_kernel(const SelK p) {
             nd[i] = dr[col];
             ng[i] = gr[col];
             if (zr) nz[i] = zr[col];
-            if constexpr (!kScalar) nc[i] = lane < p.n ? Store<T>::ld(Cr + lane) : 0.0f;
+            if constexpr (!kScalar) nc[i] = lane < N ? Store<T>::ld(Cr + lane) : 0.0f;
             if (loaded-- > ck.r0) {
                 dr -= p.lddt;
                 gr -= p.ldgy;
@@ -180,42 +182,50 @@ __global__ __launch_bounds__(64) void selscan_bwd_local_kernel(const SelK p) {
     const int64_t id = chunk_base(p.seq, ck.seq, ck.begin, p.shift) + ck.k;
 #pragma unroll
     for (int i = 0; i < NP; ++i)
-        if (i < p.n) p.carry[(id * p.n + i) * p.channels + c] = ag[i];
+        if (i < N) p.carry[(id * N + i) * p.channels + c] = ag[i];
     p.sums[id * p.channels + c] = sum;
 }
 
 // The join of long sequences, against the row order: carry[k] := dL/dh after
 // chunk k's last row.
+template <int V>
 __global__ __launch_bounds__(256) void selscan_bwd_join_kernel(const SelK p) {
     const int s = blockIdx.x;
     const int begin = seq_begin(p.seq, s);
     const int end = seq_end(p.seq, s, begin);
     const int count = static_cast<int>(chunks_each(end - begin, p.shift));
     if (count <= kDirectChunks) return;
-    const int e = static_cast<int>(blockIdx.y * 256 + threadIdx.x);  // n * channels + c
+    const int e = static_cast<int>(blockIdx.y * 256 + threadIdx.x) * V;  // n * channels + c
     if (e >= p.channels * p.n) return;
     const int i = e / p.channels;
     const int c = e - i * p.channels;
-    const float A2 = p.A[static_cast<int64_t>(c) * p.n + i] * kLog2E;
     const int64_t base = chunk_base(p.seq, s, begin, p.shift);
     const int64_t step = static_cast<int64_t>(p.channels) * p.n;
     float* const q = p.carry + base * step + e;
     const float* const sd = p.sums + base * p.channels + c;
-    float g = 0.0f;
-    constexpr int U = 16;
+    float A2[V], g[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        A2[v] = p.A[static_cast<int64_t>(c + v) * p.n + i] * kLog2E;
+        g[v] = 0.0f;
+    }
+    constexpr int U = V == 1 ? 16 : 8;
     for (int k0 = count - 1; k0 >= 0; k0 -= U) {
-        float own[U], d[U];
+        float own[U][V], d[U][V];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            const bool in = k0 - j > 0;  // the first chunk left nothing
-            own[j] = in ? q[(k0 - j) * step] : 0.0f;
-            d[j] = in ? sd[static_cast<int64_t>(k0 - j) * p.channels] : 0.0f;
+            // from the first chunk on the values are of no use: what follows is not stored
+            const int64_t k = k0 - j > 0 ? k0 - j : 0;
+            widen(ld_pack<float, V>(q + k * step), own[j]);
+            widen(ld_pack<float, V>(sd + k * p.channels), d[j]);
         }
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             if (k0 - j >= 0) {
-                q[(k0 - j) * step] = g;
-                g = __builtin_fmaf(__builtin_amdgcn_exp2f(d[j] * A2), g, own[j]);
+                st_pack<float, V>(q + (k0 - j) * step, g);
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    g[v] = __builtin_fmaf(__builtin_amdgcn_exp2f(d[j][v] * A2[v]), g[v], own[j][v]);
             }
         }
     }
@@ -261,13 +271,28 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
         }
         const int64_t id = chunk_base(p.seq, ck.seq, ck.begin, p.shift) + ck.k;
         // dL/dh after the chunk: the join's, or the chunks behind it here
-        const bool joined = ck.count > kDirectChunks;
-        for (int k = joined ? 0 : ck.count - 1 - ck.k; k >= (joined ? 0 : 1); --k) {
-            const float d = joined ? 0.0f : p.sums[(id + k) * p.channels + c];
+        if (ck.count > kDirectChunks) {
 #pragma unroll
-            for (int s = 0; s < SPL; ++s) {
-                const float own = n0 + s < p.n ? p.carry[((id + k) * p.n + n0 + s) * p.channels + c] : 0.0f;
-                ag[s] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * A2[s]), ag[s], own);
+            for (int s = 0; s < SPL; ++s)
+                ag[s] = n0 + s < p.n ? p.carry[(id * p.n + n0 + s) * p.channels + c] : 0.0f;
+        } else {
+            constexpr int U = 4;
+            for (int k0 = ck.count - 1 - ck.k; k0 >= 1; k0 -= U) {
+                float d[U], own[U][SPL];
+#pragma unroll
+                for (int j = 0; j < U; ++j) {
+                    const bool in = k0 - j >= 1;
+                    d[j] = in ? p.sums[(id + k0 - j) * p.channels + c] : 0.0f;
+#pragma unroll
+                    for (int s = 0; s < SPL; ++s)
+                        own[j][s] = in && n0 + s < p.n
+                                        ? p.carry[((id + k0 - j) * p.n + n0 + s) * p.channels + c] : 0.0f;
+                }
+#pragma unroll
+                for (int j = 0; j < U; ++j)  // past the last: a decay of 1 and nothing added
+#pragma unroll
+                    for (int s = 0; s < SPL; ++s)
+                        ag[s] = __builtin_fmaf(__builtin_amdgcn_exp2f(d[j] * A2[s]), ag[s], own[j][s]);
             }
         }
         const float bias = p.bias ? p.bias[c] : 0.0f;
@@ -308,7 +333,7 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
                 if (v < kTile * 2 * NP && n < p.n && r < ck.r1)
                     nbc[i] = (v / NP) % 2 == 0 ? Store<T>::ld(B + r * p.ldb + n) : Store<T>::ld(C + r * p.ldc + n);
             }
-            const float* const q = row_at<const float>(p.check, (check0 + tile) * p.n, p.channels);
+            const auto q = row_at<const float>(p.check, (check0 + tile) * p.n, p.channels);
 #pragma unroll
             for (int s = 0; s < SPL; ++s)
                 nh[s] = n0 + s < p.n ? q[static_cast<unsigned>((n0 + s) * p.channels + c)] : 0.0f;
@@ -457,14 +482,14 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
                 const int64_t t = base + i * SPLIT;
                 if (live && i * SPLIT < ck.r1 - base - sub) {
                     const float ddt = __builtin_fmaf(xv[i], gb[i], ga[i] * kLn2) * sg[i];
-                    Store<T>::st(row_at<T>(p.dx, t, p.lddx) + qx,
-                                 __builtin_fmaf(skip, gp[i], dv[i] * gb[i]));
-                    Store<T>::st(row_at<T>(p.ddt, t, p.ldddt) + qd, ddt);
+                    st_at(row_at<T>(p.dx, t, p.lddx) + qx,
+                          __builtin_fmaf(skip, gp[i], dv[i] * gb[i]));
+                    st_at(row_at<T>(p.ddt, t, p.ldddt) + qd, ddt);
                     dD = __builtin_fmaf(gp[i], xv[i], dD);
                     db += ddt;
                     if constexpr (kGate)
-                        Store<T>::st(row_at<T>(p.dz, t, p.lddz) + qz,
-                                     gz[i] * __builtin_fmaf(skip, xv[i], yv[i]));
+                        st_at(row_at<T>(p.dz, t, p.lddz) + qz,
+                              gz[i] * __builtin_fmaf(skip, xv[i], yv[i]));
                 }
             }
         }
@@ -535,7 +560,10 @@ void run_local(bool scalar, const SelK& k, dim3 grid, hipStream_t stream) {
 template <typename T>
 void run_local_n(const SelK& k, dim3 grid, hipStream_t stream) {
     const int es = sizeof(T);
-    auto scalar = [&](int np) { return k.n == np && np * es % 4 == 0 && aligned_rows(k.C, k.ldc, es, 4); };
+    auto scalar = [&](int np) {
+        return k.n == np && np * es % 4 == 0 && aligned_rows(k.C, k.ldc, es, 4) &&
+               (np < 4 || aligned_rows(k.A, k.n, 4, 16));
+    };
     if (k.n <= 1) run_local<T, 1>(sizeof(T) == 4 && scalar(1), k, grid, stream);
     else if (k.n <= 4) run_local<T, 4>(scalar(4), k, grid, stream);
     else if (k.n <= 8) run_local<T, 8>(scalar(8), k, grid, stream);
@@ -551,9 +579,11 @@ int64_t selscan_bwd_blocks(int64_t channels, int64_t groups, int64_t n) {
     return (channels / groups + bch - 1) / bch;
 }
 
-// Rows per chunk of the backward: equal sequences stay whole where they give
-// two waves a SIMD, otherwise chunks as long as two waves a SIMD allow (the
-// kernel's registers leave room for two).
+// Rows per chunk of the backward.  A cut costs the pass that finds the chunks'
+// own gradients, a quarter of the main pass; equal sequences stay whole where
+// they give two waves a SIMD, otherwise the chunks are as long as 16 waves a
+// SIMD allow (four for up to 4 states): eight sequences of 1024 rows, 2304
+// channels, 16 states took 1778 us whole, 1319 at 4 waves, 439 at 8, 412 at 16.
 int selscan_bwd_shift(int64_t rows, int64_t nseq, int64_t channels, int64_t groups, int64_t n, bool ragged) {
     const int64_t waves = 4 * groups * selscan_bwd_blocks(channels, groups, n);
     int64_t longest = rows;
@@ -562,7 +592,7 @@ int selscan_bwd_shift(int64_t rows, int64_t nseq, int64_t channels, int64_t grou
     while ((int64_t{1} << whole) < longest) ++whole;
     if (!ragged && nseq * waves >= 2048) return whole;
     int shift = whole;
-    while (shift > kMinChunkShift && (rows >> shift) * waves < GSPN_SELSCAN_BWD_WAVES) --shift;
+    while (shift > kMinChunkShift && (rows >> shift) * waves < (n > 4 ? 16384 : 4096)) --shift;
     return shift;
 }
 
@@ -591,9 +621,12 @@ hipError_t launch_selscan_bwd(const gspn_selscan_args& a, int dtype, hipStream_t
         else run_local_n<bf16_t>(k, lg, stream);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         if (needs_join(a, k.shift)) {
-            const dim3 jg(static_cast<unsigned>(a.seq.nseq), static_cast<unsigned>((a.channels * a.n + 255) / 256));
+            const int v = join_lane(a) == 4 && aligned_rows(k.carry, a.channels, 4, 16) ? 4 : 1;
+            const dim3 jg(static_cast<unsigned>(a.seq.nseq),
+                          static_cast<unsigned>((a.channels * a.n + 256 * v - 1) / (256 * v)));
             GSPN_REPLAYED("selscan_bwd_join_kernel", 256, 0);
-            hipLaunchKernelGGL(selscan_bwd_join_kernel, jg, dim3(256), 0, stream, k);
+            if (v == 4) hipLaunchKernelGGL(selscan_bwd_join_kernel<4>, jg, dim3(256), 0, stream, k);
+            else hipLaunchKernelGGL(selscan_bwd_join_kernel<1>, jg, dim3(256), 0, stream, k);
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
     }

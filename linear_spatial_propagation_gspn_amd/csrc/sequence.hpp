@@ -205,7 +205,7 @@ int64_t conv_bwd_parts(int64_t rows, int64_t nseq, int64_t c);
 
 // How a scan is cut.  shift: rows per chunk as a power of two; a forward or
 // backward of one chunk per sequence needs no carries.
-int selscan_shift(int64_t rows, int64_t nseq, int64_t channels, int64_t groups, bool ragged);
+int selscan_shift(int64_t rows, int64_t nseq, int64_t channels, int64_t groups, int64_t n, bool ragged);
 int selscan_bwd_shift(int64_t rows, int64_t nseq, int64_t channels, int64_t groups, int64_t n, bool ragged);
 int64_t selscan_bwd_blocks(int64_t channels, int64_t groups, int64_t n);  // channel blocks of the backward
 constexpr int kCheckShift = 3;  // GSPN_SCAN_CHECKPOINT_ROWS

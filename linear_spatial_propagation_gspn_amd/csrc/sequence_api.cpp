@@ -273,7 +273,7 @@ int64_t gspn_selective_scan_workspace_bytes(int64_t rows, int64_t nseq, int64_t 
                                             int ragged) {
     if (!scan_sizes_ok(rows, nseq, channels, groups, n) || nseq < 1) return -1;
     if (channels == 0) return 0;
-    const int shift = gspn::selscan_shift(rows, nseq, channels, groups, ragged != 0);
+    const int shift = gspn::selscan_shift(rows, nseq, channels, groups, n, ragged != 0);
     if ((int64_t{1} << shift) >= (ragged ? rows : rows / nseq)) return 0;
     return gspn::chunk_ids(ragged != 0, rows, nseq, shift) * (n + 1) * channels * 4;
 }
