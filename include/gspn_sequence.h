@@ -15,7 +15,7 @@
  * Conventions shared by every call here
  * -------------------------------------
  *  - Rows.  A tensor [rows][c] has unit column stride and a row stride `ld`
- *    in elements (c <= ld <= 2^27), so that the halves or slices of a projection's
+ *    in elements (c <= ld <= 2^26), so that the halves or slices of a projection's
  *    rows are taken as they are.  Alignment: the element size.  Row strides
  *    and offsets may pass 32 bits; rows < 2^31, c <= 2^19.
  *  - Storage type: x, dt, z, B, C, h, gate and their gradients and outputs

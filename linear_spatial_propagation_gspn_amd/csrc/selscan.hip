@@ -16,6 +16,8 @@
 // sequence is one chunk, only the last pass runs.
 #include "selscan.hpp"
 
+#include <type_traits>
+
 namespace gspn {
 namespace {
 
@@ -228,6 +230,196 @@ __global__ __launch_bounds__(64) void selscan_kernel(const SelK p) {
     }
 }
 
+// Whole sequences, four lanes a channel: a block takes 64 channels of one
+// sequence from its first row to its last, with no chunks to join.  Four lanes
+// share a channel (NP / 4 states each), so a sequence offers four times the
+// waves of the kernel above and a row a quarter of its instructions; each of
+// the four computes a quarter of the rows' step sizes and gates and hands them
+// to the others as DPP operands.  B and C are staged through LDS, 16 rows at a
+// time, and the next 16 rows' loads are in flight meanwhile.
+// About 175 cycles a row and wave of 16 channels (16 states), against 530 for
+// 64 channels and again 400 for the chunk sums above: it takes batches that
+// fill the GPU with whole sequences, and short ones, where it is one launch.
+template <typename T, int NP, bool kGate>
+__global__ __launch_bounds__(256) void selscan_quad_kernel(const SelK p) {
+    constexpr int SPL = NP / 4;
+    constexpr int kRows = 16;
+    constexpr int R = kRows / 4;  // rows a lane has to itself
+    constexpr int kBC = (kRows * 2 * NP + 255) / 256;
+    __shared__ __attribute__((aligned(16))) float bc[2][kRows][2 * NP];
+    const int s = blockIdx.x;
+    const int begin = seq_begin(p.seq, s);
+    const int end = seq_end(p.seq, s, begin);
+    const int g = blockIdx.y / p.blocks;
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int sub = lane & 3;
+    const int local = (blockIdx.y - g * p.blocks) * 64 + (tid >> 2);
+    const bool live = local < p.per;
+    const int c = g * p.per + (live ? local : p.per - 1);
+    const int n0 = sub * SPL;
+    const int slot = p.state ? slot_of(p.seq, s) : kNoSlot;
+
+    float A2[SPL], h[SPL];
+#pragma unroll
+    for (int i = 0; i < SPL; ++i) {
+        A2[i] = n0 + i < p.n ? p.A[static_cast<int64_t>(c) * p.n + n0 + i] * kLog2E : 0.0f;
+        h[i] = 0.0f;
+    }
+    float* const pool = p.state + (static_cast<int64_t>(slot >= 0 ? slot : 0) * p.channels + c) * p.n + n0;
+    if (slot >= 0 && p.seq.resume && p.seq.resume[s] != 0) {
+#pragma unroll
+        for (int i = 0; i < SPL; ++i)
+            if (n0 + i < p.n) h[i] = pool[i];
+    }
+    const float bias = p.bias ? p.bias[c] : 0.0f;
+    const float skip = p.D ? p.D[c] : 0.0f;
+    const T* const B = static_cast<const T*>(p.B) + static_cast<int64_t>(g) * p.n;
+    const T* const C = static_cast<const T*>(p.C) + static_cast<int64_t>(g) * p.n;
+    const int64_t check0 = chunk_base(p.seq, s, begin, kCheckShift);
+    auto place = [&](int64_t ld) { return static_cast<unsigned>(sub * static_cast<int>(ld) + c); };
+    const unsigned ox = place(p.ldx), od = place(p.lddt), oz = kGate ? place(p.ldz) : 0, oo = place(p.ldo);
+
+    // four rows of bytes each; the walks are on the next rows to load, or store
+    constexpr int es = sizeof(T);
+    RowWalk wx(p.x, begin, p.ldx, es), wd(p.dt, begin, p.lddt, es), wz(p.z, kGate ? begin : 0, p.ldz, es);
+    RowWalk wo(p.out, begin, p.ldo, es), wb(B, begin, p.ldb, es), wc(C, begin, p.ldc, es);
+    const int64_t fx = p.ldx * 4 * es, fd = p.lddt * 4 * es, fz = p.ldz * 4 * es, fo = p.ldo * 4 * es;
+    // a lane's values of B and C within 16 rows
+    unsigned obc[kBC];
+#pragma unroll
+    for (int i = 0; i < kBC; ++i) {
+        const int v = tid + i * 256;
+        const int64_t ld = (v / NP) % 2 == 0 ? p.ldb : p.ldc;
+        obc[i] = static_cast<unsigned>(v / (2 * NP) * static_cast<int>(ld) + v % NP);
+    }
+
+    T nx[R], nd[R], nz[R], nbc[kBC];
+    auto load = [&](int base) {
+        const int left = end - base - sub;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            nx[i] = nd[i] = nz[i] = T{};
+            if (i * 4 < left) {
+                nx[i] = wx.at<const T>()[ox];
+                nd[i] = wd.at<const T>()[od];
+                if constexpr (kGate) nz[i] = wz.at<const T>()[oz];
+            }
+            wx.step(fx);
+            wd.step(fd);
+            if constexpr (kGate) wz.step(fz);
+        }
+#pragma unroll
+        for (int i = 0; i < kBC; ++i) {
+            const int v = tid + i * 256;
+            nbc[i] = T{};
+            if (v < kRows * 2 * NP && v % NP < p.n && base + v / (2 * NP) < end) {
+                if ((v / NP) % 2 == 0) nbc[i] = wb.at<const T>()[obc[i]];
+                else nbc[i] = wc.at<const T>()[obc[i]];
+            }
+        }
+        wb.step(p.ldb * kRows * es);
+        wc.step(p.ldc * kRows * es);
+    };
+    if (begin < end) load(begin);
+    int buf = 0;
+    for (int base = begin; base < end; base += kRows, buf ^= 1) {
+#pragma unroll
+        for (int i = 0; i < kBC; ++i) {
+            const int v = tid + i * 256;
+            if (v < kRows * 2 * NP) (&bc[buf][0][0])[v] = Store<T>::ld(&nbc[i]);
+        }
+        float xv[R], dv[R], uv[R], f[R], yv[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            xv[i] = Store<T>::ld(&nx[i]);
+            dv[i] = Store<T>::ld(&nd[i]) + bias;
+            f[i] = 1.0f;
+            yv[i] = 0.0f;
+        }
+        if (p.softplus) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) dv[i] = softplus_f(dv[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            if constexpr (kGate) {
+                const float zv = Store<T>::ld(&nz[i]);
+                f[i] = zv * gate_sigmoid<T>(zv);
+            }
+            // a row behind the sequence: a step of zero leaves the state as it is
+            if (i * 4 >= end - base - sub) dv[i] = xv[i] = 0.0f;
+            uv[i] = dv[i] * xv[i];
+        }
+        __syncthreads();
+        if (base + kRows < end) load(base + kRows);
+
+        // Four rows at a time: their B and C come from LDS while the four
+        // before are computed, and their decays and inputs are ready before the
+        // serial products, so that a wave alone on its SIMD does not wait.
+        float b[2][4][SPL], cv[2][4][SPL];
+        auto fetch = [&](int i) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                widen(ld_pack<float, SPL>(&bc[buf][i * 4 + j][n0]), b[i & 1][j]);
+                widen(ld_pack<float, SPL>(&bc[buf][i * 4 + j][NP + n0]), cv[i & 1][j]);
+            }
+        };
+        fetch(0);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            if (i + 1 < R) fetch(i + 1);
+            float a[4][SPL], w[4][SPL], y[4];
+            auto ready = [&](auto jc) {
+                constexpr int J = decltype(jc)::value;
+                const float d = quad_of<4, J>(dv[i]);
+                const float u = quad_of<4, J>(uv[i]);
+#pragma unroll
+                for (int k = 0; k < SPL; ++k) {
+                    a[J][k] = __builtin_amdgcn_exp2f(d * A2[k]);
+                    w[J][k] = u * b[i & 1][J][k];
+                }
+            };
+            ready(std::integral_constant<int, 0>{});
+            ready(std::integral_constant<int, 1>{});
+            ready(std::integral_constant<int, 2>{});
+            ready(std::integral_constant<int, 3>{});
+            __builtin_amdgcn_sched_barrier(0);
+            if (p.check && ((i * 4) & ((1 << kCheckShift) - 1)) == 0 && base + i * 4 < end) {
+                auto q = row_at<float>(p.check, (check0 + ((base - begin + i * 4) >> kCheckShift)) * p.n, p.channels);
+#pragma unroll
+                for (int k = 0; k < SPL; ++k)
+                    if (live && n0 + k < p.n) st_at(q + static_cast<unsigned>((n0 + k) * p.channels + c), h[k]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                y[j] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < SPL; ++k) h[k] = __builtin_fmaf(a[j][k], h[k], w[j][k]);
+#pragma unroll
+                for (int k = 0; k < SPL; ++k) y[j] = __builtin_fmaf(cv[i & 1][j][k], h[k], y[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                y[j] = quad_sum<4>(y[j]);
+                yv[i] = sub == j ? y[j] : yv[i];
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            float y = __builtin_fmaf(skip, xv[i], yv[i]) * f[i];
+            if (slot == kBadSlot) y = __builtin_nanf("");
+            if (live && i * 4 < end - base - sub) st_at(wo.at<T>() + oo, y);
+            wo.step(fo);
+        }
+    }
+    if (slot < 0 || !live) return;
+#pragma unroll
+    for (int i = 0; i < SPL; ++i)
+        if (n0 + i < p.n) pool[i] = h[i];
+}
+
 // The join over the chunks of a long sequence: carry[k] := the state before
 // chunk k.  A lane takes V channels of one state; the chunks' values are loaded
 // 32 / V at a time ahead of the serial products.
@@ -372,6 +564,20 @@ void run_selscan_n(bool out, const SelK& k, dim3 grid, hipStream_t stream) {
     else run_selscan<T, 16>(out, scalar(16), k, grid, stream);
 }
 
+template <typename T, int NP>
+void run_quad(const SelK& k, dim3 grid, hipStream_t stream) {
+    if (k.z) hipLaunchKernelGGL((selscan_quad_kernel<T, NP, true>), grid, dim3(256), 0, stream, k);
+    else hipLaunchKernelGGL((selscan_quad_kernel<T, NP, false>), grid, dim3(256), 0, stream, k);
+}
+
+template <typename T>
+void run_quad_n(const SelK& k, hipStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(k.seq.nseq), static_cast<unsigned>(k.groups * k.blocks));
+    if (k.n <= 4) run_quad<T, 4>(k, grid, stream);
+    else if (k.n <= 8) run_quad<T, 8>(k, grid, stream);
+    else run_quad<T, 16>(k, grid, stream);
+}
+
 template <typename T>
 void run_step(const SelK& k, bool vec, hipStream_t stream) {
     const int split = k.n <= 1 ? 1 : 4;
@@ -386,21 +592,35 @@ void run_step(const SelK& k, bool vec, hipStream_t stream) {
 
 }  // namespace
 
-// Rows per chunk.  Cutting a sequence costs a second pass over all but its
-// last chunk, so equal sequences stay whole where they fill the GPU by
-// themselves (a wave and a half a SIMD).  Otherwise the chunks, of 16 rows at
-// least, are as long as eight waves a SIMD allow (four for up to 4 states,
-// whose rows are short work against the join): one sequence of 65536 rows and
-// 2048 channels with 16 states took 1027 us at 4 waves, 923 at 8, 902 at 16,
-// 16 ragged prompts of 4096 channels 344, 300 and 301, four of 3136 rows with
-// one state (768 channels, fp32) 52 at 4 against 59 at 8.
+// How the forward is cut: kWholeQuad, or rows per chunk (a power of two; one
+// chunk that holds the longest sequence: whole sequences, one lane a channel).
+//
+// The three ways by their measured cycles: whole sequences with four lanes a
+// channel take longest x (194 R + 90) where R counts their waves over the
+// SIMDs, one lane a channel longest x (600 R + 300), chunks 980 for each wave
+// and row spread over the SIMDs and some 48000 for three launches.  Measured
+// (16 states, bf16, four lanes against chunks): 57 rows of 1152 channels 10.1
+// against 17.1 us, 512 rows 63 against 23; 4 x 1024 rows of 4096 channels 126.5
+// and 126.7, 8 x 1024 of 2304 178 against 142, 16 x 1024 of 4096 332 against
+// 426.  Packed sequences are taken as one, the longest they can hold.
+//
+// Chunks, of 16 rows at least, are as long as eight waves a SIMD allow (four
+// for up to 4 states, whose rows are short work against the join): one
+// sequence of 65536 rows and 2048 channels with 16 states took 1027 us at 4
+// waves, 923 at 8, 902 at 16, 16 ragged prompts of 4096 channels 344, 300 and
+// 301, four of 3136 rows with one state (768 channels, fp32) 52 at 4 against 59
+// at 8.
 int selscan_shift(int64_t rows, int64_t nseq, int64_t channels, int64_t groups, int64_t n, bool ragged) {
     const int64_t waves = groups * ((channels / groups + 63) / 64);
-    int64_t longest = rows;
-    if (!ragged && nseq > 0) longest = rows / nseq;
+    const int64_t longest = ragged || nseq < 1 ? rows : rows / nseq;
+    auto per_simd = [](int64_t w) { return (w + 1023) / 1024; };
+    const int64_t chunks = rows * waves * 980 / 1024 + 48000;
+    const int64_t lanes1 = longest * (600 * per_simd(nseq * waves) + 300);
+    const int64_t lanes4 = longest * (194 * per_simd(nseq * waves * 4) + 90);
+    if (n > 1 && lanes4 <= lanes1 && lanes4 <= chunks) return kWholeQuad;
     int whole = kMinChunkShift;
     while ((int64_t{1} << whole) < longest) ++whole;
-    if (!ragged && nseq * waves >= 1536) return whole;
+    if (lanes1 <= chunks) return whole;
     int shift = whole;
     while (shift > kMinChunkShift && (rows >> shift) * waves < (n > 4 ? 8192 : 4096)) --shift;
     return shift;
@@ -410,6 +630,15 @@ hipError_t launch_selscan_fwd(const gspn_selscan_args& a, int dtype, hipStream_t
     SelK k = selscan_params(a);
     const bool ragged = a.seq.cu != nullptr;
     k.shift = selscan_shift(a.seq.rows, a.seq.nseq, a.channels, a.groups, a.n, ragged);
+    if (k.shift == kWholeQuad) {
+#ifdef GSPN_CHECK_LAUNCHES
+        replay_selscan("selscan_quad_kernel", a, k, 0, dtype == kF32 ? 4 : 2);
+#endif
+        GSPN_REPLAYED("selscan_quad_kernel", 256, 2 * 16 * 32 * 4);
+        if (dtype == kF32) run_quad_n<float>(k, stream);
+        else run_quad_n<bf16_t>(k, stream);
+        return hipGetLastError();
+    }
     const int64_t ids = chunk_ids(ragged, a.seq.rows, a.seq.nseq, k.shift);
     const bool cut = (int64_t{1} << k.shift) < (ragged ? a.seq.rows : a.seq.rows / a.seq.nseq);
     if (cut) {

@@ -100,6 +100,61 @@ __device__ __forceinline__ float lane_value(float v, int lane) {
     return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
 }
 
+template <int kCtrl>
+__device__ __forceinline__ float dpp(float v) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), kCtrl, 0xf, 0xf, true));
+}
+
+// A uniform pointer to `row` of a tensor, kept in scalar registers: without
+// this the compiler carries a 64-bit vector address for every tensor and row of
+// a tile over the loop, and spills.
+template <typename T>
+__device__ __forceinline__ __attribute__((address_space(1))) T* row_at(const void* p, int64_t row, int64_t ld) {
+    uintptr_t a = reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(row * ld) * sizeof(T);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a >> 32));
+    a = (static_cast<uintptr_t>(hi) << 32) | lo;
+    asm volatile("" : "+s"(a));
+    return (__attribute__((address_space(1))) T*)a;
+}
+
+// A uniform pointer that steps over the rows of a tensor, in scalar registers.
+struct RowWalk {
+    uintptr_t a;
+    __device__ __forceinline__ RowWalk(const void* p, int64_t row, int64_t ld, int es) {
+        a = reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(row * ld * es);
+        const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a));
+        const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a >> 32));
+        a = (static_cast<uintptr_t>(hi) << 32) | lo;
+    }
+    template <typename T>
+    __device__ __forceinline__ __attribute__((address_space(1))) T* at() const {
+        return (__attribute__((address_space(1))) T*)a;
+    }
+    __device__ __forceinline__ void step(int64_t bytes) {
+        a += static_cast<uintptr_t>(bytes);
+        asm volatile("" : "+s"(a));
+    }
+};
+
+__device__ __forceinline__ void st_at(__attribute__((address_space(1))) float* p, float v) { *p = v; }
+__device__ __forceinline__ void st_at(__attribute__((address_space(1))) bf16_t* p, float v) { *p = f32_to_bf16(v); }
+
+// Lane J of each quad to all four (SPLIT 4), or the lane's own value.
+template <int SPLIT, int J>
+__device__ __forceinline__ float quad_of(float v) {
+    if constexpr (SPLIT == 1) return v;
+    return dpp<J * 0x55>(v);
+}
+
+template <int SPLIT>
+__device__ __forceinline__ float quad_sum(float v) {
+    if constexpr (SPLIT == 1) return v;
+    v += dpp<0xB1>(v);  // lanes 1 0 3 2
+    v += dpp<0x4E>(v);  // lanes 2 3 0 1
+    return v;
+}
+
 // Sequences of up to this many chunks need no launch to join them: a chunk
 // walks over those before it (or behind it, in the backward) by itself, at
 // about one row's work each.

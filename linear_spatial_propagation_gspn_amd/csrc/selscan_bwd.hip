@@ -29,39 +29,6 @@ namespace {
 constexpr float kLn2 = 0.693147180559945309417f;
 constexpr int kTile = 1 << kCheckShift;  // rows rerun together
 
-template <int kCtrl>
-__device__ __forceinline__ float dpp(float v) {
-    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), kCtrl, 0xf, 0xf, true));
-}
-
-// A uniform pointer to `row` of a tensor, kept in scalar registers: without
-// this the compiler carries a 64-bit vector address for every tensor and row of
-// a tile over the loop, and spills.
-template <typename T>
-__device__ __forceinline__ __attribute__((address_space(1))) T* row_at(const void* p, int64_t row, int64_t ld) {
-    uintptr_t a = reinterpret_cast<uintptr_t>(p) + static_cast<uintptr_t>(row * ld) * sizeof(T);
-    asm volatile("" : "+s"(a));
-    return (__attribute__((address_space(1))) T*)a;
-}
-
-__device__ __forceinline__ void st_at(__attribute__((address_space(1))) float* p, float v) { *p = v; }
-__device__ __forceinline__ void st_at(__attribute__((address_space(1))) bf16_t* p, float v) { *p = f32_to_bf16(v); }
-
-// Lane J of each quad to all four (SPLIT 4), or the lane's own value.
-template <int SPLIT, int J>
-__device__ __forceinline__ float quad_of(float v) {
-    if constexpr (SPLIT == 1) return v;
-    return dpp<J * 0x55>(v);
-}
-
-template <int SPLIT>
-__device__ __forceinline__ float quad_sum(float v) {
-    if constexpr (SPLIT == 1) return v;
-    v += dpp<0xB1>(v);  // lanes 1 0 3 2
-    v += dpp<0x4E>(v);  // lanes 2 3 0 1
-    return v;
-}
-
 __device__ __forceinline__ float swap_add32(float a, float b) {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
@@ -308,31 +275,53 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
         const unsigned qx = place(p.lddx), qd = place(p.ldddt), qz = kGate ? place(p.lddz) : 0;
 
         constexpr int kBC = (kTile * 2 * NP + 255) / 256;  // values of B and C a lane stages
-        T nx[R], nd[R], ng[R], nz[R];
-        float nbc[kBC], nh[SPL];
+        const int tiles = (ck.r1 - ck.r0 + kTile - 1) / kTile;
+        // The walks are on the first rows of the tile to load, or to store,
+        // against the row order; within a tile they step by SPLIT rows.
+        constexpr int es = sizeof(T);
+        const int64_t top = ck.r0 + (tiles - 1) * kTile;
+        RowWalk wx(p.x, top, p.ldx, es), wd(p.dt, top, p.lddt, es), wg(p.gy, top, p.ldgy, es);
+        RowWalk wz(p.z, kGate ? top : 0, p.ldz, es), wb(B, top, p.ldb, es), wc(C, top, p.ldc, es);
+        RowWalk vx(p.dx, top, p.lddx, es), vd(p.ddt, top, p.ldddt, es), vz(p.dz, kGate ? top : 0, p.lddz, es);
+        // after a tile's R groups: back to its first row and a tile up
+        auto next = [&](RowWalk& w, int64_t ld, int i) { w.step(ld * es * (i + 1 < R ? SPLIT : SPLIT - 2 * kTile)); };
+        unsigned obc[kBC];
+#pragma unroll
+        for (int i = 0; i < kBC; ++i) {
+            const int v = tid + i * 256;
+            const int64_t ld = (v / NP) % 2 == 0 ? p.ldb : p.ldc;
+            obc[i] = static_cast<unsigned>(v / (2 * NP) * static_cast<int>(ld) + v % NP);
+        }
+        T nx[R], nd[R], ng[R], nz[R], nbc[kBC];
+        float nh[SPL];
         auto load = [&](int tile) {
             const int base = ck.r0 + tile * kTile;
             const int left = ck.r1 - base - sub;
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const int64_t t = base + i * SPLIT;
                 nx[i] = nd[i] = ng[i] = nz[i] = T{};
                 if (i * SPLIT < left) {
-                    nx[i] = row_at<const T>(p.x, t, p.ldx)[ox];
-                    nd[i] = row_at<const T>(p.dt, t, p.lddt)[od];
-                    ng[i] = row_at<const T>(p.gy, t, p.ldgy)[og];
-                    if constexpr (kGate) nz[i] = row_at<const T>(p.z, t, p.ldz)[oz];
+                    nx[i] = wx.at<const T>()[ox];
+                    nd[i] = wd.at<const T>()[od];
+                    ng[i] = wg.at<const T>()[og];
+                    if constexpr (kGate) nz[i] = wz.at<const T>()[oz];
                 }
+                next(wx, p.ldx, i);
+                next(wd, p.lddt, i);
+                next(wg, p.ldgy, i);
+                if constexpr (kGate) next(wz, p.ldz, i);
             }
 #pragma unroll
             for (int i = 0; i < kBC; ++i) {
                 const int v = tid + i * 256;
-                const int r = base + v / (2 * NP);
-                const int n = v % NP;
-                nbc[i] = 0.0f;
-                if (v < kTile * 2 * NP && n < p.n && r < ck.r1)
-                    nbc[i] = (v / NP) % 2 == 0 ? Store<T>::ld(B + r * p.ldb + n) : Store<T>::ld(C + r * p.ldc + n);
+                nbc[i] = T{};
+                if (v < kTile * 2 * NP && v % NP < p.n && base + v / (2 * NP) < ck.r1) {
+                    if ((v / NP) % 2 == 0) nbc[i] = wb.at<const T>()[obc[i]];
+                    else nbc[i] = wc.at<const T>()[obc[i]];
+                }
             }
+            wb.step(-p.ldb * kTile * es);
+            wc.step(-p.ldc * kTile * es);
             const auto q = row_at<const float>(p.check, (check0 + tile) * p.n, p.channels);
 #pragma unroll
             for (int s = 0; s < SPL; ++s)
@@ -356,7 +345,6 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
             }
         };
 
-        const int tiles = (ck.r1 - ck.r0 + kTile - 1) / kTile;
         load(tiles - 1);
         int buf = 0;
         for (int tile = tiles - 1; tile >= 0; --tile, buf ^= 1) {
@@ -364,7 +352,7 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
 #pragma unroll
             for (int i = 0; i < kBC; ++i) {
                 const int v = tid + i * 256;
-                if (v < kTile * 2 * NP) (&bc[buf][0][0])[v] = nbc[i];
+                if (v < kTile * 2 * NP) (&bc[buf][0][0])[v] = Store<T>::ld(&nbc[i]);
             }
             float xv[R], dv[R], uv[R], gp[R], sg[R], gz[R], yv[R], h[SPL];
 #pragma unroll
@@ -479,18 +467,17 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
 
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const int64_t t = base + i * SPLIT;
                 if (live && i * SPLIT < ck.r1 - base - sub) {
                     const float ddt = __builtin_fmaf(xv[i], gb[i], ga[i] * kLn2) * sg[i];
-                    st_at(row_at<T>(p.dx, t, p.lddx) + qx,
-                          __builtin_fmaf(skip, gp[i], dv[i] * gb[i]));
-                    st_at(row_at<T>(p.ddt, t, p.ldddt) + qd, ddt);
+                    st_at(vx.at<T>() + qx, __builtin_fmaf(skip, gp[i], dv[i] * gb[i]));
+                    st_at(vd.at<T>() + qd, ddt);
                     dD = __builtin_fmaf(gp[i], xv[i], dD);
                     db += ddt;
-                    if constexpr (kGate)
-                        st_at(row_at<T>(p.dz, t, p.lddz) + qz,
-                              gz[i] * __builtin_fmaf(skip, xv[i], yv[i]));
+                    if constexpr (kGate) st_at(vz.at<T>() + qz, gz[i] * __builtin_fmaf(skip, xv[i], yv[i]));
                 }
+                next(vx, p.lddx, i);
+                next(vd, p.ldddt, i);
+                if constexpr (kGate) next(vz, p.lddz, i);
             }
         }
         __syncthreads();

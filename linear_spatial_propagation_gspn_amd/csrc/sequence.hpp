@@ -37,13 +37,15 @@ GSPN_HD int64_t chunk_ids(bool ragged, int64_t rows, int64_t nseq, int shift) {
 
 __device__ __forceinline__ int clamp_row(const SeqK& s, int v) { return v < 0 ? 0 : v > s.rows ? s.rows : v; }
 
+// A sequence's rows (i the same for the whole wave, so the rows are put into
+// scalar registers).
 __device__ __forceinline__ int seq_begin(const SeqK& s, int i) {
-    return s.cu ? clamp_row(s, s.cu[i]) : i * s.len;
+    return s.cu ? __builtin_amdgcn_readfirstlane(clamp_row(s, s.cu[i])) : i * s.len;
 }
 
 __device__ __forceinline__ int seq_end(const SeqK& s, int i, int begin) {
     if (!s.cu) return begin + s.len;
-    const int e = clamp_row(s, s.cu[i + 1]);
+    const int e = __builtin_amdgcn_readfirstlane(clamp_row(s, s.cu[i + 1]));
     return e < begin ? begin : e;
 }
 
@@ -108,7 +110,7 @@ constexpr int kBadSlot = -2;
 
 __device__ __forceinline__ int slot_of(const SeqK& s, int i) {
     if (!s.slots) return i;
-    const int v = s.slots[i];
+    const int v = __builtin_amdgcn_readfirstlane(s.slots[i]);
     if (v < 0) return kNoSlot;
     if (v >= s.nslots) return kBadSlot;
     const int lane = __lane_id();
@@ -210,6 +212,7 @@ int selscan_bwd_shift(int64_t rows, int64_t nseq, int64_t channels, int64_t grou
 int64_t selscan_bwd_blocks(int64_t channels, int64_t groups, int64_t n);  // channel blocks of the backward
 constexpr int kCheckShift = 3;  // GSPN_SCAN_CHECKPOINT_ROWS
 constexpr int kMinChunkShift = 4;
+constexpr int kWholeQuad = 63;  // of selscan_shift: no chunks
 
 hipError_t launch_selscan_fwd(const gspn_selscan_args& a, int dtype, hipStream_t stream);
 hipError_t launch_selscan_step(const gspn_selscan_args& a, int dtype, hipStream_t stream);

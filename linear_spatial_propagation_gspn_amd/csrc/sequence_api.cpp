@@ -15,7 +15,7 @@ namespace {
 
 constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxChannels = int64_t{1} << 19;
-constexpr int64_t kMaxStride = int64_t{1} << 27;
+constexpr int64_t kMaxStride = int64_t{1} << 26;
 
 bool valid_dtype(int64_t dt) { return dt == GSPN_F32 || dt == GSPN_BF16; }
 int64_t elem_size(int64_t dt) { return dt == GSPN_F32 ? 4 : 2; }
@@ -274,7 +274,7 @@ int64_t gspn_selective_scan_workspace_bytes(int64_t rows, int64_t nseq, int64_t 
     if (!scan_sizes_ok(rows, nseq, channels, groups, n) || nseq < 1) return -1;
     if (channels == 0) return 0;
     const int shift = gspn::selscan_shift(rows, nseq, channels, groups, n, ragged != 0);
-    if ((int64_t{1} << shift) >= (ragged ? rows : rows / nseq)) return 0;
+    if (shift == gspn::kWholeQuad || (int64_t{1} << shift) >= (ragged ? rows : rows / nseq)) return 0;
     return gspn::chunk_ids(ragged != 0, rows, nseq, shift) * (n + 1) * channels * 4;
 }
 

@@ -244,6 +244,14 @@ SCAN_CASES = [
     (BF16, 17, 1, 13, True, True, True, True, True, [5, 0, 0, 16], 0),
     (F32, 8, 1, 2, False, True, True, False, False, [16, 16, 16], 0),
     (F32, 4, 2, 16, True, True, True, True, False, [1] * 70, 0),
+    # batches that are cut into chunks: sequences that the chunks join by themselves, and longer ones
+    (F32, 70, 1, 16, True, True, True, True, False, [50, 64, 16, 17, 0, 33, 1], 1),
+    (BF16, 64, 1, 16, True, True, True, True, True, [150, 1, 16, 0, 65], 0),
+    (BF16, 40, 2, 8, False, True, True, True, False, [200, 48], 3),
+    (F32, 12, 1, 4, True, False, True, True, True, [3, 190, 64], 0),
+    (BF16, 33, 1, 11, True, True, False, True, False, [64, 120, 7], 0),
+    (F32, 66, 2, 1, True, True, True, True, False, [130, 80], 2),
+    (BF16, 20, 1, 6, True, True, True, False, True, [1] * 100 + [90], 0),
 ]
 
 
@@ -308,10 +316,11 @@ def test_scan_many_chunks(dtype):
     assert torch.equal(run_fwd(batch).view(700, 66), out)
 
 
+@pytest.mark.parametrize("long", [50, 220])
 @pytest.mark.parametrize("dtype,n", [(F32, 16), (BF16, 16), (F32, 1), (BF16, 6), (F32, 8), (BF16, 4)])
-def test_scan_pool(dtype, n):
+def test_scan_pool(dtype, n, long):
     g = gen(17)
-    c, lengths = 72, [50, 0, 1, 4, 0, 18, 3, 2]
+    c, lengths = 72, [long, 0, 1, 4, 0, 18, 3, 2]
     slots = [4, 7, 0, -1, 2, 5, 5, 99]
     resume = [True, True, False, True, False, True, True, True]
     k = scan_case(g, sum(lengths), c, 1, n, dtype)
@@ -513,8 +522,8 @@ def test_empty_calls():
 
 
 def test_rows_beyond_32_bits():
-    """The widest row stride, 2^27 elements: the last of 34 rows lies 8.25 GiB in, past 2^32 elements."""
-    ld, c, rows = 1 << 27, 16, 34
+    """The widest row stride, 2^26 elements: the last of 70 rows lies past 2^32 elements."""
+    ld, c, rows = 1 << 26, 16, 70
     big = torch.empty((rows - 1) * ld + 1024, dtype=BF16, device=DEV)
     g = gen(6)
     far = lambda at: torch.as_strided(big, (rows, c), (ld, 1), at)  # noqa: E731
