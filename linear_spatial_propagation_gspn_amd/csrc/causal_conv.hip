@@ -4,9 +4,13 @@
 //
 // Each output reads width <= 4 rows of its own channel, so the work is a few
 // fma an element and the kernels are bound by the bytes of x and y.  A lane
-// takes 16 bytes of channels (one channel where sizes or alignment forbid)
-// and walks down a run of rows with the last width - 1 rows in registers, so
-// every row is read once but for the halo at the run's start.
+// takes two channels (one where sizes or alignment forbid) and walks down a
+// run of rows with the last width - 1 rows in registers, so every row is read
+// once but for the halo at the run's start.  Two channels a lane, so that many
+// waves with few registers each keep the loads in flight: with eight (16
+// bytes of bf16) 8192 rows of 2304 channels took 19.8 us forward and 42
+// backward, with four 16.9 and 29.0, with two 16.3 and 28.2 (5.2 TB/s of x and
+// y would be 14.5 and 21.7).
 #include "sequence.hpp"
 
 namespace gspn {
@@ -230,7 +234,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvK p) {
 #pragma unroll
                         for (int j = 0; j + 1 < K; ++j) e[j][v] = e[j + 1][v];
                         float d = gv[v];
-                        if (p.silu) d *= silu_grad(pre[v], gate_sigmoid<float>(pre[v]));
+                        if (p.silu) d *= silu_grad(pre[v], gate_sigmoid<T>(pre[v]));
                         e[K - 1][v] = t < ck.end ? d : 0.0f;
                         if (t < ck.r1) {
 #pragma unroll
@@ -300,11 +304,12 @@ __global__ __launch_bounds__(64 * kReduceRuns) void reduce_parts_kernel(const Re
     }
 }
 
-// Rows per chunk: the longest of 64, 32, 16, 8 that still gives two waves a
-// SIMD (lanes of eight channels).  A longer run re-reads fewer halo rows.
+// Rows per chunk: the longest of 64, 32, 16, 8 that still gives four waves a
+// SIMD (of 128 channels).  A longer run re-reads fewer halo rows: 8192 rows of
+// 2304 channels backward took 28.2 us at 32 and at 16 rows, 33.8 at 8.
 int conv_shift_for(int64_t rows, int64_t c) {
     int shift = 6;
-    while (shift > 3 && ((rows >> shift) + 1) * ((c + 511) / 512) < 2048) --shift;
+    while (shift > 3 && ((rows >> shift) + 1) * ((c + 127) / 128) < 4096) --shift;
     return shift;
 }
 
@@ -349,13 +354,13 @@ ConvK conv_params(const gspn_conv_args& a) {
 hipError_t launch_conv(int which, const gspn_conv_args& a, int dtype, hipStream_t stream) {
     ConvK k = conv_params(a);
     const int es = dtype == kF32 ? 4 : 2;
-    const int v = 16 / es;
-    bool vec = a.c % v == 0 && aligned_rows(a.x, a.ldx, es, 16);
+    const int v = 2, vb = v * es;
+    bool vec = a.c % v == 0 && aligned_rows(a.x, a.ldx, es, vb);
     if (which == 2) {
-        vec = vec && aligned_rows(a.gy, a.ldgy, es, 16) && aligned_rows(a.dx, a.lddx, es, 16) &&
-              aligned_rows(a.workspace, a.c, 4, 16);
+        vec = vec && aligned_rows(a.gy, a.ldgy, es, vb) && aligned_rows(a.dx, a.lddx, es, vb) &&
+              aligned_rows(a.workspace, a.c, 4, 8);
     } else {
-        vec = vec && aligned_rows(a.y, a.ldy, es, 16) && (!a.state || aligned_rows(a.state, a.c, es, 16));
+        vec = vec && aligned_rows(a.y, a.ldy, es, vb) && (!a.state || aligned_rows(a.state, a.c, es, vb));
     }
     const int lanev = vec ? v : 1;
     k.shift = conv_shift_for(a.seq.rows, a.c);
@@ -376,10 +381,10 @@ hipError_t launch_conv(int which, const gspn_conv_args& a, int dtype, hipStream_
     GSPN_REPLAY_ROWS(kn, "weight", a.weight, a.c, a.width, a.width, 4);
     GSPN_REPLAYED(kn, kConvThreads, 0);
     if (dtype == kF32) {
-        if (vec) run_conv_width<float, 4>(which, a.width, k, grid, stream);
+        if (vec) run_conv_width<float, 2>(which, a.width, k, grid, stream);
         else run_conv_width<float, 1>(which, a.width, k, grid, stream);
     } else {
-        if (vec) run_conv_width<bf16_t, 8>(which, a.width, k, grid, stream);
+        if (vec) run_conv_width<bf16_t, 2>(which, a.width, k, grid, stream);
         else run_conv_width<bf16_t, 1>(which, a.width, k, grid, stream);
     }
     return hipGetLastError();
