@@ -4,14 +4,16 @@
 //
 // Row by row; every tensor is read once and written once, so the kernels are
 // bound by those bytes.  A row lives in the registers of the lanes that share
-// it: a wave for up to 1024 channels, 256 lanes for up to 4096, 1024 lanes
-// above.  The backward keeps the columns' sums for the parameters' gradients
+// it, eight channels each: a wave for up to 512 channels, a workgroup of as
+// many waves as the row fills above.  The backward keeps the columns' sums for the parameters' gradients
 // in registers over all the rows a workgroup walks and leaves one partial row
 // each, joined in a fixed order.
 #include "sequence.hpp"
 
 namespace gspn {
 namespace {
+
+constexpr int64_t kWaveRow = 512;  // channels up to which a wave takes a row
 
 struct JoinK {
     int32_t rows, c;
@@ -33,53 +35,59 @@ struct JoinK {
     int64_t ldh, ldg, ldr, ldj, ldn, ldgj, ldgn, lddh, lddg, lddr;
 };
 
-// The sums of two values over the TPR lanes of a row, the same bits in each.
-template <int TPR>
-__device__ __forceinline__ void row_sums(float& a, float& b, float (*lds)[2]) {
-#pragma unroll
-    for (int m = 32; m; m >>= 1) {
-        a += __shfl_xor(a, m);
-        b += __shfl_xor(b, m);
+// How a row lies on the lanes.  kWave: one wave a row, four rows a block;
+// otherwise the whole block, as many waves as the row fills, up to MAXT lanes.
+template <bool kWave, int MAXT>
+struct Row {
+    static __device__ __forceinline__ int lanes() { return kWave ? 64 : static_cast<int>(blockDim.x); }
+    static __device__ __forceinline__ int lane() {
+        return kWave ? static_cast<int>(threadIdx.x & 63) : static_cast<int>(threadIdx.x);
     }
-    if constexpr (TPR > 64) {
-        constexpr int W = TPR / 64;
-        __syncthreads();  // the last sums have been read
-        if ((threadIdx.x & 63) == 0) {
-            lds[threadIdx.x >> 6][0] = a;
-            lds[threadIdx.x >> 6][1] = b;
-        }
-        __syncthreads();
-        a = b = 0.0f;
+    static __device__ __forceinline__ int per_block() { return kWave ? 4 : 1; }
+    static __device__ __forceinline__ int of_block() { return kWave ? static_cast<int>(threadIdx.x >> 6) : 0; }
+
+    // The sums of K values over the lanes of a row, the same bits in each.
+    // lds: two buffers taken in turn, so that one barrier a sum is enough.
+    template <int K>
+    static __device__ __forceinline__ void sums(float (&v)[K], float (*lds)[MAXT / 64][3], int* turn) {
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-            a += lds[w][0];
-            b += lds[w][1];
+        for (int k = 0; k < K; ++k) v[k] = wave_sum(v[k]);
+        if constexpr (!kWave) {
+            float (*const buf)[3] = lds[*turn];
+            *turn ^= 1;
+            if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) buf[threadIdx.x >> 6][k] = v[k];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < K; ++k) v[k] = 0.0f;
+            for (int w = 0; w < static_cast<int>(blockDim.x >> 6); ++w)
+#pragma unroll
+                for (int k = 0; k < K; ++k) v[k] += buf[w][k];
         }
     }
-}
+};
 
 // 1 / rms of a row from its sum of squares (hardware root, 1 ulp).
 __device__ __forceinline__ float rnorm(float ss, float c, float eps) {
     return __builtin_amdgcn_rsqf(__builtin_fmaf(ss, 1.0f / c, eps));
 }
 
-template <int TPR>
-constexpr int threads_for() {
-    return TPR > 256 ? TPR : 256;
-}
-
-template <typename T, typename RT, int V, int NV, int TPR>
-__global__ __launch_bounds__(threads_for<TPR>()) void join_fwd_kernel(const JoinK p) {
-    __shared__ float lds[TPR / 64][2];
-    constexpr int WPB = threads_for<TPR>() / TPR;
-    const int lane = threadIdx.x % TPR;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * WPB + threadIdx.x / TPR;
+template <typename T, typename RT, int V, int NV, bool kWave, int MAXT>
+__global__ __launch_bounds__(kWave ? 256 : MAXT) void join_fwd_kernel(const JoinK p) {
+    typedef Row<kWave, MAXT> L;
+    __shared__ float lds[2][MAXT / 64][3];
+    int turn = 0;
+    const int TPR = L::lanes();
+    const int lane = L::lane();
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * L::per_block() + L::of_block();
     if (row >= p.rows) return;  // a whole wave, or the whole block
     const float cf = static_cast<float>(p.c);
     float e[NV][V], o[NV][V];
     Pack<T, V> g[NV];
     Pack<RT, V> r[NV];
-    float ss = 0.0f, unused = 0.0f;
+    float ss[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int col = (i * TPR + lane) * V;
@@ -91,14 +99,14 @@ __global__ __launch_bounds__(threads_for<TPR>()) void join_fwd_kernel(const Join
             if (p.res) r[i] = ld_pack<RT, V>(static_cast<const RT*>(p.res) + row * p.ldr + col);
         }
 #pragma unroll
-        for (int v = 0; v < V; ++v) ss = __builtin_fmaf(e[i][v], e[i][v], ss);
+        for (int v = 0; v < V; ++v) ss[0] = __builtin_fmaf(e[i][v], e[i][v], ss[0]);
     }
     float r1 = 1.0f;
     if (p.post) {
-        row_sums<TPR>(ss, unused, lds);
-        r1 = rnorm(ss, cf, p.eps);
+        L::template sums<1>(ss, lds, &turn);
+        r1 = rnorm(ss[0], cf, p.eps);
     }
-    ss = unused = 0.0f;
+    ss[0] = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int col = (i * TPR + lane) * V;
@@ -131,12 +139,12 @@ __global__ __launch_bounds__(threads_for<TPR>()) void join_fwd_kernel(const Join
             RT s;  // the norm is that of the rows as they are stored
             Store<RT>::st(&s, e[i][v]);
             o[i][v] = Store<RT>::ld(&s);
-            if (col < p.c) ss = __builtin_fmaf(o[i][v], o[i][v], ss);
+            if (col < p.c) ss[0] = __builtin_fmaf(o[i][v], o[i][v], ss[0]);
         }
     }
     if (!p.pre) return;
-    row_sums<TPR>(ss, unused, lds);
-    const float r2 = rnorm(ss, cf, p.eps);
+    L::template sums<1>(ss, lds, &turn);
+    const float r2 = rnorm(ss[0], cf, p.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int col = (i * TPR + lane) * V;
@@ -152,13 +160,17 @@ __global__ __launch_bounds__(threads_for<TPR>()) void join_fwd_kernel(const Join
 
 // With o = joined, gw = gnormed pre: do = gjoined + r2 (gw - o r2^2 mean(gw o));
 // then back through the residual, scale, gate and the first norm.
-template <typename T, typename RT, int V, int NV, int TPR>
-__global__ __launch_bounds__(threads_for<TPR>()) void join_bwd_kernel(const JoinK p) {
-    __shared__ float lds[TPR / 64][2];
-    constexpr int WPB = threads_for<TPR>() / TPR;
-    const int lane = threadIdx.x % TPR;
-    const int worker = static_cast<int>(blockIdx.x) * WPB + static_cast<int>(threadIdx.x) / TPR;
-    const int workers = static_cast<int>(gridDim.x) * WPB;
+// Where the registers allow (kAhead) the next row's loads are in flight while
+// a row is computed: its two sums over the row leave no other work between.
+template <typename T, typename RT, int V, int NV, bool kWave, int MAXT, bool kAhead>
+__global__ __launch_bounds__(kWave ? 256 : MAXT) void join_bwd_kernel(const JoinK p) {
+    typedef Row<kWave, MAXT> L;
+    __shared__ float lds[2][MAXT / 64][3];
+    int turn = 0;
+    const int TPR = L::lanes();
+    const int lane = L::lane();
+    const int worker = static_cast<int>(blockIdx.x) * L::per_block() + L::of_block();
+    const int workers = static_cast<int>(gridDim.x) * L::per_block();
     const float cf = static_cast<float>(p.c);
     const float inv = 1.0f / cf;
     float sp[NV][V], sc[NV][V], sn[NV][V];
@@ -167,24 +179,55 @@ __global__ __launch_bounds__(threads_for<TPR>()) void join_bwd_kernel(const Join
 #pragma unroll
         for (int v = 0; v < V; ++v) sp[i][v] = sc[i][v] = sn[i][v] = 0.0f;
 
-    for (int64_t row = worker; row < p.rows; row += workers) {
-        Pack<T, V> hp[NV], gp[NV], np[NV];
-        Pack<RT, V> op[NV], jp[NV];
-        float go[NV][V];
-        float ss = 0.0f, so = 0.0f, dot = 0.0f, unused = 0.0f;
+    // The parameters of a lane's columns, held over the rows where there is
+    // room: loaded at each row's turn they were three waits a row.
+    constexpr bool kHold = V * NV <= (MAXT > 512 ? 4 : 8);
+    float wpost[NV][V], wscale[NV][V], wpre[NV][V];
+    auto param = [&](const float* q, int i, float (&w)[V]) {
+        const int col = (i * TPR + lane) * V;
+#pragma unroll
+        for (int v = 0; v < V; ++v) w[v] = 1.0f;
+        if (q && col < p.c) widen(ld_pack<float, V>(q + col), w);
+    };
+    if (kHold) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            param(p.post, i, wpost[i]);
+            param(p.scale, i, wscale[i]);
+            param(p.pre, i, wpre[i]);
+        }
+    }
+    Pack<T, V> hp[NV], gp[NV], np[NV], hq[NV], gq[NV], nq[NV];
+    Pack<RT, V> op[NV], jp[NV], oq[NV], jq[NV];
+    auto load = [&](int64_t row) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int col = (i * TPR + lane) * V;
             if (col < p.c) {
-                hp[i] = ld_pack<T, V>(static_cast<const T*>(p.h) + row * p.ldh + col);
-                if (p.gate) gp[i] = ld_pack<T, V>(static_cast<const T*>(p.gate) + row * p.ldg + col);
-                if (p.gjoined) jp[i] = ld_pack<RT, V>(static_cast<const RT*>(p.gjoined) + row * p.ldgj + col);
+                hq[i] = ld_pack<T, V>(static_cast<const T*>(p.h) + row * p.ldh + col);
+                if (p.gate) gq[i] = ld_pack<T, V>(static_cast<const T*>(p.gate) + row * p.ldg + col);
+                if (p.gjoined) jq[i] = ld_pack<RT, V>(static_cast<const RT*>(p.gjoined) + row * p.ldgj + col);
                 if (p.pre) {
-                    op[i] = ld_pack<RT, V>(static_cast<const RT*>(p.joined) + row * p.ldj + col);
-                    np[i] = ld_pack<T, V>(static_cast<const T*>(p.gnormed) + row * p.ldgn + col);
+                    oq[i] = ld_pack<RT, V>(static_cast<const RT*>(p.joined) + row * p.ldj + col);
+                    nq[i] = ld_pack<T, V>(static_cast<const T*>(p.gnormed) + row * p.ldgn + col);
                 }
             }
         }
+    };
+    if (kAhead && worker < p.rows) load(worker);
+    for (int64_t row = worker; row < p.rows; row += workers) {
+        if (!kAhead) load(row);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            hp[i] = hq[i];
+            gp[i] = gq[i];
+            np[i] = nq[i];
+            op[i] = oq[i];
+            jp[i] = jq[i];
+        }
+        if (kAhead && row + workers < p.rows) load(row + workers);
+        float go[NV][V];
+        float sum[3] = {0.0f, 0.0f, 0.0f};  // of h^2, o^2 and gw o
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int col = (i * TPR + lane) * V;
@@ -195,33 +238,35 @@ __global__ __launch_bounds__(threads_for<TPR>()) void join_bwd_kernel(const Join
                 widen(hp[i], h);
                 if (p.gjoined) widen(jp[i], go[i]);
 #pragma unroll
-                for (int v = 0; v < V; ++v) ss = __builtin_fmaf(h[v], h[v], ss);
+                for (int v = 0; v < V; ++v) sum[0] = __builtin_fmaf(h[v], h[v], sum[0]);
                 if (p.pre) {
-                    float o[V], n[V], w[V];
+                    float o[V], n[V];
                     widen(op[i], o);
                     widen(np[i], n);
-                    widen(ld_pack<float, V>(p.pre + col), w);
+                    if (!kHold) param(p.pre, i, wpre[i]);
+                    const float (&w)[V] = wpre[i];
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
-                        so = __builtin_fmaf(o[v], o[v], so);
-                        dot = __builtin_fmaf(n[v] * w[v], o[v], dot);
+                        sum[1] = __builtin_fmaf(o[v], o[v], sum[1]);
+                        sum[2] = __builtin_fmaf(n[v] * w[v], o[v], sum[2]);
                     }
                 }
             }
         }
-        float r1 = 1.0f;
+        if (p.pre || p.post) L::template sums<3>(sum, lds, &turn);
+        const float r1 = p.post ? rnorm(sum[0], cf, p.eps) : 1.0f;
         if (p.pre) {
-            row_sums<TPR>(so, dot, lds);
-            const float r2 = rnorm(so, cf, p.eps);
-            const float k = r2 * r2 * dot * inv;
+            const float r2 = rnorm(sum[1], cf, p.eps);
+            const float k = r2 * r2 * sum[2] * inv;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int col = (i * TPR + lane) * V;
                 if (col < p.c) {
-                    float o[V], n[V], w[V];
+                    float o[V], n[V];
                     widen(op[i], o);
                     widen(np[i], n);
-                    widen(ld_pack<float, V>(p.pre + col), w);
+                    if (!kHold) param(p.pre, i, wpre[i]);
+                    const float (&w)[V] = wpre[i];
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
                         go[i][v] = __builtin_fmaf(r2, __builtin_fmaf(-o[v], k, n[v] * w[v]), go[i][v]);
@@ -230,26 +275,25 @@ __global__ __launch_bounds__(threads_for<TPR>()) void join_bwd_kernel(const Join
                 }
             }
         }
-        if (p.post) {
-            row_sums<TPR>(ss, unused, lds);
-            r1 = rnorm(ss, cf, p.eps);
-        }
-        dot = unused = 0.0f;
+        float dot[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int col = (i * TPR + lane) * V;
             if (col < p.c) {
                 if (p.dres) st_pack<RT, V>(static_cast<RT*>(p.dres) + row * p.lddr + col, go[i]);
-                float h[V], q[V], w[V], a[V], gv[V], dg[V];
+                float h[V], q[V], a[V], gv[V], dg[V];
                 widen(hp[i], h);
+                if (!kHold) {
+                    param(p.post, i, wpost[i]);
+                    param(p.scale, i, wscale[i]);
+                }
+                const float (&w)[V] = wpost[i];
+                const float (&s)[V] = wscale[i];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    w[v] = 1.0f;
                     a[v] = 1.0f;
+                    q[v] = h[v] * (r1 * w[v]);
                 }
-                if (p.post) widen(ld_pack<float, V>(p.post + col), w);
-#pragma unroll
-                for (int v = 0; v < V; ++v) q[v] = h[v] * (r1 * w[v]);
                 if (p.gate) {
                     widen(gp[i], gv);
 #pragma unroll
@@ -260,8 +304,6 @@ __global__ __launch_bounds__(threads_for<TPR>()) void join_bwd_kernel(const Join
                     }
                 }
                 if (p.scale) {
-                    float s[V];
-                    widen(ld_pack<float, V>(p.scale + col), s);
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
                         sc[i][v] = __builtin_fmaf(go[i][v], q[v] * a[v], sc[i][v]);
@@ -279,7 +321,7 @@ __global__ __launch_bounds__(threads_for<TPR>()) void join_bwd_kernel(const Join
                     if (p.post) {
                         sp[i][v] = __builtin_fmaf(go[i][v], h[v] * r1, sp[i][v]);
                         go[i][v] *= w[v];
-                        dot = __builtin_fmaf(go[i][v], h[v], dot);
+                        dot[0] = __builtin_fmaf(go[i][v], h[v], dot[0]);
                     }
                 }
             }
@@ -287,8 +329,8 @@ __global__ __launch_bounds__(threads_for<TPR>()) void join_bwd_kernel(const Join
         if (!p.dh) continue;
         float k = 0.0f;
         if (p.post) {
-            row_sums<TPR>(dot, unused, lds);
-            k = r1 * r1 * dot * inv;
+            L::template sums<1>(dot, lds, &turn);
+            k = r1 * r1 * dot[0] * inv;
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -346,32 +388,44 @@ JoinK join_params(const gspn_join_args& a) {
     return k;
 }
 
-// Lanes a row takes (see the top of the file).
-int lanes_for(int64_t c) { return c <= 1024 ? 64 : c <= 4096 ? 256 : 1024; }
+// Lanes of a row of c channels, V at a time.
+int lanes_for(int64_t c, int v) { return static_cast<int>((c + 64 * v - 1) / (64 * v) * 64); }
 
-template <typename T, typename RT, int V, int NV, int TPR>
-void run_join(bool bwd, const JoinK& k, int64_t workers, hipStream_t stream) {
-    constexpr int th = threads_for<TPR>();
-    constexpr int wpb = th / TPR;
-    const dim3 grid(static_cast<unsigned>((workers + wpb - 1) / wpb));
-    if (bwd) hipLaunchKernelGGL((join_bwd_kernel<T, RT, V, NV, TPR>), grid, dim3(th), 0, stream, k);
-    else hipLaunchKernelGGL((join_fwd_kernel<T, RT, V, NV, TPR>), grid, dim3(th), 0, stream, k);
+// NV values of V channels a lane: as many lanes as the row fills, or all.
+template <typename T, typename RT, int V, int NV, bool kWave, int MAXT>
+void run_join_fwd(const JoinK& k, int64_t workers, hipStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(kWave ? (workers + 3) / 4 : workers));
+    const dim3 block(kWave ? 256 : NV > 1 ? MAXT : lanes_for(k.c, V));
+    hipLaunchKernelGGL((join_fwd_kernel<T, RT, V, NV, kWave, MAXT>), grid, block, 0, stream, k);
+}
+
+template <typename T, typename RT, int V, int NV, bool kWave, int MAXT, bool kAhead>
+void run_join_bwd(const JoinK& k, int64_t workers, hipStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(kWave ? (workers + 3) / 4 : workers));
+    const dim3 block(kWave ? 256 : NV > 1 ? MAXT : lanes_for(k.c, V));
+    hipLaunchKernelGGL((join_bwd_kernel<T, RT, V, NV, kWave, MAXT, kAhead>), grid, block, 0, stream, k);
 }
 
 template <typename T, typename RT>
 void run_join_c(bool bwd, bool vec, const JoinK& k, int64_t workers, hipStream_t stream) {
-    if (vec) {
-        if (k.c <= 512) run_join<T, RT, 8, 1, 64>(bwd, k, workers, stream);
-        else if (k.c <= 1024) run_join<T, RT, 8, 2, 64>(bwd, k, workers, stream);
-        else if (k.c <= 2048) run_join<T, RT, 8, 1, 256>(bwd, k, workers, stream);
-        else if (k.c <= 4096) run_join<T, RT, 8, 2, 256>(bwd, k, workers, stream);
-        else if (k.c <= 8192) run_join<T, RT, 8, 1, 1024>(bwd, k, workers, stream);
-        else run_join<T, RT, 8, 2, 1024>(bwd, k, workers, stream);
+    if (!bwd && vec) {
+        if (k.c <= kWaveRow) run_join_fwd<T, RT, 8, 1, true, 64>(k, workers, stream);
+        else if (k.c <= 4096) run_join_fwd<T, RT, 8, 1, false, 512>(k, workers, stream);
+        else if (k.c <= 8192) run_join_fwd<T, RT, 8, 1, false, 1024>(k, workers, stream);
+        else run_join_fwd<T, RT, 8, 2, false, 1024>(k, workers, stream);
+    } else if (!bwd) {
+        if (k.c <= kWaveRow) run_join_fwd<T, RT, 1, 8, true, 64>(k, workers, stream);
+        else if (k.c <= 4096) run_join_fwd<T, RT, 1, 8, false, 512>(k, workers, stream);
+        else run_join_fwd<T, RT, 1, 16, false, 1024>(k, workers, stream);
+    } else if (vec) {
+        if (k.c <= kWaveRow) run_join_bwd<T, RT, 4, 2, true, 64, true>(k, workers, stream);
+        else if (k.c <= 4096) run_join_bwd<T, RT, 4, 1, false, 1024, true>(k, workers, stream);
+        else if (k.c <= 8192) run_join_bwd<T, RT, 8, 1, false, 1024, false>(k, workers, stream);
+        else run_join_bwd<T, RT, 8, 2, false, 1024, false>(k, workers, stream);
     } else {
-        if (k.c <= 256) run_join<T, RT, 1, 4, 64>(bwd, k, workers, stream);
-        else if (k.c <= 1024) run_join<T, RT, 1, 16, 64>(bwd, k, workers, stream);
-        else if (k.c <= 4096) run_join<T, RT, 1, 16, 256>(bwd, k, workers, stream);
-        else run_join<T, RT, 1, 16, 1024>(bwd, k, workers, stream);
+        if (k.c <= kWaveRow) run_join_bwd<T, RT, 1, 8, true, 64, false>(k, workers, stream);
+        else if (k.c <= 4096) run_join_bwd<T, RT, 1, 8, false, 512, false>(k, workers, stream);
+        else run_join_bwd<T, RT, 1, 16, false, 1024, false>(k, workers, stream);
     }
 }
 
@@ -410,7 +464,7 @@ hipError_t launch_join(bool bwd, const gspn_join_args& a, const JoinK& k, int64_
         vec = vec && aligned_rows(w, 0, 4, 16);
         GSPN_REPLAY_ROWS(kn, "parameter", w, 1, a.c, a.c, 4);
     }
-    GSPN_REPLAYED(kn, a.c > 4096 ? 1024 : 256, lanes_for(a.c) / 64 * 8);
+    GSPN_REPLAYED(kn, a.c > kWaveRow ? 1024 : 256, 2 * 16 * 3 * 4);
     if (dtype == kF32) run_join_c<float, float>(bwd, vec, k, workers, stream);
     else if (a.residual_dtype == kF32) run_join_c<bf16_t, float>(bwd, vec, k, workers, stream);
     else run_join_c<bf16_t, bf16_t>(bwd, vec, k, workers, stream);
@@ -419,14 +473,17 @@ hipError_t launch_join(bool bwd, const gspn_join_args& a, const JoinK& k, int64_
 
 }  // namespace
 
-// Workers (rows in flight) of the backward: enough to fill the GPU, few
-// enough that their partial rows stay a small part of the traffic; a multiple
-// of the rows a workgroup takes.
+// Workers (rows in flight) of the backward: what is resident at once (some 20
+// waves a CU, of 256 channels), fewer where that leaves each under four rows;
+// their partial rows stay a small part of the traffic.  A multiple of the rows
+// a workgroup takes.
 int64_t join_bwd_parts(int64_t rows, int64_t c) {
-    const int64_t cap = c <= 1024 ? 4096 : c <= 4096 ? 1024 : 512;
+    const int64_t waves = c <= kWaveRow ? 1 : (c + 255) / 256;
+    int64_t a_cu = 20 / waves;
+    if (a_cu < 1) a_cu = 1;
     int64_t w = (rows + 3) / 4;
-    if (w > cap) w = cap;
-    if (c <= 1024) w = (w + 3) / 4 * 4;
+    if (w > 256 * a_cu) w = 256 * a_cu;
+    if (c <= kWaveRow) w = (w + 3) / 4 * 4;
     return w < 1 ? 1 : w;
 }
 

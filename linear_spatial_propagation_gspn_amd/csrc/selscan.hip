@@ -520,8 +520,7 @@ __global__ __launch_bounds__(256) void selscan_step_kernel(const SelK p) {
         h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * (A2[i] * kLog2E)), h[i], u * b[i]);
         y = __builtin_fmaf(cv[i], h[i], y);
     }
-#pragma unroll
-    for (int m = 1; m < SPLIT; m *= 2) y += __shfl_xor(y, m);
+    y = quad_sum<SPLIT>(y);
     if (!live) return;
     if constexpr (kVec) {
         st_pack<float, SPL>(pool, h);

@@ -100,11 +100,6 @@ __device__ __forceinline__ float lane_value(float v, int lane) {
     return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
 }
 
-template <int kCtrl>
-__device__ __forceinline__ float dpp(float v) {
-    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), kCtrl, 0xf, 0xf, true));
-}
-
 // A uniform pointer to `row` of a tensor, kept in scalar registers: without
 // this the compiler carries a 64-bit vector address for every tensor and row of
 // a tile over the loop, and spills.

@@ -29,16 +29,6 @@ namespace {
 constexpr float kLn2 = 0.693147180559945309417f;
 constexpr int kTile = 1 << kCheckShift;  // rows rerun together
 
-__device__ __forceinline__ float swap_add32(float a, float b) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
-    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
-
-__device__ __forceinline__ float swap_add16(float a, float b) {
-    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
-    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
-
 // Four values summed over the wave's channels (lanes equal modulo SPLIT): the
 // 16-lane row r of the wave receives the sum of v[r == 1 ? 2 : r == 2 ? 1 : r].
 template <int SPLIT>

@@ -167,6 +167,36 @@ __device__ __forceinline__ float silu_grad(float v, float sg) {
     return sg * __builtin_fmaf(v, 1.0f - sg, 1.0f);
 }
 
+// Cross-lane sums without a trip through LDS: DPP within rows of 16 lanes,
+// swaps between halves and rows of the wave.
+template <int kCtrl>
+__device__ __forceinline__ float dpp(float v) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), kCtrl, 0xf, 0xf, true));
+}
+
+// Lanes 0-31 receive a's sum with its upper half, lanes 32-63 b's; likewise
+// between the even and odd rows of 16 lanes.
+__device__ __forceinline__ float swap_add32(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+__device__ __forceinline__ float swap_add16(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// The sum over the wave, the same bits in every lane (each step adds the same
+// two partial sums in all the lanes that share them).
+__device__ __forceinline__ float wave_sum(float v) {
+    v += dpp<0xB1>(v);   // lanes 1 0 3 2 of each quad
+    v += dpp<0x4E>(v);   // lanes 2 3 0 1
+    v += dpp<0x128>(v);  // rows of 16 rotated by 8
+    v += dpp<0x124>(v);  // by 4
+    v = swap_add16(v, v);
+    return swap_add32(v, v);
+}
+
 // Partial sums [parts][cols] (rows `ld` floats apart) summed over the parts in
 // a fixed order.  The columns are consecutive planes of `c` (column = plane *
 // c + channel); plane p's channel ch goes to the output that holds the plane.
