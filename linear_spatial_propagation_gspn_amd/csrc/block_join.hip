@@ -10,6 +10,8 @@
 // each, joined in a fixed order.
 #include "sequence.hpp"
 
+#include <type_traits>
+
 namespace gspn {
 namespace {
 
@@ -31,7 +33,7 @@ struct JoinK {
     void* dh;
     void* dgate;
     void* dres;
-    float* part;  // [worker][3][c]: sums for dpost, dscale, dpre
+    float* part;  // [workgroup][3][c]: sums for dpost, dscale, dpre
     int64_t ldh, ldg, ldr, ldj, ldn, ldgj, ldgn, lddh, lddg, lddr;
 };
 
@@ -160,8 +162,11 @@ __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_fwd_kernel(const Join
 
 // With o = joined, gw = gnormed pre: do = gjoined + r2 (gw - o r2^2 mean(gw o));
 // then back through the residual, scale, gate and the first norm.
-// Where the registers allow (kAhead) the next row's loads are in flight while
-// a row is computed: its two sums over the row leave no other work between.
+// kAhead, for up to eight channels a lane: the row stays in registers and the
+// next row's loads are in flight while it is computed (its two sums over the
+// row leave no other work between).  Otherwise each phase reads the row again,
+// from the caches: held, 16 channels a lane spilled and took three times the
+// time that the memory needs.
 template <typename T, typename RT, int V, int NV, bool kWave, int MAXT, bool kAhead>
 __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_bwd_kernel(const JoinK p) {
     typedef Row<kWave, MAXT> L;
@@ -181,7 +186,7 @@ __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_bwd_kernel(const Join
 
     // The parameters of a lane's columns, held over the rows where there is
     // room: loaded at each row's turn they were three waits a row.
-    constexpr bool kHold = V * NV <= (MAXT > 512 ? 4 : 8);
+    constexpr bool kHold = kAhead;
     float wpost[NV][V], wscale[NV][V], wpre[NV][V];
     auto param = [&](const float* q, int i, float (&w)[V]) {
         const int col = (i * TPR + lane) * V;
@@ -216,16 +221,22 @@ __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_bwd_kernel(const Join
     };
     if (kAhead && worker < p.rows) load(worker);
     for (int64_t row = worker; row < p.rows; row += workers) {
-        if (!kAhead) load(row);
+        if (kAhead) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            hp[i] = hq[i];
-            gp[i] = gq[i];
-            np[i] = nq[i];
-            op[i] = oq[i];
-            jp[i] = jq[i];
+            for (int i = 0; i < NV; ++i) {
+                hp[i] = hq[i];
+                gp[i] = gq[i];
+                np[i] = nq[i];
+                op[i] = oq[i];
+                jp[i] = jq[i];
+            }
+            if (row + workers < p.rows) load(row + workers);
         }
-        if (kAhead && row + workers < p.rows) load(row + workers);
+        auto get = [&](const auto& held, const void* q, int64_t ld, int i, float (&f)[V]) {
+            typedef std::remove_const_t<std::remove_reference_t<decltype(held.e[0])>> E;
+            if constexpr (kAhead) widen(held, f);
+            else widen(ld_pack<E, V>(static_cast<const E*>(q) + row * ld + (i * TPR + lane) * V), f);
+        };
         float go[NV][V];
         float sum[3] = {0.0f, 0.0f, 0.0f};  // of h^2, o^2 and gw o
 #pragma unroll
@@ -235,14 +246,14 @@ __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_bwd_kernel(const Join
             for (int v = 0; v < V; ++v) go[i][v] = 0.0f;
             if (col < p.c) {
                 float h[V];
-                widen(hp[i], h);
-                if (p.gjoined) widen(jp[i], go[i]);
+                get(hp[i], p.h, p.ldh, i, h);
+                if (p.gjoined) get(jp[i], p.gjoined, p.ldgj, i, go[i]);
 #pragma unroll
                 for (int v = 0; v < V; ++v) sum[0] = __builtin_fmaf(h[v], h[v], sum[0]);
                 if (p.pre) {
                     float o[V], n[V];
-                    widen(op[i], o);
-                    widen(np[i], n);
+                    get(op[i], p.joined, p.ldj, i, o);
+                    get(np[i], p.gnormed, p.ldgn, i, n);
                     if (!kHold) param(p.pre, i, wpre[i]);
                     const float (&w)[V] = wpre[i];
 #pragma unroll
@@ -263,8 +274,8 @@ __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_bwd_kernel(const Join
                 const int col = (i * TPR + lane) * V;
                 if (col < p.c) {
                     float o[V], n[V];
-                    widen(op[i], o);
-                    widen(np[i], n);
+                    get(op[i], p.joined, p.ldj, i, o);
+                    get(np[i], p.gnormed, p.ldgn, i, n);
                     if (!kHold) param(p.pre, i, wpre[i]);
                     const float (&w)[V] = wpre[i];
 #pragma unroll
@@ -282,7 +293,7 @@ __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_bwd_kernel(const Join
             if (col < p.c) {
                 if (p.dres) st_pack<RT, V>(static_cast<RT*>(p.dres) + row * p.lddr + col, go[i]);
                 float h[V], q[V], a[V], gv[V], dg[V];
-                widen(hp[i], h);
+                get(hp[i], p.h, p.ldh, i, h);
                 if (!kHold) {
                     param(p.post, i, wpost[i]);
                     param(p.scale, i, wscale[i]);
@@ -295,7 +306,7 @@ __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_bwd_kernel(const Join
                     q[v] = h[v] * (r1 * w[v]);
                 }
                 if (p.gate) {
-                    widen(gp[i], gv);
+                    get(gp[i], p.gate, p.ldg, i, gv);
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
                         const float sg = gate_sigmoid<float>(gv[v]);
@@ -337,7 +348,7 @@ __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_bwd_kernel(const Join
             const int col = (i * TPR + lane) * V;
             if (col < p.c) {
                 float h[V];
-                widen(hp[i], h);
+                get(hp[i], p.h, p.ldh, i, h);
 #pragma unroll
                 for (int v = 0; v < V; ++v) go[i][v] = r1 * __builtin_fmaf(-h[v], k, go[i][v]);
                 st_pack<T, V>(static_cast<T*>(p.dh) + row * p.lddh + col, go[i]);
@@ -345,14 +356,37 @@ __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_bwd_kernel(const Join
         }
     }
     if (!p.part) return;
-    float* const part = p.part + static_cast<int64_t>(worker) * 3 * p.c;
+    if constexpr (kWave) {  // the block's four waves leave one partial row
+        __shared__ float all[4][3][kWaveRow];
+        float (*const mine)[kWaveRow] = all[L::of_block()];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int col = (i * TPR + lane) * V;
-        if (col < p.c) {
-            st_pack<float, V>(part + col, sp[i]);
-            st_pack<float, V>(part + p.c + col, sc[i]);
-            st_pack<float, V>(part + 2 * static_cast<int64_t>(p.c) + col, sn[i]);
+        for (int i = 0; i < NV; ++i) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int col = (i * TPR + lane) * V + v;
+                mine[0][col] = sp[i][v];
+                mine[1][col] = sc[i][v];
+                mine[2][col] = sn[i][v];
+            }
+        }
+        __syncthreads();
+        float* const part = p.part + static_cast<int64_t>(blockIdx.x) * 3 * p.c;
+        for (int e = threadIdx.x; e < 3 * static_cast<int>(kWaveRow); e += 256) {
+            const int plane = e / static_cast<int>(kWaveRow), col = e % static_cast<int>(kWaveRow);
+            if (col < p.c)
+                part[plane * p.c + col] =
+                    (all[0][plane][col] + all[1][plane][col]) + (all[2][plane][col] + all[3][plane][col]);
+        }
+    } else {
+        float* const part = p.part + static_cast<int64_t>(worker) * 3 * p.c;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int col = (i * TPR + lane) * V;
+            if (col < p.c) {
+                st_pack<float, V>(part + col, sp[i]);
+                st_pack<float, V>(part + p.c + col, sc[i]);
+                st_pack<float, V>(part + 2 * static_cast<int64_t>(p.c) + col, sn[i]);
+            }
         }
     }
 }
@@ -424,7 +458,7 @@ void run_join_c(bool bwd, bool vec, const JoinK& k, int64_t workers, hipStream_t
         else run_join_bwd<T, RT, 8, 2, false, 1024, false>(k, workers, stream);
     } else {
         if (k.c <= kWaveRow) run_join_bwd<T, RT, 1, 8, true, 64, false>(k, workers, stream);
-        else if (k.c <= 4096) run_join_bwd<T, RT, 1, 8, false, 512, false>(k, workers, stream);
+        else if (k.c <= 4096) run_join_bwd<T, RT, 1, 8, false, 512, true>(k, workers, stream);
         else run_join_bwd<T, RT, 1, 16, false, 1024, false>(k, workers, stream);
     }
 }
@@ -453,7 +487,7 @@ hipError_t launch_join(bool bwd, const gspn_join_args& a, const JoinK& k, int64_
         rows("dresidual", a.dresidual, a.lddres, rs);
         if (k.part) {
             vec = vec && aligned_rows(k.part, a.c, 4, 16);
-            GSPN_REPLAY_ROWS(kn, "partial sums", k.part, workers * 3, a.c, a.c, 4);
+            GSPN_REPLAY_ROWS(kn, "partial sums", k.part, join_bwd_parts(a.rows, a.c) * 3, a.c, a.c, 4);
         }
     } else {
         rows("residual", a.residual, a.ldres, rs);
@@ -464,7 +498,7 @@ hipError_t launch_join(bool bwd, const gspn_join_args& a, const JoinK& k, int64_
         vec = vec && aligned_rows(w, 0, 4, 16);
         GSPN_REPLAY_ROWS(kn, "parameter", w, 1, a.c, a.c, 4);
     }
-    GSPN_REPLAYED(kn, a.c > kWaveRow ? 1024 : 256, 2 * 16 * 3 * 4);
+    GSPN_REPLAYED(kn, a.c > kWaveRow ? 1024 : 256, a.c > kWaveRow ? 2 * 16 * 3 * 4 : 4 * 3 * kWaveRow * 4 + 24);
     if (dtype == kF32) run_join_c<float, float>(bwd, vec, k, workers, stream);
     else if (a.residual_dtype == kF32) run_join_c<bf16_t, float>(bwd, vec, k, workers, stream);
     else run_join_c<bf16_t, bf16_t>(bwd, vec, k, workers, stream);
@@ -477,14 +511,19 @@ hipError_t launch_join(bool bwd, const gspn_join_args& a, const JoinK& k, int64_
 // waves a CU, of 256 channels), fewer where that leaves each under four rows;
 // their partial rows stay a small part of the traffic.  A multiple of the rows
 // a workgroup takes.
-int64_t join_bwd_parts(int64_t rows, int64_t c) {
+int64_t join_bwd_workers(int64_t rows, int64_t c) {
     const int64_t waves = c <= kWaveRow ? 1 : (c + 255) / 256;
     int64_t a_cu = 20 / waves;
     if (a_cu < 1) a_cu = 1;
     int64_t w = (rows + 3) / 4;
     if (w > 256 * a_cu) w = 256 * a_cu;
-    if (c <= kWaveRow) w = (w + 3) / 4 * 4;
-    return w < 1 ? 1 : w;
+    if (w < 1) w = 1;
+    return c <= kWaveRow ? (w + 3) / 4 * 4 : w;
+}
+
+// Partial rows, one a workgroup.
+int64_t join_bwd_parts(int64_t rows, int64_t c) {
+    return join_bwd_workers(rows, c) / (c <= kWaveRow ? 4 : 1);
 }
 
 hipError_t launch_join_fwd(const gspn_join_args& a, int dtype, hipStream_t stream) {
@@ -495,12 +534,12 @@ hipError_t launch_join_bwd(const gspn_join_args& a, int dtype, hipStream_t strea
     JoinK k = join_params(a);
     const bool sums = a.dpost || a.dscale || a.dpre;
     if (sums) k.part = static_cast<float*>(a.workspace);
-    const int64_t workers = join_bwd_parts(a.rows, a.c);
+    const int64_t workers = join_bwd_workers(a.rows, a.c);
     const hipError_t e = launch_join(true, a, k, workers, dtype, stream);
     if (e != hipSuccess || !sums) return e;
     ReduceK r{};
     r.part = k.part;
-    r.parts = workers;
+    r.parts = join_bwd_parts(a.rows, a.c);
     r.c = a.c;
     r.ld = r.cols = 3 * a.c;
     r.o[0] = {a.dpost, 1, 1, 0};
