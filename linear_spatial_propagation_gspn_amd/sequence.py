@@ -159,6 +159,14 @@ def _rows(t, name: str, shape: tuple, dtype, index: int, tail: int = 1) -> int:
 
 def _ptr_rows(t, name: str, shape: tuple, dtype, index: int, tail: int = 1) -> tuple:
     """A checked row tensor's pointer and row stride."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index >= 0 and t.shape == shape:
+        stride = t.stride()  # the usual layouts at once; anything else, and every error, below
+        if tail == 1:
+            if len(shape) == 2 and stride[1] == 1 and stride[0] >= shape[1] > 0 and shape[0] > 1:
+                return t.data_ptr(), stride[0]
+        elif len(shape) == 3 and stride[2] == 1 and stride[1] == shape[2] and shape[0] > 1:
+            if stride[0] >= shape[1] * shape[2] > 0:
+                return t.data_ptr(), stride[0]
     ld = _rows(t, name, shape, dtype, index, tail)
     return t.data_ptr(), ld
 
@@ -167,6 +175,9 @@ def _flat(t, name: str, shape: tuple, dtype, index: int):
     """Checks a contiguous tensor (or None) and returns its pointer."""
     if t is None:
         return None
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index >= 0 and t.shape == shape
+            and t.is_contiguous()):
+        return t.data_ptr()
     _tensor(t, name, dtype, index)
     if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
@@ -318,7 +329,8 @@ def gspn_causal_conv_bwd(x, weight, bias, gy, silu: bool = True, cu=None, nseq=N
 # --------------------------------------------------------------------------------------------- selective scan
 
 def _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, seq) -> SelscanArgs:
-    c, dev = x.shape[-1], x.get_device()
+    shape, dtype, dev = x.shape, x.dtype, x.get_device()
+    c = shape[-1]
     a = SelscanArgs()
     a.seq = seq
     if not isinstance(A, torch.Tensor) or A.dim() != 2:
@@ -329,13 +341,13 @@ def _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, seq) -> SelscanArgs:
     if groups < 1 or c % groups:
         raise ValueError("%d channels are not %d equal groups" % (c, groups))
     a.channels, a.groups, a.n, a.softplus = c, groups, n, 1 if softplus else 0
-    a.x, a.ldx = _ptr_rows(x, "x", x.shape, x.dtype, dev)
-    a.dt, a.lddt = _ptr_rows(dt, "dt", x.shape, x.dtype, dev)
+    a.x, a.ldx = _ptr_rows(x, "x", shape, dtype, dev)
+    a.dt, a.lddt = _ptr_rows(dt, "dt", shape, dtype, dev)
     if z is not None:
-        a.z, a.ldz = _ptr_rows(z, "z", x.shape, x.dtype, dev)
-    bshape = (*x.shape[:-1], groups, n)
-    a.B, a.ldb = _ptr_rows(B, "B", bshape, x.dtype, dev, 2)
-    a.C, a.ldc = _ptr_rows(C, "C", bshape, x.dtype, dev, 2)
+        a.z, a.ldz = _ptr_rows(z, "z", shape, dtype, dev)
+    bshape = (*shape[:-1], groups, n)
+    a.B, a.ldb = _ptr_rows(B, "B", bshape, dtype, dev, 2)
+    a.C, a.ldc = _ptr_rows(C, "C", bshape, dtype, dev, 2)
     a.A = _flat(A, "A", (c, n), torch.float32, dev)
     a.D = _flat(D, "D", (c,), torch.float32, dev)
     a.dt_bias = _flat(dt_bias, "dt_bias", (c,), torch.float32, dev)
