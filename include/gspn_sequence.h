@@ -25,9 +25,11 @@
  *    rounded once, at its store.
  *  - Sequences.  `rows` rows hold nseq sequences, one after another.
  *    cu == NULL: equal lengths rows / nseq (nseq must divide rows).
+ *    At most 2^23 sequences.
  *    Otherwise cu is a device array of nseq + 1 offsets, not decreasing,
  *    0 <= cu[i] <= rows: sequence i is rows [cu[i], cu[i+1]); it may be
- *    empty.  Rows outside every sequence are neither read nor written.
+ *    empty.  Rows outside every sequence are not read, and not written but
+ *    by the backward calls, which give them zero gradients.
  *    Offsets that break these rules give unspecified results inside the
  *    caller's buffers (they are clamped to [0, rows]).
  *  - Slots.  A call that carries state works on a pool of nslots entries.

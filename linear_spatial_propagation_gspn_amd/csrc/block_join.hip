@@ -83,79 +83,81 @@ __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_fwd_kernel(const Join
     int turn = 0;
     const int TPR = L::lanes();
     const int lane = L::lane();
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * L::per_block() + L::of_block();
-    if (row >= p.rows) return;  // a whole wave, or the whole block
     const float cf = static_cast<float>(p.c);
-    float e[NV][V], o[NV][V];
-    Pack<T, V> g[NV];
-    Pack<RT, V> r[NV];
-    float ss[1] = {0.0f};
+    // one row, unless there are more than a grid holds
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * L::per_block() + L::of_block(); row < p.rows;
+         row += static_cast<int64_t>(gridDim.x) * L::per_block()) {
+        float e[NV][V], o[NV][V];
+        Pack<T, V> g[NV];
+        Pack<RT, V> r[NV];
+        float ss[1] = {0.0f};
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int col = (i * TPR + lane) * V;
+        for (int i = 0; i < NV; ++i) {
+            const int col = (i * TPR + lane) * V;
 #pragma unroll
-        for (int v = 0; v < V; ++v) e[i][v] = 0.0f;
-        if (col < p.c) {
-            widen(ld_pack<T, V>(static_cast<const T*>(p.h) + row * p.ldh + col), e[i]);
-            if (p.gate) g[i] = ld_pack<T, V>(static_cast<const T*>(p.gate) + row * p.ldg + col);
-            if (p.res) r[i] = ld_pack<RT, V>(static_cast<const RT*>(p.res) + row * p.ldr + col);
+            for (int v = 0; v < V; ++v) e[i][v] = 0.0f;
+            if (col < p.c) {
+                widen(ld_pack<T, V>(static_cast<const T*>(p.h) + row * p.ldh + col), e[i]);
+                if (p.gate) g[i] = ld_pack<T, V>(static_cast<const T*>(p.gate) + row * p.ldg + col);
+                if (p.res) r[i] = ld_pack<RT, V>(static_cast<const RT*>(p.res) + row * p.ldr + col);
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) ss[0] = __builtin_fmaf(e[i][v], e[i][v], ss[0]);
         }
+        float r1 = 1.0f;
+        if (p.post) {
+            L::template sums<1>(ss, lds, &turn);
+            r1 = rnorm(ss[0], cf, p.eps);
+        }
+        ss[0] = 0.0f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) ss[0] = __builtin_fmaf(e[i][v], e[i][v], ss[0]);
-    }
-    float r1 = 1.0f;
-    if (p.post) {
+        for (int i = 0; i < NV; ++i) {
+            const int col = (i * TPR + lane) * V;
+            if (col < p.c) {
+                float w[V];
+                if (p.post) {
+                    widen(ld_pack<float, V>(p.post + col), w);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) e[i][v] *= r1 * w[v];
+                }
+                if (p.gate) {
+                    widen(g[i], w);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) e[i][v] *= w[v] * gate_sigmoid<float>(w[v]);
+                }
+                if (p.scale) {
+                    widen(ld_pack<float, V>(p.scale + col), w);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) e[i][v] *= w[v];
+                }
+                if (p.res) {
+                    widen(r[i], w);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) e[i][v] += w[v];
+                }
+                st_pack<RT, V>(static_cast<RT*>(p.joined) + row * p.ldj + col, e[i]);
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                RT s;  // the norm is that of the rows as they are stored
+                Store<RT>::st(&s, e[i][v]);
+                o[i][v] = Store<RT>::ld(&s);
+                if (col < p.c) ss[0] = __builtin_fmaf(o[i][v], o[i][v], ss[0]);
+            }
+        }
+        if (!p.pre) continue;
         L::template sums<1>(ss, lds, &turn);
-        r1 = rnorm(ss[0], cf, p.eps);
-    }
-    ss[0] = 0.0f;
+        const float r2 = rnorm(ss[0], cf, p.eps);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int col = (i * TPR + lane) * V;
-        if (col < p.c) {
-            float w[V];
-            if (p.post) {
-                widen(ld_pack<float, V>(p.post + col), w);
+        for (int i = 0; i < NV; ++i) {
+            const int col = (i * TPR + lane) * V;
+            if (col < p.c) {
+                float w[V];
+                widen(ld_pack<float, V>(p.pre + col), w);
 #pragma unroll
-                for (int v = 0; v < V; ++v) e[i][v] *= r1 * w[v];
+                for (int v = 0; v < V; ++v) w[v] *= o[i][v] * r2;
+                st_pack<T, V>(static_cast<T*>(p.normed) + row * p.ldn + col, w);
             }
-            if (p.gate) {
-                widen(g[i], w);
-#pragma unroll
-                for (int v = 0; v < V; ++v) e[i][v] *= w[v] * gate_sigmoid<float>(w[v]);
-            }
-            if (p.scale) {
-                widen(ld_pack<float, V>(p.scale + col), w);
-#pragma unroll
-                for (int v = 0; v < V; ++v) e[i][v] *= w[v];
-            }
-            if (p.res) {
-                widen(r[i], w);
-#pragma unroll
-                for (int v = 0; v < V; ++v) e[i][v] += w[v];
-            }
-            st_pack<RT, V>(static_cast<RT*>(p.joined) + row * p.ldj + col, e[i]);
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            RT s;  // the norm is that of the rows as they are stored
-            Store<RT>::st(&s, e[i][v]);
-            o[i][v] = Store<RT>::ld(&s);
-            if (col < p.c) ss[0] = __builtin_fmaf(o[i][v], o[i][v], ss[0]);
-        }
-    }
-    if (!p.pre) return;
-    L::template sums<1>(ss, lds, &turn);
-    const float r2 = rnorm(ss[0], cf, p.eps);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int col = (i * TPR + lane) * V;
-        if (col < p.c) {
-            float w[V];
-            widen(ld_pack<float, V>(p.pre + col), w);
-#pragma unroll
-            for (int v = 0; v < V; ++v) w[v] *= o[i][v] * r2;
-            st_pack<T, V>(static_cast<T*>(p.normed) + row * p.ldn + col, w);
         }
     }
 }
@@ -527,7 +529,8 @@ int64_t join_bwd_parts(int64_t rows, int64_t c) {
 }
 
 hipError_t launch_join_fwd(const gspn_join_args& a, int dtype, hipStream_t stream) {
-    return launch_join(false, a, join_params(a), a.rows, dtype, stream);
+    const int64_t most = int64_t{1} << 21;  // rows of a grid; beyond, a workgroup takes several
+    return launch_join(false, a, join_params(a), a.rows < most ? a.rows : most, dtype, stream);
 }
 
 hipError_t launch_join_bwd(const gspn_join_args& a, int dtype, hipStream_t stream) {

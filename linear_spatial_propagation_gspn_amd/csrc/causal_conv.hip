@@ -304,6 +304,31 @@ __global__ __launch_bounds__(64 * kReduceRuns) void reduce_parts_kernel(const Re
     }
 }
 
+// One wave a row of the rows outside; where the sequences cover every row, as
+// they mostly do, a launch of a few microseconds against a pass over all the
+// gradients to clear them beforehand.
+__global__ __launch_bounds__(256) void zero_outside_kernel(const OutsideK k) {
+    const int lo = seq_begin(k.seq, 0);
+    const int last = k.seq.nseq - 1;
+    const int hi = seq_end(k.seq, last, seq_begin(k.seq, last));
+    const int64_t outside = lo + static_cast<int64_t>(k.seq.rows > hi ? k.seq.rows - hi : 0);
+    const int lane = threadIdx.x & 63;
+    for (int64_t i = blockIdx.x * 4 + (threadIdx.x >> 6); i < outside; i += gridDim.x * 4) {
+        const int64_t row = i < lo ? i : hi + (i - lo);
+#pragma unroll
+        for (int j = 0; j < 5; ++j) {
+            if (!k.t[j].p) continue;
+            if (k.es == 4) {
+                float* const q = static_cast<float*>(k.t[j].p) + row * k.t[j].ld;
+                for (int64_t e = lane; e < k.t[j].c; e += 64) q[e] = 0.0f;
+            } else {
+                bf16_t* const q = static_cast<bf16_t*>(k.t[j].p) + row * k.t[j].ld;
+                for (int64_t e = lane; e < k.t[j].c; e += 64) q[e] = 0;
+            }
+        }
+    }
+}
+
 // Rows per chunk: the longest of 64, 32, 16, 8 that still gives four waves a
 // SIMD (of 128 channels).  A longer run re-reads fewer halo rows: 8192 rows of
 // 2304 channels backward took 28.2 us at 32 and at 16 rows, 33.8 at 8.
@@ -408,8 +433,15 @@ hipError_t launch_conv_step(const gspn_conv_args& a, int dtype, hipStream_t stre
 }
 
 hipError_t launch_conv_bwd(const gspn_conv_args& a, int dtype, hipStream_t stream) {
-    const hipError_t e = launch_conv(2, a, dtype, stream);
+    hipError_t e = launch_conv(2, a, dtype, stream);
     if (e != hipSuccess) return e;
+    if (a.seq.cu) {
+        OutsideK o{};
+        o.seq = make_seq(a.seq);
+        o.es = dtype == kF32 ? 4 : 2;
+        o.t[0] = {a.dx, a.lddx, a.c};
+        if ((e = launch_zero_outside(o, stream)) != hipSuccess) return e;
+    }
     ReduceK r{};
     r.part = static_cast<const float*>(a.workspace);
     r.parts = chunk_ids(a.seq.cu != nullptr, a.seq.rows, a.seq.nseq, conv_shift_for(a.seq.rows, a.c));
@@ -420,6 +452,18 @@ hipError_t launch_conv_bwd(const gspn_conv_args& a, int dtype, hipStream_t strea
     r.o[1] = {a.dbias, 1, 1, 0};
     r.o[2] = {nullptr, 0, 0, 0};
     return launch_reduce_parts(r, stream);
+}
+
+hipError_t launch_zero_outside(const OutsideK& k, hipStream_t stream) {
+    for (const auto& t : k.t) {
+        (void)t;
+        GSPN_REPLAY_ROWS("zero_outside_kernel", "gradient", t.p, k.seq.rows, t.ld, t.c, k.es);
+    }
+    GSPN_REPLAYED("zero_outside_kernel", 256, 0);
+    const int64_t blocks = (static_cast<int64_t>(k.seq.rows) + 3) / 4;
+    hipLaunchKernelGGL(zero_outside_kernel, dim3(static_cast<unsigned>(blocks < 1 ? 1 : blocks < 512 ? blocks : 512)),
+                       dim3(256), 0, stream, k);
+    return hipGetLastError();
 }
 
 hipError_t launch_reduce_parts(const ReduceK& k, hipStream_t stream) {

@@ -493,25 +493,26 @@ template <typename T>
 __global__ __launch_bounds__(256) void selscan_bc_kernel(const SelK p, T* __restrict__ dB, T* __restrict__ dC) {
     const int64_t gn = static_cast<int64_t>(p.groups) * p.n;
     const int64_t per = static_cast<int64_t>(p.seq.rows) * 2 * gn;
-    const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (e >= per) return;
-    const int64_t row = e / (2 * gn);
-    const int64_t m = e - row * 2 * gn;
     const int lo = seq_begin(p.seq, 0);
     const int hi = seq_end(p.seq, p.seq.nseq - 1, seq_begin(p.seq, p.seq.nseq - 1));
-    if (row < lo || row >= hi) return;
-    float s = 0.0f;
-    int b = 0;
-    for (; b + 8 <= p.blocks; b += 8) {
-        float v[8];
+    for (int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; e < per;
+         e += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t row = e / (2 * gn);
+        const int64_t m = e - row * 2 * gn;
+        if (row < lo || row >= hi) continue;
+        float s = 0.0f;
+        int b = 0;
+        for (; b + 8 <= p.blocks; b += 8) {
+            float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = p.partbc[(b + j) * per + e];
+            for (int j = 0; j < 8; ++j) v[j] = p.partbc[(b + j) * per + e];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s += v[j];
+            for (int j = 0; j < 8; ++j) s += v[j];
+        }
+        for (; b < p.blocks; ++b) s += p.partbc[b * per + e];
+        if (m < gn) Store<T>::st(dB + row * gn + m, s);
+        else Store<T>::st(dC + row * gn + (m - gn), s);
     }
-    for (; b < p.blocks; ++b) s += p.partbc[b * per + e];
-    if (m < gn) Store<T>::st(dB + row * gn + m, s);
-    else Store<T>::st(dC + row * gn + (m - gn), s);
 }
 
 template <typename T, int NP>
@@ -625,9 +626,21 @@ hipError_t launch_selscan_bwd(const gspn_selscan_args& a, int dtype, hipStream_t
     else run_bwd_n<bf16_t>(k, grid, stream);
     if ((e = hipGetLastError()) != hipSuccess) return e;
 
+    if (ragged) {
+        OutsideK o{};
+        o.seq = k.seq;
+        o.es = es;
+        o.t[0] = {a.dx, a.lddx, a.channels};
+        o.t[1] = {a.ddt, a.ldddt, a.channels};
+        o.t[2] = {a.z ? a.dz : nullptr, a.lddz, a.channels};
+        o.t[3] = {a.dB, a.groups * a.n, a.groups * a.n};
+        o.t[4] = {a.dC, a.groups * a.n, a.groups * a.n};
+        if ((e = launch_zero_outside(o, stream)) != hipSuccess) return e;
+    }
     const int64_t values = a.seq.rows * 2 * a.groups * a.n;
     if (values > 0) {
-        const dim3 bg(static_cast<unsigned>((values + 255) / 256));
+        const int64_t most = int64_t{1} << 20;  // workgroups; beyond, each takes several runs of values
+        const dim3 bg(static_cast<unsigned>((values + 255) / 256 < most ? (values + 255) / 256 : most));
         GSPN_REPLAY_ROWS("selscan_bc_kernel", "dB", a.dB, a.seq.rows, a.groups * a.n, a.groups * a.n, es);
         GSPN_REPLAY_ROWS("selscan_bc_kernel", "dC", a.dC, a.seq.rows, a.groups * a.n, a.groups * a.n, es);
         GSPN_REPLAYED("selscan_bc_kernel", 256, 0);

@@ -114,8 +114,15 @@ __device__ __forceinline__ int slot_of(const SeqK& s, int i) {
     if (v < 0) return kNoSlot;
     if (v >= s.nslots) return kBadSlot;
     const int lane = __lane_id();
-    for (int j0 = 0; j0 < i; j0 += 64)
-        if (__any(j0 + lane < i && s.slots[j0 + lane] == v)) return kBadSlot;
+    for (int j0 = 0; j0 < i; j0 += 256) {
+        bool same = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int at = j0 + j * 64 + lane;
+            same = same || (at < i && s.slots[at] == v);
+        }
+        if (__any(same)) return kBadSlot;
+    }
     return v;
 }
 
@@ -211,6 +218,18 @@ struct ReduceK {
     ReduceOut o[3];
 };
 hipError_t launch_reduce_parts(const ReduceK& k, hipStream_t stream);
+
+// Zeros in the rows before the first and behind the last packed sequence, of
+// up to five tensors (p null: none; es: bytes of an element).
+struct OutsideK {
+    SeqK seq;
+    int32_t es;
+    struct {
+        void* p;
+        int64_t ld, c;
+    } t[5];
+};
+hipError_t launch_zero_outside(const OutsideK& k, hipStream_t stream);
 
 // Host side ---------------------------------------------------------------
 

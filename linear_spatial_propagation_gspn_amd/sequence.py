@@ -313,10 +313,10 @@ def gspn_causal_conv_bwd(x, weight, bias, gy, silu: bool = True, cu=None, nseq=N
     dt = _need_rows(x, "x")
     a = _conv_args(x, weight, bias, silu, _sequences(x, cu, nseq))
     a.gy, a.ldgy = _ptr_rows(gy, "gy", x.shape, x.dtype, x.get_device())
-    dx = (x.new_empty if cu is None else x.new_zeros)(x.shape)
-    a.dx, a.lddx = dx.data_ptr(), a.c
     if a.seq.nseq == 0:
-        return dx, torch.zeros_like(weight), None if bias is None else torch.zeros_like(bias)
+        return torch.zeros_like(x, memory_format=torch.contiguous_format), torch.zeros_like(weight), None if bias is None else torch.zeros_like(bias)
+    dx = x.new_empty(x.shape)
+    a.dx, a.lddx = dx.data_ptr(), max(a.c, 1)
     dweight = torch.empty_like(weight)
     dbias = None if bias is None else torch.empty_like(bias)
     a.dweight, a.dbias = dweight.data_ptr(), None if dbias is None else dbias.data_ptr()
@@ -428,10 +428,10 @@ def gspn_selective_scan_bwd(x, dt, A, B, C, gy, D=None, z=None, dt_bias=None, so
     dev = x.get_device()
     a = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, _sequences(x, cu, nseq))
     a.gy, a.ldgy = _ptr_rows(gy, "gy", x.shape, x.dtype, dev)
-    new = x.new_empty if cu is None else x.new_zeros
+    none = a.seq.nseq == 0
+    new = x.new_zeros if none else x.new_empty
     dx, ddt, dz = new(x.shape), new(x.shape), None if z is None else new(x.shape)
     dB, dC = new(B.shape), new(B.shape)
-    none = a.seq.nseq == 0
     like = torch.zeros_like if none else torch.empty_like
     dA, dD, dbias = like(A), None if D is None else like(D), None if dt_bias is None else like(dt_bias)
     grads = (dx, ddt, dA, dB, dC, dD, dz, dbias)
@@ -543,6 +543,16 @@ def gspn_block_join_bwd(h, gjoined, gnormed, joined, gate=None, residual=None, p
 
 # --------------------------------------------------------------------------------------------------- autograd
 
+def _wants_grad(*tensors) -> bool:
+    """Whether autograd will ask for a gradient; if not, nothing is kept for a backward."""
+    return torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in tensors)
+
+
+def _clear(x, cu):
+    """With packed sequences, an output whose rows outside them are zero."""
+    return None if cu is None or not isinstance(x, torch.Tensor) else x.new_zeros(x.shape)
+
+
 def _grad_rows(g, like):
     """A gradient in its tensor's dtype, with contiguous columns."""
     return g.to(like).contiguous()
@@ -553,8 +563,7 @@ class _CausalConv(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, silu, cu, nseq, x, weight, bias):
-        out = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if cu is not None else None
-        y = gspn_causal_conv_fwd(x, weight, bias, silu, cu, nseq, out=out)
+        y = gspn_causal_conv_fwd(x, weight, bias, silu, cu, nseq, out=_clear(x, cu))
         ctx.silu, ctx.nseq = silu, nseq
         ctx.save_for_backward(x, weight, bias, cu)
         return y
@@ -570,6 +579,8 @@ class _CausalConv(torch.autograd.Function):
 def causal_conv(x, weight, bias=None, silu: bool = True, cu=None, nseq=None) -> torch.Tensor:
     """The short causal convolution as a differentiable op (no state); rows
     outside the sequences of ``cu`` are zero."""
+    if not _wants_grad(x, weight, bias):
+        return gspn_causal_conv_fwd(x, weight, bias, silu, cu, nseq, out=_clear(x, cu))
     return _CausalConv.apply(bool(silu), cu, nseq, x, weight, bias)
 
 
@@ -579,9 +590,8 @@ class _SelectiveScan(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, softplus, cu, nseq, x, dt, A, B, C, D, z, dt_bias):
-        out = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if cu is not None else None
         y, kept = gspn_selective_scan_fwd(x, dt, A, B, C, D, z, dt_bias, softplus, cu, nseq, checkpoints=True,
-                                          out=out)
+                                          out=_clear(x, cu))
         ctx.softplus, ctx.nseq = softplus, nseq
         ctx.save_for_backward(x, dt, A, B, C, D, z, dt_bias, cu, kept)
         return y
@@ -600,6 +610,8 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus: bool 
     """The selective scan as a differentiable op (no state); rows outside the
     sequences of ``cu`` are zero.  The forward keeps its states before every
     8th row (n / 2 bytes an element of x) until the backward."""
+    if not _wants_grad(x, dt, A, B, C, D, z, dt_bias):
+        return gspn_selective_scan_fwd(x, dt, A, B, C, D, z, dt_bias, softplus, cu, nseq, out=_clear(x, cu))
     return _SelectiveScan.apply(bool(softplus), cu, nseq, x, dt, A, B, C, D, z, dt_bias)
 
 
@@ -632,4 +644,6 @@ class _BlockJoin(torch.autograd.Function):
 def block_join(h, gate=None, residual=None, post=None, scale=None, pre=None, eps: float = 1e-6) -> tuple:
     """The join of a block's output to the residual stream as a differentiable
     op: (joined, normed), normed None without pre."""
+    if not _wants_grad(h, gate, residual, post, scale, pre):
+        return gspn_block_join_fwd(h, gate, residual, post, scale, pre, eps)
     return _BlockJoin.apply(float(eps), h, gate, residual, post, scale, pre)
