@@ -6,7 +6,7 @@
 //   dx = d sum_n g B + D gy'      dd = sum_n g (A a h_{t-1} + x B)
 //   dA = sum_t g d a h_{t-1}      ddt = dd softplus'(dt + bias)
 // The states come back from the forward's checkpoints, one every 8 rows: a
-// wave reruns 8 rows forward, keeping a_t and a_t h_{t-1} in registers, and
+// wave reruns 8 rows forward, keeping the decays and states in registers, and
 // walks back over them.  Four lanes share a channel (SPL states each), which
 // keeps those 8 rows within 64 registers.  Each of the four takes a quarter
 // of the rows for what is per row and channel (softplus, gate, the outputs);
@@ -30,7 +30,8 @@ constexpr float kLn2 = 0.693147180559945309417f;
 constexpr int kTile = 1 << kCheckShift;  // rows rerun together
 
 // Four values summed over the wave's channels (lanes equal modulo SPLIT): the
-// 16-lane row r of the wave receives the sum of v[r == 1 ? 2 : r == 2 ? 1 : r].
+// 16-lane row r of the wave receives the sum of v[r == 1 ? 2 : r == 2 ? 1 : r],
+// the same bits in the lanes that share it.
 template <int SPLIT>
 __device__ __forceinline__ float channel_sum(const float (&v)[4]) {
     float s = swap_add16(swap_add32(v[0], v[1]), swap_add32(v[2], v[3]));
@@ -344,7 +345,7 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
                 const int v = tid + i * 256;
                 if (v < kTile * 2 * NP) (&bc[buf][0][0])[v] = Store<T>::ld(&nbc[i]);
             }
-            float xv[R], dv[R], uv[R], gp[R], sg[R], gz[R], yv[R], h[SPL];
+            float xv[R], dv[R], uv[R], gp[R], sg[R], gz[R], yv[R];
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const bool in = live && base + i * SPLIT + sub < ck.r1;
@@ -364,13 +365,12 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
                 }
                 uv[i] = dv[i] * xv[i];
             }
-#pragma unroll
-            for (int s = 0; s < SPL; ++s) h[s] = nh[s];
             __syncthreads();
             if (tile + 1 < tiles) flush(tile + 1, buf ^ 1);
+            float a[kTile][SPL], hs[kTile + 1][SPL];  // decays; states before each row, and the last
+#pragma unroll
+            for (int s = 0; s < SPL; ++s) hs[0][s] = nh[s];
             if (tile > 0) load(tile - 1);
-
-            float a[kTile][SPL], q[kTile][SPL];  // q = a_t h_{t-1}
             auto forward = [&](auto jc, int i) {
                 constexpr int J = decltype(jc)::value;
                 const int t = i * SPLIT + J;
@@ -381,14 +381,13 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
 #pragma unroll
                 for (int s = 0; s < SPL; ++s) {
                     a[t][s] = __builtin_amdgcn_exp2f(d * A2[s]);
-                    q[t][s] = a[t][s] * h[s];
-                    h[s] = __builtin_fmaf(u, b[s], q[t][s]);
+                    hs[t + 1][s] = __builtin_fmaf(a[t][s], hs[t][s], u * b[s]);
                 }
                 if constexpr (kGate) {
                     float cv[SPL], y = 0.0f;
                     widen(ld_pack<float, SPL>(&bc[buf][t][NP + n0]), cv);
 #pragma unroll
-                    for (int s = 0; s < SPL; ++s) y = __builtin_fmaf(cv[s], h[s], y);
+                    for (int s = 0; s < SPL; ++s) y = __builtin_fmaf(cv[s], hs[t + 1][s], y);
                     y = quad_sum<SPLIT>(y);
                     yv[i] = SPLIT == 1 || sub == J ? y : yv[i];
                 }
@@ -418,13 +417,13 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
                 for (int s = 0; s < SPL; ++s) {
                     const float gt = __builtin_fmaf(cv[s], y, ag[s]);
                     const int m = ((kTile - 1 - t) * SPL + s) % 4;
-                    vC[m] = y * __builtin_fmaf(u, b[s], q[t][s]);
+                    vC[m] = y * hs[t + 1][s];
                     vB[m] = gt * u;
                     sb = __builtin_fmaf(gt, b[s], sb);
-                    const float gq = gt * q[t][s];
+                    ag[s] = a[t][s] * gt;
+                    const float gq = ag[s] * hs[t][s];  // g a h_{t-1}
                     sa = __builtin_fmaf(gq, A2[s], sa);
                     dA[s] = __builtin_fmaf(gq, d, dA[s]);
-                    ag[s] = a[t][s] * gt;
                 }
                 sb = quad_sum<SPLIT>(sb);
                 sa = quad_sum<SPLIT>(sa);
@@ -438,11 +437,11 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
                     const float rc = channel_sum<SPLIT>(vC);
                     const int r = lane >> 4;
                     const int m = r == 1 ? 2 : r == 2 ? 1 : r;
-                    if ((lane & 15) < SPLIT) {
-                        float* const o = &red[buf][wave][t + 4 / SPL - 1 - m / SPL][n0 + m % SPL];
-                        o[0] = rb;
-                        o[NP] = rc;
-                    }
+                    // every lane of a row holds the same bits for its state, and writes
+                    // them: a branch for one quad alone cost five instructions a row
+                    float* const o = &red[buf][wave][t + 4 / SPL - 1 - m / SPL][n0 + m % SPL];
+                    o[0] = rb;
+                    o[NP] = rc;
                 }
             };
 #pragma unroll
