@@ -399,11 +399,7 @@ __global__ __launch_bounds__(256) void selscan_quad_kernel(const SelK p) {
 #pragma unroll
                 for (int k = 0; k < SPL; ++k) y[j] = __builtin_fmaf(cv[i & 1][j][k], h[k], y[j]);
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                y[j] = quad_sum<4>(y[j]);
-                yv[i] = sub == j ? y[j] : yv[i];
-            }
+            yv[i] = quad_gather(y, sub);
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll

@@ -150,6 +150,15 @@ __device__ __forceinline__ float quad_sum(float v) {
     return v;
 }
 
+// Four values summed over each quad; lane J of the quad receives the sum of
+// v[J].  Each step keeps half of the values and hands over the other half.
+__device__ __forceinline__ float quad_gather(const float (&v)[4], int sub) {
+    const bool odd = (sub & 1) != 0, high = (sub & 2) != 0;
+    const float a = (odd ? v[1] : v[0]) + dpp<0xB1>(odd ? v[0] : v[1]);
+    const float b = (odd ? v[3] : v[2]) + dpp<0xB1>(odd ? v[2] : v[3]);
+    return (high ? b : a) + dpp<0x4E>(high ? a : b);
+}
+
 // Sequences of up to this many chunks need no launch to join them: a chunk
 // walks over those before it (or behind it, in the backward) by itself, at
 // about one row's work each.

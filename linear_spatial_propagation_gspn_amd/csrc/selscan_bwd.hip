@@ -371,6 +371,7 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
 #pragma unroll
             for (int s = 0; s < SPL; ++s) hs[0][s] = nh[s];
             if (tile > 0) load(tile - 1);
+            float sy[4], sb4[4], sa4[4];  // of four rows, until their sums over the quad
             auto forward = [&](auto jc, int i) {
                 constexpr int J = decltype(jc)::value;
                 const int t = i * SPLIT + J;
@@ -388,8 +389,8 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
                     widen(ld_pack<float, SPL>(&bc[buf][t][NP + n0]), cv);
 #pragma unroll
                     for (int s = 0; s < SPL; ++s) y = __builtin_fmaf(cv[s], hs[t + 1][s], y);
-                    y = quad_sum<SPLIT>(y);
-                    yv[i] = SPLIT == 1 || sub == J ? y : yv[i];
+                    if constexpr (SPLIT == 1) yv[i] = y;
+                    else sy[J] = y;
                 }
             };
 #pragma unroll
@@ -399,6 +400,7 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
                     forward(std::integral_constant<int, 1>{}, i);
                     forward(std::integral_constant<int, 2>{}, i);
                     forward(std::integral_constant<int, 3>{}, i);
+                    if constexpr (kGate) yv[i] = quad_gather(sy, sub);
                 }
             }
 
@@ -425,11 +427,12 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
                     sa = __builtin_fmaf(gq, A2[s], sa);
                     dA[s] = __builtin_fmaf(gq, d, dA[s]);
                 }
-                sb = quad_sum<SPLIT>(sb);
-                sa = quad_sum<SPLIT>(sa);
-                if (SPLIT == 1 || sub == J) {
+                if constexpr (SPLIT == 1) {
                     gb[i] = sb;
                     ga[i] = sa;
+                } else {
+                    sb4[J] = sb;
+                    sa4[J] = sa;
                 }
                 if (((kTile - 1 - t) * SPL + SPL) % 4 == 0) {
                     // row r of the wave holds value m(r): row t + 4 / SPL - 1 - m / SPL, state m % SPL
@@ -452,6 +455,10 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
                     back(std::integral_constant<int, 1>{}, i);
                 }
                 back(std::integral_constant<int, 0>{}, i);
+                if constexpr (SPLIT == 4) {
+                    gb[i] = quad_gather(sb4, sub);
+                    ga[i] = quad_gather(sa4, sub);
+                }
             }
 
 #pragma unroll
