@@ -548,7 +548,7 @@ hipError_t launch_join_bwd(const gspn_join_args& a, int dtype, hipStream_t strea
     r.o[0] = {a.dpost, 1, 1, 0};
     r.o[1] = {a.dscale, 1, 1, 0};
     r.o[2] = {a.dpre, 1, 1, 0};
-    return launch_reduce_parts(r, stream);
+    return launch_reduce_parts(r, OutsideK{}, stream);
 }
 
 }  // namespace gspn

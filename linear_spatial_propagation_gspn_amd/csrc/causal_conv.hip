@@ -264,14 +264,45 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvK p) {
         st_pack<float, V>(p.part + (static_cast<int64_t>(blockIdx.x) * (K + 1) + j) * p.c + c0, dw[j]);
 }
 
-// A column of partial sums per lane, 64 columns and 16 runs of parts a block:
-// each run adds its parts in order, then the runs are added in order.
-constexpr int kReduceRuns = 16;
+// Zeros in the rows outside the sequences, one wave a row.  Where the sequences
+// cover every row, as they mostly do, it costs next to nothing, against a pass
+// over all the gradients to clear them beforehand.
+__device__ __forceinline__ void zero_outside(const OutsideK& k, int64_t wave, int64_t waves, int lane) {
+    const int lo = seq_begin(k.seq, 0);
+    const int last = k.seq.nseq - 1;
+    const int hi = seq_end(k.seq, last, seq_begin(k.seq, last));
+    const int64_t outside = lo + static_cast<int64_t>(k.seq.rows > hi ? k.seq.rows - hi : 0);
+    for (int64_t i = wave; i < outside; i += waves) {
+        const int64_t row = i < lo ? i : hi + (i - lo);
+#pragma unroll
+        for (int j = 0; j < 5; ++j) {
+            if (!k.t[j].p) continue;
+            if (k.es == 4) {
+                float* const q = static_cast<float*>(k.t[j].p) + row * k.t[j].ld;
+                for (int64_t e = lane; e < k.t[j].c; e += 64) q[e] = 0.0f;
+            } else {
+                bf16_t* const q = static_cast<bf16_t*>(k.t[j].p) + row * k.t[j].ld;
+                for (int64_t e = lane; e < k.t[j].c; e += 64) q[e] = 0;
+            }
+        }
+    }
+}
 
-__global__ __launch_bounds__(64 * kReduceRuns) void reduce_parts_kernel(const ReduceK k) {
+// A column of partial sums per lane, 64 columns and 16 runs of parts a block:
+// each run adds its parts in order, then the runs are added in order.  The
+// blocks behind those clear the rows outside the sequences.
+constexpr int kReduceRuns = 16;
+constexpr int kOutsideBlocks = 64;
+
+__global__ __launch_bounds__(64 * kReduceRuns) void reduce_parts_kernel(const ReduceK k, const OutsideK o) {
     __shared__ float sums[kReduceRuns][64];
     const int lane = threadIdx.x & 63;
     const int run = threadIdx.x >> 6;
+    const int64_t mine = (k.cols + 63) / 64;
+    if (blockIdx.x >= mine) {
+        zero_outside(o, (blockIdx.x - mine) * kReduceRuns + run, kOutsideBlocks * kReduceRuns, lane);
+        return;
+    }
     const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + lane;
     const int64_t each = (k.parts + kReduceRuns - 1) / kReduceRuns;
     const int64_t p0 = run * each;
@@ -301,31 +332,6 @@ __global__ __launch_bounds__(64 * kReduceRuns) void reduce_parts_kernel(const Re
         if (plane >= 0 && plane < k.o[o].planes && k.o[o].out)
             k.o[o].out[ch * k.o[o].sc + plane * k.o[o].sp] = s;
         plane -= k.o[o].planes;
-    }
-}
-
-// One wave a row of the rows outside; where the sequences cover every row, as
-// they mostly do, a launch of a few microseconds against a pass over all the
-// gradients to clear them beforehand.
-__global__ __launch_bounds__(256) void zero_outside_kernel(const OutsideK k) {
-    const int lo = seq_begin(k.seq, 0);
-    const int last = k.seq.nseq - 1;
-    const int hi = seq_end(k.seq, last, seq_begin(k.seq, last));
-    const int64_t outside = lo + static_cast<int64_t>(k.seq.rows > hi ? k.seq.rows - hi : 0);
-    const int lane = threadIdx.x & 63;
-    for (int64_t i = blockIdx.x * 4 + (threadIdx.x >> 6); i < outside; i += gridDim.x * 4) {
-        const int64_t row = i < lo ? i : hi + (i - lo);
-#pragma unroll
-        for (int j = 0; j < 5; ++j) {
-            if (!k.t[j].p) continue;
-            if (k.es == 4) {
-                float* const q = static_cast<float*>(k.t[j].p) + row * k.t[j].ld;
-                for (int64_t e = lane; e < k.t[j].c; e += 64) q[e] = 0.0f;
-            } else {
-                bf16_t* const q = static_cast<bf16_t*>(k.t[j].p) + row * k.t[j].ld;
-                for (int64_t e = lane; e < k.t[j].c; e += 64) q[e] = 0;
-            }
-        }
     }
 }
 
@@ -433,15 +439,12 @@ hipError_t launch_conv_step(const gspn_conv_args& a, int dtype, hipStream_t stre
 }
 
 hipError_t launch_conv_bwd(const gspn_conv_args& a, int dtype, hipStream_t stream) {
-    hipError_t e = launch_conv(2, a, dtype, stream);
+    const hipError_t e = launch_conv(2, a, dtype, stream);
     if (e != hipSuccess) return e;
-    if (a.seq.cu) {
-        OutsideK o{};
-        o.seq = make_seq(a.seq);
-        o.es = dtype == kF32 ? 4 : 2;
-        o.t[0] = {a.dx, a.lddx, a.c};
-        if ((e = launch_zero_outside(o, stream)) != hipSuccess) return e;
-    }
+    OutsideK o{};
+    o.seq = make_seq(a.seq);
+    o.es = dtype == kF32 ? 4 : 2;
+    o.t[0] = {a.dx, a.lddx, a.c};
     ReduceK r{};
     r.part = static_cast<const float*>(a.workspace);
     r.parts = chunk_ids(a.seq.cu != nullptr, a.seq.rows, a.seq.nseq, conv_shift_for(a.seq.rows, a.c));
@@ -451,26 +454,18 @@ hipError_t launch_conv_bwd(const gspn_conv_args& a, int dtype, hipStream_t strea
     r.o[0] = {a.dweight, static_cast<int32_t>(a.width), a.width, 1};
     r.o[1] = {a.dbias, 1, 1, 0};
     r.o[2] = {nullptr, 0, 0, 0};
-    return launch_reduce_parts(r, stream);
+    return launch_reduce_parts(r, o, stream);
 }
 
-hipError_t launch_zero_outside(const OutsideK& k, hipStream_t stream) {
-    for (const auto& t : k.t) {
+hipError_t launch_reduce_parts(const ReduceK& k, const OutsideK& o, hipStream_t stream) {
+    const dim3 grid(static_cast<unsigned>((k.cols + 63) / 64 + (o.seq.cu ? kOutsideBlocks : 0)));
+    for (const auto& t : o.t) {
         (void)t;
-        GSPN_REPLAY_ROWS("zero_outside_kernel", "gradient", t.p, k.seq.rows, t.ld, t.c, k.es);
+        if (o.seq.cu) GSPN_REPLAY_ROWS("reduce_parts_kernel", "gradient", t.p, o.seq.rows, t.ld, t.c, o.es);
     }
-    GSPN_REPLAYED("zero_outside_kernel", 256, 0);
-    const int64_t blocks = (static_cast<int64_t>(k.seq.rows) + 3) / 4;
-    hipLaunchKernelGGL(zero_outside_kernel, dim3(static_cast<unsigned>(blocks < 1 ? 1 : blocks < 512 ? blocks : 512)),
-                       dim3(256), 0, stream, k);
-    return hipGetLastError();
-}
-
-hipError_t launch_reduce_parts(const ReduceK& k, hipStream_t stream) {
-    const dim3 grid(static_cast<unsigned>((k.cols + 63) / 64));
     GSPN_REPLAY_ROWS("reduce_parts_kernel", "partial sums", k.part, k.parts, k.ld, k.cols, 4);
     GSPN_REPLAYED("reduce_parts_kernel", 64 * kReduceRuns, 64 * kReduceRuns * 4);
-    hipLaunchKernelGGL(reduce_parts_kernel, grid, dim3(64 * kReduceRuns), 0, stream, k);
+    hipLaunchKernelGGL(reduce_parts_kernel, grid, dim3(64 * kReduceRuns), 0, stream, k, o);
     return hipGetLastError();
 }
 

@@ -635,17 +635,6 @@ hipError_t launch_selscan_bwd(const gspn_selscan_args& a, int dtype, hipStream_t
     else run_bwd_n<bf16_t>(k, grid, stream);
     if ((e = hipGetLastError()) != hipSuccess) return e;
 
-    if (ragged) {
-        OutsideK o{};
-        o.seq = k.seq;
-        o.es = es;
-        o.t[0] = {a.dx, a.lddx, a.channels};
-        o.t[1] = {a.ddt, a.ldddt, a.channels};
-        o.t[2] = {a.z ? a.dz : nullptr, a.lddz, a.channels};
-        o.t[3] = {a.dB, a.groups * a.n, a.groups * a.n};
-        o.t[4] = {a.dC, a.groups * a.n, a.groups * a.n};
-        if ((e = launch_zero_outside(o, stream)) != hipSuccess) return e;
-    }
     const int64_t values = a.seq.rows * 2 * a.groups * a.n;
     if (values > 0) {
         const int64_t most = int64_t{1} << 20;  // workgroups; beyond, each takes several runs of values
@@ -669,7 +658,15 @@ hipError_t launch_selscan_bwd(const gspn_selscan_args& a, int dtype, hipStream_t
     r.o[0] = {a.dA, static_cast<int32_t>(a.n), a.n, 1};
     r.o[1] = {a.dD, 1, 1, 0};
     r.o[2] = {a.ddt_bias, 1, 1, 0};
-    return launch_reduce_parts(r, stream);
+    OutsideK o{};
+    o.seq = k.seq;
+    o.es = es;
+    o.t[0] = {a.dx, a.lddx, a.channels};
+    o.t[1] = {a.ddt, a.ldddt, a.channels};
+    o.t[2] = {a.z ? a.dz : nullptr, a.lddz, a.channels};
+    o.t[3] = {a.dB, a.groups * a.n, a.groups * a.n};
+    o.t[4] = {a.dC, a.groups * a.n, a.groups * a.n};
+    return launch_reduce_parts(r, o, stream);
 }
 
 }  // namespace gspn

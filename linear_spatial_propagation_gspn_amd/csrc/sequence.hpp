@@ -217,10 +217,10 @@ struct ReduceK {
     int64_t parts, ld, c, cols;
     ReduceOut o[3];
 };
-hipError_t launch_reduce_parts(const ReduceK& k, hipStream_t stream);
 
 // Zeros in the rows before the first and behind the last packed sequence, of
-// up to five tensors (p null: none; es: bytes of an element).
+// up to five tensors (p null: none; es: bytes of an element).  It rides on the
+// reduction's launch; seq.cu null: nothing to do.
 struct OutsideK {
     SeqK seq;
     int32_t es;
@@ -229,7 +229,7 @@ struct OutsideK {
         int64_t ld, c;
     } t[5];
 };
-hipError_t launch_zero_outside(const OutsideK& k, hipStream_t stream);
+hipError_t launch_reduce_parts(const ReduceK& k, const OutsideK& o, hipStream_t stream);
 
 // Host side ---------------------------------------------------------------
 
