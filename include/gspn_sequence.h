@@ -17,7 +17,7 @@
  *  - Rows.  A tensor [rows][c] has unit column stride and a row stride `ld`
  *    in elements (c <= ld <= 2^26), so that the halves or slices of a projection's
  *    rows are taken as they are.  Alignment: the element size.  Row strides
- *    and offsets may pass 32 bits; rows < 2^31, c <= 2^19.
+ *    and offsets may pass 32 bits; rows <= 2^30, c <= 2^19.
  *  - Storage type: x, dt, z, B, C, h, gate and their gradients and outputs
  *    are GSPN_F32 or GSPN_BF16, one type per call.  Parameters (weights,
  *    biases, scales, A, D, dt_bias), their gradients and the scan's states
@@ -25,13 +25,13 @@
  *    rounded once, at its store.
  *  - Sequences.  `rows` rows hold nseq sequences, one after another.
  *    cu == NULL: equal lengths rows / nseq (nseq must divide rows).
- *    At most 2^23 sequences.
  *    Otherwise cu is a device array of nseq + 1 offsets, not decreasing,
  *    0 <= cu[i] <= rows: sequence i is rows [cu[i], cu[i+1]); it may be
  *    empty.  Rows outside every sequence are not read, and not written but
  *    by the backward calls, which give them zero gradients.
  *    Offsets that break these rules give unspecified results inside the
  *    caller's buffers (they are clamped to [0, rows]).
+ *    At most 2^23 sequences (rows + nseq <= 2^30), 2^16 with slots.
  *  - Slots.  A call that carries state works on a pool of nslots entries.
  *    slots == NULL: sequence i uses entry i (nslots >= nseq).  Otherwise
  *    slots is a device array of nseq indices.  A negative index is a padding
@@ -126,7 +126,8 @@ gspn_status gspn_causal_conv_bwd(const gspn_conv_args* args, int dtype, void* st
  *   d_t = softplus ? log(1 + exp(dt_t + dt_bias)) : dt_t + dt_bias
  *   h_t[n] = exp(d_t A[c][n]) h_{t-1}[n] + d_t x_t B_t[g][n]
  *   y_t = sum_n C_t[g][n] h_t[n] + D[c] x_t;   out_t = y_t silu(z_t)
- * from h = 0 or the resumed pool entry.  dt = -Inf skips a row (softplus).
+ * from h = 0 or the resumed pool entry.  dt = -Inf
+ * skips a row whose x and B are finite (softplus).
  *   x, dt, z, out  [rows][channels]; z NULL: no gate; D, dt_bias NULL: 0
  *   B, C           [rows][groups][n], row strides ldb, ldc (groups and n
  *                  contiguous); groups divides channels

@@ -352,7 +352,8 @@ __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_bwd_kernel(const Join
                 float h[V];
                 get(hp[i], p.h, p.ldh, i, h);
 #pragma unroll
-                for (int v = 0; v < V; ++v) go[i][v] = r1 * __builtin_fmaf(-h[v], k, go[i][v]);
+                for (int v = 0; v < V; ++v)  // without the norm h has no part in it, whatever it holds
+                    if (p.post) go[i][v] = r1 * __builtin_fmaf(-h[v], k, go[i][v]);
                 st_pack<T, V>(static_cast<T*>(p.dh) + row * p.lddh + col, go[i]);
             }
         }

@@ -72,22 +72,13 @@ __global__ __launch_bounds__(64) void selscan_kernel(const SelK p) {
         for (int i = 0; i < NP; ++i)
             if (i < N) h[i] = carry[i * plane + c];
     } else if (kOut) {
-        constexpr int U = 1;
-        for (int k = -ck.k; k < 0; k += U) {
-            float d[U], last[U][NP];
+        for (int k = -ck.k; k < 0; ++k) {
+            const float d = 0.5f * p.sums[(id + k) * plane + c];
 #pragma unroll
-            for (int j = 0; j < U; ++j) {
-                const bool in = k + j < 0;
-                d[j] = in ? p.sums[(id + k + j) * plane + c] : 0.0f;
-#pragma unroll
-                for (int i = 0; i < NP; ++i)
-                    last[j][i] = in && i < N ? carry[((k + j) * static_cast<int64_t>(N) + i) * plane + c] : 0.0f;
+            for (int i = 0; i < NP; ++i) {
+                const float last = i < N ? carry[(k * static_cast<int64_t>(N) + i) * plane + c] : 0.0f;
+                h[i] = carry_over(d * A2[i], h[i], last);
             }
-#pragma unroll
-            for (int j = 0; j < U; ++j)  // past the last: a decay of 1 and nothing added
-#pragma unroll
-                for (int i = 0; i < NP; ++i)
-                    h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(d[j] * A2[i]), h[i], last[j][i]);
         }
     }
     const float bias = p.bias ? p.bias[c] : 0.0f;
@@ -437,7 +428,7 @@ __global__ __launch_bounds__(256) void selscan_join_kernel(const SelK p) {
     float A2[V], h[V];
     widen(ld_pack<float, V>(q + (count - 1) * step), h);  // the state before the sequence
 #pragma unroll
-    for (int v = 0; v < V; ++v) A2[v] = p.A[static_cast<int64_t>(c + v) * p.n + i] * kLog2E;
+    for (int v = 0; v < V; ++v) A2[v] = p.A[static_cast<int64_t>(c + v) * p.n + i] * (0.5f * kLog2E);
     constexpr int U = V == 1 ? 16 : 8;
     for (int k0 = 0; k0 < count; k0 += U) {
         float last[U][V], d[U][V];
@@ -455,8 +446,7 @@ __global__ __launch_bounds__(256) void selscan_join_kernel(const SelK p) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     // the first chunk's last state includes the one it began with
-                    const float a = k0 + j > 0 ? __builtin_amdgcn_exp2f(d[j][v] * A2[v]) : 0.0f;
-                    h[v] = __builtin_fmaf(a, h[v], last[j][v]);
+                    h[v] = carry_over(d[j][v] * A2[v], k0 + j > 0 ? h[v] : 0.0f, last[j][v]);
                 }
             }
         }

@@ -96,6 +96,15 @@ __device__ __forceinline__ void ld_states(const float* p, int n, float (&v)[NP])
     }
 }
 
+// A state (or gradient) h taken over a chunk whose decay is 2^(2 half), plus
+// the chunk's own.  In two halves, capped where every h but zero overflows: a
+// decay past the range of fp32 (A > 0) leaves zero at zero and gives a small h
+// what the rows one by one give it.
+__device__ __forceinline__ float carry_over(float half, float h, float own) {
+    const float e = __builtin_amdgcn_exp2f(half < 127.0f ? half : 127.0f);
+    return __builtin_fmaf(h * e, e, own);
+}
+
 __device__ __forceinline__ float lane_value(float v, int lane) {
     return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
 }

@@ -164,7 +164,7 @@ __global__ __launch_bounds__(256) void selscan_bwd_join_kernel(const SelK p) {
     float A2[V], g[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        A2[v] = p.A[static_cast<int64_t>(c + v) * p.n + i] * kLog2E;
+        A2[v] = p.A[static_cast<int64_t>(c + v) * p.n + i] * (0.5f * kLog2E);
         g[v] = 0.0f;
     }
     constexpr int U = V == 1 ? 16 : 8;
@@ -182,8 +182,7 @@ __global__ __launch_bounds__(256) void selscan_bwd_join_kernel(const SelK p) {
             if (k0 - j >= 0) {
                 st_pack<float, V>(q + (k0 - j) * step, g);
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    g[v] = __builtin_fmaf(__builtin_amdgcn_exp2f(d[j][v] * A2[v]), g[v], own[j][v]);
+                for (int v = 0; v < V; ++v) g[v] = carry_over(d[j][v] * A2[v], g[v], own[j][v]);
             }
         }
     }
@@ -234,24 +233,20 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
             for (int s = 0; s < SPL; ++s)
                 ag[s] = n0 + s < p.n ? p.carry[(id * p.n + n0 + s) * p.channels + c] : 0.0f;
         } else {
-            constexpr int U = 4;
-            for (int k0 = ck.count - 1 - ck.k; k0 >= 1; k0 -= U) {
-                float d[U], own[U][SPL];
+            constexpr int U = kDirectChunks - 1;
+            float d[U], own[U][SPL];
 #pragma unroll
-                for (int j = 0; j < U; ++j) {
-                    const bool in = k0 - j >= 1;
-                    d[j] = in ? p.sums[(id + k0 - j) * p.channels + c] : 0.0f;
+            for (int j = 0; j < U; ++j) {
+                const bool in = ck.k + 1 + j < ck.count;
+                d[j] = in ? 0.5f * p.sums[(id + 1 + j) * p.channels + c] : 0.0f;
 #pragma unroll
-                    for (int s = 0; s < SPL; ++s)
-                        own[j][s] = in && n0 + s < p.n
-                                        ? p.carry[((id + k0 - j) * p.n + n0 + s) * p.channels + c] : 0.0f;
-                }
-#pragma unroll
-                for (int j = 0; j < U; ++j)  // past the last: a decay of 1 and nothing added
-#pragma unroll
-                    for (int s = 0; s < SPL; ++s)
-                        ag[s] = __builtin_fmaf(__builtin_amdgcn_exp2f(d[j] * A2[s]), ag[s], own[j][s]);
+                for (int s = 0; s < SPL; ++s)
+                    own[j][s] = in && n0 + s < p.n ? p.carry[((id + 1 + j) * p.n + n0 + s) * p.channels + c] : 0.0f;
             }
+#pragma unroll
+            for (int j = U - 1; j >= 0; --j)  // behind the last: nothing yet, and nothing added
+#pragma unroll
+                for (int s = 0; s < SPL; ++s) ag[s] = carry_over(d[j] * A2[s], ag[s], own[j][s]);
         }
         const float bias = p.bias ? p.bias[c] : 0.0f;
         const float skip = p.D ? p.D[c] : 0.0f;

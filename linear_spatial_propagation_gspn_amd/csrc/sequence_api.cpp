@@ -13,8 +13,9 @@
 
 namespace {
 
-constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1;
+constexpr int64_t kMaxRows = int64_t{1} << 30;  // row numbers and a tile behind them stay within 32 bits
 constexpr int64_t kMaxSeqs = int64_t{1} << 23;
+constexpr int64_t kMaxSlotSeqs = int64_t{1} << 16;  // each looks through the slots before it
 constexpr int64_t kMaxChannels = int64_t{1} << 19;
 constexpr int64_t kMaxStride = int64_t{1} << 26;
 
@@ -89,7 +90,7 @@ class Buffers {
 gspn_status check_seq(const gspn_sequences& s, bool pool, bool step, bool* empty, Buffers* b) {
     if (s.rows < 0 || s.rows > kMaxRows || s.nseq < 0 || s.nseq > kMaxRows || s.nslots < 0 || s.nslots > kMaxRows)
         return GSPN_ERR_BAD_SHAPE;
-    if (s.nseq > kMaxSeqs) return GSPN_ERR_UNSUPPORTED;
+    if (s.nseq > kMaxSeqs || (s.slots && s.nseq > kMaxSlotSeqs)) return GSPN_ERR_UNSUPPORTED;
     if (s.rows + s.nseq > kMaxRows) return GSPN_ERR_BAD_SHAPE;  // chunk ids
     *empty = s.nseq == 0;
     if (s.nseq == 0) return s.rows == 0 || s.cu ? GSPN_OK : GSPN_ERR_BAD_SHAPE;

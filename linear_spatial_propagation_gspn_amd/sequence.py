@@ -22,7 +22,9 @@ entry.
 Gradients have autograd forms (``causal_conv``, ``selective_scan``,
 ``block_join``) on top of the ``_fwd`` / ``_bwd`` calls.  Nothing here
 synchronises; outputs and workspaces are allocated by torch unless given, so
-every call can be captured in a HIP graph.
+every call can be captured in a HIP graph.  As for any autograd node, a backward
+is captured with no eager graph of the same leaves alive: torch would tie the
+capture to the stream on which that graph found them.
 """
 from __future__ import annotations
 
@@ -228,7 +230,7 @@ def _sequences(x, cu, nseq, state=None, slots=None, resume=None) -> Sequences:
     elif s.nslots < s.nseq:
         raise ValueError("state holds %d entries for %d sequences" % (s.nslots, s.nseq))
     if resume is not None:
-        if resume.dtype not in (torch.bool, torch.uint8):
+        if not isinstance(resume, torch.Tensor) or resume.dtype not in (torch.bool, torch.uint8):
             raise TypeError("resume must be a bool (or uint8) tensor")
         s.resume = _flat(resume, "resume", (s.nseq,), resume.dtype, dev)
     return s

@@ -423,6 +423,38 @@ def test_scan_nan_stays_in_its_channel_and_sequence():
     assert torch.isnan(out[5:30, 7]).all()
 
 
+@pytest.mark.parametrize("n", [16, 5, 1])
+def test_scan_growth_past_the_range_of_a_chunk(n):
+    """A > 0: 16 rows of step 6 multiply a state by up to e^96, past fp32.  States that are zero stay zero, and a
+    small one that the rows one by one keep in range is what they make it; the same against the row order."""
+    g = gen(37)
+    lengths = [209, 33]  # one joined by its own launch, one by its chunks
+    seqs = R.spans(lengths, 0)
+    k = scan_case(g, 242, 12, 1, n, F32, gate=False, skip=False, bias=False)
+    k["A"] = 1.0 - 0.2 * torch.rand(12, n, generator=g)
+    k["dt"] = torch.full((242, 12), 6.0)
+    gy = torch.zeros(242, 12)
+    x = torch.zeros(242, 12)
+    for begin, end in seqs:
+        k["dt"][begin:begin + 16] = 0.01
+        x[end - 18] = 1e-30 * k["x"][end - 18]  # the last row of the last whole chunk but one
+        gy[begin + 32] = 1e-30
+    k["x"] = x
+    args = ref_args(k)
+    ry, _, last, sy, ms = R.scan(*args, False, seqs)
+    ref, mag = R.scan_backward(*args, False, seqs, wide(gy))
+    assert all(float(t.abs().max()) < 1e30 for t in ref.values() if t is not None)
+    o = on_gpu(k)
+    state = torch.zeros(2, 12, n, device=DEV)
+    out = run_fwd(o, softplus=False, cu=cu_of(lengths), state=state)
+    count = R.scan_roundings(args[0], args[1], args[2], args[7], False, seqs)
+    check(out, ry, sy, count, "out")
+    check(state, torch.stack(last), torch.stack([ms[208], ms[241]]), count, "state")
+    got = run_bwd(o, dev(gy), softplus=False, cu=cu_of(lengths))
+    for name, more in {"dx": n, "ddt": n, "dB": 12, "dC": 12, "dA": 242}.items():
+        check(got[name], ref[name], mag[name], 2 * count + 16 + more, name)
+
+
 # ------------------------------------------------------------------------------------------------- block join
 
 JOIN_PARTS = ["grosp", "r", "rp", "os", "gp", "o", "", "rsp", "go"]
@@ -482,6 +514,15 @@ def test_join_strided_rows_and_one_sided_gradients(c):
     zero = S.gspn_block_join_bwd(dev(h), torch.zeros_like(a[0]), dev(gate), a[0], dev(gate), dev(res), pre=dev(pre))
     for x, y in zip(only, zero):
         assert (x is None and y is None) or torch.equal(x, y)
+
+
+@pytest.mark.parametrize("c", [96, 1032, 5000, 33])
+def test_join_without_a_norm_keeps_infinities_out_of_dh(c):
+    g = gen(43)
+    h, scale, gj = rnd(g, 3, c), rnd(g, c), rnd(g, 3, c)
+    h[0, 1], h[1, 0], h[2, c - 1] = math.inf, -math.inf, math.nan
+    dh = S.gspn_block_join_bwd(dev(h), dev(gj), None, None, residual=dev(gj), scale=dev(scale))[0]
+    assert torch.equal(dh.cpu(), gj * scale)
 
 
 def test_join_zero_rows_and_row_of_zeros():
@@ -585,6 +626,27 @@ def test_autograd_forms_give_the_backward_calls(packed):
     got = torch.autograd.grad(S.block_join(h, gate, res, pre=pre)[1].float().sum(), [res])[0]
     ref = S.gspn_block_join_bwd(h, None, torch.ones_like(gy), j.detach(), gate, res, pre=pre)[2]
     assert torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_autograd_forms_without_a_gradient(packed):
+    """No leaf, or no gradients wanted: the same values, and nothing kept for a backward."""
+    g = gen(51)
+    kw = {"cu": cu_of([9, 14], 1)} if packed else {"nseq": 2}
+    k = on_gpu(scan_case(g, 24, 40, 1, 16, BF16))
+    w, pre = dev(rnd(g, 40, 4)), dev(rnd(g, 40))
+    names = ("x", "dt", "A", "B", "C", "D", "z", "dt_bias")
+    calls = [(lambda x, w: S.causal_conv(x, w, **kw), (k["x"], w)),
+             (lambda *a: S.selective_scan(*a, **kw), [k[n] for n in names]),
+             (lambda h, p: S.block_join(h, pre=p)[0], (k["x"], pre)), (lambda h, p: S.block_join(h, pre=p)[1], (k["x"], pre))]
+    for f, ts in calls:
+        ref = f(*leaves(*ts))
+        assert ref.grad_fn is not None
+        plain = f(*ts)
+        with torch.no_grad():
+            off = f(*leaves(*ts))
+        for y in (plain, off):
+            assert y.grad_fn is None and torch.equal(y, ref)
 
 
 @pytest.mark.parametrize("op", ["conv", "scan", "join"])

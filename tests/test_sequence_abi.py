@@ -212,6 +212,7 @@ def test_conv_validation(lib):
         refuse(lib, "conv", kind, SHAPE, seq_rows=-1)
         refuse(lib, "conv", kind, SHAPE, seq_rows=(1 << 31) - 1)  # with the sequences past 2^31 chunk ids
         refuse(lib, "conv", kind, UNSUP, seq_rows=1 << 24, seq_nseq=(1 << 23) + 1)
+        refuse(lib, "conv", kind, SHAPE, seq_rows=(1 << 30) + 2)
         refuse(lib, "conv", kind, SHAPE, seq_nseq=3)          # does not divide 40 rows
         refuse(lib, "conv", kind, SHAPE, seq_nseq=0)          # rows without a sequence
         refuse(lib, "conv", kind, SHAPE, ldx=23)
@@ -222,6 +223,7 @@ def test_conv_validation(lib):
         refuse(lib, "conv", kind, MISAL, seq_cu=2)
         refuse(lib, "conv", kind, SHAPE, seq_resume=64)       # no pool to resume from
     refuse(lib, "conv", "fwd", NULLP, y=None)
+    refuse(lib, "conv", "step", UNSUP, seq_rows=(1 << 16) + 1, seq_nseq=(1 << 16) + 1, seq_slots=64, seq_nslots=1 << 17)
     refuse(lib, "conv", "fwd", ALIAS, y=lambda a: a.x + 8)
     refuse(lib, "conv", "fwd", ALIAS, y=lambda a: a.weight)
     # column slices of one matrix: a slice that reaches into the other, or past its row's end into the next
