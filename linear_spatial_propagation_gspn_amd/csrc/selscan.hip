@@ -408,16 +408,18 @@ __global__ __launch_bounds__(256) void selscan_quad_kernel(const SelK p) {
 }
 
 // The join over the chunks of a long sequence: carry[k] := the state before
-// chunk k.  A lane takes V channels of one state; the chunks' values are loaded
-// 32 / V at a time ahead of the serial products.
-template <int V>
+// chunk k.  A lane takes one state of one channel; 16 chunks' values are loaded
+// ahead of their serial products.  Bound by that latency and the carries'
+// bytes: 30 us for 65536 rows of 2048 channels (256 MB read and written).
+// Four channels a lane, in wider loads, left too few lanes: 852 against 877 us
+// for that scan.
 __global__ __launch_bounds__(256) void selscan_join_kernel(const SelK p) {
     const int s = blockIdx.x;
     const int begin = seq_begin(p.seq, s);
     const int end = seq_end(p.seq, s, begin);
     const int count = static_cast<int>(chunks_each(end - begin, p.shift));
     if (count <= kDirectChunks) return;
-    const int e = static_cast<int>(blockIdx.y * 256 + threadIdx.x) * V;  // n * channels + c
+    const int e = static_cast<int>(blockIdx.y * 256 + threadIdx.x);  // n * channels + c
     if (e >= p.channels * p.n) return;
     const int i = e / p.channels;
     const int c = e - i * p.channels;
@@ -425,29 +427,24 @@ __global__ __launch_bounds__(256) void selscan_join_kernel(const SelK p) {
     const int64_t step = static_cast<int64_t>(p.channels) * p.n;
     float* const q = p.carry + base * step + e;
     const float* const sd = p.sums + base * p.channels + c;
-    float A2[V], h[V];
-    widen(ld_pack<float, V>(q + (count - 1) * step), h);  // the state before the sequence
-#pragma unroll
-    for (int v = 0; v < V; ++v) A2[v] = p.A[static_cast<int64_t>(c + v) * p.n + i] * (0.5f * kLog2E);
-    constexpr int U = V == 1 ? 16 : 8;
+    const float A2 = p.A[static_cast<int64_t>(c) * p.n + i] * (0.5f * kLog2E);
+    float h = q[(count - 1) * step];  // the state before the sequence
+    constexpr int U = 16;
     for (int k0 = 0; k0 < count; k0 += U) {
-        float last[U][V], d[U][V];
+        float last[U], d[U];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             // from the last chunk on the values are of no use: what follows is not stored
             const int64_t k = k0 + j < count ? k0 + j : count - 1;
-            widen(ld_pack<float, V>(q + k * step), last[j]);
-            widen(ld_pack<float, V>(sd + k * p.channels), d[j]);
+            last[j] = q[k * step];
+            d[j] = sd[k * p.channels];
         }
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             if (k0 + j < count) {
-                st_pack<float, V>(q + (k0 + j) * step, h);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    // the first chunk's last state includes the one it began with
-                    h[v] = carry_over(d[j][v] * A2[v], k0 + j > 0 ? h[v] : 0.0f, last[j][v]);
-                }
+                q[(k0 + j) * step] = h;
+                // the first chunk's last state includes the one it began with
+                h = carry_over(d[j] * A2, k0 + j > 0 ? h : 0.0f, last[j]);
             }
         }
     }
@@ -584,17 +581,18 @@ void run_step(const SelK& k, bool vec, hipStream_t stream) {
 // channel take longest x (194 R + 90) where R counts their waves over the
 // SIMDs, one lane a channel longest x (600 R + 300), chunks 980 for each wave
 // and row spread over the SIMDs and some 48000 for three launches.  Measured
-// (16 states, bf16, four lanes against chunks): 57 rows of 1152 channels 10.1
-// against 17.1 us, 512 rows 63 against 23; 4 x 1024 rows of 4096 channels 126.5
-// and 126.7, 8 x 1024 of 2304 178 against 142, 16 x 1024 of 4096 332 against
-// 426.  Packed sequences are taken as one, the longest they can hold.
+// (16 states, bf16, four lanes against chunks): 57 rows of 1152 channels 11.1
+// against 18.0 us, 512 rows 63.5 against 24.1; 4 x 1024 rows of 4096 channels
+// 122 and 125, 8 x 1024 of 2304 176 against 141, 16 x 1024 of 4096 324 against
+// 431.  Packed sequences are taken as one, the longest they can hold.
 //
-// Chunks, of 16 rows at least, are as long as eight waves a SIMD allow (four
-// for up to 4 states, whose rows are short work against the join): one
-// sequence of 65536 rows and 2048 channels with 16 states took 1027 us at 4
-// waves, 923 at 8, 902 at 16, 16 ragged prompts of 4096 channels 344, 300 and
-// 301, four of 3136 rows with one state (768 channels, fp32) 52 at 4 against 59
-// at 8.
+// Chunks are as long as 16 waves a SIMD allow, but below 32 rows (to 16) only
+// as eight ask for (four for up to 4 states, whose rows are short work against
+// the join).  At 4, 8, 16 and 32 waves: one sequence of 65536 rows and 2048
+// channels with 16 states 948, 849, 830 and 876 us, 16 ragged prompts in 8192
+// rows of 4096 285, 261, 240 and 278; 8 x 1024 rows of 2304 139 at 32-row chunks,
+// 142 at 16; four of 3136 rows with one state (768 channels, fp32) 54 at 4
+// against 61 at 8.
 int selscan_shift(int64_t rows, int64_t nseq, int64_t channels, int64_t groups, int64_t n, bool ragged) {
     const int64_t waves = groups * ((channels / groups + 63) / 64);
     const int64_t longest = ragged || nseq < 1 ? rows : rows / nseq;
@@ -607,7 +605,7 @@ int selscan_shift(int64_t rows, int64_t nseq, int64_t channels, int64_t groups, 
     while ((int64_t{1} << whole) < longest) ++whole;
     if (lanes1 <= chunks) return whole;
     int shift = whole;
-    while (shift > kMinChunkShift && (rows >> shift) * waves < (n > 4 ? 8192 : 4096)) --shift;
+    while (shift > kMinChunkShift && (rows >> shift) * waves < (n <= 4 ? 4096 : shift > 5 ? 16384 : 8192)) --shift;
     return shift;
 }
 
@@ -643,12 +641,10 @@ hipError_t launch_selscan_fwd(const gspn_selscan_args& a, int dtype, hipStream_t
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         if (needs_join(a, k.shift)) {
-            const int v = join_lane(a);
             const dim3 jg(static_cast<unsigned>(a.seq.nseq),
-                          static_cast<unsigned>((a.channels * a.n + 256 * v - 1) / (256 * v)));
+                          static_cast<unsigned>((a.channels * a.n + 255) / 256));
             GSPN_REPLAYED("selscan_join_kernel", 256, 0);
-            if (v == 4) hipLaunchKernelGGL(selscan_join_kernel<4>, jg, dim3(256), 0, stream, k);
-            else hipLaunchKernelGGL(selscan_join_kernel<1>, jg, dim3(256), 0, stream, k);
+            hipLaunchKernelGGL(selscan_join_kernel, jg, dim3(256), 0, stream, k);
             e = hipGetLastError();
             if (e != hipSuccess) return e;
         }

@@ -170,22 +170,13 @@ __device__ __forceinline__ float quad_gather(const float (&v)[4], int sub) {
 
 // Sequences of up to this many chunks need no launch to join them: a chunk
 // walks over those before it (or behind it, in the backward) by itself, at
-// about one row's work each.
-// (Longer walks cost more than the launch: 16 prompts in 8192 rows of 4096
-// channels took 343 us at 16 chunks against 320.)
+// about one row's work each.  Longer walks cost more than the launch: 16
+// prompts in 2048 rows of 4096 channels took 84 us, and 92 at 16 chunks; their
+// backward 219 and 242.
 constexpr int kDirectChunks = 4;
 
 inline bool needs_join(const gspn_selscan_args& a, int shift) {
     return (a.seq.cu ? (a.seq.rows >> shift) + 1 : chunks_each(a.seq.rows / a.seq.nseq, shift)) > kDirectChunks;
-}
-
-// Channels a lane of the joins takes: four where that still leaves a wave a
-// SIMD (16 prompts of 4096 channels: 26 us against 33 at one),
-// else one, whose longer loads ahead suit few lanes.
-inline int join_lane(const gspn_selscan_args& a) {
-    return a.channels % 4 == 0 && aligned_rows(a.workspace, a.channels, 4, 16) &&
-                   a.seq.nseq * a.channels * a.n >= 4 * 65536
-               ? 4 : 1;
 }
 
 inline SelK selscan_params(const gspn_selscan_args& a) {

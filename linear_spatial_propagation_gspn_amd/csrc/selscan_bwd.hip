@@ -146,14 +146,13 @@ __global__ __launch_bounds__(64) void selscan_bwd_local_kernel(const SelK p) {
 
 // The join of long sequences, against the row order: carry[k] := dL/dh after
 // chunk k's last row.
-template <int V>
 __global__ __launch_bounds__(256) void selscan_bwd_join_kernel(const SelK p) {
     const int s = blockIdx.x;
     const int begin = seq_begin(p.seq, s);
     const int end = seq_end(p.seq, s, begin);
     const int count = static_cast<int>(chunks_each(end - begin, p.shift));
     if (count <= kDirectChunks) return;
-    const int e = static_cast<int>(blockIdx.y * 256 + threadIdx.x) * V;  // n * channels + c
+    const int e = static_cast<int>(blockIdx.y * 256 + threadIdx.x);  // n * channels + c
     if (e >= p.channels * p.n) return;
     const int i = e / p.channels;
     const int c = e - i * p.channels;
@@ -161,28 +160,23 @@ __global__ __launch_bounds__(256) void selscan_bwd_join_kernel(const SelK p) {
     const int64_t step = static_cast<int64_t>(p.channels) * p.n;
     float* const q = p.carry + base * step + e;
     const float* const sd = p.sums + base * p.channels + c;
-    float A2[V], g[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        A2[v] = p.A[static_cast<int64_t>(c + v) * p.n + i] * (0.5f * kLog2E);
-        g[v] = 0.0f;
-    }
-    constexpr int U = V == 1 ? 16 : 8;
+    const float A2 = p.A[static_cast<int64_t>(c) * p.n + i] * (0.5f * kLog2E);
+    float g = 0.0f;
+    constexpr int U = 16;
     for (int k0 = count - 1; k0 >= 0; k0 -= U) {
-        float own[U][V], d[U][V];
+        float own[U], d[U];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             // from the first chunk on the values are of no use: what follows is not stored
             const int64_t k = k0 - j > 0 ? k0 - j : 0;
-            widen(ld_pack<float, V>(q + k * step), own[j]);
-            widen(ld_pack<float, V>(sd + k * p.channels), d[j]);
+            own[j] = q[k * step];
+            d[j] = sd[k * p.channels];
         }
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             if (k0 - j >= 0) {
-                st_pack<float, V>(q + (k0 - j) * step, g);
-#pragma unroll
-                for (int v = 0; v < V; ++v) g[v] = carry_over(d[j][v] * A2[v], g[v], own[j][v]);
+                q[(k0 - j) * step] = g;
+                g = carry_over(d[j] * A2, g, own[j]);
             }
         }
     }
@@ -562,17 +556,30 @@ int64_t selscan_bwd_blocks(int64_t channels, int64_t groups, int64_t n) {
 }
 
 // Rows per chunk of the backward.  A cut costs the pass that finds the chunks'
-// own gradients, a quarter of the main pass; equal sequences stay whole where
-// they give two waves a SIMD, otherwise the chunks are as long as 16 waves a
-// SIMD allow (four for up to 4 states): eight sequences of 1024 rows, 2304
-// channels, 16 states took 1778 us whole, 1319 at 4 waves, 439 at 8, 412 at 16.
+// own gradients, a quarter of the main pass; whole sequences leave SIMDs idle
+// where their waves are no multiple of the two a SIMD holds.  By their measured
+// times: whole sequences take 485 ns a row for every 2048 waves and 325 for a
+// last turn of one wave a SIMD, chunks 0.29 ns for each wave and row.  Measured
+// (bf16, 16 states, whole against cut): 8 x 1024 rows of 2304 channels 483 and
+// 369 us, 16 x 1024 of 2048 497 and 625, 16 x 1024 of 2304 743 and 687, 32 x
+// 1024 of 2304 1175 and 1318, 2 x 2048 of 4096 665 and 339.  For up to 4 states,
+// whose waves stand closer, whole from two waves a SIMD (n = 4, 16 x 1024 of
+// 2304: 347 and 494; 8 x 1024: 263 and 242).  Packed sequences are always cut.
+//
+// Chunks are as long as 16 waves a SIMD allow (four for up to 4 states): 8 x
+// 1024 rows of 2304 channels took 448 us at 4 waves, 374 at 8, 369 at 16; four
+// of 3136 rows with one state (768 channels, fp32) 95 at 4, 103 at 8.
 int selscan_bwd_shift(int64_t rows, int64_t nseq, int64_t channels, int64_t groups, int64_t n, bool ragged) {
     const int64_t waves = 4 * groups * selscan_bwd_blocks(channels, groups, n);
     int64_t longest = rows;
     if (!ragged && nseq > 0) longest = rows / nseq;
     int whole = kMinChunkShift;
     while ((int64_t{1} << whole) < longest) ++whole;
-    if (!ragged && nseq * waves >= 2048) return whole;
+    if (!ragged) {
+        const int64_t all = nseq * waves, rest = all % 2048;
+        const int64_t turns = all / 2048 * 485 + (rest == 0 ? 0 : rest <= 1024 ? 325 : 485);
+        if (n > 4 ? longest * turns <= rows * waves * 29 / 100 + 15000 : all >= 2048) return whole;
+    }
     int shift = whole;
     while (shift > kMinChunkShift && (rows >> shift) * waves < (n > 4 ? 16384 : 4096)) --shift;
     return shift;
@@ -603,12 +610,10 @@ hipError_t launch_selscan_bwd(const gspn_selscan_args& a, int dtype, hipStream_t
         else run_local_n<bf16_t>(k, lg, stream);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         if (needs_join(a, k.shift)) {
-            const int v = join_lane(a) == 4 && aligned_rows(k.carry, a.channels, 4, 16) ? 4 : 1;
             const dim3 jg(static_cast<unsigned>(a.seq.nseq),
-                          static_cast<unsigned>((a.channels * a.n + 256 * v - 1) / (256 * v)));
+                          static_cast<unsigned>((a.channels * a.n + 255) / 256));
             GSPN_REPLAYED("selscan_bwd_join_kernel", 256, 0);
-            if (v == 4) hipLaunchKernelGGL(selscan_bwd_join_kernel<4>, jg, dim3(256), 0, stream, k);
-            else hipLaunchKernelGGL(selscan_bwd_join_kernel<1>, jg, dim3(256), 0, stream, k);
+            hipLaunchKernelGGL(selscan_bwd_join_kernel, jg, dim3(256), 0, stream, k);
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
     }
