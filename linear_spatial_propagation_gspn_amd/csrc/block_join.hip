@@ -3,11 +3,13 @@
 // the next block reads.
 //
 // Row by row; every tensor is read once and written once, so the kernels are
-// bound by those bytes.  A row lives in the registers of the lanes that share
+// bound by those bytes: 16384 rows of 2304 channels (bf16, gate, fp32 residual,
+// all parts) take 106 us forward and 163 + 6 backward, 5.0 and 4.9 TB/s against
+// the 5.2 of a large copy.  A row lives in the registers of the lanes that share
 // it, eight channels each: a wave for up to 512 channels, a workgroup of as
-// many waves as the row fills above.  The backward keeps the columns' sums for the parameters' gradients
-// in registers over all the rows a workgroup walks and leaves one partial row
-// each, joined in a fixed order.
+// many waves as the row fills above.  The backward keeps the columns' sums for
+// the parameters' gradients in registers over all the rows a workgroup walks and
+// leaves one partial row each, joined in a fixed order.
 #include "sequence.hpp"
 
 #include <type_traits>

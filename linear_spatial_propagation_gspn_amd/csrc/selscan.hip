@@ -14,13 +14,18 @@
 // sum of d), a join over the chunks (the decay of a whole chunk is
 // exp(A sum d)), then every chunk again from its true first state.  Where a
 // sequence is one chunk, only the last pass runs.
+//
+// Measured (bf16, 16 states, gated): one sequence of 65536 rows and 2048
+// channels 376 + 67 + 517 us by its kernels, 840 in a row of calls.  The states'
+// 5 and 4 instructions alone are 24 + 20 cycles a wave (an exponential counts
+// 8), 600 us at 2.4 GHz; the rest is what is per row (step size, gate, loads)
+// and the join; x, dt, z, out twice over would be 260 us of memory traffic.
 #include "selscan.hpp"
 
 #include <type_traits>
 
 namespace gspn {
 namespace {
-
 
 // One wave: one chunk of one sequence, 64 channels of one group.
 // kOut false: the chunk from zero; its last state and sum of d to carry/sums.
@@ -228,9 +233,10 @@ __global__ __launch_bounds__(64) void selscan_kernel(const SelK p) {
 // the four computes a quarter of the rows' step sizes and gates and hands them
 // to the others as DPP operands.  B and C are staged through LDS, 16 rows at a
 // time, and the next 16 rows' loads are in flight meanwhile.
-// About 175 cycles a row and wave of 16 channels (16 states), against 530 for
-// 64 channels and again 400 for the chunk sums above: it takes batches that
-// fill the GPU with whole sequences, and short ones, where it is one launch.
+// A wave of 16 channels (16 states) takes 284 cycles a row alone on its SIMD and
+// 194 among others: it takes batches that fill the GPU with whole sequences,
+// and short ones, where it is one launch (57 rows of 1152 channels, fp32: 11.6
+// us, a latency of 200 ns a row).
 template <typename T, int NP, bool kGate>
 __global__ __launch_bounds__(256) void selscan_quad_kernel(const SelK p) {
     constexpr int SPL = NP / 4;
@@ -409,8 +415,10 @@ __global__ __launch_bounds__(256) void selscan_quad_kernel(const SelK p) {
 
 // The join over the chunks of a long sequence: carry[k] := the state before
 // chunk k.  A lane takes one state of one channel; 16 chunks' values are loaded
-// ahead of their serial products.  Bound by that latency and the carries'
-// bytes: 30 us for 65536 rows of 2048 channels (256 MB read and written).
+// ahead of their serial products.  Bound by the latency of those loads where the
+// sequences are few (65536 rows of 2048 channels: 32 turns in 67 us), by the
+// carries' bytes where they are many.  At 8 ahead that scan took 854 us in all,
+// at 16 840, at 32 835; 16 ragged prompts of 4096 channels 261, 263 and 275.
 // Four channels a lane, in wider loads, left too few lanes: 852 against 877 us
 // for that scan.
 __global__ __launch_bounds__(256) void selscan_join_kernel(const SelK p) {
@@ -452,7 +460,9 @@ __global__ __launch_bounds__(256) void selscan_join_kernel(const SelK p) {
 
 // One token per sequence.  SPLIT lanes share a channel, each with NP / SPLIT
 // neighbouring states, so that the pool is read and written in whole cache
-// lines; y is summed over the SPLIT lanes.  Bound by the pool's bytes.
+// lines; y is summed over the SPLIT lanes.  Bound by the pool's bytes: 64
+// sequences of 4096 channels with 16 states 9.9 us, 3.6 TB/s of 36 MB, most of
+// it the latency of one load, one exponential and one store.
 template <typename T, int NP, int SPLIT, bool kVec>
 __global__ __launch_bounds__(256) void selscan_step_kernel(const SelK p) {
     constexpr int SPL = NP / SPLIT;

@@ -18,7 +18,10 @@
 // fixed order.  The sums over rows (dA, dD, ddt_bias) stay in registers per
 // chunk and are joined the same way.
 //
-// Bound by the vector ALU: about 20 instructions an element and state.
+// Bound by the vector ALU (79% of the cycles issue one of its instructions, at
+// two waves a SIMD): 8 x 1024 rows of 2304 channels, 16 states, bf16, gated, take
+// 304 us here, 78 + 10 for the chunks' own gradients and their join, 16 for the
+// sums; the bytes alone would be 58.
 #include "selscan.hpp"
 
 #include <type_traits>
@@ -486,7 +489,8 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
 }
 
 // dB and dC from the channel blocks' sums [block][row][2][groups * n], in the
-// blocks' order; rows outside the sequences have no sums and stay as they are.
+// blocks' order; rows outside the sequences have no sums and are not written here.
+// Bound by the sums' bytes: 38 MB in 8.6 us for 8192 rows of 2304 channels.
 template <typename T>
 __global__ __launch_bounds__(256) void selscan_bc_kernel(const SelK p, T* __restrict__ dB, T* __restrict__ dC) {
     const int64_t gn = static_cast<int64_t>(p.groups) * p.n;
