@@ -106,16 +106,17 @@ def _bytes(name: str, *args) -> int:
     return _calls[name](*args)
 
 
-# The current stream's handle without building a Stream object, where torch offers it.
+# The current stream's handle without building a Stream object, and the current device, where torch offers them.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(name: str, args: ctypes.Structure, dtype: int, index: int) -> None:
     if not _calls:
         lib()
     # the launches go to the tensors' device whatever the current one is
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         st = _calls[name](ctypes.byref(args), dtype, _raw_stream(index))
     else:
         with torch.cuda.device(index):
@@ -186,6 +187,15 @@ def _flat(t, name: str, shape: tuple, dtype, index: int):
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     return t.data_ptr()
+
+
+def _new_like(x, dtype=None) -> torch.Tensor:
+    """New contiguous rows of x's shape."""
+    return torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
+
+
+def _zeros_like(x) -> torch.Tensor:
+    return torch.zeros_like(x, memory_format=torch.contiguous_format)
 
 
 def _need_rows(x, name: str) -> int:
@@ -266,7 +276,7 @@ def _conv_out(a: ConvArgs, x, state, out):
     if state is not None:
         a.state = _flat(state, "state", (state.shape[0], a.width - 1, a.c), x.dtype, x.get_device())
     if out is None:
-        out = x.new_empty(x.shape)
+        out = _new_like(x)
         a.y, a.ldy = out.data_ptr(), max(a.c, 1)
     else:
         a.y, a.ldy = _ptr_rows(out, "out", x.shape, x.dtype, x.get_device())
@@ -316,11 +326,11 @@ def gspn_causal_conv_bwd(x, weight, bias, gy, silu: bool = True, cu=None, nseq=N
     a = _conv_args(x, weight, bias, silu, _sequences(x, cu, nseq))
     a.gy, a.ldgy = _ptr_rows(gy, "gy", x.shape, x.dtype, x.get_device())
     if a.seq.nseq == 0:
-        return torch.zeros_like(x, memory_format=torch.contiguous_format), torch.zeros_like(weight), None if bias is None else torch.zeros_like(bias)
-    dx = x.new_empty(x.shape)
+        return _zeros_like(x), _zeros_like(weight), None if bias is None else _zeros_like(bias)
+    dx = _new_like(x)
     a.dx, a.lddx = dx.data_ptr(), max(a.c, 1)
-    dweight = torch.empty_like(weight)
-    dbias = None if bias is None else torch.empty_like(bias)
+    dweight = _new_like(weight)
+    dbias = None if bias is None else _new_like(bias)
     a.dweight, a.dbias = dweight.data_ptr(), None if dbias is None else dbias.data_ptr()
     ws = _workspace(a, workspace, _bytes("gspn_causal_conv_bwd_workspace_bytes", a.seq.rows, a.seq.nseq, a.c, a.width),
                     x)
@@ -379,7 +389,7 @@ def gspn_selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, softpl
     if state is not None:
         a.state = _flat(state, "state", (state.shape[0], a.channels, a.n), torch.float32, dev)
     if out is None:
-        out = x.new_empty(x.shape)
+        out = _new_like(x)
         a.out, a.ldo = out.data_ptr(), max(a.channels, 1)
     else:
         a.out, a.ldo = _ptr_rows(out, "out", x.shape, x.dtype, dev)
@@ -410,7 +420,7 @@ def gspn_selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None
     dev = x.get_device()
     a.state = _flat(state, "state", (state.shape[0], a.channels, a.n), torch.float32, dev)
     if out is None:
-        out = x.new_empty(x.shape)
+        out = _new_like(x)
         a.out, a.ldo = out.data_ptr(), max(a.channels, 1)
     else:
         a.out, a.ldo = _ptr_rows(out, "out", x.shape, x.dtype, dev)
@@ -431,11 +441,9 @@ def gspn_selective_scan_bwd(x, dt, A, B, C, gy, D=None, z=None, dt_bias=None, so
     a = _scan_args(x, dt, A, B, C, D, z, dt_bias, softplus, _sequences(x, cu, nseq))
     a.gy, a.ldgy = _ptr_rows(gy, "gy", x.shape, x.dtype, dev)
     none = a.seq.nseq == 0
-    new = x.new_zeros if none else x.new_empty
-    dx, ddt, dz = new(x.shape), new(x.shape), None if z is None else new(x.shape)
-    dB, dC = new(B.shape), new(B.shape)
-    like = torch.zeros_like if none else torch.empty_like
-    dA, dD, dbias = like(A), None if D is None else like(D), None if dt_bias is None else like(dt_bias)
+    like = _zeros_like if none else _new_like
+    dx, ddt, dB, dC, dA = (like(t) for t in (x, x, B, B, A))
+    dD, dz, dbias = (None if t is None else like(t) for t in (D, z, dt_bias))
     grads = (dx, ddt, dA, dB, dC, dD, dz, dbias)
     if none:
         return grads
@@ -489,7 +497,7 @@ def gspn_block_join_fwd(h, gate=None, residual=None, post=None, scale=None, pre=
     a = _join_args(h, gate, residual, post, scale, pre, eps, wide)
     dev = h.get_device()
     if out is None:
-        out = h.new_empty(h.shape, dtype=wide)
+        out = _new_like(h, wide)
         a.joined, a.ldjoined = out.data_ptr(), max(a.c, 1)
     else:
         a.joined, a.ldjoined = _ptr_rows(out, "out", h.shape, wide, dev)
@@ -498,7 +506,7 @@ def gspn_block_join_fwd(h, gate=None, residual=None, post=None, scale=None, pre=
             raise ValueError("normed needs pre, the weight of the norm")
     else:
         if normed is None:
-            normed = h.new_empty(h.shape)
+            normed = _new_like(h)
             a.normed, a.ldnormed = normed.data_ptr(), max(a.c, 1)
         else:
             a.normed, a.ldnormed = _ptr_rows(normed, "normed", h.shape, h.dtype, dev)
@@ -525,16 +533,16 @@ def gspn_block_join_bwd(h, gjoined, gnormed, joined, gate=None, residual=None, p
         a.joined, a.ldjoined = _ptr_rows(joined, "joined", h.shape, wide, dev)
     elif gnormed is not None:
         raise ValueError("gnormed needs pre, the weight of the norm")
-    dh = h.new_empty(h.shape)
+    dh = _new_like(h)
     a.dh, a.lddh = dh.data_ptr(), c
     dgate = dres = None
     if gate is not None:
-        dgate = h.new_empty(h.shape)
+        dgate = _new_like(h)
         a.dgate, a.lddgate = dgate.data_ptr(), c
     if residual is not None:
-        dres = h.new_empty(h.shape, dtype=wide)
+        dres = _new_like(h, wide)
         a.dresidual, a.lddres = dres.data_ptr(), c
-    dpost, dscale, dpre = (None if t is None else torch.empty_like(t) for t in (post, scale, pre))
+    dpost, dscale, dpre = (None if t is None else _new_like(t) for t in (post, scale, pre))
     a.dpost, a.dscale, a.dpre = (None if t is None else t.data_ptr() for t in (dpost, dscale, dpre))
     ws = None
     if post is not None or scale is not None or pre is not None:
@@ -636,7 +644,7 @@ class _BlockJoin(torch.autograd.Function):
         if gjoined is not None:
             gjoined = _grad_rows(gjoined, wide)
         if pre is not None:
-            gnormed = torch.zeros_like(h, memory_format=torch.contiguous_format) if gnormed is None \
+            gnormed = _zeros_like(h) if gnormed is None \
                 else _grad_rows(gnormed, h.dtype)
         dh, dgate, dres, dpost, dscale, dpre = gspn_block_join_bwd(h, gjoined, gnormed, joined, gate, residual, post,
                                                                    scale, pre, ctx.eps)
