@@ -39,6 +39,56 @@ struct JoinK {
     int64_t ldh, ldg, ldr, ldj, ldn, ldgj, ldgn, lddh, lddg, lddr;
 };
 
+// V columns of a row from `col` < c on.  kAny: the row starts at any element
+// (the memory takes 16 bytes at any address) and may end within them (c >= V):
+// its last lane loads the row's last V columns instead, and shifts them once
+// they are used, zeros behind the end.  16384 bf16 rows of 2305 channels, fp32
+// residual, took 133 us forward and 214 backward (2312: 106 and 163), 262 and
+// 243 column by column; with a last lane that loads its columns one by one,
+// where the whole wave then waits, 146 and 301.
+template <bool kAny, int V, typename T>
+__device__ __forceinline__ Pack<T, V> ld_cols(const T* p, int col, int c) {
+    if constexpr (!kAny) return ld_pack<T, V>(p + col);
+    Pack<T, V> r;
+    __builtin_memcpy(&r, p + (col + V <= c ? col : c - V), sizeof r);
+    return r;
+}
+
+// Those columns, widened.
+template <bool kAny, int V, typename T>
+__device__ __forceinline__ void widen_cols(const Pack<T, V>& r, int col, int c, float (&f)[V]) {
+    widen(r, f);
+    if constexpr (kAny && V > 1) {
+        const int s = col + V - c;
+        if (s > 0) {
+#pragma unroll
+            for (int k = 1; k < V; k *= 2) {
+                if (s & k) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) f[v] = v + k < V ? f[v + k] : 0.0f;
+                }
+            }
+        }
+    }
+}
+
+template <bool kAny, int V, typename T>
+__device__ __forceinline__ void st_cols(T* p, int col, int c, const float (&f)[V]) {
+    if constexpr (!kAny) {
+        st_pack<T, V>(p + col, f);
+    } else {
+        Pack<T, V> r;
+        st_pack<T, V>(&r.e[0], f);
+        if (col + V <= c) {
+            __builtin_memcpy(p + col, &r, sizeof r);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (col + v < c) p[col + v] = r.e[v];
+        }
+    }
+}
+
 // How a row lies on the lanes.  kWave: one wave a row, four rows a block;
 // otherwise the whole block, as many waves as the row fills, up to MAXT lanes.
 template <bool kWave, int MAXT>
@@ -78,7 +128,7 @@ __device__ __forceinline__ float rnorm(float ss, float c, float eps) {
     return __builtin_amdgcn_rsqf(__builtin_fmaf(ss, 1.0f / c, eps));
 }
 
-template <typename T, typename RT, int V, int NV, bool kWave, int MAXT>
+template <typename T, typename RT, int V, int NV, bool kWave, int MAXT, bool kAny>
 __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_fwd_kernel(const JoinK p) {
     typedef Row<kWave, MAXT> L;
     __shared__ float lds[2][MAXT / 64][3];
@@ -90,19 +140,23 @@ __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_fwd_kernel(const Join
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * L::per_block() + L::of_block(); row < p.rows;
          row += static_cast<int64_t>(gridDim.x) * L::per_block()) {
         float e[NV][V], o[NV][V];
-        Pack<T, V> g[NV];
+        Pack<T, V> h[NV], g[NV];
         Pack<RT, V> r[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int col = (i * TPR + lane) * V;
+            h[i] = Pack<T, V>{};
+            if (col < p.c) {
+                h[i] = ld_cols<kAny, V>(static_cast<const T*>(p.h) + row * p.ldh, col, p.c);
+                if (p.gate) g[i] = ld_cols<kAny, V>(static_cast<const T*>(p.gate) + row * p.ldg, col, p.c);
+                if (p.res) r[i] = ld_cols<kAny, V>(static_cast<const RT*>(p.res) + row * p.ldr, col, p.c);
+            }
+        }
         float ss[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int col = (i * TPR + lane) * V;
-#pragma unroll
-            for (int v = 0; v < V; ++v) e[i][v] = 0.0f;
-            if (col < p.c) {
-                widen(ld_pack<T, V>(static_cast<const T*>(p.h) + row * p.ldh + col), e[i]);
-                if (p.gate) g[i] = ld_pack<T, V>(static_cast<const T*>(p.gate) + row * p.ldg + col);
-                if (p.res) r[i] = ld_pack<RT, V>(static_cast<const RT*>(p.res) + row * p.ldr + col);
-            }
+            widen_cols<kAny>(h[i], col, p.c, e[i]);
 #pragma unroll
             for (int v = 0; v < V; ++v) ss[0] = __builtin_fmaf(e[i][v], e[i][v], ss[0]);
         }
@@ -118,26 +172,26 @@ __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_fwd_kernel(const Join
             if (col < p.c) {
                 float w[V];
                 if (p.post) {
-                    widen(ld_pack<float, V>(p.post + col), w);
+                    widen_cols<kAny>(ld_cols<kAny, V>(p.post, col, p.c), col, p.c, w);
 #pragma unroll
                     for (int v = 0; v < V; ++v) e[i][v] *= r1 * w[v];
                 }
                 if (p.gate) {
-                    widen(g[i], w);
+                    widen_cols<kAny>(g[i], col, p.c, w);
 #pragma unroll
                     for (int v = 0; v < V; ++v) e[i][v] *= w[v] * gate_sigmoid<float>(w[v]);
                 }
                 if (p.scale) {
-                    widen(ld_pack<float, V>(p.scale + col), w);
+                    widen_cols<kAny>(ld_cols<kAny, V>(p.scale, col, p.c), col, p.c, w);
 #pragma unroll
                     for (int v = 0; v < V; ++v) e[i][v] *= w[v];
                 }
                 if (p.res) {
-                    widen(r[i], w);
+                    widen_cols<kAny>(r[i], col, p.c, w);
 #pragma unroll
                     for (int v = 0; v < V; ++v) e[i][v] += w[v];
                 }
-                st_pack<RT, V>(static_cast<RT*>(p.joined) + row * p.ldj + col, e[i]);
+                st_cols<kAny, V>(static_cast<RT*>(p.joined) + row * p.ldj, col, p.c, e[i]);
             }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -155,10 +209,10 @@ __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_fwd_kernel(const Join
             const int col = (i * TPR + lane) * V;
             if (col < p.c) {
                 float w[V];
-                widen(ld_pack<float, V>(p.pre + col), w);
+                widen_cols<kAny>(ld_cols<kAny, V>(p.pre, col, p.c), col, p.c, w);
 #pragma unroll
                 for (int v = 0; v < V; ++v) w[v] *= o[i][v] * r2;
-                st_pack<T, V>(static_cast<T*>(p.normed) + row * p.ldn + col, w);
+                st_cols<kAny, V>(static_cast<T*>(p.normed) + row * p.ldn, col, p.c, w);
             }
         }
     }
@@ -171,7 +225,7 @@ __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_fwd_kernel(const Join
 // row leave no other work between).  Otherwise each phase reads the row again,
 // from the caches: held, 16 channels a lane spilled and took three times the
 // time that the memory needs.
-template <typename T, typename RT, int V, int NV, bool kWave, int MAXT, bool kAhead>
+template <typename T, typename RT, int V, int NV, bool kWave, int MAXT, bool kAhead, bool kAny>
 __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_bwd_kernel(const JoinK p) {
     typedef Row<kWave, MAXT> L;
     __shared__ float lds[2][MAXT / 64][3];
@@ -196,7 +250,7 @@ __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_bwd_kernel(const Join
         const int col = (i * TPR + lane) * V;
 #pragma unroll
         for (int v = 0; v < V; ++v) w[v] = 1.0f;
-        if (q && col < p.c) widen(ld_pack<float, V>(q + col), w);
+        if (q && col < p.c) widen_cols<kAny>(ld_cols<kAny, V>(q, col, p.c), col, p.c, w);
     };
     if (kHold) {
 #pragma unroll
@@ -213,12 +267,12 @@ __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_bwd_kernel(const Join
         for (int i = 0; i < NV; ++i) {
             const int col = (i * TPR + lane) * V;
             if (col < p.c) {
-                hq[i] = ld_pack<T, V>(static_cast<const T*>(p.h) + row * p.ldh + col);
-                if (p.gate) gq[i] = ld_pack<T, V>(static_cast<const T*>(p.gate) + row * p.ldg + col);
-                if (p.gjoined) jq[i] = ld_pack<RT, V>(static_cast<const RT*>(p.gjoined) + row * p.ldgj + col);
+                hq[i] = ld_cols<kAny, V>(static_cast<const T*>(p.h) + row * p.ldh, col, p.c);
+                if (p.gate) gq[i] = ld_cols<kAny, V>(static_cast<const T*>(p.gate) + row * p.ldg, col, p.c);
+                if (p.gjoined) jq[i] = ld_cols<kAny, V>(static_cast<const RT*>(p.gjoined) + row * p.ldgj, col, p.c);
                 if (p.pre) {
-                    oq[i] = ld_pack<RT, V>(static_cast<const RT*>(p.joined) + row * p.ldj + col);
-                    nq[i] = ld_pack<T, V>(static_cast<const T*>(p.gnormed) + row * p.ldgn + col);
+                    oq[i] = ld_cols<kAny, V>(static_cast<const RT*>(p.joined) + row * p.ldj, col, p.c);
+                    nq[i] = ld_cols<kAny, V>(static_cast<const T*>(p.gnormed) + row * p.ldgn, col, p.c);
                 }
             }
         }
@@ -238,8 +292,9 @@ __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_bwd_kernel(const Join
         }
         auto get = [&](const auto& held, const void* q, int64_t ld, int i, float (&f)[V]) {
             typedef std::remove_const_t<std::remove_reference_t<decltype(held.e[0])>> E;
-            if constexpr (kAhead) widen(held, f);
-            else widen(ld_pack<E, V>(static_cast<const E*>(q) + row * ld + (i * TPR + lane) * V), f);
+            const int col = (i * TPR + lane) * V;
+            if constexpr (kAhead) widen_cols<kAny>(held, col, p.c, f);
+            else widen_cols<kAny>(ld_cols<kAny, V>(static_cast<const E*>(q) + row * ld, col, p.c), col, p.c, f);
         };
         float go[NV][V];
         float sum[3] = {0.0f, 0.0f, 0.0f};  // of h^2, o^2 and gw o
@@ -295,7 +350,7 @@ __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_bwd_kernel(const Join
         for (int i = 0; i < NV; ++i) {
             const int col = (i * TPR + lane) * V;
             if (col < p.c) {
-                if (p.dres) st_pack<RT, V>(static_cast<RT*>(p.dres) + row * p.lddr + col, go[i]);
+                if (p.dres) st_cols<kAny, V>(static_cast<RT*>(p.dres) + row * p.lddr, col, p.c, go[i]);
                 float h[V], q[V], a[V], gv[V], dg[V];
                 get(hp[i], p.h, p.ldh, i, h);
                 if (!kHold) {
@@ -328,7 +383,7 @@ __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_bwd_kernel(const Join
                 if (p.gate && p.dgate) {
 #pragma unroll
                     for (int v = 0; v < V; ++v) dg[v] *= go[i][v] * q[v];
-                    st_pack<T, V>(static_cast<T*>(p.dgate) + row * p.lddg + col, dg);
+                    st_cols<kAny, V>(static_cast<T*>(p.dgate) + row * p.lddg, col, p.c, dg);
                 }
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
@@ -356,7 +411,7 @@ __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_bwd_kernel(const Join
 #pragma unroll
                 for (int v = 0; v < V; ++v)  // without the norm h has no part in it, whatever it holds
                     if (p.post) go[i][v] = r1 * __builtin_fmaf(-h[v], k, go[i][v]);
-                st_pack<T, V>(static_cast<T*>(p.dh) + row * p.lddh + col, go[i]);
+                st_cols<kAny, V>(static_cast<T*>(p.dh) + row * p.lddh, col, p.c, go[i]);
             }
         }
     }
@@ -388,9 +443,9 @@ __global__ __launch_bounds__(kWave ? 256 : MAXT) void join_bwd_kernel(const Join
         for (int i = 0; i < NV; ++i) {
             const int col = (i * TPR + lane) * V;
             if (col < p.c) {
-                st_pack<float, V>(part + col, sp[i]);
-                st_pack<float, V>(part + p.c + col, sc[i]);
-                st_pack<float, V>(part + 2 * static_cast<int64_t>(p.c) + col, sn[i]);
+                st_cols<kAny, V>(part, col, p.c, sp[i]);
+                st_cols<kAny, V>(part + p.c, col, p.c, sc[i]);
+                st_cols<kAny, V>(part + 2 * static_cast<int64_t>(p.c), col, p.c, sn[i]);
             }
         }
     }
@@ -431,41 +486,43 @@ JoinK join_params(const gspn_join_args& a) {
 int lanes_for(int64_t c, int v) { return static_cast<int>((c + 64 * v - 1) / (64 * v) * 64); }
 
 // NV values of V channels a lane: as many lanes as the row fills, or all.
-template <typename T, typename RT, int V, int NV, bool kWave, int MAXT>
+template <typename T, typename RT, int V, int NV, bool kWave, int MAXT, bool kAny>
 void run_join_fwd(const JoinK& k, int64_t workers, hipStream_t stream) {
     const dim3 grid(static_cast<unsigned>(kWave ? (workers + 3) / 4 : workers));
-    const dim3 block(kWave ? 256 : NV > 1 ? MAXT : lanes_for(k.c, V));
-    hipLaunchKernelGGL((join_fwd_kernel<T, RT, V, NV, kWave, MAXT>), grid, block, 0, stream, k);
+    const dim3 block(kWave ? 256 : lanes_for(k.c, V * NV));
+    hipLaunchKernelGGL((join_fwd_kernel<T, RT, V, NV, kWave, MAXT, kAny>), grid, block, 0, stream, k);
 }
 
-template <typename T, typename RT, int V, int NV, bool kWave, int MAXT, bool kAhead>
+template <typename T, typename RT, int V, int NV, bool kWave, int MAXT, bool kAhead, bool kAny>
 void run_join_bwd(const JoinK& k, int64_t workers, hipStream_t stream) {
     const dim3 grid(static_cast<unsigned>(kWave ? (workers + 3) / 4 : workers));
-    const dim3 block(kWave ? 256 : NV > 1 ? MAXT : lanes_for(k.c, V));
-    hipLaunchKernelGGL((join_bwd_kernel<T, RT, V, NV, kWave, MAXT, kAhead>), grid, block, 0, stream, k);
+    const dim3 block(kWave ? 256 : lanes_for(k.c, V * NV));
+    hipLaunchKernelGGL((join_bwd_kernel<T, RT, V, NV, kWave, MAXT, kAhead, kAny>), grid, block, 0, stream, k);
+}
+
+template <typename T, typename RT, bool kAny>
+void run_join_c(bool bwd, const JoinK& k, int64_t workers, hipStream_t stream) {
+    if (kAny && k.c < 8) {  // no whole vector to load a row's end from
+        if (!bwd) run_join_fwd<T, RT, 1, 1, true, 64, kAny>(k, workers, stream);
+        else run_join_bwd<T, RT, 1, 1, true, 64, true, kAny>(k, workers, stream);
+    } else if (!bwd) {
+        if (k.c <= kWaveRow) run_join_fwd<T, RT, 8, 1, true, 64, kAny>(k, workers, stream);
+        // four columns at a time where they lie anywhere: 11107 fp32 rows of 1418 took 60 us against 71 at eight
+        else if (k.c <= 4096) run_join_fwd<T, RT, kAny ? 4 : 8, kAny ? 2 : 1, false, 512, kAny>(k, workers, stream);
+        else if (k.c <= 8192) run_join_fwd<T, RT, 8, 1, false, 1024, kAny>(k, workers, stream);
+        else run_join_fwd<T, RT, 8, 2, false, 1024, kAny>(k, workers, stream);
+    } else {
+        if (k.c <= kWaveRow) run_join_bwd<T, RT, 4, 2, true, 64, true, kAny>(k, workers, stream);
+        else if (k.c <= 4096) run_join_bwd<T, RT, 4, 1, false, 1024, true, kAny>(k, workers, stream);
+        else if (k.c <= 8192) run_join_bwd<T, RT, 8, 1, false, 1024, false, kAny>(k, workers, stream);
+        else run_join_bwd<T, RT, 8, 2, false, 1024, false, kAny>(k, workers, stream);
+    }
 }
 
 template <typename T, typename RT>
-void run_join_c(bool bwd, bool vec, const JoinK& k, int64_t workers, hipStream_t stream) {
-    if (!bwd && vec) {
-        if (k.c <= kWaveRow) run_join_fwd<T, RT, 8, 1, true, 64>(k, workers, stream);
-        else if (k.c <= 4096) run_join_fwd<T, RT, 8, 1, false, 512>(k, workers, stream);
-        else if (k.c <= 8192) run_join_fwd<T, RT, 8, 1, false, 1024>(k, workers, stream);
-        else run_join_fwd<T, RT, 8, 2, false, 1024>(k, workers, stream);
-    } else if (!bwd) {
-        if (k.c <= kWaveRow) run_join_fwd<T, RT, 1, 8, true, 64>(k, workers, stream);
-        else if (k.c <= 4096) run_join_fwd<T, RT, 1, 8, false, 512>(k, workers, stream);
-        else run_join_fwd<T, RT, 1, 16, false, 1024>(k, workers, stream);
-    } else if (vec) {
-        if (k.c <= kWaveRow) run_join_bwd<T, RT, 4, 2, true, 64, true>(k, workers, stream);
-        else if (k.c <= 4096) run_join_bwd<T, RT, 4, 1, false, 1024, true>(k, workers, stream);
-        else if (k.c <= 8192) run_join_bwd<T, RT, 8, 1, false, 1024, false>(k, workers, stream);
-        else run_join_bwd<T, RT, 8, 2, false, 1024, false>(k, workers, stream);
-    } else {
-        if (k.c <= kWaveRow) run_join_bwd<T, RT, 1, 8, true, 64, false>(k, workers, stream);
-        else if (k.c <= 4096) run_join_bwd<T, RT, 1, 8, false, 512, true>(k, workers, stream);
-        else run_join_bwd<T, RT, 1, 16, false, 1024, false>(k, workers, stream);
-    }
+void run_join(bool bwd, bool vec, const JoinK& k, int64_t workers, hipStream_t stream) {
+    if (vec) run_join_c<T, RT, false>(bwd, k, workers, stream);
+    else run_join_c<T, RT, true>(bwd, k, workers, stream);
 }
 
 hipError_t launch_join(bool bwd, const gspn_join_args& a, const JoinK& k, int64_t workers, int dtype,
@@ -504,9 +561,9 @@ hipError_t launch_join(bool bwd, const gspn_join_args& a, const JoinK& k, int64_
         GSPN_REPLAY_ROWS(kn, "parameter", w, 1, a.c, a.c, 4);
     }
     GSPN_REPLAYED(kn, a.c > kWaveRow ? 1024 : 256, a.c > kWaveRow ? 2 * 16 * 3 * 4 : 4 * 3 * kWaveRow * 4 + 24);
-    if (dtype == kF32) run_join_c<float, float>(bwd, vec, k, workers, stream);
-    else if (a.residual_dtype == kF32) run_join_c<bf16_t, float>(bwd, vec, k, workers, stream);
-    else run_join_c<bf16_t, bf16_t>(bwd, vec, k, workers, stream);
+    if (dtype == kF32) run_join<float, float>(bwd, vec, k, workers, stream);
+    else if (a.residual_dtype == kF32) run_join<bf16_t, float>(bwd, vec, k, workers, stream);
+    else run_join<bf16_t, bf16_t>(bwd, vec, k, workers, stream);
     return hipGetLastError();
 }
 

@@ -498,6 +498,35 @@ def test_join_forward_and_backward(dtype, rt, c, rows, parts):
         check(got[name], ref[name], mag[name], back + (rows if name in ("dpost", "dscale", "dpre") else 0), name)
 
 
+@pytest.mark.parametrize("parts", ["grosp", "rp"])
+@pytest.mark.parametrize("dtype,rt", [(F32, F32), (BF16, F32), (BF16, BF16)])
+@pytest.mark.parametrize("c", [2, 7, 8, 9, 12, 17, 67, 511, 515, 1023, 4093, 8190, 8199])
+def test_join_rows_of_any_width(c, dtype, rt, parts):
+    """Widths around the lanes' eight and four columns, the wave's 512 and the workgroups' 4096 and 8192."""
+    test_join_forward_and_backward(dtype, rt, c, 3, parts)
+
+
+@pytest.mark.parametrize("c", [5, 9, 64, 130, 515, 5003, 8201])
+def test_join_writes_its_rows_alone(c):
+    """Outputs as columns of wider rows whose other columns hold 7: they still do, and the values are the plain call's
+    (within the roundings of another order, as in the strided test)."""
+    g = gen(44)
+    h, gate, res = (rnd(g, 4, c, dtype=BF16) for _ in range(3))
+    w = [rnd(g, c, by=0.3) + 1 for _ in range(3)]
+    out, normed = strided(torch.zeros_like(h)), strided(torch.zeros_like(h))
+    for v in (out, normed):
+        v.fill_(0)
+    a = S.gspn_block_join_fwd(dev(h), dev(gate), dev(res), *map(dev, w))
+    S.gspn_block_join_fwd(dev(h), dev(gate), dev(res), *map(dev, w), out=out, normed=normed)
+    steps = torch.finfo(BF16).eps + c * R.U
+    for v, ref in ((out, a[0]), (normed, a[1])):
+        whole = v._base if v._base is not None else v
+        assert (whole[:, :c + 3] == 7.0).all()
+        # joined: the gated term's rounding and the sum's, of terms not larger than |ref| + |res|; normed: that times
+        # pre / rms, which is below 2 for rows of such sums
+        assert (v.float() - ref.float()).abs().le((ref.float().abs() + dev(res).float().abs()) * 2 * steps).all()
+
+
 @pytest.mark.parametrize("c", [96, 2050])
 def test_join_strided_rows_and_one_sided_gradients(c):
     g = gen(41)
