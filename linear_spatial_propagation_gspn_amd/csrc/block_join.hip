@@ -569,15 +569,18 @@ hipError_t launch_join(bool bwd, const gspn_join_args& a, const JoinK& k, int64_
 
 }  // namespace
 
-// Workers (rows in flight) of the backward: what is resident at once (some 20
-// waves a CU, of 256 channels), fewer where that leaves each under four rows;
-// their partial rows stay a small part of the traffic.  A multiple of the rows
-// a workgroup takes.
+// Workers (rows in flight) of the backward: a row each up to a workgroup a CU,
+// then up to four rows each, up to what is resident at once (some 20 waves a CU,
+// of 256 channels); their partial rows stay a small part of the traffic.  64 rows
+// of 8192 channels take 18 us at a row each and 31 at four, 1024 rows of 2304
+// 22 and 19.5.  A multiple of the rows a workgroup takes.
 int64_t join_bwd_workers(int64_t rows, int64_t c) {
     const int64_t waves = c <= kWaveRow ? 1 : (c + 255) / 256;
     int64_t a_cu = 20 / waves;
     if (a_cu < 1) a_cu = 1;
+    const int64_t first = c <= kWaveRow ? 1024 : 256;
     int64_t w = (rows + 3) / 4;
+    if (w < first) w = rows < first ? rows : first;
     if (w > 256 * a_cu) w = 256 * a_cu;
     if (w < 1) w = 1;
     return c <= kWaveRow ? (w + 3) / 4 * 4 : w;
