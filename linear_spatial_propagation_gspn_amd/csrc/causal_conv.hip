@@ -337,12 +337,15 @@ __global__ __launch_bounds__(64 * kReduceRuns) void reduce_parts_kernel(const Re
     }
 }
 
-// Rows per chunk: the longest of 64, 32, 16, 8 that still gives four waves a
-// SIMD (of 128 channels).  A longer run re-reads fewer halo rows: 8192 rows of
-// 2304 channels backward took 28.2 us at 32 and at 16 rows, 33.8 at 8.
+// Rows per chunk: the longest of 64, 32, 16 that still gives four waves a SIMD
+// (of 128 channels), 8 where 16 give less than two.  A longer run re-reads fewer
+// halo rows and leaves fewer partial sums: backward, with the reduction, 8192
+// rows of 2304 channels took 33 us at 32 and at 16 rows, 928 fp32 rows of 5343
+// (2.4 waves a SIMD at 16) 23 at 16 and 29 at 8, 512 rows of 2304 11.6 at 8, 11.8
+// at 16 and 15.4 at 32.
 int conv_shift_for(int64_t rows, int64_t c) {
     int shift = 6;
-    while (shift > 3 && ((rows >> shift) + 1) * ((c + 127) / 128) < 4096) --shift;
+    while (shift > 3 && ((rows >> shift) + 1) * ((c + 127) / 128) < (shift > 4 ? 4096 : 2048)) --shift;
     return shift;
 }
 
