@@ -596,13 +596,15 @@ void run_step(const SelK& k, bool vec, hipStream_t stream) {
 // 122 and 125, 8 x 1024 of 2304 176 against 141, 16 x 1024 of 4096 324 against
 // 431.  Packed sequences are taken as one, the longest they can hold.
 //
-// Chunks are as long as 16 waves a SIMD allow, but below 32 rows (to 16) only
-// as eight ask for (four for up to 4 states, whose rows are short work against
-// the join).  At 4, 8, 16 and 32 waves: one sequence of 65536 rows and 2048
-// channels with 16 states 948, 849, 830 and 876 us, 16 ragged prompts in 8192
-// rows of 4096 285, 261, 240 and 278; 8 x 1024 rows of 2304 139 at 32-row chunks,
-// 142 at 16; four of 3136 rows with one state (768 channels, fp32) 54 at 4
-// against 61 at 8.
+// Chunks of L rows, 16 at least, are as long as their cost is least: the passes'
+// uneven end, which grows with L (some 2 (220 + 50 n) L cycles), against the
+// join's walk, 312 cycles a chunk of the longest sequence (packed ones are taken
+// to hold up to twice the mean), and the carries' bytes.  Measured at 16, 32, 64,
+// 128 and 256 rows (us): 8 x 1024 rows of 2304 channels 142, 139 (and 79, 75, 84
+// with 4 states), 16 ragged prompts in 8192 rows of 4096 278 at 16, 240 at 32,
+// 261 at 64; 32 x 1024 of 2304 493 at 32, 466, 499 at 128; one of 65536 and 2048
+// channels 876 at 64, 830, 849 at 256; four of 3136 rows with one state (768
+// channels, fp32) 61, 53, 57.
 int selscan_shift(int64_t rows, int64_t nseq, int64_t channels, int64_t groups, int64_t n, bool ragged) {
     const int64_t waves = groups * ((channels / groups + 63) / 64);
     const int64_t longest = ragged || nseq < 1 ? rows : rows / nseq;
@@ -614,9 +616,18 @@ int selscan_shift(int64_t rows, int64_t nseq, int64_t channels, int64_t groups, 
     int whole = kMinChunkShift;
     while ((int64_t{1} << whole) < longest) ++whole;
     if (lanes1 <= chunks) return whole;
-    int shift = whole;
-    while (shift > kMinChunkShift && (rows >> shift) * waves < (n <= 4 ? 4096 : shift > 5 ? 16384 : 8192)) --shift;
-    return shift;
+    const int64_t walk = ragged && longest > 2 * rows / nseq ? 2 * rows / nseq : longest;
+    const int64_t per_chunk = 312 * walk + rows * waves * n * 36 / 100;
+    int best = kMinChunkShift;
+    int64_t least = 0;
+    for (int shift = kMinChunkShift; shift <= whole; ++shift) {
+        const int64_t cost = ((440 + 100 * n) << shift) + (per_chunk >> shift);
+        if (shift == kMinChunkShift || cost < least) {
+            least = cost;
+            best = shift;
+        }
+    }
+    return best;
 }
 
 hipError_t launch_selscan_fwd(const gspn_selscan_args& a, int dtype, hipStream_t stream) {

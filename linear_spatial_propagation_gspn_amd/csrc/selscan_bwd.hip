@@ -566,13 +566,15 @@ int64_t selscan_bwd_blocks(int64_t channels, int64_t groups, int64_t n) {
 // last turn of one wave a SIMD, chunks 0.29 ns for each wave and row.  Measured
 // (bf16, 16 states, whole against cut): 8 x 1024 rows of 2304 channels 483 and
 // 369 us, 16 x 1024 of 2048 497 and 625, 16 x 1024 of 2304 743 and 687, 32 x
-// 1024 of 2304 1175 and 1318, 2 x 2048 of 4096 665 and 339.  For up to 4 states,
-// whose waves stand closer, whole from two waves a SIMD (n = 4, 16 x 1024 of
-// 2304: 347 and 494; 8 x 1024: 263 and 242).  Packed sequences are always cut.
+// 1024 of 2304 1175 and 1318, 2 x 2048 of 4096 665 and 339; with 4 states, whose
+// times are in the same proportion, 263 and 181, 275 and 295, 346 and 330.  With
+// one state, whose waves take 64 channels, whole from two waves a SIMD.  Packed
+// sequences are always cut.
 //
-// Chunks are as long as 16 waves a SIMD allow (four for up to 4 states): 8 x
-// 1024 rows of 2304 channels took 448 us at 4 waves, 374 at 8, 369 at 16; four
-// of 3136 rows with one state (768 channels, fp32) 95 at 4, 103 at 8.
+// Chunks are as long as 16 waves a SIMD allow (four with one state): 8 x 1024
+// rows of 2304 channels took 448 us at 4 waves, 374 at 8, 369 at 16 (with 4
+// states 243, 197, 181); four of 3136 rows with one state (768 channels, fp32)
+// 94 at 4, 103 at 8.
 int selscan_bwd_shift(int64_t rows, int64_t nseq, int64_t channels, int64_t groups, int64_t n, bool ragged) {
     const int64_t waves = 4 * groups * selscan_bwd_blocks(channels, groups, n);
     int64_t longest = rows;
@@ -582,10 +584,10 @@ int selscan_bwd_shift(int64_t rows, int64_t nseq, int64_t channels, int64_t grou
     if (!ragged) {
         const int64_t all = nseq * waves, rest = all % 2048;
         const int64_t turns = all / 2048 * 485 + (rest == 0 ? 0 : rest <= 1024 ? 325 : 485);
-        if (n > 4 ? longest * turns <= rows * waves * 29 / 100 + 15000 : all >= 2048) return whole;
+        if (n > 1 ? longest * turns <= rows * waves * 29 / 100 + 15000 : all >= 2048) return whole;
     }
     int shift = whole;
-    while (shift > kMinChunkShift && (rows >> shift) * waves < (n > 4 ? 16384 : 4096)) --shift;
+    while (shift > kMinChunkShift && (rows >> shift) * waves < (n > 1 ? 16384 : 4096)) --shift;
     return shift;
 }
 
