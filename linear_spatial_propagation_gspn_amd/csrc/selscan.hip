@@ -102,12 +102,13 @@ __global__ __launch_bounds__(64) void selscan_kernel(const SelK p) {
     T* outr = kOut ? static_cast<T*>(p.out) + first * p.ldo : nullptr;
     const int lane = threadIdx.x;
     const bool mine = lane < 2 * NP && (lane & (NP - 1)) < N;
-    const unsigned bcol = static_cast<unsigned>(lane & (NP - 1));
+    // lanes without a value read the last one: a load that only some lanes make
+    // is waited for at once (16 x 1024 rows of 2304 channels with one state: 196 us)
+    const unsigned bcol = static_cast<unsigned>((lane & (NP - 1)) < N ? lane & (NP - 1) : N - 1);
 
     constexpr int kSelRows = NP == 1 ? 8 : 4;  // rows whose loads are in flight together
     float sum = 0.0f;
-    T nx[kSelRows], nd[kSelRows], nz[kSelRows];
-    float nb[kSelRows];
+    T nx[kSelRows], nd[kSelRows], nz[kSelRows], nb[kSelRows];
     int loaded = ck.r0;  // the row that the pointers are on
     auto load = [&]() {
 #pragma unroll
@@ -115,7 +116,7 @@ __global__ __launch_bounds__(64) void selscan_kernel(const SelK p) {
             nx[i] = xr[col];
             nd[i] = dr[col];
             if (gated) nz[i] = zr[col];
-            if constexpr (!kScalar) nb[i] = mine ? Store<T>::ld((lane < NP ? Br : Cr) + bcol) : 0.0f;
+            if constexpr (!kScalar) nb[i] = (lane < NP ? Br : Cr)[bcol];
             if (++loaded < ck.r1) {
                 xr += p.ldx;
                 dr += p.lddt;
@@ -152,7 +153,7 @@ __global__ __launch_bounds__(64) void selscan_kernel(const SelK p) {
             xv[i] = Store<T>::ld(&nx[i]);
             d[i] = Store<T>::ld(&nd[i]) + bias;
             f[i] = 1.0f;
-            if constexpr (!kScalar) bv[i] = nb[i];
+            if constexpr (!kScalar) bv[i] = mine ? Store<T>::ld(&nb[i]) : 0.0f;
         }
         if (p.softplus) {
 #pragma unroll

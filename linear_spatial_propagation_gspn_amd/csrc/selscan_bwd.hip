@@ -75,8 +75,8 @@ __global__ __launch_bounds__(64) void selscan_bwd_local_kernel(const SelK p) {
     const int lane = threadIdx.x;
     float sum = 0.0f;
     constexpr int U = NP == 1 ? 8 : 4;
-    T nd[U], ng[U], nz[U];
-    float nc[U];
+    T nd[U], ng[U], nz[U], nc[U];
+    const int bcol = lane < N ? lane : N - 1;
     int loaded = ck.r1 - 1;  // the row that the pointers are on
     auto load = [&]() {      // the next U rows against the row order; past the chunk, its first row again
 #pragma unroll
@@ -84,7 +84,7 @@ __global__ __launch_bounds__(64) void selscan_bwd_local_kernel(const SelK p) {
             nd[i] = dr[col];
             ng[i] = gr[col];
             if (zr) nz[i] = zr[col];
-            if constexpr (!kScalar) nc[i] = lane < N ? Store<T>::ld(Cr + lane) : 0.0f;
+            if constexpr (!kScalar) nc[i] = Cr[bcol];
             if (loaded-- > ck.r0) {
                 dr -= p.lddt;
                 gr -= p.ldgy;
@@ -103,7 +103,7 @@ __global__ __launch_bounds__(64) void selscan_bwd_local_kernel(const SelK p) {
         for (int i = 0; i < U; ++i) {
             d[i] = Store<T>::ld(&nd[i]) + bias;
             gp[i] = Store<T>::ld(&ng[i]);
-            if constexpr (!kScalar) cv[i] = nc[i];
+            if constexpr (!kScalar) cv[i] = lane < N ? Store<T>::ld(&nc[i]) : 0.0f;
         }
         if (p.softplus) {
 #pragma unroll
