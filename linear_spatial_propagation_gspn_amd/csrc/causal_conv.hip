@@ -88,45 +88,50 @@ __global__ __launch_bounds__(kConvThreads) void conv_fwd_kernel(const ConvK p) {
     T* __restrict__ y = static_cast<T*>(p.y) + c0;
     T* const pool = static_cast<T*>(p.state) + (slot >= 0 ? static_cast<int64_t>(slot) * (K - 1) * p.c + c0 : 0);
 
-    float hist[K - 1][V];
+    // Nothing loaded is converted before everything that a run starts with is
+    // under way: each conversion between the loads would wait for one of them.
+    Pack<T, V> before[K - 1], raw[kConvRows];
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
         const int t = ck.r0 - (K - 1) + j;
-#pragma unroll
-        for (int v = 0; v < V; ++v) hist[j][v] = 0.0f;
+        before[j] = Pack<T, V>{};
         if (t >= ck.begin) {
-            widen(ld_pack<T, V>(x + t * p.ldx), hist[j]);
+            before[j] = ld_pack<T, V>(x + t * p.ldx);
         } else if (resumed) {
-            widen(ld_pack<T, V>(pool + static_cast<int64_t>(t - ck.begin + K - 1) * p.c), hist[j]);
+            before[j] = ld_pack<T, V>(pool + static_cast<int64_t>(t - ck.begin + K - 1) * p.c);
         }
     }
-    if (ck.k == 0 && slot >= 0) {
-        const int n = ck.end - ck.begin;
-        float tail[K - 1][V];  // all read before the first is written: short sequences shift the entry
-#pragma unroll
-        for (int j = 0; j < K - 1; ++j) {
-            const int t = n - (K - 1) + j;  // row of the sequence, negative: of the entry
-#pragma unroll
-            for (int v = 0; v < V; ++v) tail[j][v] = 0.0f;
-            if (t >= 0) {
-                widen(ld_pack<T, V>(x + (ck.begin + static_cast<int64_t>(t)) * p.ldx), tail[j]);
-            } else if (resumed) {
-                widen(ld_pack<T, V>(pool + static_cast<int64_t>(t + K - 1) * p.c), tail[j]);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < K - 1; ++j) st_pack<T, V>(pool + static_cast<int64_t>(j) * p.c, tail[j]);
-    }
-
-    float w[K][V], b[V];
-    conv_weights<K, V>(p, c0, w, b);
-    for (int t0 = ck.r0; t0 < ck.r1; t0 += kConvRows) {
-        Pack<T, V> raw[kConvRows];
+    auto load = [&](int t0) {
 #pragma unroll
         for (int i = 0; i < kConvRows; ++i) {
             const int t = t0 + i < ck.r1 ? t0 + i : ck.r1 - 1;
             raw[i] = ld_pack<T, V>(x + t * p.ldx);
         }
+    };
+    float w[K][V], b[V];
+    conv_weights<K, V>(p, c0, w, b);
+    if (ck.r0 < ck.r1) load(ck.r0);
+    if (ck.k == 0 && slot >= 0) {
+        const int n = ck.end - ck.begin;
+        Pack<T, V> tail[K - 1];  // all read before the first is written: short sequences shift the entry
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) {
+            const int t = n - (K - 1) + j;  // row of the sequence, negative: of the entry
+            tail[j] = Pack<T, V>{};
+            if (t >= 0) {
+                tail[j] = ld_pack<T, V>(x + (ck.begin + static_cast<int64_t>(t)) * p.ldx);
+            } else if (resumed) {
+                tail[j] = ld_pack<T, V>(pool + static_cast<int64_t>(t + K - 1) * p.c);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) *reinterpret_cast<Pack<T, V>*>(pool + static_cast<int64_t>(j) * p.c) = tail[j];
+    }
+    float hist[K - 1][V];
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) widen(before[j], hist[j]);
+    for (int t0 = ck.r0; t0 < ck.r1; t0 += kConvRows) {
+        if (t0 > ck.r0) load(t0);
 #pragma unroll
         for (int i = 0; i < kConvRows; ++i) {
             if (t0 + i < ck.r1) {
@@ -205,23 +210,28 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvK p) {
         for (int j = 0; j < K; ++j)
 #pragma unroll
             for (int v = 0; v < V; ++v) e[j][v] = 0.0f;
+        constexpr int R = kConvRows / 2;
+        const int stop = ck.r1 + K - 1;
+        Pack<T, V> before[K - 1], rx[R], rg[R];  // converted once the run's first loads are all under way
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) {
             const int t = ck.r0 - (K - 1) + j;
-#pragma unroll
-            for (int v = 0; v < V; ++v) hist[j][v] = 0.0f;
-            if (t >= ck.begin) widen(ld_pack<T, V>(x + t * p.ldx), hist[j]);
+            before[j] = Pack<T, V>{};
+            if (t >= ck.begin) before[j] = ld_pack<T, V>(x + t * p.ldx);
         }
-        constexpr int R = kConvRows / 2;
-        const int stop = ck.r1 + K - 1;
-        for (int t0 = ck.r0; t0 < stop; t0 += R) {
-            Pack<T, V> rx[R], rg[R];
+        auto load = [&](int t0) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const int t = t0 + i < ck.end ? t0 + i : ck.end - 1;
                 rx[i] = ld_pack<T, V>(x + t * p.ldx);
                 rg[i] = ld_pack<T, V>(gy + t * p.ldgy);
             }
+        };
+        load(ck.r0);
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) widen(before[j], hist[j]);
+        for (int t0 = ck.r0; t0 < stop; t0 += R) {
+            if (t0 > ck.r0) load(t0);
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const int t = t0 + i;

@@ -258,10 +258,12 @@ __global__ __launch_bounds__(256) void selscan_quad_kernel(const SelK p) {
     const int n0 = sub * SPL;
     const int slot = p.state ? slot_of(p.seq, s) : kNoSlot;
 
+    // The first loads all at once: states beyond n read the last one, and become
+    // zero once every load is under way.
     float A2[SPL], h[SPL];
 #pragma unroll
     for (int i = 0; i < SPL; ++i) {
-        A2[i] = n0 + i < p.n ? p.A[static_cast<int64_t>(c) * p.n + n0 + i] * kLog2E : 0.0f;
+        A2[i] = p.A[static_cast<int64_t>(c) * p.n + (n0 + i < p.n ? n0 + i : p.n - 1)];
         h[i] = 0.0f;
     }
     float* const pool = p.state + (static_cast<int64_t>(slot >= 0 ? slot : 0) * p.channels + c) * p.n + n0;
@@ -320,6 +322,8 @@ __global__ __launch_bounds__(256) void selscan_quad_kernel(const SelK p) {
         wc.step(p.ldc * kRows * es);
     };
     if (begin < end) load(begin);
+#pragma unroll
+    for (int i = 0; i < SPL; ++i) A2[i] = n0 + i < p.n ? A2[i] * kLog2E : 0.0f;
     int buf = 0;
     for (int base = begin; base < end; base += kRows, buf ^= 1) {
 #pragma unroll
@@ -495,17 +499,29 @@ __global__ __launch_bounds__(256) void selscan_step_kernel(const SelK p) {
             cv[i] = Store<T>::ld(C + i);
         }
     } else {
+        // states beyond n read the last one: loads that every lane makes, none waited for by itself
 #pragma unroll
         for (int i = 0; i < SPL; ++i) {
-            const bool in = n0 + i < p.n;
-            h[i] = in ? pool[i] : 0.0f;
-            A2[i] = in ? Ar[i] : 0.0f;
-            b[i] = in ? Store<T>::ld(B + i) : 0.0f;
-            cv[i] = in ? Store<T>::ld(C + i) : 0.0f;
+            const int at = (n0 + i < p.n ? n0 + i : p.n - 1) - n0;
+            h[i] = pool[at];
+            A2[i] = Ar[at];
+            b[i] = Store<T>::ld(B + at);
+            cv[i] = Store<T>::ld(C + at);
         }
     }
-    const float xv = Store<T>::ld(static_cast<const T*>(p.x) + s * p.ldx + cc);
-    float d = Store<T>::ld(static_cast<const T*>(p.dt) + s * p.lddt + cc) + (p.bias ? p.bias[cc] : 0.0f);
+    const T xr = static_cast<const T*>(p.x)[s * p.ldx + cc];
+    const T dr = static_cast<const T*>(p.dt)[s * p.lddt + cc];
+    T zr{};
+    if (p.z) zr = static_cast<const T*>(p.z)[s * p.ldz + cc];
+    const float bias = p.bias ? p.bias[cc] : 0.0f;
+    const float skip = p.D ? p.D[cc] : 0.0f;
+    if constexpr (!kVec) {
+#pragma unroll
+        for (int i = 0; i < SPL; ++i)
+            if (n0 + i >= p.n) h[i] = A2[i] = b[i] = cv[i] = 0.0f;
+    }
+    const float xv = Store<T>::ld(&xr);
+    float d = Store<T>::ld(&dr) + bias;
     if (p.softplus) d = softplus_f(d);
     const float u = d * xv;
     float y = 0.0f;
@@ -524,9 +540,9 @@ __global__ __launch_bounds__(256) void selscan_step_kernel(const SelK p) {
             if (n0 + i < p.n) pool[i] = h[i];
     }
     if (sub == 0) {
-        if (p.D) y = __builtin_fmaf(p.D[cc], xv, y);
+        if (p.D) y = __builtin_fmaf(skip, xv, y);
         if (p.z) {
-            const float zv = Store<T>::ld(static_cast<const T*>(p.z) + s * p.ldz + cc);
+            const float zv = Store<T>::ld(&zr);
             y *= zv * gate_sigmoid<T>(zv);
         }
         Store<T>::st(out, y);

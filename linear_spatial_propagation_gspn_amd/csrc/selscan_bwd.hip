@@ -216,34 +216,46 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
     for (int s = 0; s < SPL; ++s) dA[s] = 0.0f;
 
     if (ck.seq >= 0 && ck.r1 > ck.r0) {
+        // states beyond n read the last one, and become zero once the loads are under way
+        auto state = [&](int s) { return n0 + s < p.n ? n0 + s : p.n - 1; };
         float A2[SPL], ag[SPL];
 #pragma unroll
         for (int s = 0; s < SPL; ++s) {
-            const bool in = n0 + s < p.n;
-            A2[s] = in ? p.A[static_cast<int64_t>(c) * p.n + n0 + s] * kLog2E : 0.0f;
+            A2[s] = p.A[static_cast<int64_t>(c) * p.n + state(s)];
             ag[s] = 0.0f;
         }
         const int64_t id = chunk_base(p.seq, ck.seq, ck.begin, p.shift) + ck.k;
         // dL/dh after the chunk: the join's, or the chunks behind it here
         if (ck.count > kDirectChunks) {
 #pragma unroll
-            for (int s = 0; s < SPL; ++s)
-                ag[s] = n0 + s < p.n ? p.carry[(id * p.n + n0 + s) * p.channels + c] : 0.0f;
+            for (int s = 0; s < SPL; ++s) ag[s] = p.carry[(id * p.n + state(s)) * p.channels + c];
+#pragma unroll
+            for (int s = 0; s < SPL; ++s) {
+                A2[s] = n0 + s < p.n ? A2[s] * kLog2E : 0.0f;
+                ag[s] = n0 + s < p.n ? ag[s] : 0.0f;
+            }
         } else {
             constexpr int U = kDirectChunks - 1;
             float d[U], own[U][SPL];
 #pragma unroll
             for (int j = 0; j < U; ++j) {
-                const bool in = ck.k + 1 + j < ck.count;
-                d[j] = in ? 0.5f * p.sums[(id + 1 + j) * p.channels + c] : 0.0f;
+                d[j] = 0.0f;
 #pragma unroll
-                for (int s = 0; s < SPL; ++s)
-                    own[j][s] = in && n0 + s < p.n ? p.carry[((id + 1 + j) * p.n + n0 + s) * p.channels + c] : 0.0f;
+                for (int s = 0; s < SPL; ++s) own[j][s] = 0.0f;
+                if (ck.k + 1 + j < ck.count) {
+                    d[j] = p.sums[(id + 1 + j) * p.channels + c];
+#pragma unroll
+                    for (int s = 0; s < SPL; ++s)
+                        own[j][s] = p.carry[((id + 1 + j) * p.n + state(s)) * p.channels + c];
+                }
             }
+#pragma unroll
+            for (int s = 0; s < SPL; ++s) A2[s] = n0 + s < p.n ? A2[s] * kLog2E : 0.0f;
 #pragma unroll
             for (int j = U - 1; j >= 0; --j)  // behind the last: nothing yet, and nothing added
 #pragma unroll
-                for (int s = 0; s < SPL; ++s) ag[s] = carry_over(d[j] * A2[s], ag[s], own[j][s]);
+                for (int s = 0; s < SPL; ++s)
+                    ag[s] = carry_over(0.5f * d[j] * A2[s], ag[s], n0 + s < p.n ? own[j][s] : 0.0f);
         }
         const float bias = p.bias ? p.bias[c] : 0.0f;
         const float skip = p.D ? p.D[c] : 0.0f;
@@ -307,8 +319,7 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
             wc.step(-p.ldc * kTile * es);
             const auto q = row_at<const float>(p.check, (check0 + tile) * p.n, p.channels);
 #pragma unroll
-            for (int s = 0; s < SPL; ++s)
-                nh[s] = n0 + s < p.n ? q[static_cast<unsigned>((n0 + s) * p.channels + c)] : 0.0f;
+            for (int s = 0; s < SPL; ++s) nh[s] = q[static_cast<unsigned>(state(s) * p.channels + c)];
         };
         // the block's sums of dB and dC of a finished tile
         auto flush = [&](int tile, int buf) {
@@ -361,7 +372,7 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
             if (tile + 1 < tiles) flush(tile + 1, buf ^ 1);
             float a[kTile][SPL], hs[kTile + 1][SPL];  // decays; states before each row, and the last
 #pragma unroll
-            for (int s = 0; s < SPL; ++s) hs[0][s] = nh[s];
+            for (int s = 0; s < SPL; ++s) hs[0][s] = n0 + s < p.n ? nh[s] : 0.0f;
             float sy[4], sb4[4], sa4[4];  // of four rows, until their sums over the quad
             auto forward = [&](auto jc, int i) {
                 constexpr int J = decltype(jc)::value;
