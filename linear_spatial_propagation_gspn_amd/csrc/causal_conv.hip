@@ -9,7 +9,7 @@
 // once but for the halo at the run's start.  Two channels a lane, so that many
 // waves with few registers each keep the loads in flight: with eight (16
 // bytes of bf16) 8192 rows of 2304 channels took 19.8 us forward and 42
-// backward, with four 16.9 and 29.0, with two 16.3 and 28.2 (5.2 TB/s of x and
+// backward, with four 16.9 and 29.0, with two 16.3 and 27.4 (5.2 TB/s of x and
 // y would be 14.5 and 21.7).
 #include "sequence.hpp"
 
