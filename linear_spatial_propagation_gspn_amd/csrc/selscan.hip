@@ -245,14 +245,15 @@ __global__ __launch_bounds__(256) void selscan_quad_kernel(const SelK p) {
     constexpr int R = kRows / 4;  // rows a lane has to itself
     constexpr int kBC = (kRows * 2 * NP + 255) / 256;
     __shared__ __attribute__((aligned(16))) float bc[2][kRows][2 * NP];
-    const int s = blockIdx.x;
+    if (sequence_of_grid() >= p.seq.nseq) return;
+    const int s = static_cast<int>(sequence_of_grid());
     const int begin = seq_begin(p.seq, s);
     const int end = seq_end(p.seq, s, begin);
-    const int g = blockIdx.y / p.blocks;
+    const int g = blockIdx.x / p.blocks;
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int sub = lane & 3;
-    const int local = (blockIdx.y - g * p.blocks) * 64 + (tid >> 2);
+    const int local = (blockIdx.x - g * p.blocks) * 64 + (tid >> 2);
     const bool live = local < p.per;
     const int c = g * p.per + (live ? local : p.per - 1);
     const int n0 = sub * SPL;
@@ -423,16 +424,18 @@ __global__ __launch_bounds__(256) void selscan_quad_kernel(const SelK p) {
 // ahead of their serial products.  Bound by the latency of those loads where the
 // sequences are few (65536 rows of 2048 channels: 32 turns in 67 us), by the
 // carries' bytes where they are many.  At 8 ahead that scan took 854 us in all,
-// at 16 840, at 32 835; 16 ragged prompts of 4096 channels 261, 263 and 275.
+// at 16 840, at 32 835; 16 ragged prompts of 4096 channels, 24 us slower then,
+// 261, 263 and 275.
 // Four channels a lane, in wider loads, left too few lanes: 852 against 877 us
 // for that scan.
 __global__ __launch_bounds__(256) void selscan_join_kernel(const SelK p) {
-    const int s = blockIdx.x;
+    if (sequence_of_grid() >= p.seq.nseq) return;
+    const int s = static_cast<int>(sequence_of_grid());
     const int begin = seq_begin(p.seq, s);
     const int end = seq_end(p.seq, s, begin);
     const int count = static_cast<int>(chunks_each(end - begin, p.shift));
     if (count <= kDirectChunks) return;
-    const int e = static_cast<int>(blockIdx.y * 256 + threadIdx.x);  // n * channels + c
+    const int e = static_cast<int>(blockIdx.x * 256 + threadIdx.x);  // n * channels + c
     if (e >= p.channels * p.n) return;
     const int i = e / p.channels;
     const int c = e - i * p.channels;
@@ -581,7 +584,7 @@ void run_quad(const SelK& k, dim3 grid, hipStream_t stream) {
 
 template <typename T>
 void run_quad_n(const SelK& k, hipStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(k.seq.nseq), static_cast<unsigned>(k.groups * k.blocks));
+    const dim3 grid = sequence_grid(static_cast<int64_t>(k.groups) * k.blocks, k.seq.nseq);
     if (k.n <= 4) run_quad<T, 4>(k, grid, stream);
     else if (k.n <= 8) run_quad<T, 8>(k, grid, stream);
     else run_quad<T, 16>(k, grid, stream);
@@ -616,7 +619,7 @@ void run_step(const SelK& k, bool vec, hipStream_t stream) {
 // Chunks of L rows, 16 at least, are as long as their cost is least: the passes'
 // uneven end, which grows with L (some 2 (220 + 50 n) L cycles), against the
 // join's walk, 312 cycles a chunk of the longest sequence (packed ones are taken
-// to hold up to twice the mean), and the carries' bytes.  Measured at 16, 32, 64,
+// to hold up to twice the mean, or a quarter of the rows), and the carries' bytes.  Measured at 16, 32, 64,
 // 128 and 256 rows (us): 8 x 1024 rows of 2304 channels 142, 139 (and 79, 75, 84
 // with 4 states), 16 ragged prompts in 8192 rows of 4096 278 at 16, 240 at 32,
 // 261 at 64; 32 x 1024 of 2304 493 at 32, 466, 499 at 128; one of 65536 and 2048
@@ -633,7 +636,11 @@ int selscan_shift(int64_t rows, int64_t nseq, int64_t channels, int64_t groups, 
     int whole = kMinChunkShift;
     while ((int64_t{1} << whole) < longest) ++whole;
     if (lanes1 <= chunks) return whole;
-    const int64_t walk = ragged && longest > 2 * rows / nseq ? 2 * rows / nseq : longest;
+    int64_t walk = longest;
+    if (ragged) {
+        const int64_t likely = 2 * rows / nseq > rows / 4 ? 2 * rows / nseq : rows / 4;
+        if (walk > likely) walk = likely;
+    }
     const int64_t per_chunk = 312 * walk + rows * waves * n * 36 / 100;
     int best = kMinChunkShift;
     int64_t least = 0;
@@ -679,8 +686,7 @@ hipError_t launch_selscan_fwd(const gspn_selscan_args& a, int dtype, hipStream_t
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         if (needs_join(a, k.shift)) {
-            const dim3 jg(static_cast<unsigned>(a.seq.nseq),
-                          static_cast<unsigned>((a.channels * a.n + 255) / 256));
+            const dim3 jg = sequence_grid((a.channels * a.n + 255) / 256, a.seq.nseq);
             GSPN_REPLAYED("selscan_join_kernel", 256, 0);
             hipLaunchKernelGGL(selscan_join_kernel, jg, dim3(256), 0, stream, k);
             e = hipGetLastError();

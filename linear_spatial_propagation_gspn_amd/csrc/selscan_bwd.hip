@@ -150,12 +150,13 @@ __global__ __launch_bounds__(64) void selscan_bwd_local_kernel(const SelK p) {
 // The join of long sequences, against the row order: carry[k] := dL/dh after
 // chunk k's last row.
 __global__ __launch_bounds__(256) void selscan_bwd_join_kernel(const SelK p) {
-    const int s = blockIdx.x;
+    if (sequence_of_grid() >= p.seq.nseq) return;
+    const int s = static_cast<int>(sequence_of_grid());
     const int begin = seq_begin(p.seq, s);
     const int end = seq_end(p.seq, s, begin);
     const int count = static_cast<int>(chunks_each(end - begin, p.shift));
     if (count <= kDirectChunks) return;
-    const int e = static_cast<int>(blockIdx.y * 256 + threadIdx.x);  // n * channels + c
+    const int e = static_cast<int>(blockIdx.x * 256 + threadIdx.x);  // n * channels + c
     if (e >= p.channels * p.n) return;
     const int i = e / p.channels;
     const int c = e - i * p.channels;
@@ -627,8 +628,7 @@ hipError_t launch_selscan_bwd(const gspn_selscan_args& a, int dtype, hipStream_t
         else run_local_n<bf16_t>(k, lg, stream);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         if (needs_join(a, k.shift)) {
-            const dim3 jg(static_cast<unsigned>(a.seq.nseq),
-                          static_cast<unsigned>((a.channels * a.n + 255) / 256));
+            const dim3 jg = sequence_grid((a.channels * a.n + 255) / 256, a.seq.nseq);
             GSPN_REPLAYED("selscan_bwd_join_kernel", 256, 0);
             hipLaunchKernelGGL(selscan_bwd_join_kernel, jg, dim3(256), 0, stream, k);
             if ((e = hipGetLastError()) != hipSuccess) return e;
