@@ -455,6 +455,37 @@ def test_scan_growth_past_the_range_of_a_chunk(n):
         check(got[name], ref[name], mag[name], 2 * count + 16 + more, name)
 
 
+@pytest.mark.parametrize("long", [0, 300])
+def test_scan_of_more_sequences_than_a_grid_is_wide(long):
+    """70000 sequences of one row, which is then D x + sum_n C d x B, and behind them, packed, one that is cut."""
+    g = gen(39)
+    many, c, n = 70000, 4, 2
+    rows = many + long
+    k = scan_case(g, rows, c, 1, n, F32, gate=False)
+    o = on_gpu(k)
+    kw = {"cu": cu_of([1] * many + [long])} if long else {"nseq": many}
+    out = run_fwd(o, **kw)
+    gy = rnd(g, rows, c)
+    got = run_bwd(o, dev(gy), **kw)
+    args = ref_args(k)
+    x, d = args[0][:many], torch.nn.functional.softplus(args[1][:many] + args[7])
+    terms = args[4][:many, 0, None, :] * (d * x)[..., None] * args[3][:many, 0, None, :]
+    skip = args[5] * x
+    # d: an exponential, a logarithm and their sum; then products and a sum of n + 1 terms
+    count = R.scan_roundings(args[0][:1], args[1][:many], args[2], args[7], True, [(0, 1)]) + 2 * n + 16
+    check(out[:many], terms.sum(-1) + skip, terms.abs().sum(-1) + skip.abs(), count, "out")
+    ddx = (args[4][:many, 0, None, :] * args[3][:many, 0, None, :]).sum(-1) * d + args[5]
+    mag = (args[4][:many, 0, None, :] * args[3][:many, 0, None, :]).abs().sum(-1) * d + args[5].abs()
+    check(got["dx"][:many], wide(gy)[:many] * ddx, wide(gy)[:many].abs() * mag, count, "dx")
+    if long:
+        tail = [t[many:] if t is not None and t.shape[0] == rows else t for t in args]
+        ry, _, _, sy, _ = R.scan(*tail, True, [(0, long)])
+        ref, m = R.scan_backward(*tail, True, [(0, long)], wide(gy)[many:])
+        count = R.scan_roundings(tail[0], tail[1], tail[2], tail[7], True, [(0, long)])
+        check(out[many:], ry, sy, count, "out of the last")
+        check(got["dx"][many:], ref["dx"], m["dx"], 2 * count + 16 + n, "dx of the last")
+
+
 # ------------------------------------------------------------------------------------------------- block join
 
 JOIN_PARTS = ["grosp", "r", "rp", "os", "gp", "o", "", "rsp", "go"]
