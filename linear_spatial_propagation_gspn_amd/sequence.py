@@ -20,7 +20,8 @@ the pool alone), ``resume`` (bool [nseq]) says which prompts continue their
 entry.
 
 Gradients have autograd forms (``causal_conv``, ``selective_scan``,
-``block_join``) on top of the ``_fwd`` / ``_bwd`` calls.  Nothing here
+``block_join``) on top of the ``_fwd`` / ``_bwd`` calls, reverse mode only: a
+tensor with a forward-mode tangent is refused.  Nothing here
 synchronises; outputs and workspaces are allocated by torch unless given, so
 every call can be captured in a HIP graph.  As for any autograd node, a backward
 is captured with no eager graph of the same leaves alive: torch would tie the
@@ -31,6 +32,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd import forward_ad
 
 from . import gspn as G
 
@@ -558,6 +560,14 @@ def _wants_grad(*tensors) -> bool:
     return torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in tensors)
 
 
+def _no_tangents(*tensors) -> None:
+    """Refuses forward-mode derivatives: the calls read a tensor's values alone, and an output without a tangent would
+    be taken for one whose derivative is zero."""
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError("the sequence operators have no forward-mode derivative")
+
+
 def _clear(x, cu):
     """With packed sequences, an output whose rows outside them are zero."""
     return None if cu is None or not isinstance(x, torch.Tensor) else x.new_zeros(x.shape)
@@ -565,6 +575,7 @@ def _clear(x, cu):
 
 def _grad_rows(g, like):
     """A gradient in its tensor's dtype, with contiguous columns."""
+    _no_tangents(g)
     return g.to(like).contiguous()
 
 
@@ -589,6 +600,7 @@ class _CausalConv(torch.autograd.Function):
 def causal_conv(x, weight, bias=None, silu: bool = True, cu=None, nseq=None) -> torch.Tensor:
     """The short causal convolution as a differentiable op (no state); rows
     outside the sequences of ``cu`` are zero."""
+    _no_tangents(x, weight, bias)
     if not _wants_grad(x, weight, bias):
         return gspn_causal_conv_fwd(x, weight, bias, silu, cu, nseq, out=_clear(x, cu))
     return _CausalConv.apply(bool(silu), cu, nseq, x, weight, bias)
@@ -620,6 +632,7 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus: bool 
     """The selective scan as a differentiable op (no state); rows outside the
     sequences of ``cu`` are zero.  The forward keeps its states before every
     8th row (n / 2 bytes an element of x) until the backward."""
+    _no_tangents(x, dt, A, B, C, D, z, dt_bias)
     if not _wants_grad(x, dt, A, B, C, D, z, dt_bias):
         return gspn_selective_scan_fwd(x, dt, A, B, C, D, z, dt_bias, softplus, cu, nseq, out=_clear(x, cu))
     return _SelectiveScan.apply(bool(softplus), cu, nseq, x, dt, A, B, C, D, z, dt_bias)
@@ -654,6 +667,7 @@ class _BlockJoin(torch.autograd.Function):
 def block_join(h, gate=None, residual=None, post=None, scale=None, pre=None, eps: float = 1e-6) -> tuple:
     """The join of a block's output to the residual stream as a differentiable
     op: (joined, normed), normed None without pre."""
+    _no_tangents(h, gate, residual, post, scale, pre)
     if not _wants_grad(h, gate, residual, post, scale, pre):
         return gspn_block_join_fwd(h, gate, residual, post, scale, pre, eps)
     return _BlockJoin.apply(float(eps), h, gate, residual, post, scale, pre)
