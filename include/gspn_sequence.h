@@ -28,7 +28,8 @@
  *    Otherwise cu is a device array of nseq + 1 offsets, not decreasing,
  *    0 <= cu[i] <= rows: sequence i is rows [cu[i], cu[i+1]); it may be
  *    empty.  Rows outside every sequence are not read, and not written but
- *    by the backward calls, which give them zero gradients.
+ *    by the backward calls, which give them zero gradients (with nseq == 0:
+ *    to every row, and to the parameters; no workspace or checkpoints then).
  *    Offsets that break these rules give unspecified results inside the
  *    caller's buffers (they are clamped to [0, rows]).
  *    At most 2^23 sequences (rows + nseq <= 2^30), 2^16 with slots.
@@ -42,8 +43,8 @@
  *    entry of the pool is touched for it.
  *    resume (prompts; device bytes [nseq]): nonzero continues from the
  *    entry, zero starts from zeros; NULL: every sequence starts from zeros.
- *  - Empty calls (no rows and no sequence, or no channel) return GSPN_OK and
- *    queue nothing.
+ *  - Empty calls (no rows and no sequence, a forward without a sequence, or
+ *    no channel) return GSPN_OK and queue nothing.
  *  - Aliasing: an output, a state pool, a workspace may overlap nothing else
  *    (inputs may overlap inputs).  Row tensors of the same row stride in
  *    bytes may be column slices of one matrix; of different strides they are

@@ -279,9 +279,12 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvK p) {
 // cover every row, as they mostly do, it costs next to nothing, against a pass
 // over all the gradients to clear them beforehand.
 __device__ __forceinline__ void zero_outside(const OutsideK& k, int64_t wave, int64_t waves, int lane) {
-    const int lo = seq_begin(k.seq, 0);
-    const int last = k.seq.nseq - 1;
-    const int hi = seq_end(k.seq, last, seq_begin(k.seq, last));
+    int lo = 0, hi = 0;
+    if (!k.all) {
+        lo = seq_begin(k.seq, 0);
+        const int last = k.seq.nseq - 1;
+        hi = seq_end(k.seq, last, seq_begin(k.seq, last));
+    }
     const int64_t outside = lo + static_cast<int64_t>(k.seq.rows > hi ? k.seq.rows - hi : 0);
     for (int64_t i = wave; i < outside; i += waves) {
         const int64_t row = i < lo ? i : hi + (i - lo);
@@ -454,15 +457,17 @@ hipError_t launch_conv_step(const gspn_conv_args& a, int dtype, hipStream_t stre
 }
 
 hipError_t launch_conv_bwd(const gspn_conv_args& a, int dtype, hipStream_t stream) {
-    const hipError_t e = launch_conv(2, a, dtype, stream);
+    const bool none = a.seq.nseq == 0;  // every row is outside, and the sums are over no parts
+    const hipError_t e = none ? hipSuccess : launch_conv(2, a, dtype, stream);
     if (e != hipSuccess) return e;
     OutsideK o{};
     o.seq = make_seq(a.seq);
+    o.all = none;
     o.es = dtype == kF32 ? 4 : 2;
     o.t[0] = {a.dx, a.lddx, a.c};
     ReduceK r{};
     r.part = static_cast<const float*>(a.workspace);
-    r.parts = chunk_ids(a.seq.cu != nullptr, a.seq.rows, a.seq.nseq, conv_shift_for(a.seq.rows, a.c));
+    if (!none) r.parts = chunk_ids(a.seq.cu != nullptr, a.seq.rows, a.seq.nseq, conv_shift_for(a.seq.rows, a.c));
     r.ld = (a.width + 1) * a.c;
     r.c = a.c;
     r.cols = r.ld;
@@ -473,10 +478,11 @@ hipError_t launch_conv_bwd(const gspn_conv_args& a, int dtype, hipStream_t strea
 }
 
 hipError_t launch_reduce_parts(const ReduceK& k, const OutsideK& o, hipStream_t stream) {
-    const dim3 grid(static_cast<unsigned>((k.cols + 63) / 64 + (o.seq.cu ? kOutsideBlocks : 0)));
+    const bool outside = o.seq.cu || o.all;
+    const dim3 grid(static_cast<unsigned>((k.cols + 63) / 64 + (outside ? kOutsideBlocks : 0)));
     for (const auto& t : o.t) {
         (void)t;
-        if (o.seq.cu) GSPN_REPLAY_ROWS("reduce_parts_kernel", "gradient", t.p, o.seq.rows, t.ld, t.c, o.es);
+        if (outside) GSPN_REPLAY_ROWS("reduce_parts_kernel", "gradient", t.p, o.seq.rows, t.ld, t.c, o.es);
     }
     GSPN_REPLAY_ROWS("reduce_parts_kernel", "partial sums", k.part, k.parts, k.ld, k.cols, 4);
     GSPN_REPLAYED("reduce_parts_kernel", 64 * kReduceRuns, 64 * kReduceRuns * 4);

@@ -603,7 +603,36 @@ int selscan_bwd_shift(int64_t rows, int64_t nseq, int64_t channels, int64_t grou
     return shift;
 }
 
+namespace {
+
+// The sums over `parts` chunks that lie in `part`, and zeros in the rows
+// outside the sequences (none: in every row).
+hipError_t finish_selscan_bwd(const gspn_selscan_args& a, const float* part, int64_t parts, bool none, int es,
+                              hipStream_t stream) {
+    ReduceK r{};
+    r.part = part;
+    r.parts = parts;
+    r.c = a.channels;
+    r.ld = r.cols = (a.n + 2) * a.channels;
+    r.o[0] = {a.dA, static_cast<int32_t>(a.n), a.n, 1};
+    r.o[1] = {a.dD, 1, 1, 0};
+    r.o[2] = {a.ddt_bias, 1, 1, 0};
+    OutsideK o{};
+    o.seq = make_seq(a.seq);
+    o.es = es;
+    o.all = none;
+    o.t[0] = {a.dx, a.lddx, a.channels};
+    o.t[1] = {a.ddt, a.ldddt, a.channels};
+    o.t[2] = {a.z ? a.dz : nullptr, a.lddz, a.channels};
+    o.t[3] = {a.dB, a.groups * a.n, a.groups * a.n};
+    o.t[4] = {a.dC, a.groups * a.n, a.groups * a.n};
+    return launch_reduce_parts(r, o, stream);
+}
+
+}  // namespace
+
 hipError_t launch_selscan_bwd(const gspn_selscan_args& a, int dtype, hipStream_t stream) {
+    if (a.seq.nseq == 0) return finish_selscan_bwd(a, nullptr, 0, true, dtype == kF32 ? 4 : 2, stream);
     SelK k = selscan_params(a);
     const bool ragged = a.seq.cu != nullptr;
     k.shift = selscan_bwd_shift(a.seq.rows, a.seq.nseq, a.channels, a.groups, a.n, ragged);
@@ -667,23 +696,7 @@ hipError_t launch_selscan_bwd(const gspn_selscan_args& a, int dtype, hipStream_t
                                static_cast<bf16_t*>(a.dC));
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    ReduceK r{};
-    r.part = k.part;
-    r.parts = ids;
-    r.c = a.channels;
-    r.ld = r.cols = (a.n + 2) * a.channels;
-    r.o[0] = {a.dA, static_cast<int32_t>(a.n), a.n, 1};
-    r.o[1] = {a.dD, 1, 1, 0};
-    r.o[2] = {a.ddt_bias, 1, 1, 0};
-    OutsideK o{};
-    o.seq = k.seq;
-    o.es = es;
-    o.t[0] = {a.dx, a.lddx, a.channels};
-    o.t[1] = {a.ddt, a.ldddt, a.channels};
-    o.t[2] = {a.z ? a.dz : nullptr, a.lddz, a.channels};
-    o.t[3] = {a.dB, a.groups * a.n, a.groups * a.n};
-    o.t[4] = {a.dC, a.groups * a.n, a.groups * a.n};
-    return launch_reduce_parts(r, o, stream);
+    return finish_selscan_bwd(a, k.part, ids, false, es, stream);
 }
 
 }  // namespace gspn

@@ -218,12 +218,13 @@ struct ReduceK {
     ReduceOut o[3];
 };
 
-// Zeros in the rows before the first and behind the last packed sequence, of
-// up to five tensors (p null: none; es: bytes of an element).  It rides on the
-// reduction's launch; seq.cu null: nothing to do.
+// Zeros in the rows before the first and behind the last packed sequence (all:
+// in every row), of up to five tensors (p null: none; es: bytes of an element).
+// It rides on the reduction's launch; seq.cu null and not all: nothing to do.
 struct OutsideK {
     SeqK seq;
     int32_t es;
+    int32_t all;
     struct {
         void* p;
         int64_t ld, c;
@@ -240,7 +241,7 @@ inline SeqK make_seq(const gspn_sequences& s) {
     k.resume = s.resume;
     k.rows = static_cast<int32_t>(s.rows);
     k.nseq = static_cast<int32_t>(s.nseq);
-    k.len = s.cu ? 0 : static_cast<int32_t>(s.rows / s.nseq);
+    k.len = s.cu || s.nseq == 0 ? 0 : static_cast<int32_t>(s.rows / s.nseq);
     k.nslots = static_cast<int32_t>(s.nslots);
     return k;
 }
@@ -251,6 +252,7 @@ inline bool aligned_rows(const void* p, int64_t ld, int es, int bytes) {
 
 hipError_t launch_conv_fwd(const gspn_conv_args& a, int dtype, hipStream_t stream);
 hipError_t launch_conv_step(const gspn_conv_args& a, int dtype, hipStream_t stream);
+// (no sequence: zero gradients)
 hipError_t launch_conv_bwd(const gspn_conv_args& a, int dtype, hipStream_t stream);
 int64_t conv_bwd_parts(int64_t rows, int64_t nseq, int64_t c);
 
@@ -265,6 +267,7 @@ constexpr int kWholeQuad = 63;  // of selscan_shift: no chunks
 
 hipError_t launch_selscan_fwd(const gspn_selscan_args& a, int dtype, hipStream_t stream);
 hipError_t launch_selscan_step(const gspn_selscan_args& a, int dtype, hipStream_t stream);
+// (no sequence: zero gradients)
 hipError_t launch_selscan_bwd(const gspn_selscan_args& a, int dtype, hipStream_t stream);
 
 hipError_t launch_join_fwd(const gspn_join_args& a, int dtype, hipStream_t stream);

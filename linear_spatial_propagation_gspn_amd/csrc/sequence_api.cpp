@@ -86,7 +86,7 @@ class Buffers {
     }
 };
 
-// Sequences of a call.  step: one row each.
+// Sequences of a call.  step: one row each.  empty: no sequence.
 gspn_status check_seq(const gspn_sequences& s, bool pool, bool step, bool* empty, Buffers* b) {
     if (s.rows < 0 || s.rows > kMaxRows || s.nseq < 0 || s.nseq > kMaxRows || s.nslots < 0 || s.nslots > kMaxRows)
         return GSPN_ERR_BAD_SHAPE;
@@ -116,7 +116,9 @@ gspn_status check_conv(const gspn_conv_args* a, int dtype, int which, bool* empt
     Buffers b;
     const gspn_status s = check_seq(a->seq, pool || which == 1, which == 1, empty, &b);
     if (s != GSPN_OK) return s;
-    *empty = *empty || a->c == 0;
+    // a backward has rows outside the sequences to clear, also where there is no sequence
+    const bool none = *empty;
+    *empty = (none && (which != 2 || rows == 0)) || a->c == 0;
     if (*empty) return GSPN_OK;
     if (which == 1 && !a->state) return GSPN_ERR_NULL_POINTER;
     b.rows(a->x, rows, a->ldx, a->c, es, false);
@@ -127,7 +129,7 @@ gspn_status check_conv(const gspn_conv_args* a, int dtype, int which, bool* empt
         b.rows(a->dx, rows, a->lddx, a->c, es, true);
         b.flat(a->dweight, a->c * a->width * 4, 4, true);
         b.flat(a->dbias, a->c * 4, 4, true, true);
-        const int64_t need = gspn_causal_conv_bwd_workspace_bytes(rows, a->seq.nseq, a->c, a->width);
+        const int64_t need = none ? 0 : gspn_causal_conv_bwd_workspace_bytes(rows, a->seq.nseq, a->c, a->width);
         if (a->workspace_bytes < need) return GSPN_ERR_WORKSPACE;
         b.flat(a->workspace, need, 4, true);
     } else {
@@ -156,7 +158,8 @@ gspn_status check_scan(const gspn_selscan_args* a, int dtype, int which, bool* e
     Buffers b;
     const gspn_status s = check_seq(a->seq, pool || which == 1, which == 1, empty, &b);
     if (s != GSPN_OK) return s;
-    *empty = *empty || a->channels == 0;
+    const bool none = *empty;  // as in the convolution
+    *empty = (none && (which != 2 || rows == 0)) || a->channels == 0;
     if (*empty) return GSPN_OK;
     if (which == 1 && !a->state) return GSPN_ERR_NULL_POINTER;
     const int64_t c = a->channels, gn = a->groups * a->n;
@@ -169,7 +172,7 @@ gspn_status check_scan(const gspn_selscan_args* a, int dtype, int which, bool* e
     b.flat(a->A, c * a->n * 4, 4, false);
     b.flat(a->D, c * 4, 4, false, true);
     b.flat(a->dt_bias, c * 4, 4, false, true);
-    const int64_t kept = gspn_selective_scan_checkpoint_bytes(rows, nseq, c, a->n, ragged);
+    const int64_t kept = none ? 0 : gspn_selective_scan_checkpoint_bytes(rows, nseq, c, a->n, ragged);
     if (which == 2) {
         b.rows(a->gy, rows, a->ldgy, c, es, false);
         b.flat(a->checkpoints, kept, 4, false);
@@ -181,7 +184,8 @@ gspn_status check_scan(const gspn_selscan_args* a, int dtype, int which, bool* e
         b.flat(a->dA, c * a->n * 4, 4, true);
         b.flat(a->dD, c * 4, 4, true, true);
         b.flat(a->ddt_bias, c * 4, 4, true, true);
-        const int64_t need = gspn_selective_scan_bwd_workspace_bytes(rows, nseq, c, a->groups, a->n, ragged);
+        const int64_t need =
+            none ? 0 : gspn_selective_scan_bwd_workspace_bytes(rows, nseq, c, a->groups, a->n, ragged);
         if (a->workspace_bytes < need) return GSPN_ERR_WORKSPACE;
         b.flat(a->workspace, need, 4, true);
     } else {

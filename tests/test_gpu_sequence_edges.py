@@ -1,0 +1,50 @@
+"""The sequence operators on the GPU where calls and values are at their edges: nothing to sum over, values at the ends
+of their type's range."""
+import math
+
+import pytest
+import torch
+
+import sequence_reference as R
+from linear_spatial_propagation_gspn_amd import sequence as S
+from test_gpu_sequence import (BF16, DEV, F32, _gpu, _say, check, cu_of, dev, gate_count, gen, on_gpu, ref_args, rnd,  # noqa: F401
+                               run_bwd, run_fwd, scan_case, wide)
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------------------------------------ nothing to sum
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,c,n", [(1, 1, 1), (40, 70, 16), (3000, 5, 3)])
+def test_rows_without_a_sequence_get_zero_gradients(dtype, rows, c, n):
+    """The C calls themselves (the binding answers such a call without one): every gradient is written."""
+    none = torch.zeros(1, dtype=torch.int32, device=DEV)
+    code = 0 if dtype == F32 else 1
+    g = gen(1)
+    k = on_gpu(scan_case(g, rows, c, 1, n, dtype))
+    seq = S._sequences(k["x"], none, None)
+    wide_dx = torch.full((rows, c + 3), 7.0, dtype=dtype, device=DEV)
+    full = lambda like: torch.full(like.shape, 7.0, dtype=like.dtype, device=DEV)  # noqa: E731
+
+    w, b = dev(rnd(g, c, 4)), dev(rnd(g, c))
+    a = S._conv_args(k["x"], w, b, True, seq)
+    a.gy, a.ldgy = k["x"].data_ptr(), c
+    outs = [wide_dx[:, :c], full(w), full(b)]
+    a.dx, a.lddx = outs[0].data_ptr(), c + 3
+    a.dweight, a.dbias = outs[1].data_ptr(), outs[2].data_ptr()
+    S._call("gspn_causal_conv_bwd", a, code, 0)
+    assert all((t == 0).all() for t in outs) and (wide_dx[:, c:] == 7.0).all()
+
+    a = S._scan_args(k["x"], k["dt"], k["A"], k["B"], k["C"], k["D"], k["z"], k["dt_bias"], True, seq)
+    a.gy, a.ldgy = k["x"].data_ptr(), c
+    wide_dx.fill_(7.0)
+    outs = {"dx": wide_dx[:, :c], "ddt": full(k["x"]), "dz": full(k["x"]), "dB": full(k["B"]), "dC": full(k["C"]),
+            "dA": full(k["A"]), "dD": full(k["D"]), "ddt_bias": full(k["D"])}
+    for name, t in outs.items():
+        setattr(a, name, t.data_ptr())
+    a.lddx, a.ldddt, a.lddz = c + 3, c, c
+    S._call("gspn_selective_scan_bwd", a, code, 0)
+    for name, t in outs.items():
+        assert (t == 0).all(), name
+    assert (wide_dx[:, c:] == 7.0).all()
