@@ -44,7 +44,8 @@
  *    resume (prompts; device bytes [nseq]): nonzero continues from the
  *    entry, zero starts from zeros; NULL: every sequence starts from zeros.
  *  - Empty calls (no rows and no sequence, a forward without a sequence, or
- *    no channel) return GSPN_OK and queue nothing.
+ *    no channel) return GSPN_OK and queue nothing; the scan's backward of rows
+ *    without a channel gives them zero dB and dC.
  *  - Aliasing: an output, a state pool, a workspace may overlap nothing else
  *    (inputs may overlap inputs).  Row tensors of the same row stride in
  *    bytes may be column slices of one matrix; of different strides they are

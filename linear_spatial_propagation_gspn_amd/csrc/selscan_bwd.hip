@@ -632,7 +632,8 @@ hipError_t finish_selscan_bwd(const gspn_selscan_args& a, const float* part, int
 }  // namespace
 
 hipError_t launch_selscan_bwd(const gspn_selscan_args& a, int dtype, hipStream_t stream) {
-    if (a.seq.nseq == 0) return finish_selscan_bwd(a, nullptr, 0, true, dtype == kF32 ? 4 : 2, stream);
+    if (a.seq.nseq == 0 || a.channels == 0)
+        return finish_selscan_bwd(a, nullptr, 0, true, dtype == kF32 ? 4 : 2, stream);
     SelK k = selscan_params(a);
     const bool ragged = a.seq.cu != nullptr;
     k.shift = selscan_bwd_shift(a.seq.rows, a.seq.nseq, a.channels, a.groups, a.n, ragged);

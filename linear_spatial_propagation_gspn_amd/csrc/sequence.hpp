@@ -267,7 +267,7 @@ constexpr int kWholeQuad = 63;  // of selscan_shift: no chunks
 
 hipError_t launch_selscan_fwd(const gspn_selscan_args& a, int dtype, hipStream_t stream);
 hipError_t launch_selscan_step(const gspn_selscan_args& a, int dtype, hipStream_t stream);
-// (no sequence: zero gradients)
+// (no sequence, or no channel: zero gradients)
 hipError_t launch_selscan_bwd(const gspn_selscan_args& a, int dtype, hipStream_t stream);
 
 hipError_t launch_join_fwd(const gspn_join_args& a, int dtype, hipStream_t stream);

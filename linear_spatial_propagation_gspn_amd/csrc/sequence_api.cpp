@@ -158,8 +158,9 @@ gspn_status check_scan(const gspn_selscan_args* a, int dtype, int which, bool* e
     Buffers b;
     const gspn_status s = check_seq(a->seq, pool || which == 1, which == 1, empty, &b);
     if (s != GSPN_OK) return s;
-    const bool none = *empty;  // as in the convolution
-    *empty = (none && (which != 2 || rows == 0)) || a->channels == 0;
+    // as in the convolution; without a channel dB and dC are sums over none
+    const bool none = *empty || a->channels == 0;
+    *empty = none && (which != 2 || rows == 0);
     if (*empty) return GSPN_OK;
     if (which == 1 && !a->state) return GSPN_ERR_NULL_POINTER;
     const int64_t c = a->channels, gn = a->groups * a->n;

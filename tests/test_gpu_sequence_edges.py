@@ -48,3 +48,18 @@ def test_rows_without_a_sequence_get_zero_gradients(dtype, rows, c, n):
     for name, t in outs.items():
         assert (t == 0).all(), name
     assert (wide_dx[:, c:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("kw", [{}, {"nseq": 2}, {"cu": [1, 5]}, {"cu": [0]}])
+def test_rows_without_a_channel_have_zero_sums(dtype, kw):
+    kw = {n: cu_of([b - a for a, b in zip(v, v[1:])], v[0]) if n == "cu" else v for n, v in kw.items()}
+    x, A = torch.empty(6, 0, dtype=dtype, device=DEV), torch.empty(0, 5, device=DEV)
+    bc = torch.randn(6, 3, 5, device=DEV).to(dtype)
+    assert S.gspn_selective_scan_fwd(x, x, A, bc, bc, **kw).shape == (6, 0)
+    grads = S.gspn_selective_scan_bwd(x, x, A, bc, bc, x, **kw)
+    for t, shape in zip(grads[:5], ((6, 0), (6, 0), (0, 5), (6, 3, 5), (6, 3, 5))):
+        assert t.shape == shape and (t == 0).all()
+    leaf = bc.clone().requires_grad_()
+    S.selective_scan(x, x, A, leaf, leaf, **kw).sum().backward()
+    assert (leaf.grad == 0).all()
