@@ -30,6 +30,7 @@ capture to the stream on which that graph found them.
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 from torch.autograd import forward_ad
@@ -142,14 +143,14 @@ def _rows(t, name: str, shape: tuple, dtype, index: int, tail: int = 1) -> int:
     if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     stride = t.stride()
+    if t.numel() == 0:  # whose strides mean nothing
+        return max(math.prod(shape[-tail:]), 1)
     want = 1
     for d in range(tail):
         if stride[-1 - d] != want and shape[-1 - d] != 1:
             raise ValueError("%s must have contiguous columns (strides %s)" % (name, stride))
         want *= shape[-1 - d]
     lead = len(shape) - tail
-    if t.numel() == 0:
-        return max(want, 1)
     ld = stride[lead - 1] if shape[lead - 1] != 1 else want
     if lead == 2:
         n, length = shape[0], shape[1]

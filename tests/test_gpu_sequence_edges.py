@@ -63,3 +63,13 @@ def test_rows_without_a_channel_have_zero_sums(dtype, kw):
     leaf = bc.clone().requires_grad_()
     S.selective_scan(x, x, A, leaf, leaf, **kw).sum().backward()
     assert (leaf.grad == 0).all()
+
+
+def test_gradients_of_an_empty_batch():
+    """No rows: the sums over them are zero, also for a gradient whose strides are those of an expanded scalar."""
+    x, bc = (torch.empty(0, *s, device=DEV, requires_grad=True) for s in ((12,), (1, 4)))
+    w, A, pre = (torch.randn(*s, device=DEV).requires_grad_() for s in ((12, 4), (12, 4), (12,)))
+    for f, leaves in ((lambda: S.causal_conv(x, w), (x, w)), (lambda: S.selective_scan(x, x, A, bc, bc), (x, A, bc)),
+                      (lambda: S.block_join(x, x, x, pre=pre)[1], (x, pre))):
+        for t, g in zip(leaves, torch.autograd.grad(f().sum(), leaves)):
+            assert g.shape == t.shape and (g == 0).all()

@@ -68,3 +68,14 @@ def test_plain_calls_stay_plain_at_a_dual_level(op):
         leaf = ts[0].clone().requires_grad_()
         y = f(leaf, *ts[1:])
         assert torch.equal(torch.autograd.grad(y, leaf, torch.ones_like(y))[0], torch.zeros_like(leaf))
+
+
+@pytest.mark.parametrize("shape,tail,ld", [((0, 5), 1, 5), ((6, 0), 1, 1), ((2, 0, 5), 1, 5), ((0, 3, 4), 2, 12),
+                                           ((6, 1, 0), 2, 1)])
+def test_an_empty_tensor_has_rows_whatever_its_strides(monkeypatch, shape, tail, ld):
+    """The gradient of an empty output's sum is an expanded scalar, all of whose strides are zero, and torch's
+    contiguous() leaves it so."""
+    monkeypatch.setattr(S, "_tensor", lambda *a: None)  # its device
+    gy = torch.ones(()).expand(shape).contiguous()
+    assert set(gy.stride()) == {0}
+    assert S._rows(gy, "gy", gy.shape, gy.dtype, 0, tail) == ld
