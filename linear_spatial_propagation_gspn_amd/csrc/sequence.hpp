@@ -160,12 +160,16 @@ __device__ __forceinline__ void st_pack(T* p, const float (&f)[V]) {
 }
 
 // The logistic function of a gate whose result goes to storage type T.  For
-// fp32 the compensated form; for bf16 the exponent's argument is rounded once
+// fp32 the compensated form, which stops at v = -87; a gate multiplies by v,
+// so the tail beyond it counts (v = -3e38 gave silu(v) = -5) and is continued
+// as e^{v + 87}.  For bf16 the exponent's argument is rounded once
 // (relative error at most |v| 2^-24 + 3 ulp, under a hundredth of the half
-// step 2^-9 of a bf16 result wherever silu is not negligible).
+// step 2^-8 of a bf16 result), and a result below 2^-126 is 0 (at v = -87.4: an
+// error of 1.1e-36 in silu at most).
 template <typename T>
 __device__ __forceinline__ float gate_sigmoid(float v) {
-    if constexpr (sizeof(T) == 4) return sigmoid(v);
+    if constexpr (sizeof(T) == 4)
+        return sigmoid(v) * __builtin_amdgcn_exp2f(__builtin_fminf(v + 87.0f, 0.0f) * 1.44269504088896340736f);
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504088896340736f));
 }
 

@@ -73,3 +73,65 @@ def test_gradients_of_an_empty_batch():
                       (lambda: S.block_join(x, x, x, pre=pre)[1], (x, pre))):
         for t, g in zip(leaves, torch.autograd.grad(f().sum(), leaves)):
             assert g.shape == t.shape and (g == 0).all()
+
+
+# ------------------------------------------------------------------------------------------ gates far from zero
+
+GATES = [-60.0, -86.5, -87.0, -87.25, -88.0, -89.5, -95.0, -104.0, -110.0, -200.0, -1000.0, -1e6, -1e20, -1e30, -3e38,
+         0.0, 1.0, 60.0, 88.0, 200.0, 1e20, 3e38]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gates_far_from_zero(dtype):
+    """silu and its slope over the whole range of the type: what a gate of the type's lowest value closes stays closed
+    (its silu is -0).  Roundings: the gate's argument (2 |v|) and 8, as everywhere, of what is not yet zero.  bf16's
+    form takes a logistic below the normal numbers of fp32 as zero: there all of silu may be lost."""
+    c = len(GATES)
+    v = torch.tensor([GATES, GATES[::-1]]).to(dtype)
+    v[0, 14], v[1, 7] = torch.finfo(dtype).min, torch.finfo(dtype).min
+    one, gy = torch.ones(2, c, dtype=dtype), torch.ones(2, c, dtype=dtype)
+    w, s, ds = wide(v), R.silu(wide(v)), R.dsilu(wide(v))
+    count = 2 * w.abs().clamp(max=110) + 8
+    slope, size = R.dsilu_scale(w), s.abs()
+    if dtype != F32:
+        lost = torch.sigmoid(w) < 2.0 ** -126
+        size, slope = torch.where(lost, size / (count * R.U), size), torch.where(lost, slope / (count * R.U), slope)
+
+    taps = torch.tensor([0.0, 1.0]).expand(c, 2).contiguous()  # the pre-activation is the row itself
+    check(S.gspn_causal_conv_fwd(dev(v), dev(taps)), s, size, count, "convolution")
+    pool = torch.zeros(2, 1, c, dtype=dtype, device=DEV)
+    check(S.gspn_causal_conv_step(dev(v), dev(taps), None, pool), s, size, count, "convolution's step")
+    dx = S.gspn_causal_conv_bwd(dev(v), dev(taps), None, dev(gy), nseq=2)[0]
+    check(dx, ds, slope, 2 * count + 8, "convolution's dx")
+
+    for n in (1, 16):  # x = 1, B = 0, D = 1: the gate's value is the row
+        k = dict(x=dev(one), dt=dev(one), A=-torch.ones(c, n, device=DEV), B=torch.zeros(2, 1, n, dtype=dtype, device=DEV),
+                 C=torch.ones(2, 1, n, dtype=dtype, device=DEV), D=torch.ones(c, device=DEV), z=dev(v), dt_bias=None)
+        for kw in ({}, {"nseq": 2}):
+            check(run_fwd(k, **kw), s, size, count + 2, "scan")
+            got = run_bwd(k, dev(gy), **kw)
+            check(got["dx"], s, size, count + 4, "scan's dx")
+            check(got["dz"], ds, slope, 2 * count + 10, "scan's dz")
+        pool = torch.zeros(2, c, n, device=DEV)
+        y = S.gspn_selective_scan_step(k["x"], k["dt"], k["A"], k["B"], k["C"], pool, k["D"], k["z"])
+        check(y, s, size, count + 2, "scan's step")
+
+    joined = S.gspn_block_join_fwd(dev(one), dev(v))[0]
+    check(joined, s, size, count + 2, "join")
+    dh, dgate = S.gspn_block_join_bwd(dev(one), dev(gy), None, None, dev(v))[:2]
+    check(dh, s, size, count + 2, "join's dh")
+    check(dgate, ds, slope, 2 * count + 8, "join's dgate")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_gate_of_minus_infinity_is_what_the_formula_says(dtype):
+    """-Inf times a logistic of 0: NaN, in that element alone, whichever storage type."""
+    c = 8
+    one = torch.ones(1, c, dtype=dtype, device=DEV)
+    v = one.clone()
+    v[0, 3] = -math.inf
+    taps = torch.tensor([0.0, 1.0], device=DEV).expand(c, 2).contiguous()
+    k = dict(x=one, dt=one, A=-torch.ones(c, 1, device=DEV), B=torch.zeros(1, 1, 1, dtype=dtype, device=DEV),
+             C=torch.ones(1, 1, 1, dtype=dtype, device=DEV), D=torch.ones(c, device=DEV), z=v, dt_bias=None)
+    for y in (S.gspn_causal_conv_fwd(v, taps), run_fwd(k), S.gspn_block_join_fwd(one, v)[0]):
+        assert torch.isnan(y[0, 3]) and torch.isfinite(y[0, torch.arange(c) != 3]).all()
