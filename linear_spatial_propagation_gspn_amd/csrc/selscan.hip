@@ -53,7 +53,7 @@ __global__ __launch_bounds__(64) void selscan_kernel(const SelK p) {
     ld_states<NP, kScalar>(p.A + static_cast<int64_t>(c) * N, N, A2);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-        A2[i] *= kLog2E;
+        A2[i] = decay_rate(A2[i]);
         h[i] = 0.0f;
     }
     const int64_t plane = static_cast<int64_t>(p.channels);
@@ -324,7 +324,7 @@ __global__ __launch_bounds__(256) void selscan_quad_kernel(const SelK p) {
     };
     if (begin < end) load(begin);
 #pragma unroll
-    for (int i = 0; i < SPL; ++i) A2[i] = n0 + i < p.n ? A2[i] * kLog2E : 0.0f;
+    for (int i = 0; i < SPL; ++i) A2[i] = n0 + i < p.n ? decay_rate(A2[i]) : 0.0f;
     int buf = 0;
     for (int base = begin; base < end; base += kRows, buf ^= 1) {
 #pragma unroll
@@ -443,7 +443,7 @@ __global__ __launch_bounds__(256) void selscan_join_kernel(const SelK p) {
     const int64_t step = static_cast<int64_t>(p.channels) * p.n;
     float* const q = p.carry + base * step + e;
     const float* const sd = p.sums + base * p.channels + c;
-    const float A2 = p.A[static_cast<int64_t>(c) * p.n + i] * (0.5f * kLog2E);
+    const float A2 = 0.5f * decay_rate(p.A[static_cast<int64_t>(c) * p.n + i]);
     float h = q[(count - 1) * step];  // the state before the sequence
     constexpr int U = 16;
     for (int k0 = 0; k0 < count; k0 += U) {
@@ -530,7 +530,7 @@ __global__ __launch_bounds__(256) void selscan_step_kernel(const SelK p) {
     float y = 0.0f;
 #pragma unroll
     for (int i = 0; i < SPL; ++i) {
-        h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * (A2[i] * kLog2E)), h[i], u * b[i]);
+        h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * decay_rate(A2[i])), h[i], u * b[i]);
         y = __builtin_fmaf(cv[i], h[i], y);
     }
     y = quad_sum<SPLIT>(y);

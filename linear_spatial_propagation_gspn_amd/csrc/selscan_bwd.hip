@@ -62,7 +62,7 @@ __global__ __launch_bounds__(64) void selscan_bwd_local_kernel(const SelK p) {
     ld_states<NP, kScalar>(p.A + static_cast<int64_t>(c) * N, N, A2);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-        A2[i] *= kLog2E;
+        A2[i] = decay_rate(A2[i]);
         ag[i] = 0.0f;
     }
     const float bias = p.bias ? p.bias[c] : 0.0f;
@@ -164,7 +164,7 @@ __global__ __launch_bounds__(256) void selscan_bwd_join_kernel(const SelK p) {
     const int64_t step = static_cast<int64_t>(p.channels) * p.n;
     float* const q = p.carry + base * step + e;
     const float* const sd = p.sums + base * p.channels + c;
-    const float A2 = p.A[static_cast<int64_t>(c) * p.n + i] * (0.5f * kLog2E);
+    const float A2 = 0.5f * decay_rate(p.A[static_cast<int64_t>(c) * p.n + i]);
     float g = 0.0f;
     constexpr int U = 16;
     for (int k0 = count - 1; k0 >= 0; k0 -= U) {
@@ -232,7 +232,7 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
             for (int s = 0; s < SPL; ++s) ag[s] = p.carry[(id * p.n + state(s)) * p.channels + c];
 #pragma unroll
             for (int s = 0; s < SPL; ++s) {
-                A2[s] = n0 + s < p.n ? A2[s] * kLog2E : 0.0f;
+                A2[s] = n0 + s < p.n ? decay_rate(A2[s]) : 0.0f;
                 ag[s] = n0 + s < p.n ? ag[s] : 0.0f;
             }
         } else {
@@ -251,7 +251,7 @@ __global__ __launch_bounds__(256, 2) void selscan_bwd_kernel(const SelK p) {
                 }
             }
 #pragma unroll
-            for (int s = 0; s < SPL; ++s) A2[s] = n0 + s < p.n ? A2[s] * kLog2E : 0.0f;
+            for (int s = 0; s < SPL; ++s) A2[s] = n0 + s < p.n ? decay_rate(A2[s]) : 0.0f;
 #pragma unroll
             for (int j = U - 1; j >= 0; --j)  // behind the last: nothing yet, and nothing added
 #pragma unroll

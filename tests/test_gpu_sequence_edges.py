@@ -135,3 +135,57 @@ def test_a_gate_of_minus_infinity_is_what_the_formula_says(dtype):
              C=torch.ones(1, 1, 1, dtype=dtype, device=DEV), D=torch.ones(c, device=DEV), z=v, dt_bias=None)
     for y in (S.gspn_causal_conv_fwd(v, taps), run_fwd(k), S.gspn_block_join_fwd(one, v)[0]):
         assert torch.isnan(y[0, 3]) and torch.isfinite(y[0, torch.arange(c) != 3]).all()
+
+
+# ------------------------------------------------------------------------------- decays at the end of the range
+
+FORGET = [-torch.finfo(F32).max, -3e38, -2.4e38, -1e30]
+
+
+@pytest.mark.parametrize("n", [16, 8, 5, 1])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("lengths", [[37, 1, 0, 16, 17, 2], [150, 1, 16, 0, 65], [18, 18, 18], [5]])
+def test_scan_with_decay_rates_at_the_end_of_the_range(lengths, dtype, n):
+    """A so low that A log2 e passes fp32: a step of the scan forgets everything (e^(d A) = 0), a skipped row (d = 0)
+    nothing, and the rows that a kernel computes past a sequence's end are not seen.  A state is then that of the last
+    row that was not skipped: a product of three factors, no decay's roundings in it."""
+    g = gen(n + len(lengths))
+    c, rows = len(FORGET), sum(lengths)
+    seqs = R.spans(lengths)
+    k = scan_case(g, rows, c, 1, n, dtype)
+    k["A"] = torch.tensor(FORGET)[:, None].expand(c, n).contiguous()
+    gy = rnd(g, rows, c, dtype=dtype)
+    equal = len(set(lengths)) == 1
+    kw = {"nseq": len(lengths)} if equal else {"cu": cu_of(lengths)}
+
+    def count(args):
+        return R.scan_roundings(args[0], args[1], torch.zeros_like(args[2]), args[7], True, seqs)
+
+    def lowest(o):  # -Inf forgets no more than the lowest number does
+        o = dict(o, A=o["A"].clone())
+        o["A"][0] = -math.inf
+        return o
+
+    args = ref_args(k)
+    ref, mag = R.scan_backward(*args, True, seqs, wide(gy))
+    got, low = run_bwd(on_gpu(k), dev(gy), **kw), run_bwd(lowest(on_gpu(k)), dev(gy), **kw)
+    both = 2 * (count(args) + 2 * gate_count(k)) + 16
+    for name, more in {"dx": n, "ddt": n, "dz": n, "dB": c, "dC": c, "dA": rows, "dD": rows, "dbias": rows + n}.items():
+        check(got[name], ref[name], mag[name], both + more, name)
+        assert torch.equal(got[name], low[name]), name
+
+    k["dt"][rows // 2:rows // 2 + 9:2] = -math.inf
+    k["dt"][rows - 1] = -math.inf
+    args = ref_args(k)
+    ry, _, last, sy, _ = R.scan(*args, True, seqs)
+    state, other = (torch.zeros(len(lengths), c, n, device=DEV) for _ in range(2))
+    out = run_fwd(on_gpu(k), state=state, **kw)
+    check(out, ry, sy, count(args) + gate_count(k), "out")
+    check(state, torch.stack(last), torch.stack(last).abs(), count(args), "state")
+    assert torch.equal(run_fwd(lowest(on_gpu(k)), state=other, **kw), out) and torch.equal(other, state)
+
+    h0 = torch.randn(rows, c, n, generator=g)  # and a token that continues a state, or skips
+    pool, o = dev(h0.clone()), lowest(on_gpu(k))
+    S.gspn_selective_scan_step(o["x"], o["dt"], o["A"], o["B"], o["C"], pool, o["D"], o["z"], o["dt_bias"])
+    last = R.scan(*args, True, R.spans([1] * rows), list(wide(h0)))[2]
+    check(pool, torch.stack(last), torch.stack(last).abs(), count(args), "state after a token")
