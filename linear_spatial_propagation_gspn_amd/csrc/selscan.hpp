@@ -106,12 +106,15 @@ __device__ __forceinline__ void ld_states(const float* p, int n, float (&v)[NP])
 }
 
 // A state (or gradient) h taken over a chunk whose decay is 2^(2 half), plus
-// the chunk's own.  In two halves, capped where every h but zero overflows: a
-// decay past the range of fp32 (A > 0) leaves zero at zero and gives a small h
-// what the rows one by one give it.
+// the chunk's own.  In two halves up to 2^254, where every normal h overflows,
+// and a third factor beyond, for a subnormal one, up to 2^381, where that does
+// too: a decay past the range of fp32 (A > 0) leaves zero at zero and gives a
+// small h what the rows one by one give it.
 __device__ __forceinline__ float carry_over(float half, float h, float own) {
     const float e = __builtin_amdgcn_exp2f(half < 127.0f ? half : 127.0f);
-    return __builtin_fmaf(h * e, e, own);
+    const float over = __builtin_fmaf(2.0f, half, -254.0f);
+    const float f = __builtin_amdgcn_exp2f(__builtin_fminf(__builtin_fmaxf(over, 0.0f), 127.0f));
+    return __builtin_fmaf(h * e * f, e, own);
 }
 
 __device__ __forceinline__ float lane_value(float v, int lane) {

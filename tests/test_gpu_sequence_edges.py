@@ -189,3 +189,27 @@ def test_scan_with_decay_rates_at_the_end_of_the_range(lengths, dtype, n):
     S.gspn_selective_scan_step(o["x"], o["dt"], o["A"], o["B"], o["C"], pool, o["D"], o["z"], o["dt_bias"])
     last = R.scan(*args, True, R.spans([1] * rows), list(wide(h0)))[2]
     check(pool, torch.stack(last), torch.stack(last).abs(), count(args), "state after a token")
+
+
+@pytest.mark.parametrize("n", [16, 5, 1])
+@pytest.mark.parametrize("lengths", [[240], [48], [64]])  # joined by its own launch; by its chunks
+def test_scan_growth_of_a_subnormal_state(lengths, n):
+    """16 rows that multiply by e^192 lie past fp32 also for a state below its normal numbers: the rows one by one
+    overflow, and so do the chunks.  Forward with the state 1.2e-40 before those rows; the same against the row order."""
+    rows, = lengths
+    c = 8
+    k = dict(x=torch.zeros(rows, c), dt=torch.full((rows, c), 0.01), A=torch.ones(c, n), B=torch.ones(rows, 1, n),
+             C=torch.ones(rows, 1, n), D=None, z=None, dt_bias=None)
+    k["dt"][15], k["dt"][16:32] = 12.0, 12.0
+    k["x"][15, ::2] = 1e-41
+    cu = cu_of(lengths + [1] * 40, 0)  # packed with tokens, so that it is cut
+    pad = lambda t: torch.cat([t, torch.zeros(40, *t.shape[1:])])  # noqa: E731
+    o = on_gpu({m: pad(t) if t is not None and t.shape[0] == rows else t for m, t in k.items()})
+    state = torch.zeros(41, c, n, device=DEV)
+    out = run_fwd(o, softplus=False, cu=cu, state=state)
+    assert (state[0, ::2] == math.inf).all() and (state[0, 1::2] == 0).all()
+    assert (out[31:rows, ::2] == math.inf).all() and (out[:rows, 1::2] == 0).all()
+    gy = torch.zeros(rows + 40, c, device=DEV)
+    gy[32, ::2] = 1e-40  # dL/dh before row 16: e^192 times that
+    got = run_bwd(o, gy, softplus=False, cu=cu)
+    assert (got["dx"][:16, ::2] == math.inf).all() and (got["dx"][:32, 1::2] == 0).all()
