@@ -212,7 +212,7 @@ __global__ __launch_bounds__(64) void selscan_kernel(const SelK p) {
 #pragma unroll
         for (int i = 0; i < NP; ++i)
             if (i < N) p.carry[(id * N + i) * plane + c] = h[i];
-        p.sums[id * plane + c] = sum;
+        p.sums[id * plane + c] = step_sum(sum);
     } else if (slot >= 0 && ck.k + 1 == ck.count) {
 #pragma unroll
         for (int i = 0; i < NP; ++i) {

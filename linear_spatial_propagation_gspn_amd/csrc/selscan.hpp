@@ -105,6 +105,15 @@ __device__ __forceinline__ void ld_states(const float* p, int n, float (&v)[NP])
     }
 }
 
+// A chunk's sum of d, for its whole decay.  Steps that add up to Inf are taken as
+// the most that fp32 holds, so that A = 0 still leaves a state as it is.  (A step
+// that is Inf or NaN itself has made a NaN of the chunk's own state, or a zero of
+// its decay, either way.)
+__device__ __forceinline__ float step_sum(float sum) {
+    const float most = 3.402823466e38f;
+    return __builtin_fmaxf(__builtin_fminf(sum, most), -most);
+}
+
 // A state (or gradient) h taken over a chunk whose decay is 2^(2 half), plus
 // the chunk's own.  In two halves up to 2^254, where every normal h overflows,
 // and a third factor beyond, for a subnormal one, up to 2^381, where that does

@@ -144,7 +144,7 @@ __global__ __launch_bounds__(64) void selscan_bwd_local_kernel(const SelK p) {
 #pragma unroll
     for (int i = 0; i < NP; ++i)
         if (i < N) p.carry[(id * N + i) * p.channels + c] = ag[i];
-    p.sums[id * p.channels + c] = sum;
+    p.sums[id * p.channels + c] = step_sum(sum);
 }
 
 // The join of long sequences, against the row order: carry[k] := dL/dh after

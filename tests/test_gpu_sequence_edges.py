@@ -213,3 +213,29 @@ def test_scan_growth_of_a_subnormal_state(lengths, n):
     gy[32, ::2] = 1e-40  # dL/dh before row 16: e^192 times that
     got = run_bwd(o, gy, softplus=False, cu=cu)
     assert (got["dx"][:16, ::2] == math.inf).all() and (got["dx"][:32, 1::2] == 0).all()
+
+
+@pytest.mark.parametrize("n", [16, 5, 1])
+@pytest.mark.parametrize("lengths", [[240], [48], [64]])
+def test_scan_steps_whose_sum_passes_the_range(lengths, n):
+    """Steps of 3e38 with A = 0 leave a state as it is, row by row and therefore chunk by chunk, whose sum of steps is
+    past fp32; with A < 0 they forget it.  x is zero in those rows, so that nothing else overflows."""
+    rows, = lengths
+    c = 8
+    k = dict(x=torch.zeros(rows, c), dt=torch.full((rows, c), 3e38), A=torch.zeros(c, n), B=torch.ones(rows, 1, n),
+             C=torch.ones(rows, 1, n), D=None, z=None, dt_bias=None)
+    k["dt"][0], k["x"][0] = 1.0, 2.0
+    k["A"][1::2] = -1.0
+    pad = lambda t: torch.cat([t, torch.zeros(40, *t.shape[1:])])  # noqa: E731
+    o = on_gpu({m: pad(t) if t is not None and t.shape[0] == rows else t for m, t in k.items()})
+    cu = cu_of(lengths + [1] * 40, 0)
+    state = torch.zeros(41, c, n, device=DEV)
+    out = run_fwd(o, softplus=False, cu=cu, state=state)
+    assert (state[0, ::2] == 2).all() and (state[0, 1::2] == 0).all()
+    assert (out[:rows, ::2] == 2 * n).all() and (out[1:rows, 1::2] == 0).all()
+    gy = torch.zeros(rows + 40, c, device=DEV)
+    gy[rows - 1] = 1.0
+    got = run_bwd(o, gy, softplus=False, cu=cu)
+    # row 0: d = 1, x = 2, and dL/dh = C = 1 in the channels that forget nothing
+    assert (got["dx"][0, ::2] == n).all() and (got["dx"][0, 1::2] == 0).all()
+    assert (got["dB"][0] == 2 * c // 2).all()
