@@ -1,10 +1,12 @@
 """The sequence operators on the GPU, held to bounds that follow each element's own errors (sequence_bounds.py): the
-plans that larger calls take, sums over many blocks of channels, norms whose energy sits in a row's last columns."""
+plans that larger calls take, sums over many blocks of channels, norms whose energy sits in a row's last columns, and
+gradients against differences along directions in which they are large."""
 import pytest
 import torch
 
 import sequence_bounds as Q
 import sequence_cases as P
+import sequence_differences as D
 import sequence_reference as R
 from linear_spatial_propagation_gspn_amd import sequence as S
 from test_gpu_sequence import (BF16, DEV, F32, _gpu, _say, check, cu_of, dev, gen, leaves, on_gpu, ref_args, rnd,  # noqa: F401
@@ -91,3 +93,15 @@ def test_join_with_its_energy_in_the_last_columns(c, dtype, rt, tail):
     for name in ("dgate", "dscale", "dpost"):
         check(got[name], ref[name], mag[name], back + norm + rows, name)
     check(got["dh"], ref["dh"], mag["dh"], back + do, "dh")
+
+
+@pytest.mark.parametrize("op", D.OPS)
+def test_gradients_along_their_own_direction(op):
+    g = gen(61)
+    ts, f, ref = D.case(op, g)
+    gy = rnd(g, *ts[0].shape)
+    td = [dev(t) for t in ts]
+    ls = leaves(*td)
+    grads = torch.autograd.grad(f(S, *ls), ls, dev(gy))
+    for i in range(len(ts)):
+        D.compare(ts, gy, i, grads[i].cpu(), lambda *a: f(S, *map(dev, a)).cpu(), ref)

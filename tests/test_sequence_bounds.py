@@ -5,6 +5,7 @@ import torch
 
 import sequence_bounds as Q
 import sequence_cases as P
+import sequence_differences as D
 import sequence_reference as R
 from test_sequence_abi import BF16 as BF16CODE, F32 as F32CODE, chk, lib, replay  # noqa: F401
 
@@ -82,3 +83,19 @@ def test_cases_take_the_plans_they_are_for(chk, lib, case):  # noqa: F811
         assert chunk(ids) == bwd
     else:
         assert chunk(ids) >= max(lengths) > 8  # one chunk a sequence, of several tiles
+
+
+@pytest.mark.parametrize("op", D.OPS)
+def test_differences_accept_the_gradient_and_reject_others(op):
+    """The definition in fp32, with its own gradient, passes; zero, negated and doubled gradients are rejected by the
+    comparison itself."""
+    g = torch.Generator().manual_seed(61)
+    ts, _, ref = D.case(op, g)
+    gy = rnd(g, *ts[0].shape)
+    for i, t in enumerate(ts):
+        leaf = t.clone().requires_grad_()
+        grad, = torch.autograd.grad(ref(*ts[:i], leaf, *ts[i + 1:])[0], leaf, gy)
+        D.compare(ts, gy, i, grad, lambda *a: ref(*a)[0], ref)
+        for wrong in (0 * grad, -grad, 2 * grad):
+            with pytest.raises(AssertionError):
+                D.compare(ts, gy, i, wrong, lambda *a: ref(*a)[0], ref)
