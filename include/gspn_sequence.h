@@ -129,8 +129,8 @@ gspn_status gspn_causal_conv_bwd(const gspn_conv_args* args, int dtype, void* st
  *   h_t[n] = exp(d_t A[c][n]) h_{t-1}[n] + d_t x_t B_t[g][n]
  *   y_t = sum_n C_t[g][n] h_t[n] + D[c] x_t;   out_t = y_t silu(z_t)
  * from h = 0 or the resumed pool entry.  dt = -Inf
- * skips a row whose x and B are finite (softplus), whatever A: A log2 e past
- * the range of fp32, -Inf too, is taken as the end of the range.
+ * skips a row whose x and B are finite (softplus), whatever A <= 0: A log2 e
+ * below the range of fp32, -Inf too, is taken as the range's lower end.
  *   x, dt, z, out  [rows][channels]; z NULL: no gate; D, dt_bias NULL: 0
  *   B, C           [rows][groups][n], row strides ldb, ldc (groups and n
  *                  contiguous); groups divides channels

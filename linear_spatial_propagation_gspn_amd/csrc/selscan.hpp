@@ -49,13 +49,13 @@ __device__ __forceinline__ float softplus_f(float v, float* slope = nullptr) {
     return (v > 0.0f ? v : 0.0f) + l;
 }
 
-// A in units of log2, so that a row's decay is 2^(d A2).  Where that passes
-// the range of fp32 the end of the range stands for it: it forgets (or grows)
-// as fast, and a step of zero, a skipped row's or one past a chunk's end,
-// leaves a state as it is instead of making 0 x Inf of it.
+// A in units of log2, so that a row's decay is 2^(d A2).  Where that falls
+// below the range of fp32 the range's lower end stands for it: it forgets as
+// fast, and a step of zero, a skipped row's or one past a chunk's end, leaves a
+// state as it is instead of making 0 x Inf of it.
 __device__ __forceinline__ float decay_rate(float A) {
-    const float v = A * kLog2E, most = 3.402823466e38f;
-    return v > most ? most : v < -most ? -most : v;
+    const float v = A * kLog2E, least = -3.402823466e38f;
+    return v < least ? least : v;
 }
 
 // A wave's B_t and C_t: N values each, the same for every lane.

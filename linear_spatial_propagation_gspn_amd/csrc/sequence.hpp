@@ -169,7 +169,8 @@ __device__ __forceinline__ void st_pack(T* p, const float (&f)[V]) {
 template <typename T>
 __device__ __forceinline__ float gate_sigmoid(float v) {
     if constexpr (sizeof(T) == 4)
-        return sigmoid(v) * __builtin_amdgcn_exp2f(__builtin_fminf(v + 87.0f, 0.0f) * 1.44269504088896340736f);
+        return sigmoid(v) * __builtin_amdgcn_exp2f(
+                                __builtin_fminf(__builtin_fmaf(v, 1.44269504088896340736f, 125.514468f), 0.0f));
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504088896340736f));
 }
 
