@@ -133,7 +133,9 @@ gspn_status gspn_causal_conv_bwd(const gspn_conv_args* args, int dtype, void* st
  * below the range of fp32, -Inf too, is taken as the range's lower end.
  *   x, dt, z, out  [rows][channels]; z NULL: no gate; D, dt_bias NULL: 0
  *   B, C           [rows][groups][n], row strides ldb, ldc (groups and n
- *                  contiguous); groups divides channels
+ *                  contiguous); groups divides channels; groups times the
+ *                  64-channel blocks of a group at most 65535 (else
+ *                  GSPN_ERR_UNSUPPORTED)
  *   A              [channels][n], n 1 to 16 (else GSPN_ERR_UNSUPPORTED)
  *   state          pool [nslots][channels][n] fp32 or NULL: receives h after
  *                  the last row (an empty sequence as in the convolution)
@@ -204,7 +206,8 @@ gspn_status gspn_selective_scan_bwd(const gspn_selscan_args* args, int dtype, vo
  *   normed = joined / rms(joined) * pre     (pre given; of joined as stored)
  * h, gate, normed [rows][c] in the storage type; post, scale, pre [c] fp32 or
  * NULL; residual and joined in residual_dtype (the storage type, or GSPN_F32
- * for a wide residual stream; without a residual, the storage type).
+ * for a wide residual stream; without a residual, the storage type).  A norm's
+ * sum of squares is fp32: rows past 1e19 lose theirs to Inf.
  * c <= 16384.  gspn_block_join_bwd: from joined (read where pre is given),
  * gjoined (NULL: zero) and gnormed (where pre is given) writes dh, dgate,
  * dresidual (where the input is given and the gradient wanted), dpost,

@@ -152,7 +152,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_fwd_kernel(const ConvK p) {
 
 // One token per sequence: the entry's rows and x in, one row out, the entry
 // shifted by one row.  Bound by latency: 64 sequences of 4096 channels (4 MB)
-// take 3.4 us.
+// take 3.7 us.
 template <typename T, int K, int V>
 __global__ __launch_bounds__(kConvThreads) void conv_step_kernel(const ConvK p) {
     const int s = blockIdx.x;

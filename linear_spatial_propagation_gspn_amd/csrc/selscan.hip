@@ -16,7 +16,7 @@
 // sequence is one chunk, only the last pass runs.
 //
 // Measured (bf16, 16 states, gated): one sequence of 65536 rows and 2048
-// channels 376 + 67 + 517 us by its kernels, 840 in a row of calls.  The states'
+// channels 385 + 70 + 533 us by its kernels, 840 in a row of calls.  The states'
 // 5 and 4 instructions alone are 24 + 20 cycles a wave (an exponential counts
 // 8), 600 us at 2.4 GHz; the rest is what is per row (step size, gate, loads)
 // and the join; x, dt, z, out twice over would be 260 us of memory traffic.
@@ -236,8 +236,9 @@ __global__ __launch_bounds__(64) void selscan_kernel(const SelK p) {
 // time, and the next 16 rows' loads are in flight meanwhile.
 // A wave of 16 channels (16 states) takes 284 cycles a row alone on its SIMD and
 // 194 among others: it takes batches that fill the GPU with whole sequences,
-// and short ones, where it is one launch (57 rows of 1152 channels, fp32: 11.6
-// us, a latency of 200 ns a row).
+// and short ones, where it is one launch.  Alone, a short one is bound by latency:
+// 1 to 16 rows of 1152 channels, fp32, take 5.9 us, 57 11.7, 113 19.3 and 160 23.2,
+// which is 4 us of launch, slot and first loads and 120 ns a row.
 template <typename T, int NP, bool kGate>
 __global__ __launch_bounds__(256) void selscan_quad_kernel(const SelK p) {
     constexpr int SPL = NP / 4;
@@ -468,9 +469,10 @@ __global__ __launch_bounds__(256) void selscan_join_kernel(const SelK p) {
 
 // One token per sequence.  SPLIT lanes share a channel, each with NP / SPLIT
 // neighbouring states, so that the pool is read and written in whole cache
-// lines; y is summed over the SPLIT lanes.  Bound by the pool's bytes: 64
-// sequences of 4096 channels with 16 states 9.9 us, 3.6 TB/s of 36 MB, most of
-// it the latency of one load, one exponential and one store.
+// lines; y is summed over the SPLIT lanes.  Bound by the pool's bytes behind a
+// latency: 64 sequences of 4096 channels with 16 states 10 us, 3.6 TB/s of 36 MB.
+// Three loads follow one another there: the slot, the slots before it, and the
+// entry, whose address is the slot's; then an exponential and the store.
 template <typename T, int NP, int SPLIT, bool kVec>
 __global__ __launch_bounds__(256) void selscan_step_kernel(const SelK p) {
     constexpr int SPL = NP / SPLIT;
@@ -607,14 +609,20 @@ void run_step(const SelK& k, bool vec, hipStream_t stream) {
 // How the forward is cut: kWholeQuad, or rows per chunk (a power of two; one
 // chunk that holds the longest sequence: whole sequences, one lane a channel).
 //
-// The three ways by their measured cycles: whole sequences with four lanes a
-// channel take longest x (194 R + 90) where R counts their waves over the
-// SIMDs, one lane a channel longest x (600 R + 300), chunks 980 for each wave
-// and row spread over the SIMDs and some 48000 for three launches.  Measured
-// (16 states, bf16, four lanes against chunks): 57 rows of 1152 channels 11.1
-// against 18.0 us, 512 rows 63.5 against 24.1; 4 x 1024 rows of 4096 channels
-// 122 and 125, 8 x 1024 of 2304 176 against 141, 16 x 1024 of 4096 324 against
-// 431.  Packed sequences are taken as one, the longest they can hold.
+// The three ways by their measured cycles at 16 states, taken for any number of
+// them: whole sequences with four lanes a channel take longest x (194 R + 90)
+// where R counts their waves over the SIMDs, one lane a channel longest x (600 R
+// + 300), chunks 980 for each wave and row spread over the SIMDs and some 48000
+// for three launches.  Packed sequences are taken as one, the longest they can
+// hold.  Measured with pools, four lanes against chunks (us; 16 states): 57 fp32
+// rows of 1152 channels 12.2 and 20.4, 113 rows 20.0 and 22.0, 160 24.1 and 22.7,
+// 512 66 and 27; bf16, 8 x 1024 rows of 2304 185 and 144, 16 x 1024 of 4096 368 and
+// 426, 32 x 1024 of 2304 425 and 471; one lane, 64 x 64 of 4096 73 (four 85, chunks
+// 117).  Near a crossing it errs: 4 x 1024 of 4096 runs whole at 144 where chunks
+// take 126.  With fewer states chunks gain more than the costs say: that batch with
+// four states runs whole at 103 against 72 (8 x 512 of 2304 is cut, 53 against 63),
+// and 16 x 1024 of 4096 with one state whole at 370 against 239 (8 and 16 maps of
+// 196 rows of 768 are cut, 18 against 48 and 23 against 55).
 //
 // Chunks of L rows, 16 at least, are as long as their cost is least: the passes'
 // uneven end, which grows with L (some 2 (220 + 50 n) L cycles), against the

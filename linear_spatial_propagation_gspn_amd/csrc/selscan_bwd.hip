@@ -18,9 +18,9 @@
 // fixed order.  The sums over rows (dA, dD, ddt_bias) stay in registers per
 // chunk and are joined the same way.
 //
-// Bound by the vector ALU (79% of the cycles issue one of its instructions, at
-// two waves a SIMD): 8 x 1024 rows of 2304 channels, 16 states, bf16, gated, take
-// 304 us here, 78 + 10 for the chunks' own gradients and their join, 16 for the
+// Bound by the vector ALU (busy in 87% of the cycles, by its counter, at two
+// waves a SIMD): 8 x 1024 rows of 2304 channels, 16 states, bf16, gated, take
+// 300 us here, 79 + 11 for the chunks' own gradients and their join, 16 for the
 // sums; the bytes alone would be 58.
 #include "selscan.hpp"
 

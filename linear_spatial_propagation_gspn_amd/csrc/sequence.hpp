@@ -283,8 +283,10 @@ int64_t join_bwd_parts(int64_t rows, int64_t c);
 namespace check {
 // Host replay of row-strided accesses: every row's first and last element of
 // [rows][c] (elements of es bytes, rows ld apart) must lie in one buffer.
-// Kernels guard columns beyond c and take vectors only where c, ld and the
-// pointer are whole vectors, so a row's ends bound its accesses.
+// A row's ends bound its accesses: kernels guard columns beyond c, and take a
+// vector where it lies wholly within the row, either because c is whole vectors
+// or, in the block join, because a row's last vector starts at c - V (c >= V)
+// and its store goes column by column.
 inline void replay_rows(const char* kn, const char* what, const void* p, int64_t rows, int64_t ld, int64_t c,
                         int64_t es) {
     if (!p || rows < 1 || c < 1) return;
