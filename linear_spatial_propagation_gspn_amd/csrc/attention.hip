@@ -1,0 +1,223 @@
+// attention.hip -- softmax attention over whole prompts, with grouped heads,
+// packed sequences and prompts that continue a cache entry.
+#include "attention.hpp"
+
+#include <cmath>
+
+namespace gspn {
+namespace {
+
+template <typename T, int D>
+__global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnK a) {
+    using Tl = Tile<T, D>;
+    constexpr int BN = kTileRows<T>;
+    __shared__ __attribute__((aligned(16))) char lds[2][2][BN * Tl::kRow];
+    const AttnItem w = find_item(a.seq, a.heads, a.causal != 0, kAttnShift);
+    if (w.c.seq < 0 || w.c.r0 >= w.c.r1) return;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int rows = w.c.end - w.c.begin;
+    const Keys keys = find_keys<T>(a, w.c.seq, w.c.begin, rows, w.head / a.group);
+    const int off = keys.count - rows;  // row i sees i + off + 1 keys where later ones are hidden
+
+    const int wave0 = w.c.r0 - w.c.begin + __builtin_amdgcn_readfirstlane(tid >> 6) * 32;  // the wave's first row
+    const int row = wave0 + (lane & 31);
+    const bool mine = row < rows;
+    const int64_t at = static_cast<int64_t>(w.c.begin) + (mine ? row : 0);
+    T* const out = static_cast<T*>(a.out) + at * a.ldo + static_cast<int64_t>(w.head) * a.d;
+    float* const lse = a.lse ? a.lse + static_cast<int64_t>(w.head) * a.seq.rows + at : nullptr;
+    if (keys.state == kBadSlot) {
+        f32x16 o[D / 32];
+        for (int b = 0; b < D / 32; ++b)
+            for (int r = 0; r < 16; ++r) o[b][r] = NAN;
+        if (mine) {
+            st_result<T, D>(out, o, 1.0f, a.d);
+            if (lse && lane < 32) *lse = NAN;
+        }
+        return;
+    }
+
+    Quad q[Tl::kSteps];
+    ld_rows<T, D>(static_cast<const T*>(a.q) + at * a.ldq + static_cast<int64_t>(w.head) * a.d, mine, a.d, a.flip, q);
+    const auto seen = [&](int r) {  // keys that row r sees
+        const int n = a.causal ? r + off + 1 : keys.count;
+        return n < 0 ? 0 : n < keys.count ? n : keys.count;
+    };
+    const int last = (w.c.r1 < w.c.end ? w.c.r1 : w.c.end) - 1 - w.c.begin;
+    const int tiles = (seen(last) + BN - 1) / BN;
+    const int wave_last = wave0 + 31 < rows ? wave0 + 31 : rows - 1;
+    const int wave_keys = wave0 < rows ? seen(wave_last) : 0;  // no row of the wave sees more
+    const int wave_all = wave0 < rows ? seen(wave0) : 0;       // every one sees these
+    const int my_keys = mine ? seen(row) : 0;
+
+    Softmax<D> sm;
+    Stage<T, D, BN, kAttnThreads> sk, sv;
+    const T* const kp = static_cast<const T*>(keys.k);
+    const T* const vp = static_cast<const T*>(keys.v);
+    if (tiles > 0) {
+        sk.load(tid, kp, keys.ldk, 0, keys.count - 1, a.d);
+        sv.load(tid, vp, keys.ldv, 0, keys.count - 1, a.d);
+        sk.store(tid, lds[0][0]);
+        sv.store(tid, lds[0][1]);
+    }
+    __syncthreads();
+    for (int t = 0; t < tiles; ++t) {
+        const bool more = t + 1 < tiles;
+        if (more) {
+            sk.load(tid, kp, keys.ldk, (t + 1) * BN, keys.count - 1, a.d);
+            sv.load(tid, vp, keys.ldv, (t + 1) * BN, keys.count - 1, a.d);
+        }
+        const int key0 = t * BN;
+        if (key0 < wave_keys) {
+            const char* const kt = lds[t & 1][0];
+            const char* const vt = lds[t & 1][1];
+            f32x16 s[BN / 32];
+#pragma unroll
+            for (int n = 0; n < BN / 32; ++n) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[n][r] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < Tl::kSteps; ++i) s[n] = mma<T>(Tl::rows(kt, 32 * n, i), q[i], s[n]);
+            }
+            if (key0 + BN > wave_all) {
+#pragma unroll
+                for (int n = 0; n < BN / 32; ++n)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (key0 + 32 * n + result_row(r) >= my_keys) s[n][r] = -INFINITY;
+            }
+            sm.template tile<BN / 32>(s, a.scale_log2);
+#pragma unroll
+            for (int n = 0; n < BN / 32; ++n) {
+                const Factor<T> p(s[n]);
+#pragma unroll
+                for (int b = 0; b < D / 32; ++b) sm.o[b] = Tl::columns(vt, 32 * n, b, p.p, sm.o[b]);
+            }
+        }
+        if (more) {
+            sk.store(tid, lds[(t + 1) & 1][0]);
+            sv.store(tid, lds[(t + 1) & 1][1]);
+        }
+        __syncthreads();
+    }
+    const float l = both_sum(sm.l);
+    if (mine) {
+        st_result<T, D>(out, sm.o, my_keys > 0 ? 1.0f / l : 0.0f, a.d);
+        if (lse && lane < 32)
+            *lse = my_keys > 0 ? (sm.m * a.scale_log2 + __builtin_amdgcn_logf(l)) * 0.69314718055994530942f : -INFINITY;
+    }
+}
+
+// New rows of keys and values into their entries.
+template <typename T>
+__global__ __launch_bounds__(kAttnThreads) void attn_append_kernel(const AttnK a) {
+    const Chunk c = find_chunk(a.seq, blockIdx.x, kAppendShift);
+    if (c.seq < 0 || c.r0 >= c.r1) return;
+    const Keys keys = find_keys<T>(a, c.seq, c.begin, c.end - c.begin, 0);
+    if (keys.state != 0) return;
+    constexpr int kE = 16 / sizeof(T);
+    const int width = a.kv_heads * a.d;
+    const int chunks = (width + kE - 1) / kE;
+    const int64_t at = keys.count - (c.end - c.begin) + (c.r0 - c.begin);
+    for (int i = threadIdx.x; i < (c.r1 - c.r0) * chunks; i += kAttnThreads) {
+        const int r = i / chunks, e = (i - r * chunks) * kE;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            const T* const from = static_cast<const T*>(v ? a.v : a.k) + (c.r0 + r) * (v ? a.ldv : a.ldk) + e;
+            T* const to = const_cast<T*>(static_cast<const T*>(v ? keys.v : keys.k)) + (at + r) * width + e;
+            if (e + kE <= width) {
+                Quad x;
+                __builtin_memcpy(&x, from, 16);
+                __builtin_memcpy(to, &x, 16);
+            } else {
+                for (int j = 0; j < width - e; ++j) to[j] = from[j];
+            }
+        }
+    }
+}
+
+void replay_fwd(const char* kn, const gspn_attn_args& a, int64_t es) {
+    (void)kn;
+    (void)a;
+    (void)es;
+    GSPN_REPLAY_ROWS(kn, "q", a.q, a.seq.rows, a.ldq, a.heads * a.d, es);
+    GSPN_REPLAY_ROWS(kn, "k", a.k, a.kv_rows, a.ldk, a.kv_heads * a.d, es);
+    GSPN_REPLAY_ROWS(kn, "v", a.v, a.kv_rows, a.ldv, a.kv_heads * a.d, es);
+    GSPN_REPLAY_ROWS(kn, "out", a.out, a.seq.rows, a.ldo, a.heads * a.d, es);
+    GSPN_REPLAY_ROWS(kn, "lse", a.lse, a.heads, a.seq.rows, a.seq.rows, 4);
+    if (a.k_pool) {
+        GSPN_REPLAY_ROWS(kn, "k_pool", a.k_pool, a.seq.nslots * a.capacity, a.kv_heads * a.d, a.kv_heads * a.d, es);
+        GSPN_REPLAY_ROWS(kn, "v_pool", a.v_pool, a.seq.nslots * a.capacity, a.kv_heads * a.d, a.kv_heads * a.d, es);
+        GSPN_REPLAY_ROWS(kn, "held", a.held, 1, a.seq.nseq, a.seq.nseq, 4);
+    }
+}
+
+}  // namespace
+
+AttnK make_attn(const gspn_attn_args& a) {
+    AttnK k = {};
+    k.seq = make_seq(a.seq);
+    gspn_sequences kv = a.seq;
+    kv.rows = a.kv_rows;
+    if (a.kv_cu) kv.cu = a.kv_cu;
+    kv.slots = nullptr;
+    k.kv = make_seq(kv);
+    k.heads = static_cast<int32_t>(a.heads);
+    k.kv_heads = static_cast<int32_t>(a.kv_heads);
+    k.group = static_cast<int32_t>(a.heads / a.kv_heads);
+    k.d = static_cast<int32_t>(a.d);
+    k.causal = a.causal != 0;
+    k.flip = a.scale < 0.0;
+    k.scale = static_cast<float>(a.scale);
+    k.scale_log2 = static_cast<float>(std::fabs(a.scale) * 1.4426950408889634);
+    if (!(k.scale_log2 >= 1e-37f)) k.scale_log2 = 1e-37f;  // so that a hidden score, -Inf, stays one when it is scaled
+    k.q = a.q;
+    k.k = a.k;
+    k.v = a.v;
+    k.out = a.out;
+    k.lse = a.lse;
+    k.k_pool = a.k_pool;
+    k.v_pool = a.v_pool;
+    k.capacity = a.capacity;
+    k.held = a.held;
+    k.gout = a.gout;
+    k.dq = a.dq;
+    k.dk = a.dk;
+    k.dv = a.dv;
+    k.ldq = a.ldq;
+    k.ldk = a.ldk;
+    k.ldv = a.ldv;
+    k.ldo = a.ldo;
+    k.ldgo = a.ldgo;
+    k.lddq = a.lddq;
+    k.lddk = a.lddk;
+    k.lddv = a.lddv;
+    return k;
+}
+
+hipError_t launch_attn_fwd(const gspn_attn_args& a, int dtype, hipStream_t stream) {
+    const AttnK k = make_attn(a);
+    const int64_t es = dtype == GSPN_F32 ? 4 : 2;
+    const bool ragged = a.seq.cu != nullptr;
+    if (a.k_pool) {
+        const dim3 grid(static_cast<unsigned>(chunk_ids(ragged, a.seq.rows, a.seq.nseq, kAppendShift)));
+        replay_fwd("attn_append_kernel", a, es);
+        GSPN_REPLAYED("attn_append_kernel", kAttnThreads, 0);
+        if (dtype == GSPN_F32)
+            hipLaunchKernelGGL((attn_append_kernel<float>), grid, dim3(kAttnThreads), 0, stream, k);
+        else
+            hipLaunchKernelGGL((attn_append_kernel<bf16_t>), grid, dim3(kAttnThreads), 0, stream, k);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    const dim3 grid(static_cast<unsigned>(chunk_ids(ragged, a.seq.rows, a.seq.nseq, kAttnShift) * a.heads));
+    replay_fwd("attn_fwd_kernel", a, es);
+    attn_dispatch(dtype, a.d, [&](auto t, auto width) {
+        using T = decltype(t);
+        constexpr int D = decltype(width)::value;
+        GSPN_REPLAYED("attn_fwd_kernel", kAttnThreads, 4 * kTileRows<T> * D * static_cast<int64_t>(sizeof(T)));
+        hipLaunchKernelGGL((attn_fwd_kernel<T, D>), grid, dim3(kAttnThreads), 0, stream, k);
+    });
+    return hipGetLastError();
+}
+
+}  // namespace gspn

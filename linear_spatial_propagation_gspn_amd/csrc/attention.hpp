@@ -1,0 +1,410 @@
+// attention.hpp -- what the attention kernels share: parameters, tiles of rows
+// in LDS, matrix products of them (internal to libgspn).
+//
+// Every product here is v_mfma 32x32 with fp32 sums.  Lane l of a wave holds
+// row l % 32 of the first factor and column l % 32 of the second; h = l / 32
+// picks which of the summed indices the lane holds, and any order of those
+// will do if both factors use the same.  A result has column l % 32 in lane l
+// and rows 8 (r / 4) + 4 h + r % 4 in its registers r < 16.  So scores are
+// formed with their queries (or, for the keys' gradients, their keys) as
+// columns: a lane then holds one softmax row, and its registers are the second
+// factor of the next product as they stand, without a trip through LDS.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "../../include/gspn_attention.h"
+#include "sequence.hpp"
+
+namespace gspn {
+
+// Queries of a workgroup: four waves of 32.  Keys of a workgroup of the keys'
+// gradients likewise.
+constexpr int kAttnShift = 7;
+constexpr int kAttnRows = 1 << kAttnShift;
+constexpr int kAttnThreads = 256;
+constexpr int kAppendShift = 5;  // 32 rows a workgroup go into their entries
+
+struct AttnK {
+    SeqK seq, kv;
+    int32_t heads, kv_heads, group, d, causal;
+    int32_t flip;      // scale < 0: queries (keys) enter the scores negated
+    float scale;       // as given
+    float scale_log2;  // |scale| log2 e, at least 1e-37
+    const void* q;
+    const void* k;
+    const void* v;
+    void* out;
+    float* lse;
+    void* k_pool;
+    void* v_pool;
+    int64_t capacity;
+    const int32_t* held;
+    const void* gout;
+    void* dq;
+    void* dk;
+    void* dv;
+    float* delta;  // [heads][rows]: <gout, out> of each row
+    float* part;   // of the step's splits
+    int64_t ldq, ldk, ldv, ldo, ldgo, lddq, lddk, lddv;
+    int32_t splits;
+};
+
+template <typename T>
+constexpr bool kIsBf16 = std::is_same_v<T, bf16_t>;
+
+// Rows of a tile: 16 KB of them at the widest.
+template <typename T>
+constexpr int kTileRows = kIsBf16<T> ? 64 : 32;
+
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t Quad __attribute__((ext_vector_type(4)));
+
+// 16 bytes at any element's address, zeros behind the `left` elements that the
+// head still has.
+template <typename T>
+__device__ __forceinline__ Quad ld16(const T* p, int left) {
+    constexpr int kE = 16 / sizeof(T);
+    Quad v = {0, 0, 0, 0};
+    if (left >= kE) {
+        __builtin_memcpy(&v, p, 16);
+    } else if (left > 0) {
+        T e[kE];
+#pragma unroll
+        for (int i = 0; i < kE; ++i) e[i] = i < left ? p[i] : T(0);
+        __builtin_memcpy(&v, e, 16);
+    }
+    return v;
+}
+
+// Four consecutive elements of a head, those behind its end left out.
+template <typename T>
+__device__ __forceinline__ void st4(T* p, int left, float a, float b, float c, float d) {
+    Pack<T, 4> v;
+    const float f[4] = {a, b, c, d};
+    st_pack<T, 4>(&v.e[0], f);
+    if (left >= 4) {
+        __builtin_memcpy(p, &v, sizeof v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            if (i < left) p[i] = v.e[i];
+    }
+}
+
+// a b + c over the 32 bytes a row that two fragments hold between their halves.
+template <typename T>
+__device__ __forceinline__ f32x16 mma(Quad a, Quad b, f32x16 c) {
+    if constexpr (kIsBf16<T>) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                       0, 0);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[i]), __uint_as_float(b[i]), c, 0, 0, 0);
+        return c;
+    }
+}
+
+// A tile of rows of D elements in LDS.  Its 16-byte chunks are swizzled so that
+// eight rows' chunks of one column (row fragments) and four rows' pairs of them
+// (transposed ones) lie in banks of their own.
+template <typename T, int D>
+struct Tile {
+    static constexpr int kRow = D * static_cast<int>(sizeof(T));  // bytes
+    static constexpr int kChunks = kRow / 16;
+    static constexpr int kSteps = kRow / 32;  // products over a whole row
+    static constexpr int kE = 16 / static_cast<int>(sizeof(T));
+
+    static __device__ __forceinline__ int swizzle(int row, int chunk) {
+        if constexpr (kRow % 256 == 0) return chunk ^ ((row & 7) << 1);
+        if constexpr (kRow % 256 == 128) return chunk ^ (((row >> 1) & 3) << 1);
+        return chunk ^ ((row >> 2) & 3);
+    }
+
+    // Rows row0 + l % 32 as a first factor, summed over columns: step s.
+    static __device__ __forceinline__ Quad rows(const char* t, int row0, int s) {
+        const int lane = threadIdx.x & 63;
+        const int row = row0 + (lane & 31);
+        return *reinterpret_cast<const Quad*>(t + row * kRow + swizzle(row, 2 * s + (lane >> 5)) * 16);
+    }
+
+    // c + (columns 32 b .. of rows row0 .. row0 + 31, transposed) p: a first
+    // factor whose rows are the tile's columns, summed over the tile's rows in
+    // the order in which a result's registers p hold them.
+    static __device__ __forceinline__ f32x16 columns(const char* t, int row0, int b, const Quad (&p)[2], f32x16 c) {
+        static_assert(kIsBf16<T>);
+        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+        const int lane = threadIdx.x & 63;
+        // a group of 16 lanes reads four rows of 16 elements and gets them by columns
+        const int row = row0 + 4 * (lane >> 5) + ((lane & 15) >> 2);
+        const int chunk = 4 * b + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            s16x4 v[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = row + 16 * i + 8 * j;
+                v[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (lds_s16x4*)(t + r * kRow + swizzle(r, chunk) * 16 + 8 * (lane & 1)));
+            }
+            Quad a;
+            __builtin_memcpy(&a, v, 16);
+            c = mma<T>(a, p[i], c);
+        }
+        return c;
+    }
+
+    static __device__ __forceinline__ f32x16 columns(const char* t, int row0, int b, const float (&p)[16], f32x16 c) {
+        static_assert(!kIsBf16<T>);
+        const int lane = threadIdx.x & 63;
+        const int col = 32 * b + (lane & 31);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int row = row0 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
+            const float a = *reinterpret_cast<const float*>(t + row * kRow + swizzle(row, col >> 2) * 16 + 4 * (col & 3));
+            c = __builtin_amdgcn_mfma_f32_32x32x2f32(a, p[r], c, 0, 0, 0);
+        }
+        return c;
+    }
+};
+
+// A result's registers as a second factor of Tile::columns.
+template <typename T>
+struct Factor;
+template <>
+struct Factor<bf16_t> {
+    Quad p[2];
+    __device__ __forceinline__ explicit Factor(const f32x16& f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i / 4][i % 4] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+    }
+};
+template <>
+struct Factor<float> {
+    float p[16];
+    __device__ __forceinline__ explicit Factor(const f32x16& f) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) p[i] = f[i];
+    }
+};
+
+// ROWS rows on their way from memory to a tile, over kThreads threads.
+template <typename T, int D, int ROWS, int kThreads>
+struct Stage {
+    using Tl = Tile<T, D>;
+    static constexpr int kN = ROWS * Tl::kChunks / kThreads;
+    static_assert(ROWS * Tl::kChunks % kThreads == 0);
+    Quad v[kN];
+
+    // Rows row0 .., those behind `last` as the last again.
+    __device__ __forceinline__ void load(int tid, const T* base, int64_t ld, int row0, int last, int d) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int at = i * kThreads + tid;
+            const int r = row0 + at / Tl::kChunks, c = at % Tl::kChunks;
+            v[i] = ld16(base + (r < last ? r : last) * ld + c * Tl::kE, d - c * Tl::kE);
+        }
+    }
+    __device__ __forceinline__ void store(int tid, char* tile) const {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int at = i * kThreads + tid;
+            const int r = at / Tl::kChunks, c = at % Tl::kChunks;
+            *reinterpret_cast<Quad*>(tile + r * Tl::kRow + Tl::swizzle(r, c) * 16) = v[i];
+        }
+    }
+};
+
+// A wave's row fragments straight from memory: row `row` (this lane's) of D
+// elements, zeros where the row is not wanted.
+template <typename T, int D>
+__device__ __forceinline__ void ld_rows(const T* row, bool wanted, int d, bool flip, Quad (&f)[Tile<T, D>::kSteps]) {
+    const int h = (threadIdx.x & 63) >> 5;
+    constexpr int kE = Tile<T, D>::kE;
+    constexpr uint32_t kSign = kIsBf16<T> ? 0x80008000u : 0x80000000u;
+#pragma unroll
+    for (int s = 0; s < Tile<T, D>::kSteps; ++s) {
+        const int c = (2 * s + h) * kE;
+        f[s] = ld16(row + c, wanted ? d - c : 0);
+        if (flip) f[s] ^= Quad{kSign, kSign, kSign, kSign};
+    }
+}
+
+// The larger, and the sum, of a lane's value and the one 32 lanes away.
+__device__ __forceinline__ float both_max(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float both_sum(float v) { return swap_add32(v, v); }
+
+// The row of a result that its register r holds in this lane.
+__device__ __forceinline__ int result_row(int r) { return 8 * (r / 4) + 4 * ((threadIdx.x & 63) >> 5) + r % 4; }
+
+// One row of the result (transposed: this lane's column, blocks of 32 rows),
+// times f.
+template <typename T, int D>
+__device__ __forceinline__ void st_result(T* row, const f32x16 (&o)[D / 32], float f, int d) {
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int c = 32 * b + result_row(4 * g);
+            st4(row + c, d - c, o[b][4 * g] * f, o[b][4 * g + 1] * f, o[b][4 * g + 2] * f, o[b][4 * g + 3] * f);
+        }
+}
+
+// The softmax of the rows that a wave's lanes hold, over tiles: the running
+// maximum of the scores (unscaled), the sum of this lane's half of the
+// numerators and their products with the values.  The maximum that the
+// numerators are taken from follows the true one only once it is 2^8 behind,
+// so that the products are rarely scaled anew; no numerator exceeds 2^8.
+template <int D>
+struct Softmax {
+    float m = -INFINITY, l = 0.0f;
+    f32x16 o[D / 32];
+
+    __device__ __forceinline__ Softmax() {
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[b][r] = 0.0f;
+    }
+    // s: scores, -Inf where hidden; on return the numerators.
+    template <int N>
+    __device__ __forceinline__ void tile(f32x16 (&s)[N], float scale_log2) {
+        float t = s[0][0];
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) t = __builtin_fmaxf(t, s[n][r]);
+        t = both_max(t);
+        if (__any((t - m) * scale_log2 > 8.0f || t != t)) {
+            const float top = __builtin_fmaxf(m, t);
+            const float a = top == m ? 1.0f : __builtin_amdgcn_exp2f((m - top) * scale_log2);
+            m = top;
+            l *= a;
+#pragma unroll
+            for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[b][r] *= a;
+        }
+        const float base = m == -INFINITY ? 0.0f : m * scale_log2;
+        float sum = 0.0f;
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                s[n][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][r], scale_log2, -base));
+                sum += s[n][r];
+            }
+        l += sum;
+    }
+};
+
+// Where a sequence's keys lie, and how many there are.  state: 0 as they are,
+// kNoSlot (padding), kBadSlot (an error).
+struct Keys {
+    const void* k;
+    const void* v;
+    int64_t ldk, ldv;
+    int32_t count, state, first;  // first: the row of kv that holds the first (without a cache)
+};
+
+template <typename T>
+__device__ __forceinline__ Keys find_keys(const AttnK& a, int seq, int begin, int rows, int kv_head) {
+    Keys w;
+    w.state = 0;
+    w.ldk = a.ldk;
+    w.ldv = a.ldv;
+    w.first = begin;
+    w.count = rows;
+    int slot = kNoSlot;
+    if (a.k_pool) {
+        slot = slot_of(a.seq, seq);
+        if (slot < 0) w.state = slot;
+        if (slot >= 0) {
+            const int held = a.held ? __builtin_amdgcn_readfirstlane(a.held[seq]) : 0;
+            if (held < 0 || held > a.capacity - rows) {
+                w.state = kBadSlot;
+            } else {
+                const int64_t at = (slot * a.capacity * a.kv_heads + kv_head) * a.d;
+                w.k = static_cast<const T*>(a.k_pool) + at;
+                w.v = static_cast<const T*>(a.v_pool) + at;
+                w.ldk = w.ldv = static_cast<int64_t>(a.kv_heads) * a.d;
+                w.count = held + rows;
+                return w;
+            }
+        }
+    } else {
+        w.first = seq_begin(a.kv, seq);
+        w.count = seq_end(a.kv, seq, w.first) - w.first;
+    }
+    w.k = static_cast<const T*>(a.k) + w.first * a.ldk + static_cast<int64_t>(kv_head) * a.d;
+    w.v = static_cast<const T*>(a.v) + w.first * a.ldv + static_cast<int64_t>(kv_head) * a.d;
+    return w;
+}
+
+// A workgroup's queries and head.
+struct AttnItem {
+    Chunk c;
+    int head;
+};
+
+// The chunks' ids are counted backwards within a sequence where the last see
+// most, so that the longest walks start first.
+__device__ __forceinline__ AttnItem find_item(const SeqK& s, int heads, bool backwards, int shift) {
+    AttnItem w;
+    w.head = static_cast<int>(blockIdx.x % heads);
+    w.c = find_chunk(s, blockIdx.x / heads, shift);
+    if (backwards && w.c.seq >= 0) {
+        w.c.k = w.c.count - 1 - w.c.k;
+        w.c.r0 = w.c.begin + (w.c.k << shift);
+        const int64_t r1 = static_cast<int64_t>(w.c.r0) + (int64_t{1} << shift);
+        w.c.r1 = r1 < w.c.end ? static_cast<int>(r1) : w.c.end;
+    }
+    return w;
+}
+
+
+// Host side ---------------------------------------------------------------
+
+AttnK make_attn(const gspn_attn_args& a);
+int attn_splits(int64_t nseq, int64_t heads, int64_t kv_heads, int64_t capacity);
+constexpr int kAttnMaxSplits = 64;
+
+hipError_t launch_attn_fwd(const gspn_attn_args& a, int dtype, hipStream_t stream);
+hipError_t launch_attn_step(const gspn_attn_args& a, int dtype, hipStream_t stream);
+// (no sequence: zero gradients)
+hipError_t launch_attn_bwd(const gspn_attn_args& a, int dtype, hipStream_t stream);
+
+hipError_t launch_rotary_fwd(const gspn_rotary_args& a, int dtype, hipStream_t stream);
+hipError_t launch_rotary_bwd(const gspn_rotary_args& a, int dtype, hipStream_t stream);
+int64_t rotary_bwd_parts(int64_t rows);
+
+// Calls f with the storage type and the width of the tiles that heads of d
+// elements take.
+template <typename F>
+void attn_dispatch(int dtype, int64_t d, F&& f) {
+    auto width = [&](auto t) {
+        if (d <= 64)
+            f(t, std::integral_constant<int, 64>{});
+        else if (d <= 96)
+            f(t, std::integral_constant<int, 96>{});
+        else
+            f(t, std::integral_constant<int, 128>{});
+    };
+    if (dtype == GSPN_F32)
+        width(float{});
+    else
+        width(bf16_t{});
+}
+
+}  // namespace gspn
