@@ -6,6 +6,11 @@
 // Two kernels, one with the queries at rest (dq, and D for the other), one with
 // the keys (dk, dv, over all the heads that share them): the scores are formed
 // twice, seven products instead of five, and nothing is added through memory.
+//
+// D from a bf16 out carries its rounding, as large against ds as one over the
+// root of the keys: rows that see one tile of keys or less get theirs from the
+// weights, sum_j p_ij <gout_i, v_j>.  A row that sees one key has p = 1 whatever
+// the score: its ds is 0, not the rounding that is left of the difference.
 #include "attention.hpp"
 
 #include <array>
@@ -51,7 +56,6 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_dq_kernel(const AttnK a)
     }
     const int64_t stat = static_cast<int64_t>(w.head) * a.seq.rows + at;
     const float lse2 = a.lse[stat] * 1.44269504088896340736f;
-    if (mine && lane < 32) a.delta[stat] = delta;
 
     const auto seen = [&](int r) {
         const int n = a.causal ? r + off + 1 : keys.count;
@@ -88,9 +92,8 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_dq_kernel(const AttnK a)
         if (key0 < wave_keys) {
             const char* const kt = lds[t & 1][0];
             const char* const vt = lds[t & 1][1];
-#pragma unroll
-            for (int n = 0; n < BN / 32; ++n) {
-                f32x16 s, dp;
+            // the weights of 32 keys and their gradients
+            const auto weights = [&](int n, f32x16& s, f32x16& dp) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.0f;
 #pragma unroll
@@ -100,11 +103,33 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_dq_kernel(const AttnK a)
                 }
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], a.scale_log2, -lse2)) * (dp[r] - delta);
+                    s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], a.scale_log2, -lse2));
                 if (key0 + BN > wave_all) {
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
-                        if (key0 + 32 * n + result_row(r) >= my_keys) s[r] = 0.0f;
+                        if (key0 + 32 * n + result_row(r) >= my_keys) s[r] = dp[r] = 0.0f;
+                }
+            };
+            if (wave_keys <= BN) {
+                delta = 0.0f;
+#pragma unroll 1
+                for (int n = 0; n < BN / 32; ++n) {
+                    f32x16 s, dp;
+                    weights(n, s, dp);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) delta = __builtin_fmaf(s[r], dp[r], delta);
+                }
+                delta = both_sum(delta);
+            }
+#pragma unroll
+            for (int n = 0; n < BN / 32; ++n) {
+                f32x16 s, dp;
+                weights(n, s, dp);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[r] *= dp[r] - delta;
+                if (my_keys < 2) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) s[r] = 0.0f;
                 }
                 const Factor<T> ds(s);
 #pragma unroll
@@ -117,7 +142,10 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_dq_kernel(const AttnK a)
         }
         __syncthreads();
     }
-    if (mine) st_result<T, D>(static_cast<T*>(a.dq) + at * a.lddq + col, dq, a.scale, a.d);
+    if (mine) {
+        st_result<T, D>(static_cast<T*>(a.dq) + at * a.lddq + col, dq, a.scale, a.d);
+        if (lane < 32) a.delta[stat] = delta;
+    }
 }
 
 template <typename T, int D>
@@ -191,7 +219,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_dkv_kernel(const AttnK a
         if (wave0 < count && (!a.causal || wave0 <= r0 + BM - 1 + off)) {
             const char* const qt = lds[t & 1][0];
             const char* const gt = lds[t & 1][1];
-            const bool hides = r0 + BM > rows || (a.causal && wave0 + 31 > r0 + off);
+            const bool hides = count == 1 || r0 + BM > rows || (a.causal && wave0 + 31 > r0 + off);
 #pragma unroll
             for (int n = 0; n < BM / 32; ++n) {
                 f32x16 s, dp;
@@ -215,7 +243,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_dkv_kernel(const AttnK a
                             const int i = r0 + r + j;
                             const bool hidden = i >= rows || (a.causal && key > i + off);
                             p = hidden ? 0.0f : p;
-                            ds = hidden ? 0.0f : ds;
+                            ds = hidden || count == 1 || (a.causal && i + off < 1) ? 0.0f : ds;
                         }
                         s[4 * g + j] = p;
                         dp[4 * g + j] = ds;
