@@ -7,7 +7,7 @@
 namespace gspn {
 namespace {
 
-template <typename T, int D>
+template <typename T, int D, bool kDirect>
 __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnK a) {
     using Tl = Tile<T, D>;
     constexpr int BN = kTileRows<T>;
@@ -50,26 +50,27 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnK a
     const int my_keys = mine ? seen(row) : 0;
 
     Softmax<D> sm;
-    Stage<T, D, BN, kAttnThreads> sk, sv;
+    Stage<T, D, BN, kAttnThreads, kDirect> sk, sv;
     const T* const kp = static_cast<const T*>(keys.k);
     const T* const vp = static_cast<const T*>(keys.v);
+    clear_tiles<kDirect>(tid, kAttnThreads, lds[0][0], sizeof lds, a.d == D);
     if (tiles > 0) {
-        sk.load(tid, kp, keys.ldk, 0, keys.count - 1, a.d);
-        sv.load(tid, vp, keys.ldv, 0, keys.count - 1, a.d);
-        sk.store(tid, lds[0][0]);
-        sv.store(tid, lds[0][1]);
+        sk.fetch(tid, kp, keys.ldk, 0, keys.count - 1, a.d, lds[0][0]);
+        sv.fetch(tid, vp, keys.ldv, 0, keys.count - 1, a.d, lds[0][1]);
+        sk.commit(tid, lds[0][0]);
+        sv.commit(tid, lds[0][1]);
     }
     __syncthreads();
     for (int t = 0; t < tiles; ++t) {
         const bool more = t + 1 < tiles;
         if (more) {
-            sk.load(tid, kp, keys.ldk, (t + 1) * BN, keys.count - 1, a.d);
-            sv.load(tid, vp, keys.ldv, (t + 1) * BN, keys.count - 1, a.d);
+            sk.fetch(tid, kp, keys.ldk, (t + 1) * BN, keys.count - 1, a.d, lds[(t + 1) & 1][0]);
+            sv.fetch(tid, vp, keys.ldv, (t + 1) * BN, keys.count - 1, a.d, lds[(t + 1) & 1][1]);
         }
         const int key0 = t * BN;
         if (key0 < wave_keys) {
-            const char* const kt = lds[t & 1][0];
-            const char* const vt = lds[t & 1][1];
+            const uint32_t kt = Tl::rows_at(lds_at(lds[t & 1][0]));
+            const uint32_t vt = Tl::columns_at(lds_at(lds[t & 1][1]));
             f32x16 s[BN / 32];
 #pragma unroll
             for (int n = 0; n < BN / 32; ++n) {
@@ -94,8 +95,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnK a
             }
         }
         if (more) {
-            sk.store(tid, lds[(t + 1) & 1][0]);
-            sv.store(tid, lds[(t + 1) & 1][1]);
+            sk.commit(tid, lds[(t + 1) & 1][0]);
+            sv.commit(tid, lds[(t + 1) & 1][1]);
         }
         __syncthreads();
     }
@@ -211,11 +212,14 @@ hipError_t launch_attn_fwd(const gspn_attn_args& a, int dtype, hipStream_t strea
     }
     const dim3 grid(static_cast<unsigned>(chunk_ids(ragged, a.seq.rows, a.seq.nseq, kAttnShift) * a.heads));
     replay_fwd("attn_fwd_kernel", a, es);
-    attn_dispatch(dtype, a.d, [&](auto t, auto width) {
+    const bool direct = a.k_pool ? attn_direct(a.k_pool, 0, a.d, es) && attn_direct(a.v_pool, 0, a.d, es)
+                                 : attn_direct(a.k, a.ldk, a.d, es) && attn_direct(a.v, a.ldv, a.d, es);
+    attn_dispatch(dtype, a.d, direct, [&](auto t, auto width, auto straight) {
         using T = decltype(t);
         constexpr int D = decltype(width)::value;
+        constexpr bool kDirect = decltype(straight)::value;
         GSPN_REPLAYED("attn_fwd_kernel", kAttnThreads, 4 * kTileRows<T> * D * static_cast<int64_t>(sizeof(T)));
-        hipLaunchKernelGGL((attn_fwd_kernel<T, D>), grid, dim3(kAttnThreads), 0, stream, k);
+        hipLaunchKernelGGL((attn_fwd_kernel<T, D, kDirect>), grid, dim3(kAttnThreads), 0, stream, k);
     });
     return hipGetLastError();
 }

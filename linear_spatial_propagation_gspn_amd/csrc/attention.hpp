@@ -66,6 +66,15 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t Quad __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) char lds_char;
+typedef __attribute__((address_space(3))) float lds_float;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) Quad lds_quad;
+
+// The byte address of LDS memory within the workgroup's.
+__device__ __forceinline__ uint32_t lds_at(const void* p) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_char*)p));
+}
 
 // 16 bytes at any element's address, zeros behind the `left` elements that the
 // head still has.
@@ -113,63 +122,75 @@ __device__ __forceinline__ f32x16 mma(Quad a, Quad b, f32x16 c) {
     }
 }
 
-// A tile of rows of D elements in LDS.  Its 16-byte chunks are swizzled so that
-// eight rows' chunks of one column (row fragments) and four rows' pairs of them
-// (transposed ones) lie in banks of their own.
+// A tile of rows of D elements in LDS, by its byte address there.  Its 16-byte
+// chunks are swizzled so that eight rows' chunks of one column (row fragments)
+// and four rows' pairs of them (transposed ones) lie in banks of their own: chunk
+// c of a row lies at c ^ flip(row), which moves it within an aligned span of
+// chunks.  An address is then the lane's own, exclusive-or a constant, plus a
+// constant: one instruction a read and one register a tile.
 template <typename T, int D>
 struct Tile {
     static constexpr int kRow = D * static_cast<int>(sizeof(T));  // bytes
     static constexpr int kChunks = kRow / 16;
     static constexpr int kSteps = kRow / 32;  // products over a whole row
     static constexpr int kE = 16 / static_cast<int>(sizeof(T));
+    static constexpr int kSpan = kRow % 256 == 0 ? 16 : kRow % 256 == 128 ? 8 : 4;
+    static_assert(kRow % (kSpan * 16) == 0);
 
-    static __device__ __forceinline__ int swizzle(int row, int chunk) {
-        if constexpr (kRow % 256 == 0) return chunk ^ ((row & 7) << 1);
-        if constexpr (kRow % 256 == 128) return chunk ^ (((row >> 1) & 3) << 1);
-        return chunk ^ ((row >> 2) & 3);
+    static __device__ __forceinline__ constexpr int flip(int row) {
+        return kSpan == 16 ? (row & 7) << 1 : kSpan == 8 ? ((row >> 1) & 3) << 1 : (row >> 2) & 3;
+    }
+    static __device__ __forceinline__ int swizzle(int row, int chunk) { return chunk ^ flip(row); }
+    // Chunk c (of the constant part) from a lane's address on.
+    static __device__ __forceinline__ uint32_t at(uint32_t x, int c) {
+        return (x ^ ((c & (kSpan - 1)) * 16)) + c / kSpan * kSpan * 16;
     }
 
-    // Rows row0 + l % 32 as a first factor, summed over columns: step s.
-    static __device__ __forceinline__ Quad rows(const char* t, int row0, int s) {
+    // A lane's address for rows().
+    static __device__ __forceinline__ uint32_t rows_at(uint32_t tile) {
+        const int lane = threadIdx.x & 63, row = lane & 31;
+        return tile + row * kRow + (flip(row) ^ (lane >> 5)) * 16;
+    }
+    // Rows row0 + l % 32 (row0 a multiple of 32) as a first factor, summed over
+    // columns: step s.
+    static __device__ __forceinline__ Quad rows(uint32_t x, int row0, int s) {
+        return *(const lds_quad*)(at(x, 2 * s) + row0 * kRow);
+    }
+
+    // A lane's address for columns().
+    static __device__ __forceinline__ uint32_t columns_at(uint32_t tile) {
         const int lane = threadIdx.x & 63;
-        const int row = row0 + (lane & 31);
-        return *reinterpret_cast<const Quad*>(t + row * kRow + swizzle(row, 2 * s + (lane >> 5)) * 16);
+        if constexpr (kIsBf16<T>) {
+            // a group of 16 lanes reads four rows of 16 elements and gets them by columns
+            const int row = 4 * (lane >> 5) + ((lane & 15) >> 2);
+            const int chunk = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+            return tile + row * kRow + (flip(row) ^ chunk) * 16 + 8 * (lane & 1);
+        } else {
+            const int row = 4 * (lane >> 5);
+            return tile + row * kRow + (flip(row) ^ ((lane & 31) >> 2)) * 16 + 4 * (lane & 3);
+        }
     }
-
     // c + (columns 32 b .. of rows row0 .. row0 + 31, transposed) p: a first
     // factor whose rows are the tile's columns, summed over the tile's rows in
     // the order in which a result's registers p hold them.
-    static __device__ __forceinline__ f32x16 columns(const char* t, int row0, int b, const Quad (&p)[2], f32x16 c) {
-        static_assert(kIsBf16<T>);
-        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-        const int lane = threadIdx.x & 63;
-        // a group of 16 lanes reads four rows of 16 elements and gets them by columns
-        const int row = row0 + 4 * (lane >> 5) + ((lane & 15) >> 2);
-        const int chunk = 4 * b + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    static __device__ __forceinline__ f32x16 columns(uint32_t x, int row0, int b, const Quad (&p)[2], f32x16 c) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             s16x4 v[2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int r = row + 16 * i + 8 * j;
+            for (int j = 0; j < 2; ++j)
                 v[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (lds_s16x4*)(t + r * kRow + swizzle(r, chunk) * 16 + 8 * (lane & 1)));
-            }
+                    (lds_s16x4*)(at(x, (4 * b) ^ flip(8 * j)) + (row0 + 16 * i + 8 * j) * kRow));
             Quad a;
             __builtin_memcpy(&a, v, 16);
             c = mma<T>(a, p[i], c);
         }
         return c;
     }
-
-    static __device__ __forceinline__ f32x16 columns(const char* t, int row0, int b, const float (&p)[16], f32x16 c) {
-        static_assert(!kIsBf16<T>);
-        const int lane = threadIdx.x & 63;
-        const int col = 32 * b + (lane & 31);
+    static __device__ __forceinline__ f32x16 columns(uint32_t x, int row0, int b, const float (&p)[16], f32x16 c) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            const int row = row0 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
-            const float a = *reinterpret_cast<const float*>(t + row * kRow + swizzle(row, col >> 2) * 16 + 4 * (col & 3));
+            const float a = *(const lds_float*)(at(x, (8 * b) ^ flip(r % 4)) + (row0 + 8 * (r / 4) + r % 4) * kRow);
             c = __builtin_amdgcn_mfma_f32_32x32x2f32(a, p[r], c, 0, 0, 0);
         }
         return c;
@@ -197,31 +218,59 @@ struct Factor<float> {
 };
 
 // ROWS rows on their way from memory to a tile, over kThreads threads.
-template <typename T, int D, int ROWS, int kThreads>
+// kDirect: straight to LDS, 1 KB a wave and instruction, which the wave only
+// waits for before the barrier that hands the tile over (the prompt of 16384
+// rows: 2.9 ms through registers, 2.2 so).  It takes rows of whole, aligned
+// 16-byte chunks; the swizzle is in the chunk that a lane asks for, and chunks
+// behind the head's end keep the zeros that clear() left.
+template <typename T, int D, int ROWS, int kThreads, bool kDirect>
 struct Stage {
     using Tl = Tile<T, D>;
     static constexpr int kN = ROWS * Tl::kChunks / kThreads;
     static_assert(ROWS * Tl::kChunks % kThreads == 0);
-    Quad v[kN];
+    Quad v[kDirect ? 1 : kN];
 
     // Rows row0 .., those behind `last` as the last again.
-    __device__ __forceinline__ void load(int tid, const T* base, int64_t ld, int row0, int last, int d) {
+    __device__ __forceinline__ void fetch(int tid, const T* base, int64_t ld, int row0, int last, int d, char* tile) {
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
             const int at = i * kThreads + tid;
-            const int r = row0 + at / Tl::kChunks, c = at % Tl::kChunks;
-            v[i] = ld16(base + (r < last ? r : last) * ld + c * Tl::kE, d - c * Tl::kE);
+            const int r = at / Tl::kChunks;
+            const int row = row0 + r < last ? row0 + r : last;
+            if constexpr (kDirect) {
+                const int c = Tl::swizzle(r, at % Tl::kChunks) * Tl::kE;
+                const uint32_t to = __builtin_amdgcn_readfirstlane(lds_at(tile) + (at - (tid & 63)) * 16);
+                const T* const from = base + row * ld + c;
+                if (c < d)
+                    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
+            } else {
+                const int c = at % Tl::kChunks * Tl::kE;
+                v[i] = ld16(base + row * ld + c, d - c);
+            }
         }
     }
-    __device__ __forceinline__ void store(int tid, char* tile) const {
+    __device__ __forceinline__ void commit(int tid, char* tile) const {
+        if constexpr (kDirect) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        } else {
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const int at = i * kThreads + tid;
-            const int r = at / Tl::kChunks, c = at % Tl::kChunks;
-            *reinterpret_cast<Quad*>(tile + r * Tl::kRow + Tl::swizzle(r, c) * 16) = v[i];
+            for (int i = 0; i < kN; ++i) {
+                const int at = i * kThreads + tid;
+                const int r = at / Tl::kChunks, c = at % Tl::kChunks;
+                *reinterpret_cast<Quad*>(tile + r * Tl::kRow + Tl::swizzle(r, c) * 16) = v[i];
+            }
         }
     }
 };
+
+// Zeros in `bytes` of tiles, where some of their chunks will not be fetched.
+template <bool kDirect>
+__device__ __forceinline__ void clear_tiles(int tid, int threads, char* tiles, int bytes, bool whole) {
+    if (kDirect && !whole) {
+        for (int i = tid * 16; i < bytes; i += threads * 16) *reinterpret_cast<Quad*>(tiles + i) = Quad{0, 0, 0, 0};
+        __syncthreads();
+    }
+}
 
 // A wave's row fragments straight from memory: row `row` (this lane's) of D
 // elements, zeros where the row is not wanted.
@@ -389,22 +438,33 @@ hipError_t launch_rotary_fwd(const gspn_rotary_args& a, int dtype, hipStream_t s
 hipError_t launch_rotary_bwd(const gspn_rotary_args& a, int dtype, hipStream_t stream);
 int64_t rotary_bwd_parts(int64_t rows);
 
-// Calls f with the storage type and the width of the tiles that heads of d
-// elements take.
+// Calls f with the storage type, the width of the tiles that heads of d
+// elements take, and whether their rows go straight to LDS.
 template <typename F>
-void attn_dispatch(int dtype, int64_t d, F&& f) {
-    auto width = [&](auto t) {
+void attn_dispatch(int dtype, int64_t d, bool direct, F&& f) {
+    auto width = [&](auto t, auto straight) {
         if (d <= 64)
-            f(t, std::integral_constant<int, 64>{});
+            f(t, std::integral_constant<int, 64>{}, straight);
         else if (d <= 96)
-            f(t, std::integral_constant<int, 96>{});
+            f(t, std::integral_constant<int, 96>{}, straight);
         else
-            f(t, std::integral_constant<int, 128>{});
+            f(t, std::integral_constant<int, 128>{}, straight);
+    };
+    auto way = [&](auto t) {
+        if (direct)
+            width(t, std::true_type{});
+        else
+            width(t, std::false_type{});
     };
     if (dtype == GSPN_F32)
-        width(float{});
+        way(float{});
     else
-        width(bf16_t{});
+        way(bf16_t{});
+}
+
+// Whether rows are whole 16-byte chunks.
+inline bool attn_direct(const void* p, int64_t ld, int64_t d, int64_t es) {
+    return d * es % 16 == 0 && aligned_rows(p, ld, static_cast<int>(es), 16);
 }
 
 }  // namespace gspn

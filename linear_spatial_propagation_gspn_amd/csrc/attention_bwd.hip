@@ -19,8 +19,13 @@
 namespace gspn {
 namespace {
 
-template <typename T, int D>
-__global__ __launch_bounds__(kAttnThreads, 1) void attn_dq_kernel(const AttnK a) {
+// lse in powers of two; +Inf where there is none, so that every weight is 0.
+__device__ __forceinline__ float log2_sum(float lse) {
+    return lse == -INFINITY ? INFINITY : lse * 1.44269504088896340736f;
+}
+
+template <typename T, int D, bool kDirect>
+__global__ __launch_bounds__(kAttnThreads, 2) void attn_dq_kernel(const AttnK a) {
     using Tl = Tile<T, D>;
     constexpr int BN = kTileRows<T>;
     __shared__ __attribute__((aligned(16))) char lds[2][2][BN * Tl::kRow];
@@ -55,7 +60,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_dq_kernel(const AttnK a)
         delta = both_sum(delta);
     }
     const int64_t stat = static_cast<int64_t>(w.head) * a.seq.rows + at;
-    const float lse2 = a.lse[stat] * 1.44269504088896340736f;
+    const float lse2 = log2_sum(a.lse[stat]);
 
     const auto seen = [&](int r) {
         const int n = a.causal ? r + off + 1 : keys.count;
@@ -72,26 +77,27 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_dq_kernel(const AttnK a)
     for (int b = 0; b < D / 32; ++b)
 #pragma unroll
         for (int r = 0; r < 16; ++r) dq[b][r] = 0.0f;
-    Stage<T, D, BN, kAttnThreads> sk, sv;
+    Stage<T, D, BN, kAttnThreads, kDirect> sk, sv;
     const T* const kp = static_cast<const T*>(keys.k);
     const T* const vp = static_cast<const T*>(keys.v);
+    clear_tiles<kDirect>(tid, kAttnThreads, lds[0][0], sizeof lds, a.d == D);
     if (tiles > 0) {
-        sk.load(tid, kp, keys.ldk, 0, keys.count - 1, a.d);
-        sv.load(tid, vp, keys.ldv, 0, keys.count - 1, a.d);
-        sk.store(tid, lds[0][0]);
-        sv.store(tid, lds[0][1]);
+        sk.fetch(tid, kp, keys.ldk, 0, keys.count - 1, a.d, lds[0][0]);
+        sv.fetch(tid, vp, keys.ldv, 0, keys.count - 1, a.d, lds[0][1]);
+        sk.commit(tid, lds[0][0]);
+        sv.commit(tid, lds[0][1]);
     }
     __syncthreads();
     for (int t = 0; t < tiles; ++t) {
         const bool more = t + 1 < tiles;
         if (more) {
-            sk.load(tid, kp, keys.ldk, (t + 1) * BN, keys.count - 1, a.d);
-            sv.load(tid, vp, keys.ldv, (t + 1) * BN, keys.count - 1, a.d);
+            sk.fetch(tid, kp, keys.ldk, (t + 1) * BN, keys.count - 1, a.d, lds[(t + 1) & 1][0]);
+            sv.fetch(tid, vp, keys.ldv, (t + 1) * BN, keys.count - 1, a.d, lds[(t + 1) & 1][1]);
         }
         const int key0 = t * BN;
         if (key0 < wave_keys) {
-            const char* const kt = lds[t & 1][0];
-            const char* const vt = lds[t & 1][1];
+            const uint32_t kt = Tl::rows_at(lds_at(lds[t & 1][0])), kc = Tl::columns_at(lds_at(lds[t & 1][0]));
+            const uint32_t vt = Tl::rows_at(lds_at(lds[t & 1][1]));
             // the weights of 32 keys and their gradients
             const auto weights = [&](int n, f32x16& s, f32x16& dp) {
 #pragma unroll
@@ -133,12 +139,12 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_dq_kernel(const AttnK a)
                 }
                 const Factor<T> ds(s);
 #pragma unroll
-                for (int b = 0; b < D / 32; ++b) dq[b] = Tl::columns(kt, 32 * n, b, ds.p, dq[b]);
+                for (int b = 0; b < D / 32; ++b) dq[b] = Tl::columns(kc, 32 * n, b, ds.p, dq[b]);
             }
         }
         if (more) {
-            sk.store(tid, lds[(t + 1) & 1][0]);
-            sv.store(tid, lds[(t + 1) & 1][1]);
+            sk.commit(tid, lds[(t + 1) & 1][0]);
+            sv.commit(tid, lds[(t + 1) & 1][1]);
         }
         __syncthreads();
     }
@@ -148,8 +154,8 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_dq_kernel(const AttnK a)
     }
 }
 
-template <typename T, int D>
-__global__ __launch_bounds__(kAttnThreads, 1) void attn_dkv_kernel(const AttnK a) {
+template <typename T, int D, bool kDirect>
+__global__ __launch_bounds__(kAttnThreads, kIsBf16<T> ? 2 : 1) void attn_dkv_kernel(const AttnK a) {
     using Tl = Tile<T, D>;
     constexpr int BM = kTileRows<T>;
     __shared__ __attribute__((aligned(16))) char lds[2][2][BM * Tl::kRow];
@@ -185,26 +191,29 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_dkv_kernel(const AttnK a
 #pragma unroll
         for (int r = 0; r < 16; ++r) dk[b][r] = dv[b][r] = 0.0f;
 
-    Stage<T, D, BM, kAttnThreads> sq, sg;
+    Stage<T, D, BM, kAttnThreads, kDirect> sq, sg;
     float stat = 0.0f;
-    const auto load = [&](int head, int tile) {
+    const auto fetch = [&](int head, int tile, int buf) {
         const int64_t c = static_cast<int64_t>(w.head * a.group + head) * a.d;
-        sq.load(tid, static_cast<const T*>(a.q) + begin * a.ldq + c, a.ldq, tile * BM, rows - 1, a.d);
-        sg.load(tid, static_cast<const T*>(a.gout) + begin * a.ldgo + c, a.ldgo, tile * BM, rows - 1, a.d);
+        sq.fetch(tid, static_cast<const T*>(a.q) + begin * a.ldq + c, a.ldq, tile * BM, rows - 1, a.d, lds[buf][0]);
+        sg.fetch(tid, static_cast<const T*>(a.gout) + begin * a.ldgo + c, a.ldgo, tile * BM, rows - 1, a.d, lds[buf][1]);
         if (tid < 2 * BM) {
             const int r = tile * BM + tid % BM;
             const int64_t i = static_cast<int64_t>(w.head * a.group + head) * a.seq.rows + begin + (r < rows ? r : rows - 1);
-            stat = tid < BM ? a.lse[i] * 1.44269504088896340736f : a.delta[i];
+            stat = tid < BM ? log2_sum(a.lse[i]) : a.delta[i];
         }
     };
-    const auto store = [&](int buf) {
-        sq.store(tid, lds[buf][0]);
-        sg.store(tid, lds[buf][1]);
+    const auto commit = [&](int buf) {
+        sq.commit(tid, lds[buf][0]);
+        sg.commit(tid, lds[buf][1]);
         if (tid < 2 * BM) stats[buf][tid / BM][tid % BM] = stat;
     };
+    clear_tiles<kDirect>(tid, kAttnThreads, lds[0][0], sizeof lds, a.d == D);
+    const int lo = a.causal ? key - off : 0;   // rows lo .. rows - 1 see this lane's key
+    const int alone = count == 1 ? 0 : -off;   // the row that sees one key (with one key, every row)
     if (tiles > 0) {
-        load(0, t0);
-        store(0);
+        fetch(0, t0, 0);
+        commit(0);
     }
     __syncthreads();
     int head = 0, tile = t0;
@@ -215,49 +224,65 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_dkv_kernel(const AttnK a
             tile = t0;
             ++head;
         }
-        if (more) load(head, tile);
+        if (more) fetch(head, tile, (t + 1) & 1);
         if (wave0 < count && (!a.causal || wave0 <= r0 + BM - 1 + off)) {
-            const char* const qt = lds[t & 1][0];
-            const char* const gt = lds[t & 1][1];
-            const bool hides = count == 1 || r0 + BM > rows || (a.causal && wave0 + 31 > r0 + off);
+            const uint32_t qt = Tl::rows_at(lds_at(lds[t & 1][0])), qc = Tl::columns_at(lds_at(lds[t & 1][0]));
+            const uint32_t gt = Tl::rows_at(lds_at(lds[t & 1][1])), gc = Tl::columns_at(lds_at(lds[t & 1][1]));
+            const bool hides = r0 + BM > rows || (a.causal && wave0 + 31 > r0 + off);
+            const bool lone = count == 1 || (a.causal && alone >= r0 && alone < r0 + BM);
+            // (the barriers keep the compiler from fetching fragments of the next
+            // product early: their registers would not be there)
 #pragma unroll
             for (int n = 0; n < BM / 32; ++n) {
                 f32x16 s, dp;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.0f;
 #pragma unroll
-                for (int i = 0; i < Tl::kSteps; ++i) {
-                    s = mma<T>(Tl::rows(qt, 32 * n, i), k[i], s);
-                    dp = mma<T>(Tl::rows(gt, 32 * n, i), v[i], dp);
+                for (int i = 0; i < Tl::kSteps; ++i) s = mma<T>(Tl::rows(qt, 32 * n, i), k[i], s);
+                if (hides) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const int i = r0 + 32 * n + result_row(r);
+                        s[r] = i >= lo && i < rows ? s[r] : -INFINITY;
+                    }
                 }
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const int r = 32 * n + result_row(4 * g);
-                    const f32x4 lse2 = *reinterpret_cast<const f32x4*>(&stats[t & 1][0][r]);
-                    const f32x4 delta = *reinterpret_cast<const f32x4*>(&stats[t & 1][1][r]);
+                    const f32x4 lse2 = *reinterpret_cast<const f32x4*>(&stats[t & 1][0][32 * n + result_row(4 * g)]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * g + j], a.scale_log2, -lse2[j]));
-                        float ds = p * (dp[4 * g + j] - delta[j]);
-                        if (hides) {
-                            const int i = r0 + r + j;
-                            const bool hidden = i >= rows || (a.causal && key > i + off);
-                            p = hidden ? 0.0f : p;
-                            ds = hidden || count == 1 || (a.causal && i + off < 1) ? 0.0f : ds;
-                        }
-                        s[4 * g + j] = p;
-                        dp[4 * g + j] = ds;
-                    }
+                    for (int j = 0; j < 4; ++j)
+                        s[4 * g + j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * g + j], a.scale_log2, -lse2[j]));
                 }
-                const Factor<T> p(s), ds(dp);
+                __builtin_amdgcn_sched_barrier(0);
+                {
+                    const Factor<T> p(s);
 #pragma unroll
-                for (int b = 0; b < D / 32; ++b) {
-                    dv[b] = Tl::columns(gt, 32 * n, b, p.p, dv[b]);
-                    dk[b] = Tl::columns(qt, 32 * n, b, ds.p, dk[b]);
+                    for (int b = 0; b < D / 32; ++b) dv[b] = Tl::columns(gc, 32 * n, b, p.p, dv[b]);
                 }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int i = 0; i < Tl::kSteps; ++i) dp = mma<T>(Tl::rows(gt, 32 * n, i), v[i], dp);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const f32x4 delta = *reinterpret_cast<const f32x4*>(&stats[t & 1][1][32 * n + result_row(4 * g)]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[4 * g + j] *= dp[4 * g + j] - delta[j];
+                }
+                if (lone) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (count == 1 || r0 + 32 * n + result_row(r) == alone) s[r] = 0.0f;
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                {
+                    const Factor<T> ds(s);
+#pragma unroll
+                    for (int b = 0; b < D / 32; ++b) dk[b] = Tl::columns(qc, 32 * n, b, ds.p, dk[b]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
-        if (more) store((t + 1) & 1);
+        if (more) commit((t + 1) & 1);
         __syncthreads();
     }
     if (mine) {
@@ -310,14 +335,16 @@ hipError_t launch_attn_bwd(const gspn_attn_args& a, int dtype, hipStream_t strea
     if (a.seq.rows > 0) {
         const dim3 grid(static_cast<unsigned>(
             chunk_ids(a.seq.cu != nullptr, a.seq.rows, a.seq.nseq, kAttnShift) * a.heads));
+        const bool direct = attn_direct(a.k, a.ldk, a.d, es) && attn_direct(a.v, a.ldv, a.d, es);
         replay("attn_dq_kernel");
         GSPN_REPLAY_ROWS("attn_dq_kernel", "out", a.out, a.seq.rows, a.ldo, cq, es);
         GSPN_REPLAY_ROWS("attn_dq_kernel", "dq", a.dq, a.seq.rows, a.lddq, cq, es);
-        attn_dispatch(dtype, a.d, [&](auto t, auto width) {
+        attn_dispatch(dtype, a.d, direct, [&](auto t, auto width, auto straight) {
             using T = decltype(t);
             constexpr int D = decltype(width)::value;
+            constexpr bool kDirect = decltype(straight)::value;
             GSPN_REPLAYED("attn_dq_kernel", kAttnThreads, 4 * kTileRows<T> * D * static_cast<int64_t>(sizeof(T)));
-            hipLaunchKernelGGL((attn_dq_kernel<T, D>), grid, dim3(kAttnThreads), 0, stream, k);
+            hipLaunchKernelGGL((attn_dq_kernel<T, D, kDirect>), grid, dim3(kAttnThreads), 0, stream, k);
         });
         e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -325,15 +352,17 @@ hipError_t launch_attn_bwd(const gspn_attn_args& a, int dtype, hipStream_t strea
     if (a.kv_rows > 0) {
         const dim3 grid(static_cast<unsigned>(chunk_ids(k.kv.cu != nullptr, a.kv_rows, a.seq.nseq, kAttnShift) *
                                               a.kv_heads));
+        const bool direct = attn_direct(a.q, a.ldq, a.d, es) && attn_direct(a.gout, a.ldgo, a.d, es);
         replay("attn_dkv_kernel");
         GSPN_REPLAY_ROWS("attn_dkv_kernel", "dk", a.dk, a.kv_rows, a.lddk, ck, es);
         GSPN_REPLAY_ROWS("attn_dkv_kernel", "dv", a.dv, a.kv_rows, a.lddv, ck, es);
-        attn_dispatch(dtype, a.d, [&](auto t, auto width) {
+        attn_dispatch(dtype, a.d, direct, [&](auto t, auto width, auto straight) {
             using T = decltype(t);
             constexpr int D = decltype(width)::value;
+            constexpr bool kDirect = decltype(straight)::value;
             GSPN_REPLAYED("attn_dkv_kernel", kAttnThreads,
                           kTileRows<T> * (4 * D * static_cast<int64_t>(sizeof(T)) + 16));
-            hipLaunchKernelGGL((attn_dkv_kernel<T, D>), grid, dim3(kAttnThreads), 0, stream, k);
+            hipLaunchKernelGGL((attn_dkv_kernel<T, D, kDirect>), grid, dim3(kAttnThreads), 0, stream, k);
         });
         e = hipGetLastError();
     }

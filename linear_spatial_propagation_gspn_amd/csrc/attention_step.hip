@@ -85,6 +85,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_step_kernel(const AttnK 
     };
     char* const kt = lds[wave];
     char* const vt = lds[wave] + kStepKeys * Tl::kRow;
+    const uint32_t kr = Tl::rows_at(lds_at(kt)), vc = Tl::columns_at(lds_at(vt));
     Softmax<D> sm;
     int key0 = begin + wave * kStepKeys;
     if (key0 < end) load(key0);
@@ -103,7 +104,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_step_kernel(const AttnK 
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[0][r] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < Tl::kSteps; ++i) s[0] = mma<T>(Tl::rows(kt, 0, i), q[i], s[0]);
+        for (int i = 0; i < Tl::kSteps; ++i) s[0] = mma<T>(Tl::rows(kr, 0, i), q[i], s[0]);
         if (key0 + kStepKeys > end) {
 #pragma unroll
             for (int r = 0; r < 16; ++r)
@@ -112,7 +113,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_step_kernel(const AttnK 
         sm.template tile<1>(s, a.scale_log2);
         const Factor<T> p(s[0]);
 #pragma unroll
-        for (int b = 0; b < D / 32; ++b) sm.o[b] = Tl::columns(vt, 0, b, p.p, sm.o[b]);
+        for (int b = 0; b < D / 32; ++b) sm.o[b] = Tl::columns(vc, 0, b, p.p, sm.o[b]);
     }
 
     // the waves' results: [32][d values, sum, maximum], each on the others' scale
@@ -224,7 +225,7 @@ hipError_t launch_attn_step(const gspn_attn_args& a, int dtype, hipStream_t stre
     GSPN_REPLAY_ROWS("attn_step_kernel", "v_pool", a.v_pool, a.seq.nslots * a.capacity, ck, ck, es);
     GSPN_REPLAY_ROWS("attn_step_kernel", "held", a.held, 1, a.seq.nseq, a.seq.nseq, 4);
     if (k.splits > 1) GSPN_REPLAY_ROWS("attn_step_kernel", "runs", a.workspace, parts, a.d + 2, a.d + 2, 4);
-    attn_dispatch(dtype, a.d, [&](auto t, auto width) {
+    attn_dispatch(dtype, a.d, false, [&](auto t, auto width, auto) {
         using T = decltype(t);
         constexpr int D = decltype(width)::value;
         GSPN_REPLAYED("attn_step_kernel", kAttnThreads,
