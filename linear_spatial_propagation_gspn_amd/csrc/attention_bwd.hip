@@ -154,11 +154,23 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_dq_kernel(const AttnK a)
     }
 }
 
+// Two waves a SIMD have 256 registers each.  Heads of 128 bf16 elements leave no
+// room there for both keys and values beside the gradients': the values stay in
+// LDS, and tiles are half as long so that two workgroups still share a CU (held in
+// registers they spilled, and every reload waited for the tile on its way: 301 us
+// where this takes 190, 8 x 1024 rows, 18 heads, 6 of keys).
+template <typename T, int D>
+constexpr bool kValuesInLds = kIsBf16<T> && D == 128;
+template <typename T, int D>
+constexpr int kRowsAtOnce = kValuesInLds<T, D> ? 32 : kTileRows<T>;
+
 template <typename T, int D, bool kDirect>
 __global__ __launch_bounds__(kAttnThreads, kIsBf16<T> ? 2 : 1) void attn_dkv_kernel(const AttnK a) {
     using Tl = Tile<T, D>;
-    constexpr int BM = kTileRows<T>;
+    constexpr int BM = kRowsAtOnce<T, D>;
+    constexpr bool kHeld = !kValuesInLds<T, D>;  // values in registers
     __shared__ __attribute__((aligned(16))) char lds[2][2][BM * Tl::kRow];
+    __shared__ __attribute__((aligned(16))) char values[kHeld ? 16 : kAttnRows * Tl::kRow];
     __shared__ __attribute__((aligned(16))) float stats[2][2][BM];
     const AttnItem w = find_item(a.kv, a.kv_heads, false, kAttnShift);
     if (w.c.seq < 0 || w.c.r0 >= w.c.r1) return;
@@ -175,9 +187,16 @@ __global__ __launch_bounds__(kAttnThreads, kIsBf16<T> ? 2 : 1) void attn_dkv_ker
     const int64_t at = static_cast<int64_t>(w.c.begin) + (mine ? key : 0);
     const int64_t col = static_cast<int64_t>(w.head) * a.d;
 
-    Quad k[Tl::kSteps], v[Tl::kSteps];
+    Quad k[Tl::kSteps], v[kHeld ? Tl::kSteps : 1];
     ld_rows<T, D>(static_cast<const T*>(a.k) + at * a.ldk + col, mine, a.d, a.flip, k);
-    ld_rows<T, D>(static_cast<const T*>(a.v) + at * a.ldv + col, mine, a.d, false, v);
+    if constexpr (kHeld) {
+        ld_rows<T, D>(static_cast<const T*>(a.v) + at * a.ldv + col, mine, a.d, false, v);
+    } else {
+        Stage<T, D, kAttnRows, kAttnThreads, false> sv;
+        sv.fetch(tid, static_cast<const T*>(a.v) + w.c.begin * a.ldv + col, a.ldv, key0, count - 1, a.d, values);
+        sv.commit(tid, values);
+    }
+    const uint32_t vt = Tl::rows_at(lds_at(values)) + (wave0 - key0) * Tl::kRow;
 
     // tiles of rows from the first that sees a key of the workgroup
     const int row0 = !a.causal || key0 - off < 0 ? 0 : key0 - off;
@@ -261,7 +280,7 @@ __global__ __launch_bounds__(kAttnThreads, kIsBf16<T> ? 2 : 1) void attn_dkv_ker
                 }
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int i = 0; i < Tl::kSteps; ++i) dp = mma<T>(Tl::rows(gt, 32 * n, i), v[i], dp);
+                for (int i = 0; i < Tl::kSteps; ++i) dp = mma<T>(Tl::rows(gt, 32 * n, i), kHeld ? v[kHeld ? i : 0] : Tl::rows(vt, 0, i), dp);
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const f32x4 delta = *reinterpret_cast<const f32x4*>(&stats[t & 1][1][32 * n + result_row(4 * g)]);
@@ -361,7 +380,8 @@ hipError_t launch_attn_bwd(const gspn_attn_args& a, int dtype, hipStream_t strea
             constexpr int D = decltype(width)::value;
             constexpr bool kDirect = decltype(straight)::value;
             GSPN_REPLAYED("attn_dkv_kernel", kAttnThreads,
-                          kTileRows<T> * (4 * D * static_cast<int64_t>(sizeof(T)) + 16));
+                          kRowsAtOnce<T, D> * (4 * D * static_cast<int64_t>(sizeof(T)) + 16) +
+                              (kValuesInLds<T, D> ? kAttnRows * D * static_cast<int64_t>(sizeof(T)) : 16));
             hipLaunchKernelGGL((attn_dkv_kernel<T, D, kDirect>), grid, dim3(kAttnThreads), 0, stream, k);
         });
         e = hipGetLastError();
