@@ -12,7 +12,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnK a
     using Tl = Tile<T, D>;
     constexpr int BN = kTileRows<T>;
     __shared__ __attribute__((aligned(16))) char lds[2][2][BN * Tl::kRow];
-    const AttnItem w = find_item(a.seq, a.heads, a.causal != 0, kAttnShift);
+    const AttnItem w = find_item(a.seq, a.heads, a.causal != 0, kAttnShift, blockIdx.x);
     if (w.c.seq < 0 || w.c.r0 >= w.c.r1) return;
     const int tid = threadIdx.x, lane = tid & 63;
     const int rows = w.c.end - w.c.begin;

@@ -21,11 +21,12 @@
 
 namespace gspn {
 
-// Queries of a workgroup: four waves of 32.  Keys of a workgroup of the keys'
-// gradients likewise.
+// Queries of a workgroup: four waves of 32.
 constexpr int kAttnShift = 7;
 constexpr int kAttnRows = 1 << kAttnShift;
 constexpr int kAttnThreads = 256;
+constexpr int kKeyShift = 6;     // keys of a workgroup of their gradients
+constexpr int kKeyRows = 1 << kKeyShift;
 constexpr int kAppendShift = 5;  // 32 rows a workgroup go into their entries
 
 struct AttnK {
@@ -409,10 +410,15 @@ struct AttnItem {
 
 // The chunks' ids are counted backwards within a sequence where the last see
 // most, so that the longest walks start first.
-__device__ __forceinline__ AttnItem find_item(const SeqK& s, int heads, bool backwards, int shift) {
+__device__ __forceinline__ AttnItem find_item(const SeqK& s, int heads, bool backwards, int shift, uint32_t id) {
     AttnItem w;
-    w.head = static_cast<int>(blockIdx.x % heads);
-    w.c = find_chunk(s, blockIdx.x / heads, shift);
+    w.head = static_cast<int>(id % heads);
+    uint32_t chunk = id / heads;
+    if (!s.cu) {  // equal sequences take turns
+        const uint32_t each = static_cast<uint32_t>(chunks_each(s.len, shift));
+        chunk = chunk % s.nseq * each + chunk / s.nseq;
+    }
+    w.c = find_chunk(s, chunk, shift);
     if (backwards && w.c.seq >= 0) {
         w.c.k = w.c.count - 1 - w.c.k;
         w.c.r0 = w.c.begin + (w.c.k << shift);
@@ -428,6 +434,8 @@ __device__ __forceinline__ AttnItem find_item(const SeqK& s, int heads, bool bac
 AttnK make_attn(const gspn_attn_args& a);
 int attn_splits(int64_t nseq, int64_t heads, int64_t kv_heads, int64_t capacity);
 constexpr int kAttnMaxSplits = 64;
+int attn_bwd_parts(int64_t rows, int64_t nseq, int64_t heads, int64_t kv_rows, int64_t kv_heads);
+constexpr int kAttnMaxParts = 16;
 
 hipError_t launch_attn_fwd(const gspn_attn_args& a, int dtype, hipStream_t stream);
 hipError_t launch_attn_step(const gspn_attn_args& a, int dtype, hipStream_t stream);

@@ -94,7 +94,7 @@ gspn_status check_attn(const gspn_attn_args* a, int dtype, Which which, bool* em
         if (a->kv_cu ? pool : (a->seq.cu || pool) ? kv != rows : kv % nseq != 0) return GSPN_ERR_BAD_SHAPE;
         b.flat(a->kv_cu, (nseq + 1) * 4, 4, false, true);
         const int64_t ids = gspn::chunk_ids(true, rows, nseq, gspn::kAttnShift) * a->heads;
-        const int64_t kv_ids = gspn::chunk_ids(true, kv, nseq, gspn::kAttnShift) * a->kv_heads;
+        const int64_t kv_ids = gspn::chunk_ids(true, kv, nseq, gspn::kKeyShift) * a->kv_heads;
         const int64_t copies = pool ? gspn::chunk_ids(true, rows, nseq, gspn::kAppendShift) : 0;
         if (ids > kMaxGrid || kv_ids > kMaxGrid || copies > kMaxGrid) return GSPN_ERR_UNSUPPORTED;
     }
@@ -180,8 +180,9 @@ gspn_status gspn_attention_step(const gspn_attn_args* args, int dtype, void* str
 
 int64_t gspn_attention_bwd_workspace_bytes(int64_t rows, int64_t nseq, int64_t heads, int64_t kv_rows,
                                            int64_t kv_heads, int64_t d) {
-    if (!attn_sizes_ok(rows, nseq, heads, kv_heads, d) || !attn_sizes_ok(kv_rows, nseq, heads, kv_heads, d)) return -1;
-    return rows * heads * 4;
+    if (nseq < 1 || !attn_sizes_ok(rows, nseq, heads, kv_heads, d) || !attn_sizes_ok(kv_rows, nseq, heads, kv_heads, d)) return -1;
+    const int64_t parts = gspn::attn_bwd_parts(rows, nseq, heads, kv_rows, kv_heads);
+    return (rows * heads + 3) / 4 * 16 + (parts > 1 ? parts * 2 * kv_rows * kv_heads * d * 4 : 0);
 }
 
 gspn_status gspn_attention_bwd(const gspn_attn_args* args, int dtype, void* stream) {

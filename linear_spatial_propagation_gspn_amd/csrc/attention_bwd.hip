@@ -29,7 +29,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_dq_kernel(const AttnK a)
     using Tl = Tile<T, D>;
     constexpr int BN = kTileRows<T>;
     __shared__ __attribute__((aligned(16))) char lds[2][2][BN * Tl::kRow];
-    const AttnItem w = find_item(a.seq, a.heads, a.causal != 0, kAttnShift);
+    const AttnItem w = find_item(a.seq, a.heads, a.causal != 0, kAttnShift, blockIdx.x);
     if (w.c.seq < 0 || w.c.r0 >= w.c.r1) return;
     const int tid = threadIdx.x, lane = tid & 63;
     const int rows = w.c.end - w.c.begin;
@@ -154,55 +154,72 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_dq_kernel(const AttnK a)
     }
 }
 
-// Two waves a SIMD have 256 registers each.  Heads of 128 bf16 elements leave no
-// room there for both keys and values beside the gradients': the values stay in
-// LDS, and tiles are half as long so that two workgroups still share a CU (held in
-// registers they spilled, and every reload waited for the tile on its way: 301 us
-// where this takes 190, 8 x 1024 rows, 18 heads, 6 of keys).
+// Values of a workgroup's keys for the keys' gradients.  Two waves a SIMD have
+// 256 registers each: heads of 128 bf16 elements leave no room there for both
+// keys and values beside the gradients' sums, and spilled every reload waits for
+// the tiles on their way (301 us where values in LDS took 211).  All but the last
+// of the products' steps lie in LDS then, the last in registers, so that two
+// workgroups share a CU.  Rows of 224 bytes need no swizzle.
 template <typename T, int D>
 constexpr bool kValuesInLds = kIsBf16<T> && D == 128;
-template <typename T, int D>
-constexpr int kRowsAtOnce = kValuesInLds<T, D> ? 32 : kTileRows<T>;
+constexpr int kValueRow = 224;
+constexpr int kValueSteps = 7;
 
+// Rows of queries in a tile: 32 for each half of the waves.
+constexpr int kBwdRows = 64;
+
+// Keys at rest: two waves of 32 of them, twice, each pair for one half of every
+// tile of rows (joined in LDS at the end).  Long walks are half as long so, which
+// counts where later rows see more keys: 8 x 1024 rows, 18 heads, 6 of keys, 211
+// us with 128 keys a workgroup.
 template <typename T, int D, bool kDirect>
 __global__ __launch_bounds__(kAttnThreads, kIsBf16<T> ? 2 : 1) void attn_dkv_kernel(const AttnK a) {
     using Tl = Tile<T, D>;
-    constexpr int BM = kRowsAtOnce<T, D>;
-    constexpr bool kHeld = !kValuesInLds<T, D>;  // values in registers
+    constexpr int BM = kBwdRows;
+    constexpr bool kInLds = kValuesInLds<T, D>;
     __shared__ __attribute__((aligned(16))) char lds[2][2][BM * Tl::kRow];
-    __shared__ __attribute__((aligned(16))) char values[kHeld ? 16 : kAttnRows * Tl::kRow];
+    __shared__ __attribute__((aligned(16))) char values[kInLds ? kKeyRows * kValueRow : 16];
     __shared__ __attribute__((aligned(16))) float stats[2][2][BM];
-    const AttnItem w = find_item(a.kv, a.kv_heads, false, kAttnShift);
+    const int part = static_cast<int>(blockIdx.x % a.splits);
+    const AttnItem w = find_item(a.kv, a.kv_heads, false, kKeyShift, blockIdx.x / a.splits);
     if (w.c.seq < 0 || w.c.r0 >= w.c.r1) return;
-    const int tid = threadIdx.x, lane = tid & 63;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int half = wave >> 1;
     const int begin = seq_begin(a.seq, w.c.seq);
     const int rows = seq_end(a.seq, w.c.seq, begin) - begin;
     const int count = w.c.end - w.c.begin;
     const int off = count - rows;
 
     const int key0 = w.c.r0 - w.c.begin;
-    const int wave0 = key0 + __builtin_amdgcn_readfirstlane(tid >> 6) * 32;
+    const int wave0 = key0 + (wave & 1) * 32;
     const int key = wave0 + (lane & 31);
     const bool mine = key < count;
     const int64_t at = static_cast<int64_t>(w.c.begin) + (mine ? key : 0);
     const int64_t col = static_cast<int64_t>(w.head) * a.d;
 
-    Quad k[Tl::kSteps], v[kHeld ? Tl::kSteps : 1];
+    Quad k[Tl::kSteps], v[kInLds ? 1 : Tl::kSteps];
     ld_rows<T, D>(static_cast<const T*>(a.k) + at * a.ldk + col, mine, a.d, a.flip, k);
-    if constexpr (kHeld) {
-        ld_rows<T, D>(static_cast<const T*>(a.v) + at * a.ldv + col, mine, a.d, false, v);
+    const T* const value = static_cast<const T*>(a.v) + at * a.ldv + col;
+    const uint32_t vt = lds_at(values) + ((wave & 1) * 32 + (lane & 31)) * kValueRow + (lane >> 5) * 16;
+    if constexpr (kInLds) {
+        const int c = (lane >> 5) * Tl::kE;
+        v[0] = ld16(value + kValueSteps * 2 * Tl::kE + c, mine ? a.d - kValueSteps * 2 * Tl::kE - c : 0);
+        if (half == 0) {
+#pragma unroll
+            for (int i = 0; i < kValueSteps; ++i)
+                *(lds_quad*)(vt + 32 * i) = ld16(value + 2 * i * Tl::kE + c, mine ? a.d - 2 * i * Tl::kE - c : 0);
+        }
     } else {
-        Stage<T, D, kAttnRows, kAttnThreads, false> sv;
-        sv.fetch(tid, static_cast<const T*>(a.v) + w.c.begin * a.ldv + col, a.ldv, key0, count - 1, a.d, values);
-        sv.commit(tid, values);
+        ld_rows<T, D>(value, mine, a.d, false, v);
     }
-    const uint32_t vt = Tl::rows_at(lds_at(values)) + (wave0 - key0) * Tl::kRow;
 
-    // tiles of rows from the first that sees a key of the workgroup
+    // tiles of rows from the first that sees a key of the workgroup, for each head; this part's of them
     const int row0 = !a.causal || key0 - off < 0 ? 0 : key0 - off;
     const int t0 = row0 / BM;
     const int each = row0 < rows ? (rows + BM - 1) / BM - t0 : 0;
-    const int tiles = each * a.group;
+    const int64_t all = static_cast<int64_t>(each) * a.group;
+    const int first = static_cast<int>(all * part / a.splits);
+    const int tiles = static_cast<int>(all * (part + 1) / a.splits);
 
     f32x16 dk[D / 32], dv[D / 32];
 #pragma unroll
@@ -219,94 +236,149 @@ __global__ __launch_bounds__(kAttnThreads, kIsBf16<T> ? 2 : 1) void attn_dkv_ker
         if (tid < 2 * BM) {
             const int r = tile * BM + tid % BM;
             const int64_t i = static_cast<int64_t>(w.head * a.group + head) * a.seq.rows + begin + (r < rows ? r : rows - 1);
-            stat = tid < BM ? log2_sum(a.lse[i]) : a.delta[i];
+            stat = (tid < BM ? a.lse : a.delta)[i];  // (not used before commit: that would wait for the tiles)
         }
     };
     const auto commit = [&](int buf) {
         sq.commit(tid, lds[buf][0]);
         sg.commit(tid, lds[buf][1]);
-        if (tid < 2 * BM) stats[buf][tid / BM][tid % BM] = stat;
+        if (tid < 2 * BM) stats[buf][tid / BM][tid % BM] = tid < BM ? log2_sum(stat) : stat;
     };
     clear_tiles<kDirect>(tid, kAttnThreads, lds[0][0], sizeof lds, a.d == D);
     const int lo = a.causal ? key - off : 0;   // rows lo .. rows - 1 see this lane's key
     const int alone = count == 1 ? 0 : -off;   // the row that sees one key (with one key, every row)
-    if (tiles > 0) {
-        fetch(0, t0, 0);
+    int head = each > 0 ? first / each : 0, tile = t0 + (each > 0 ? first % each : 0);
+    if (first < tiles) {
+        fetch(head, tile, 0);
         commit(0);
     }
     __syncthreads();
-    int head = 0, tile = t0;
-    for (int t = 0; t < tiles; ++t) {
+    for (int t = first; t < tiles; ++t) {
         const bool more = t + 1 < tiles;
-        const int r0 = tile * BM;
+        const int buf = (t - first) & 1;
+        const int r0 = tile * BM + half * 32;
         if (++tile == t0 + each) {
             tile = t0;
             ++head;
         }
-        if (more) fetch(head, tile, (t + 1) & 1);
-        if (wave0 < count && (!a.causal || wave0 <= r0 + BM - 1 + off)) {
-            const uint32_t qt = Tl::rows_at(lds_at(lds[t & 1][0])), qc = Tl::columns_at(lds_at(lds[t & 1][0]));
-            const uint32_t gt = Tl::rows_at(lds_at(lds[t & 1][1])), gc = Tl::columns_at(lds_at(lds[t & 1][1]));
-            const bool hides = r0 + BM > rows || (a.causal && wave0 + 31 > r0 + off);
-            const bool lone = count == 1 || (a.causal && alone >= r0 && alone < r0 + BM);
+        if (more) fetch(head, tile, buf ^ 1);
+        if (wave0 < count && r0 < rows && (!a.causal || wave0 <= r0 + 31 + off)) {
+            const uint32_t half_at = half * 32 * Tl::kRow;
+            const uint32_t qt = Tl::rows_at(lds_at(lds[buf][0]) + half_at), qc = Tl::columns_at(lds_at(lds[buf][0]) + half_at);
+            const uint32_t gt = Tl::rows_at(lds_at(lds[buf][1]) + half_at), gc = Tl::columns_at(lds_at(lds[buf][1]) + half_at);
+            const bool hides = r0 + 32 > rows || (a.causal && wave0 + 31 > r0 + off);
+            const bool lone = count == 1 || (a.causal && alone >= r0 && alone < r0 + 32);
             // (the barriers keep the compiler from fetching fragments of the next
             // product early: their registers would not be there)
+            f32x16 s, dp;
 #pragma unroll
-            for (int n = 0; n < BM / 32; ++n) {
-                f32x16 s, dp;
+            for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.0f;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.0f;
+            for (int i = 0; i < Tl::kSteps; ++i) s = mma<T>(Tl::rows(qt, 0, i), k[i], s);
+            if (hides) {
 #pragma unroll
-                for (int i = 0; i < Tl::kSteps; ++i) s = mma<T>(Tl::rows(qt, 32 * n, i), k[i], s);
-                if (hides) {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int i = r0 + 32 * n + result_row(r);
-                        s[r] = i >= lo && i < rows ? s[r] : -INFINITY;
-                    }
+                for (int r = 0; r < 16; ++r) {
+                    const int i = r0 + result_row(r);
+                    s[r] = i >= lo && i < rows ? s[r] : -INFINITY;
                 }
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const f32x4 lse2 = *reinterpret_cast<const f32x4*>(&stats[t & 1][0][32 * n + result_row(4 * g)]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        s[4 * g + j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * g + j], a.scale_log2, -lse2[j]));
-                }
-                __builtin_amdgcn_sched_barrier(0);
-                {
-                    const Factor<T> p(s);
-#pragma unroll
-                    for (int b = 0; b < D / 32; ++b) dv[b] = Tl::columns(gc, 32 * n, b, p.p, dv[b]);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int i = 0; i < Tl::kSteps; ++i) dp = mma<T>(Tl::rows(gt, 32 * n, i), kHeld ? v[kHeld ? i : 0] : Tl::rows(vt, 0, i), dp);
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const f32x4 delta = *reinterpret_cast<const f32x4*>(&stats[t & 1][1][32 * n + result_row(4 * g)]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) s[4 * g + j] *= dp[4 * g + j] - delta[j];
-                }
-                if (lone) {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (count == 1 || r0 + 32 * n + result_row(r) == alone) s[r] = 0.0f;
-                }
-                __builtin_amdgcn_sched_barrier(0);
-                {
-                    const Factor<T> ds(s);
-#pragma unroll
-                    for (int b = 0; b < D / 32; ++b) dk[b] = Tl::columns(qc, 32 * n, b, ds.p, dk[b]);
-                }
-                __builtin_amdgcn_sched_barrier(0);
             }
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const f32x4 lse2 = *reinterpret_cast<const f32x4*>(&stats[buf][0][half * 32 + result_row(4 * g)]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    s[4 * g + j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * g + j], a.scale_log2, -lse2[j]));
+            }
+            if constexpr (kInLds) __builtin_amdgcn_sched_barrier(0);
+            {
+                const Factor<T> p(s);
+#pragma unroll
+                for (int b = 0; b < D / 32; ++b) dv[b] = Tl::columns(gc, 0, b, p.p, dv[b]);
+            }
+            if constexpr (kInLds) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < Tl::kSteps; ++i) {
+                if constexpr (kInLds)
+                    dp = mma<T>(Tl::rows(gt, 0, i), i < kValueSteps ? *(const lds_quad*)(vt + 32 * i) : v[0], dp);
+                else
+                    dp = mma<T>(Tl::rows(gt, 0, i), v[i], dp);
+            }
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const f32x4 delta = *reinterpret_cast<const f32x4*>(&stats[buf][1][half * 32 + result_row(4 * g)]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[4 * g + j] *= dp[4 * g + j] - delta[j];
+            }
+            if (lone) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (count == 1 || r0 + result_row(r) == alone) s[r] = 0.0f;
+            }
+            if constexpr (kInLds) __builtin_amdgcn_sched_barrier(0);
+            {
+                const Factor<T> ds(s);
+#pragma unroll
+                for (int b = 0; b < D / 32; ++b) dk[b] = Tl::columns(qc, 0, b, ds.p, dk[b]);
+            }
+            if constexpr (kInLds) __builtin_amdgcn_sched_barrier(0);
         }
-        if (more) commit((t + 1) & 1);
+        if (more) commit(buf ^ 1);
         __syncthreads();
     }
-    if (mine) {
+
+    // the second half of the waves hands its sums to the first
+    f32x4* const join = reinterpret_cast<f32x4*>(lds[0][0]) + (wave & 1) * (D / 4) * 64 + lane;
+    static_assert(sizeof lds >= 2 * (D / 4) * 64 * 16);
+    if (half == 1) {
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                join[(8 * b + g) * 64] = f32x4{dk[b][4 * g], dk[b][4 * g + 1], dk[b][4 * g + 2], dk[b][4 * g + 3]};
+                join[(8 * b + 4 + g) * 64] = f32x4{dv[b][4 * g], dv[b][4 * g + 1], dv[b][4 * g + 2], dv[b][4 * g + 3]};
+            }
+    }
+    __syncthreads();
+    if (half == 1 || !mine) return;
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const f32x4 x = join[(8 * b + g) * 64], y = join[(8 * b + 4 + g) * 64];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                dk[b][4 * g + j] += x[j];
+                dv[b][4 * g + j] += y[j];
+            }
+        }
+    if (a.splits > 1) {
+        const int64_t size = static_cast<int64_t>(a.kv.rows) * a.kv_heads * a.d;
+        float* const to = a.part + part * 2 * size + at * a.kv_heads * a.d + col;
+        st_result<float, D>(to, dk, a.scale, a.d);
+        st_result<float, D>(to + size, dv, 1.0f, a.d);
+    } else {
         st_result<T, D>(static_cast<T*>(a.dk) + at * a.lddk + col, dk, a.scale, a.d);
         st_result<T, D>(static_cast<T*>(a.dv) + at * a.lddv + col, dv, 1.0f, a.d);
+    }
+}
+
+// The parts' sums, in order, of the rows inside the sequences.
+template <typename T>
+__global__ __launch_bounds__(kAttnThreads) void attn_parts_kernel(const AttnK a) {
+    const int width = a.kv_heads * a.d;
+    const int64_t size = static_cast<int64_t>(a.kv.rows) * width;
+    const int last = a.kv.nseq - 1;
+    const int lo = a.kv.cu ? seq_begin(a.kv, 0) : 0;
+    const int hi = a.kv.cu ? seq_end(a.kv, last, seq_begin(a.kv, last)) : a.kv.rows;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kAttnThreads + threadIdx.x; i < 2 * size;
+         i += static_cast<int64_t>(gridDim.x) * kAttnThreads) {
+        const int64_t e = i < size ? i : i - size;
+        const int64_t row = e / width;
+        if (row < lo || row >= hi) continue;
+        float s = 0.0f;
+        for (int p = 0; p < a.splits; ++p) s += a.part[p * 2 * size + i];
+        T* const to = static_cast<T*>(i < size ? a.dk : a.dv) + row * (i < size ? a.lddk : a.lddv) + (e - row * width);
+        Store<T>::st(to, s);
     }
 }
 
@@ -330,6 +402,18 @@ hipError_t clear_rows(const SeqK& s, bool all, int es, std::initializer_list<std
 }
 
 }  // namespace
+
+// Parts that the rows which a workgroup of keys walks are cut into: as many as
+// fill two workgroups a CU, none of fewer than two tiles on average.  Their sums
+// pass through memory in fp32, little where there are few keys.
+int attn_bwd_parts(int64_t rows, int64_t nseq, int64_t heads, int64_t kv_rows, int64_t kv_heads) {
+    const int64_t groups = chunk_ids(true, kv_rows, nseq, kKeyShift) * kv_heads;
+    const int64_t tiles = (rows / nseq + kBwdRows - 1) / kBwdRows * (heads / kv_heads);
+    int64_t n = 512 / groups;
+    if (n > tiles / 2) n = tiles / 2;
+    if (n > kAttnMaxParts) n = kAttnMaxParts;
+    return n < 1 ? 1 : static_cast<int>(n);
+}
 
 hipError_t launch_attn_bwd(const gspn_attn_args& a, int dtype, hipStream_t stream) {
     AttnK k = make_attn(a);
@@ -369,21 +453,36 @@ hipError_t launch_attn_bwd(const gspn_attn_args& a, int dtype, hipStream_t strea
         if (e != hipSuccess) return e;
     }
     if (a.kv_rows > 0) {
-        const dim3 grid(static_cast<unsigned>(chunk_ids(k.kv.cu != nullptr, a.kv_rows, a.seq.nseq, kAttnShift) *
-                                              a.kv_heads));
+        k.splits = attn_bwd_parts(a.seq.rows, a.seq.nseq, a.heads, a.kv_rows, a.kv_heads);
+        k.part = k.delta + (a.heads * a.seq.rows + 3) / 4 * 4;
+        const dim3 grid(static_cast<unsigned>(chunk_ids(k.kv.cu != nullptr, a.kv_rows, a.seq.nseq, kKeyShift) *
+                                              a.kv_heads * k.splits));
         const bool direct = attn_direct(a.q, a.ldq, a.d, es) && attn_direct(a.gout, a.ldgo, a.d, es);
         replay("attn_dkv_kernel");
         GSPN_REPLAY_ROWS("attn_dkv_kernel", "dk", a.dk, a.kv_rows, a.lddk, ck, es);
         GSPN_REPLAY_ROWS("attn_dkv_kernel", "dv", a.dv, a.kv_rows, a.lddv, ck, es);
+        if (k.splits > 1) GSPN_REPLAY_ROWS("attn_dkv_kernel", "parts", k.part, 2 * k.splits * a.kv_rows, ck, ck, 4);
         attn_dispatch(dtype, a.d, direct, [&](auto t, auto width, auto straight) {
             using T = decltype(t);
             constexpr int D = decltype(width)::value;
             constexpr bool kDirect = decltype(straight)::value;
             GSPN_REPLAYED("attn_dkv_kernel", kAttnThreads,
-                          kRowsAtOnce<T, D> * (4 * D * static_cast<int64_t>(sizeof(T)) + 16) +
-                              (kValuesInLds<T, D> ? kAttnRows * D * static_cast<int64_t>(sizeof(T)) : 16));
+                          kBwdRows * (4 * D * static_cast<int64_t>(sizeof(T)) + 16) +
+                              (kValuesInLds<T, D> ? kKeyRows * kValueRow : 16));
             hipLaunchKernelGGL((attn_dkv_kernel<T, D, kDirect>), grid, dim3(kAttnThreads), 0, stream, k);
         });
+        e = hipGetLastError();
+        if (e != hipSuccess || k.splits == 1) return e;
+        const int64_t blocks = (2 * a.kv_rows * ck + kAttnThreads - 1) / kAttnThreads;
+        GSPN_REPLAY_ROWS("attn_parts_kernel", "parts", k.part, 2 * k.splits * a.kv_rows, ck, ck, 4);
+        GSPN_REPLAY_ROWS("attn_parts_kernel", "dk", a.dk, a.kv_rows, a.lddk, ck, es);
+        GSPN_REPLAY_ROWS("attn_parts_kernel", "dv", a.dv, a.kv_rows, a.lddv, ck, es);
+        GSPN_REPLAYED("attn_parts_kernel", kAttnThreads, 0);
+        const dim3 sums(static_cast<unsigned>(blocks < 2048 ? blocks : 2048));
+        if (dtype == GSPN_F32)
+            hipLaunchKernelGGL((attn_parts_kernel<float>), sums, dim3(kAttnThreads), 0, stream, k);
+        else
+            hipLaunchKernelGGL((attn_parts_kernel<bf16_t>), sums, dim3(kAttnThreads), 0, stream, k);
         e = hipGetLastError();
     }
     return e;

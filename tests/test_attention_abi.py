@@ -343,9 +343,10 @@ def test_launches_stay_in_their_buffers(chk, lib, dt, d, ld):
             assert replay(chk, lib, "attn", "fwd", dt, capacity=1300, slots=5, **kw) == ["attn_append_kernel",
                                                                                          "attn_fwd_kernel"]
             clear = ["reduce_parts_kernel"] * (2 if cu else 0)
-            assert replay(chk, lib, "attn", "bwd", dt, **kw) == clear + ["attn_dq_kernel", "attn_dkv_kernel"]
-            assert replay(chk, lib, "attn", "bwd", dt, kv_rows=60, kv_cu=True, **kw)[-2:] == ["attn_dq_kernel",
-                                                                                             "attn_dkv_kernel"]
+            parts = ["attn_parts_kernel"] * (rows == 1200)  # rows enough to be cut
+            assert replay(chk, lib, "attn", "bwd", dt, **kw) == clear + ["attn_dq_kernel", "attn_dkv_kernel"] + parts
+            assert replay(chk, lib, "attn", "bwd", dt, kv_rows=60, kv_cu=True, **kw)[-2 - len(parts):] == [
+                "attn_dq_kernel", "attn_dkv_kernel"] + parts
     assert replay(chk, lib, "attn", "step", dt, d=d, ld=ld, nseq=3, slots=5) == ["attn_step_kernel"]
     assert replay(chk, lib, "attn", "step", dt, d=d, ld=ld, nseq=3, capacity=5000) == ["attn_step_kernel",
                                                                                        "attn_step_join_kernel"]
