@@ -123,12 +123,13 @@ __device__ __forceinline__ f32x16 mma(Quad a, Quad b, f32x16 c) {
     }
 }
 
-// A tile of rows of D elements in LDS, by its byte address there.  Its 16-byte
-// chunks are swizzled so that eight rows' chunks of one column (row fragments)
-// and four rows' pairs of them (transposed ones) lie in banks of their own: chunk
-// c of a row lies at c ^ flip(row), which moves it within an aligned span of
-// chunks.  An address is then the lane's own, exclusive-or a constant, plus a
-// constant: one instruction a read and one register a tile.
+// A tile of rows of D elements in LDS, by its byte address there.  LDS gives 256
+// bytes a cycle, in banks: its 16-byte chunks are swizzled so that 16 rows'
+// chunks of one column (row fragments) and four rows' four of them (transposed
+// ones) lie apart.  Chunk c of a row lies at c ^ flip(row), which moves it within
+// an aligned span of chunks; flip is linear in the row's bits, so an address is the
+// lane's own, exclusive-or a constant, plus a constant: one instruction a read and
+// one register a tile.
 template <typename T, int D>
 struct Tile {
     static constexpr int kRow = D * static_cast<int>(sizeof(T));  // bytes
@@ -139,7 +140,9 @@ struct Tile {
     static_assert(kRow % (kSpan * 16) == 0);
 
     static __device__ __forceinline__ constexpr int flip(int row) {
-        return kSpan == 16 ? (row & 7) << 1 : kSpan == 8 ? ((row >> 1) & 3) << 1 : (row >> 2) & 3;
+        return kSpan == 16  ? (row & 3) << 2 | ((row >> 2) & 3)
+               : kSpan == 8 ? (row & 2) << 1 | ((row >> 2) & 3)
+                            : (row >> 2) & 3;
     }
     static __device__ __forceinline__ int swizzle(int row, int chunk) { return chunk ^ flip(row); }
     // Chunk c (of the constant part) from a lane's address on.
@@ -191,7 +194,7 @@ struct Tile {
     static __device__ __forceinline__ f32x16 columns(uint32_t x, int row0, int b, const float (&p)[16], f32x16 c) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            const float a = *(const lds_float*)(at(x, (8 * b) ^ flip(r % 4)) + (row0 + 8 * (r / 4) + r % 4) * kRow);
+            const float a = *(const lds_float*)(at(x, (8 * b) ^ flip(8 * (r / 4) + r % 4)) + (row0 + 8 * (r / 4) + r % 4) * kRow);
             c = __builtin_amdgcn_mfma_f32_32x32x2f32(a, p[r], c, 0, 0, 0);
         }
         return c;

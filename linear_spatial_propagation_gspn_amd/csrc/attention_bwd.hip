@@ -159,10 +159,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_dq_kernel(const AttnK a)
 // keys and values beside the gradients' sums, and spilled every reload waits for
 // the tiles on their way (301 us where values in LDS took 211).  All but the last
 // of the products' steps lie in LDS then, the last in registers, so that two
-// workgroups share a CU.  Rows of 224 bytes need no swizzle.
+// workgroups share a CU.  Rows of 240 bytes need no swizzle.
 template <typename T, int D>
 constexpr bool kValuesInLds = kIsBf16<T> && D == 128;
-constexpr int kValueRow = 224;
+constexpr int kValueRow = 240;
 constexpr int kValueSteps = 7;
 
 // Rows of queries in a tile: 32 for each half of the waves.
