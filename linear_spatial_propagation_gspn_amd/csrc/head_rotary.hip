@@ -57,94 +57,149 @@ __device__ __forceinline__ void sincos_turn(double t, float* s, float* c) {
     *c = (n == 1 || n == 2) ? -v : v;
 }
 
-// V elements from p on, `left` of them in range (the others 0).
-template <typename T, int V>
-__device__ __forceinline__ void ld_some(const T* p, int left, float (&f)[V]) {
-    if (left >= V) {
-        Pack<T, V> v;
-        __builtin_memcpy(&v, p, sizeof v);
-        widen<T, V>(v, f);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = i < left ? Store<T>::ld(p + i) : 0.0f;
-    }
-}
-
-template <typename T, int V>
-__device__ __forceinline__ void st_some(T* p, int left, const float (&f)[V]) {
-    if (left >= V) {
-        Pack<T, V> v;
-        st_pack<T, V>(&v.e[0], f);
-        __builtin_memcpy(p, &v, sizeof v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (i < left) Store<T>::st(p + i, f[i]);
-    }
-}
-
-// A lane's place in a head: its pairs (a[i], b[i]) begin at these elements, of
-// which na, nb are in range.
+// A lane's place in a head: V pairs (a[i], b[i]), their elements from these on, or
+// 2 V elements in a row behind the pairs (as a, then b).  Where units do not come
+// out even (kEven: they do), the last of either kind ends where its kind does and
+// so begins within the one before: its first `skip` values are that one's too,
+// count for nothing in sums, and are stored twice, the same bits; where there are
+// not V of a kind, `left` are in range.
 struct Place {
-    int a, b, na, nb;
-    bool turns;
+    int a, b, skip, left;
+    bool turns, idle;
 };
 
-template <int V>
+template <int V, bool kInter, bool kEven>
 __device__ __forceinline__ Place place_of(const RotaryK& k, int unit) {
     const int turning = (k.pairs + V - 1) / V;
     Place p;
     p.turns = unit < turning;
+    const int all = p.turns ? k.pairs : k.d - 2 * k.pairs;  // of its kind: pairs, or elements
+    const int each = p.turns ? V : 2 * V;
+    const int first = (p.turns ? unit : unit - turning) * each;
+    p.idle = first >= all;
+    int at = first;
+    p.skip = 0;
+    p.left = each;
+    if (!kEven && !p.idle && first + each > all) {
+        if (all >= each) {
+            at = all - each;
+            p.skip = first - at;
+        } else {
+            p.left = all;
+        }
+    }
     if (p.turns) {
-        const int j = unit * V;
-        p.na = k.pairs - j < V ? k.pairs - j : V;
-        p.nb = p.na;
-        p.a = k.interleaved ? 2 * j : j;
-        p.b = k.interleaved ? 2 * j + V : k.pairs + j;
+        p.a = kInter ? 2 * at : at;
+        p.b = kInter ? 2 * at + V : k.pairs + at;
     } else {
-        p.a = 2 * k.pairs + (unit - turning) * 2 * V;
+        p.a = 2 * k.pairs + at;
         p.b = p.a + V;
-        p.na = k.d - p.a;
-        p.nb = k.d - p.b;
-        p.na = p.na < 0 ? 0 : p.na < V ? p.na : V;
-        p.nb = p.nb < 0 ? 0 : p.nb < V ? p.nb : V;
     }
     return p;
 }
 
-// The 2 V elements of a place as pairs.  Interleaved pairs are 2 V in a row.
+// Which of a place's values are its own, in range and not another unit's too.
+template <int V, bool kEven>
+__device__ __forceinline__ bool own_a(const Place& p, int i) {
+    return kEven || (i >= p.skip && i < p.left);
+}
+template <int V, bool kEven>
+__device__ __forceinline__ bool own_b(const Place& p, int i) {
+    const int j = p.turns ? i : V + i;
+    return kEven || (j >= p.skip && j < p.left);
+}
+
+// The values of a place on their way; 0 where it is idle or out of range.
 template <typename T, int V>
-__device__ __forceinline__ void ld_pairs(const RotaryK& k, const Place& p, const T* head, float (&a)[V], float (&b)[V]) {
-    if (p.turns && k.interleaved) {
-        float f[2 * V];
-        ld_some<T, 2 * V>(head + p.a, 2 * p.na, f);
+struct Raw {
+    Pack<T, V> a, b;
+};
+
+template <typename T, int V, bool kInter, bool kEven>
+__device__ __forceinline__ Raw<T, V> ld_raw(const Place& p, const T* head) {
+    Raw<T, V> r = {};
+    if (p.idle) return r;
+    if (kEven || p.left >= (p.turns ? V : 2 * V)) {
+        __builtin_memcpy(&r.a, head + p.a, sizeof r.a);
+        __builtin_memcpy(&r.b, head + p.b, sizeof r.b);
+    } else {
+        // interleaved pairs are 2 V elements in a row, as elements behind the pairs are
+        const bool row = !p.turns || kInter;
+        const int n = p.turns && kInter ? 2 * p.left : p.left;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            a[i] = f[2 * i];
-            b[i] = f[2 * i + 1];
+            if (i < n) r.a.e[i] = head[p.a + i];
+            if ((row ? V + i : i) < n) r.b.e[i] = head[p.b + i];
         }
-    } else {
-        ld_some<T, V>(head + p.a, p.na, a);
-        ld_some<T, V>(head + p.b, p.nb, b);
+    }
+    return r;
+}
+
+template <typename T, int V, bool kInter>
+__device__ __forceinline__ void pairs_of(const Place& p, const Raw<T, V>& r, float (&a)[V], float (&b)[V]) {
+    widen<T, V>(r.a, a);
+    widen<T, V>(r.b, b);
+    if constexpr (kInter) {
+        float f[2 * V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            f[i] = a[i];
+            f[V + i] = b[i];
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            a[i] = p.turns ? f[2 * i] : f[i];
+            b[i] = p.turns ? f[2 * i + 1] : f[V + i];
+        }
     }
 }
 
-template <typename T, int V>
-__device__ __forceinline__ void st_pairs(const RotaryK& k, const Place& p, T* head, const float (&a)[V],
-                                         const float (&b)[V]) {
-    if (p.turns && k.interleaved) {
+template <typename T, int V, bool kInter, bool kEven>
+__device__ __forceinline__ void st_pairs(const Place& p, T* head, float (&a)[V], float (&b)[V]) {
+    if constexpr (kInter) {
         float f[2 * V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             f[2 * i] = a[i];
             f[2 * i + 1] = b[i];
         }
-        st_some<T, 2 * V>(head + p.a, 2 * p.na, f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            a[i] = p.turns ? f[i] : a[i];
+            b[i] = p.turns ? f[V + i] : b[i];
+        }
+    }
+    if (p.idle) return;
+    if (kEven || p.left >= (p.turns ? V : 2 * V)) {
+        Pack<T, V> v;
+        st_pack<T, V>(&v.e[0], a);
+        __builtin_memcpy(head + p.a, &v, sizeof v);
+        st_pack<T, V>(&v.e[0], b);
+        __builtin_memcpy(head + p.b, &v, sizeof v);
     } else {
-        st_some<T, V>(head + p.a, p.na, a);
-        st_some<T, V>(head + p.b, p.nb, b);
+        const bool row = !p.turns || kInter;
+        const int n = p.turns && kInter ? 2 * p.left : p.left;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (i < n) Store<T>::st(head + p.a + i, a[i]);
+            if ((row ? V + i : i) < n) Store<T>::st(head + p.b + i, b[i]);
+        }
     }
 }
+
+// A weight's values at a place, for queries or keys; loaded anew only where a
+// group of lanes goes from the ones to the others.
+template <int V>
+struct Weight {
+    float u[V], v[V];
+    int of = -1;
+    template <bool kInter, bool kEven>
+    __device__ __forceinline__ void load(const Place& p, const float* w, bool key) {
+        if (of == key) return;
+        of = key;
+        pairs_of<float, V, kInter>(p, ld_raw<float, V, kInter, kEven>(p, w), u, v);
+    }
+};
 
 // The sum over the G lanes of a group, in each of them.
 template <int G>
@@ -158,122 +213,178 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-template <int V>
-__device__ __forceinline__ void turns_of(const RotaryK& k, const Place& p, int unit, int64_t row, float (&s)[V],
-                                         float (&c)[V]) {
+// Sines and cosines of a row's pairs: a pair a lane, then to where they are
+// wanted through the wave's own LDS (each lane forming its V of them was half of
+// the whole forward's time).
+constexpr int kMaxPairs = GSPN_ROTARY_MAX_HEAD / 2;
+
+template <int V, bool kInter>
+__device__ __forceinline__ void turns_of(const RotaryK& k, const Place& p, int64_t row, float (*table)[kMaxPairs],
+                                         float (&s)[V], float (&c)[V]) {
+    const int lane = threadIdx.x & 63;
+    for (int j = lane; j < k.pairs; j += 64) {
+        int axis = 0;
+#pragma unroll
+        for (int x = 0; x < GSPN_ROTARY_MAX_AXES - 1; ++x) axis += x + 1 < k.axes && j >= k.upto[x];
+        const double t = static_cast<double>(k.pos[row * k.ldpos + axis]) * k.freqs[j];
+        sincos_turn(t * 0.15915494309189533577, &table[0][j], &table[1][j]);
+    }
+    __builtin_amdgcn_wave_barrier();
+    const int at = kInter ? p.a / 2 : p.a;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        s[i] = 0.0f;
-        c[i] = 1.0f;
-        const int j = unit * V + i;
-        if (p.turns && i < p.na) {
-            int axis = 0;
-#pragma unroll
-            for (int x = 0; x < GSPN_ROTARY_MAX_AXES - 1; ++x) axis += x + 1 < k.axes && j >= k.upto[x];
-            const double t = static_cast<double>(k.pos[row * k.ldpos + axis]) * k.freqs[j];
-            sincos_turn(t * 0.15915494309189533577, &s[i], &c[i]);
-        }
+        const bool in = p.turns && i < p.left;
+        s[i] = in ? table[0][at + i] : 0.0f;
+        c[i] = in ? table[1][at + i] : 1.0f;
     }
+    __builtin_amdgcn_wave_barrier();
 }
 
-template <typename T, int V, int G>
+// The heads of a row that a group of lanes takes, queries first.
+struct HeadAt {
+    bool key;
+    int head;
+    int64_t in;  // elements into its tensor's row
+};
+
+__device__ __forceinline__ HeadAt head_at(const RotaryK& k, int h) {
+    HeadAt w;
+    w.key = h >= k.heads;
+    w.head = w.key ? h - k.heads : h;
+    w.in = static_cast<int64_t>(w.head) * k.d;
+    return w;
+}
+
+template <typename T, int V, int G, bool kInter, bool kEven>
 __global__ __launch_bounds__(kRotaryThreads) void rotary_fwd_kernel(const RotaryK k) {
-    const int lane = threadIdx.x & 63, unit = lane % G;
-    const Place p = place_of<V>(k, unit);
-    const int total = k.heads + k.kv_heads;
+    __shared__ float table[kRotaryWaves][2][kMaxPairs];
+    const int lane = threadIdx.x & 63, unit = lane % G, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Place p = place_of<V, kInter, kEven>(k, unit);
+    const int total = k.heads + k.kv_heads, step = k.slices * (64 / G);
+    Weight<V> wt;
     const int64_t waves = static_cast<int64_t>(gridDim.x) * kRotaryWaves;
-    for (int64_t id = static_cast<int64_t>(blockIdx.x) * kRotaryWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-         id < static_cast<int64_t>(k.rows) * k.slices; id += waves) {
-    const int64_t row = id / k.slices;
-    const int slice = static_cast<int>(id - row * k.slices);
-    float s[V], c[V];
-    turns_of<V>(k, p, unit, row, s, c);
-    for (int h = slice * (64 / G) + lane / G; h < total; h += k.slices * (64 / G)) {
-        const bool key = h >= k.heads;
-        const int hh = key ? h - k.heads : h;
-        const T* const x = static_cast<const T*>(key ? k.k : k.q) + row * (key ? k.ldk : k.ldq) + hh * k.d;
-        T* const y = static_cast<T*>(key ? k.k_out : k.q_out) + row * (key ? k.ldko : k.ldqo) + hh * k.d;
-        const float* const w = key ? k.kw : k.qw;
-        float a[V], b[V];
-        ld_pairs<T, V>(k, p, x, a, b);
-        if (w) {
-            float u[V], v[V], sum = 0.0f;
-            ld_pairs<float, V>(k, p, w, u, v);
+    for (int64_t id = static_cast<int64_t>(blockIdx.x) * kRotaryWaves + wave; id < static_cast<int64_t>(k.rows) * k.slices;
+         id += waves) {
+        const int64_t row = id / k.slices;
+        int h = static_cast<int>(id - row * k.slices) * (64 / G) + lane / G;
+        const auto load = [&](int at) {
+            const HeadAt w = head_at(k, at);
+            return ld_raw<T, V, kInter, kEven>(p, static_cast<const T*>(w.key ? k.k : k.q) + row * (w.key ? k.ldk : k.ldq) + w.in);
+        };
+        // two heads are on their way while one is worked on
+        Raw<T, V> x, next;
+        if (h < total) x = load(h);
+        if (h + step < total) next = load(h + step);
+        float s[V], c[V];
+        turns_of<V, kInter>(k, p, row, table[wave], s, c);
+        for (; h < total; h += step) {
+            const HeadAt w = head_at(k, h);
+            float a[V], b[V];
+            pairs_of<T, V, kInter>(p, x, a, b);
+            x = next;
+            if (h + 2 * step < total) next = load(h + 2 * step);
+            const float* const weight = w.key ? k.kw : k.qw;
+            if (weight) {
+                float sum = 0.0f;
+                wt.template load<kInter, kEven>(p, weight, w.key);
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum = __builtin_fmaf(a[i], a[i], __builtin_fmaf(b[i], b[i], sum));
-            const float r = 1.0f / __builtin_sqrtf(group_sum<G>(sum) / static_cast<float>(k.d) + k.eps);
+                for (int i = 0; i < V; ++i) {
+                    sum = __builtin_fmaf(own_a<V, kEven>(p, i) ? a[i] : 0.0f, a[i], sum);
+                    sum = __builtin_fmaf(own_b<V, kEven>(p, i) ? b[i] : 0.0f, b[i], sum);
+                }
+                const float r = 1.0f / __builtin_sqrtf(group_sum<G>(sum) / static_cast<float>(k.d) + k.eps);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                a[i] *= r * u[i];
-                b[i] *= r * v[i];
+                for (int i = 0; i < V; ++i) {
+                    a[i] *= r * wt.u[i];
+                    b[i] *= r * wt.v[i];
+                }
             }
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float t = a[i];
             if (p.turns) {
-                a[i] = t * c[i] - b[i] * s[i];
-                b[i] = t * s[i] + b[i] * c[i];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float t = a[i];
+                    a[i] = t * c[i] - b[i] * s[i];
+                    b[i] = t * s[i] + b[i] * c[i];
+                }
             }
+            st_pairs<T, V, kInter, kEven>(p, static_cast<T*>(w.key ? k.k_out : k.q_out) + row * (w.key ? k.ldko : k.ldqo) + w.in, a, b);
         }
-        st_pairs<T, V>(k, p, y, a, b);
-    }
     }
 }
 
 // g turned back is the gradient of the normalised head; with n = x r,
 // r = 1 / rms(x): dweight = sum g n, dx = r (g w - n mean(g w n)).
-template <typename T, int V, int G>
+template <typename T, int V, int G, bool kInter, bool kEven>
 __global__ __launch_bounds__(kRotaryThreads) void rotary_bwd_kernel(const RotaryK k) {
-    __shared__ float sums[kRotaryWaves][64][4 * V];
+    __shared__ float lds[kRotaryWaves][64 * 4 * V];
+    static_assert(64 * 4 * V >= 2 * kMaxPairs);
     const int lane = threadIdx.x & 63, unit = lane % G, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const Place p = place_of<V>(k, unit);
-    const int total = k.heads + k.kv_heads;
+    float(*const table)[kMaxPairs] = reinterpret_cast<float(*)[kMaxPairs]>(lds[wave]);
+    const Place p = place_of<V, kInter, kEven>(k, unit);
+    const int total = k.heads + k.kv_heads, step = k.slices * (64 / G);
     float wa[2][V], wb[2][V];  // gradients of the weights
 #pragma unroll
     for (int i = 0; i < V; ++i) wa[0][i] = wb[0][i] = wa[1][i] = wb[1][i] = 0.0f;
+    Weight<V> wt;
     const int64_t waves = static_cast<int64_t>(gridDim.x) * kRotaryWaves;
     for (int64_t id = static_cast<int64_t>(blockIdx.x) * kRotaryWaves + wave; id < static_cast<int64_t>(k.rows) * k.slices;
          id += waves) {
         const int64_t row = id / k.slices;
-        const int slice = static_cast<int>(id - row * k.slices);
+        int h = static_cast<int>(id - row * k.slices) * (64 / G) + lane / G;
+        struct Both {
+            Raw<T, V> g, x;
+        };
+        const auto load = [&](int at) {
+            const HeadAt w = head_at(k, at);
+            Both r;
+            r.g = ld_raw<T, V, kInter, kEven>(p, static_cast<const T*>(w.key ? k.gk : k.gq) + row * (w.key ? k.ldgk : k.ldgq) + w.in);
+            if (w.key ? k.kw : k.qw)
+                r.x = ld_raw<T, V, kInter, kEven>(p, static_cast<const T*>(w.key ? k.k : k.q) + row * (w.key ? k.ldk : k.ldq) + w.in);
+            return r;
+        };
+        Both now, next;
+        if (h < total) now = load(h);
+        if (h + step < total) next = load(h + step);
         float s[V], c[V];
-        turns_of<V>(k, p, unit, row, s, c);
-        for (int h = slice * (64 / G) + lane / G; h < total; h += k.slices * (64 / G)) {
-            const bool key = h >= k.heads;
-            const int hh = key ? h - k.heads : h;
-            const T* const g = static_cast<const T*>(key ? k.gk : k.gq) + row * (key ? k.ldgk : k.ldgq) + hh * k.d;
-            T* const dx = static_cast<T*>(key ? k.k_out : k.q_out) + row * (key ? k.ldko : k.ldqo) + hh * k.d;
-            const float* const w = key ? k.kw : k.qw;
-            float ga[V], gb[V];
-            ld_pairs<T, V>(k, p, g, ga, gb);
+        turns_of<V, kInter>(k, p, row, table, s, c);
+        for (; h < total; h += step) {
+            const HeadAt w = head_at(k, h);
+            const float* const weight = w.key ? k.kw : k.qw;
+            float ga[V], gb[V], a[V], b[V];
+            pairs_of<T, V, kInter>(p, now.g, ga, gb);
+            if (weight) pairs_of<T, V, kInter>(p, now.x, a, b);
+            now = next;
+            if (h + 2 * step < total) next = load(h + 2 * step);
+            if (p.turns) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float t = ga[i];
-                if (p.turns) {
+                for (int i = 0; i < V; ++i) {
+                    const float t = ga[i];
                     ga[i] = t * c[i] + gb[i] * s[i];
                     gb[i] = gb[i] * c[i] - t * s[i];
                 }
             }
-            if (w) {
-                const T* const x = static_cast<const T*>(key ? k.k : k.q) + row * (key ? k.ldk : k.ldq) + hh * k.d;
-                float a[V], b[V], u[V], v[V], sum = 0.0f, dot = 0.0f;
-                ld_pairs<T, V>(k, p, x, a, b);
-                ld_pairs<float, V>(k, p, w, u, v);
+            if (weight) {
+                float sum = 0.0f, dot = 0.0f;
+                wt.template load<kInter, kEven>(p, weight, w.key);
 #pragma unroll
-                for (int i = 0; i < V; ++i) sum = __builtin_fmaf(a[i], a[i], __builtin_fmaf(b[i], b[i], sum));
+                for (int i = 0; i < V; ++i) {
+                    sum = __builtin_fmaf(own_a<V, kEven>(p, i) ? a[i] : 0.0f, a[i], sum);
+                    sum = __builtin_fmaf(own_b<V, kEven>(p, i) ? b[i] : 0.0f, b[i], sum);
+                }
                 const float r = 1.0f / __builtin_sqrtf(group_sum<G>(sum) / static_cast<float>(k.d) + k.eps);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     a[i] *= r;
                     b[i] *= r;
-                    wa[0][i] += key ? 0.0f : ga[i] * a[i];
-                    wb[0][i] += key ? 0.0f : gb[i] * b[i];
-                    wa[1][i] += key ? ga[i] * a[i] : 0.0f;
-                    wb[1][i] += key ? gb[i] * b[i] : 0.0f;
-                    ga[i] *= u[i];
-                    gb[i] *= v[i];
-                    dot = __builtin_fmaf(ga[i], a[i], __builtin_fmaf(gb[i], b[i], dot));
+                    const float x = ga[i] * a[i], y = gb[i] * b[i];
+                    wa[0][i] += w.key ? 0.0f : x;
+                    wb[0][i] += w.key ? 0.0f : y;
+                    wa[1][i] += w.key ? x : 0.0f;
+                    wb[1][i] += w.key ? y : 0.0f;
+                    ga[i] *= wt.u[i];
+                    gb[i] *= wt.v[i];
+                    dot = __builtin_fmaf(own_a<V, kEven>(p, i) ? ga[i] : 0.0f, a[i], dot);
+                    dot = __builtin_fmaf(own_b<V, kEven>(p, i) ? gb[i] : 0.0f, b[i], dot);
                 }
                 dot = group_sum<G>(dot) / static_cast<float>(k.d);
 #pragma unroll
@@ -282,33 +393,34 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_bwd_kernel(const Rotary
                     gb[i] = r * (gb[i] - b[i] * dot);
                 }
             }
-            st_pairs<T, V>(k, p, dx, ga, gb);
+            st_pairs<T, V, kInter, kEven>(p, static_cast<T*>(w.key ? k.k_out : k.q_out) + row * (w.key ? k.ldko : k.ldqo) + w.in, ga,
+                           gb);
         }
     }
     if (!k.part) return;
+    __syncthreads();
+    float(*const sums)[4 * V] = reinterpret_cast<float(*)[4 * V]>(lds[wave]);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        sums[wave][lane][i] = wa[0][i];
-        sums[wave][lane][V + i] = wb[0][i];
-        sums[wave][lane][2 * V + i] = wa[1][i];
-        sums[wave][lane][3 * V + i] = wb[1][i];
+        sums[lane][i] = wa[0][i];
+        sums[lane][V + i] = wb[0][i];
+        sums[lane][2 * V + i] = wa[1][i];
+        sums[lane][3 * V + i] = wb[1][i];
     }
     __syncthreads();
     // one lane a unit and value, over the groups and waves in order
     for (int at = threadIdx.x; at < G * 4 * V; at += kRotaryThreads) {
-        const int u = at / (4 * V), i = at % (4 * V);
+        const int u = at / (4 * V), i = at % (4 * V), e = i % V;
+        const bool second = i / V % 2;
+        const Place z = place_of<V, kInter, kEven>(k, u);
+        if (z.idle || !(second ? own_b<V, kEven>(z, e) : own_a<V, kEven>(z, e))) continue;
         float t = 0.0f;
         for (int w = 0; w < kRotaryWaves; ++w)
-            for (int g = 0; g < 64 / G; ++g) t += sums[w][g * G + u][i];
-        const Place z = place_of<V>(k, u);
-        const int e = i % V;
-        const bool second = i / V % 2;
-        if (e >= (second ? z.nb : z.na)) continue;
-        const int col = z.turns && k.interleaved ? z.a + 2 * e + second : (second ? z.b : z.a) + e;
+            for (int g = 0; g < 64 / G; ++g) t += reinterpret_cast<float(*)[4 * V]>(lds[w])[g * G + u][i];
+        const int col = z.turns && kInter ? z.a + 2 * e + second : (second ? z.b : z.a) + e;
         k.part[(static_cast<int64_t>(blockIdx.x) * 2 + i / (2 * V)) * k.d + col] = t;
     }
 }
-
 
 RotaryK make_rotary(const gspn_rotary_args& a) {
     RotaryK k = {};
@@ -341,26 +453,43 @@ int slices_for(int64_t rows, int64_t heads, int group) {
     return static_cast<int>(want < most ? want : most);
 }
 
-// Calls f with the storage type, the pairs a lane takes (16 bytes of them) and
-// the lanes of a head.
+// Calls f with the storage type, the pairs a lane takes (16 bytes of them, or 8
+// where only those come out even: heads of 72 bf16 elements), the lanes of a head,
+// and the two flags.
 template <typename F>
 void rotary_dispatch(int dtype, const RotaryK& k, F&& f) {
-    const auto lanes = [&](auto t, auto v) {
-        constexpr int V = decltype(v)::value;
-        const int units = (k.pairs + V - 1) / V + (k.d - 2 * k.pairs + 2 * V - 1) / (2 * V);
-        if (units <= 8)
-            f(t, v, std::integral_constant<int, 8>{});
-        else if (units <= 16)
-            f(t, v, std::integral_constant<int, 16>{});
-        else if (units <= 32)
-            f(t, v, std::integral_constant<int, 32>{});
+    const int rest = k.d - 2 * k.pairs;
+    const auto flags = [&](auto t, auto v, auto g, auto even) {
+        if (k.interleaved)
+            f(t, v, g, std::true_type{}, even);
         else
-            f(t, v, std::integral_constant<int, 64>{});
+            f(t, v, g, std::false_type{}, even);
     };
-    if (dtype == GSPN_F32)
-        lanes(float{}, std::integral_constant<int, 4>{});
-    else
-        lanes(bf16_t{}, std::integral_constant<int, 8>{});
+    const auto lanes = [&](auto t, auto v, auto even) {
+        constexpr int V = decltype(v)::value;
+        const int units = (k.pairs + V - 1) / V + (rest + 2 * V - 1) / (2 * V);
+        if (units <= 8)
+            flags(t, v, std::integral_constant<int, 8>{}, even);
+        else if (units <= 16)
+            flags(t, v, std::integral_constant<int, 16>{}, even);
+        else if (decltype(even)::value || units <= 32)
+            flags(t, v, std::integral_constant<int, 32>{}, even);
+        else if constexpr (!decltype(even)::value)
+            flags(t, v, std::integral_constant<int, 64>{}, even);
+    };
+    const auto even = [&](int v) { return k.pairs % v == 0 && rest % (2 * v) == 0; };
+    if (dtype == GSPN_F32) {
+        if (even(4))
+            lanes(float{}, std::integral_constant<int, 4>{}, std::true_type{});
+        else
+            lanes(float{}, std::integral_constant<int, 4>{}, std::false_type{});
+    } else if (even(8)) {
+        lanes(bf16_t{}, std::integral_constant<int, 8>{}, std::true_type{});
+    } else if (even(4)) {
+        lanes(bf16_t{}, std::integral_constant<int, 4>{}, std::true_type{});
+    } else {
+        lanes(bf16_t{}, std::integral_constant<int, 8>{}, std::false_type{});
+    }
 }
 
 void replay(const char* kn, const gspn_rotary_args& a, bool bwd, int64_t es) {
@@ -398,14 +527,15 @@ hipError_t launch_rotary_fwd(const gspn_rotary_args& a, int dtype, hipStream_t s
     replay("rotary_fwd_kernel", a, false, es);
     GSPN_REPLAY_ROWS("rotary_fwd_kernel", "q_out", a.q_out, a.rows, a.ldqo, a.heads * a.d, es);
     GSPN_REPLAY_ROWS("rotary_fwd_kernel", "k_out", a.k_out, a.rows, a.ldko, a.kv_heads * a.d, es);
-    rotary_dispatch(dtype, k, [&](auto t, auto v, auto g) {
+    rotary_dispatch(dtype, k, [&](auto t, auto v, auto g, auto inter, auto even) {
         using T = decltype(t);
         constexpr int V = decltype(v)::value, G = decltype(g)::value;
+        constexpr bool kInter = decltype(inter)::value, kEven = decltype(even)::value;
         k.slices = slices_for(a.rows, a.heads + a.kv_heads, G);
         const int64_t blocks = (a.rows * k.slices + kRotaryWaves - 1) / kRotaryWaves;
         const dim3 grid(static_cast<unsigned>(blocks < kRotaryBlocks ? blocks : kRotaryBlocks));
         GSPN_REPLAYED("rotary_fwd_kernel", kRotaryThreads, 0);
-        hipLaunchKernelGGL((rotary_fwd_kernel<T, V, G>), grid, dim3(kRotaryThreads), 0, stream, k);
+        hipLaunchKernelGGL((rotary_fwd_kernel<T, V, G, kInter, kEven>), grid, dim3(kRotaryThreads), 0, stream, k);
     });
     return hipGetLastError();
 }
@@ -430,12 +560,13 @@ hipError_t launch_rotary_bwd(const gspn_rotary_args& a, int dtype, hipStream_t s
         GSPN_REPLAY_ROWS("rotary_bwd_kernel", "gk", a.gk, a.rows, a.ldgk, a.kv_heads * a.d, es);
         GSPN_REPLAY_ROWS("rotary_bwd_kernel", "dk", a.dk, a.rows, a.lddk, a.kv_heads * a.d, es);
         if (sums) GSPN_REPLAY_ROWS("rotary_bwd_kernel", "partial sums", a.workspace, parts, 2 * a.d, 2 * a.d, 4);
-        rotary_dispatch(dtype, k, [&](auto t, auto v, auto g) {
+        rotary_dispatch(dtype, k, [&](auto t, auto v, auto g, auto inter, auto even) {
             using T = decltype(t);
             constexpr int V = decltype(v)::value, G = decltype(g)::value;
+        constexpr bool kInter = decltype(inter)::value, kEven = decltype(even)::value;
             k.slices = slices_for(a.rows, a.heads + a.kv_heads, G);
             GSPN_REPLAYED("rotary_bwd_kernel", kRotaryThreads, kRotaryThreads * 4 * V * 4);
-            hipLaunchKernelGGL((rotary_bwd_kernel<T, V, G>), dim3(static_cast<unsigned>(parts)), dim3(kRotaryThreads), 0,
+            hipLaunchKernelGGL((rotary_bwd_kernel<T, V, G, kInter, kEven>), dim3(static_cast<unsigned>(parts)), dim3(kRotaryThreads), 0,
                                stream, k);
         });
         const hipError_t e = hipGetLastError();
