@@ -117,22 +117,37 @@ __global__ __launch_bounds__(kAttnThreads) void attn_append_kernel(const AttnK a
     if (keys.state != 0) return;
     constexpr int kE = 16 / sizeof(T);
     const int width = a.kv_heads * a.d;
-    const int chunks = (width + kE - 1) / kE;
     const int64_t at = keys.count - (c.end - c.begin) + (c.r0 - c.begin);
-    for (int i = threadIdx.x; i < (c.r1 - c.r0) * chunks; i += kAttnThreads) {
-        const int r = i / chunks, e = (i - r * chunks) * kE;
+    const uint32_t chunks = width / kE;  // whole ones of a row; keys' and values' rows in turn
+    const uint32_t all = 2 * (c.r1 - c.r0) * chunks;
+    const auto place = [&](uint32_t row, int e, const T** from, T** to) {
+        const int r = row >> 1, value = row & 1;
+        *from = static_cast<const T*>(value ? a.v : a.k) + (c.r0 + r) * (value ? a.ldv : a.ldk) + e;
+        *to = const_cast<T*>(static_cast<const T*>(value ? keys.v : keys.k)) + (at + r) * width + e;
+    };
+    constexpr int kAhead = 4;
+    for (uint32_t i0 = threadIdx.x; i0 < all; i0 += kAhead * kAttnThreads) {
+        Quad x[kAhead];
+        T* to[kAhead];
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            const T* const from = static_cast<const T*>(v ? a.v : a.k) + (c.r0 + r) * (v ? a.ldv : a.ldk) + e;
-            T* const to = const_cast<T*>(static_cast<const T*>(v ? keys.v : keys.k)) + (at + r) * width + e;
-            if (e + kE <= width) {
-                Quad x;
-                __builtin_memcpy(&x, from, 16);
-                __builtin_memcpy(to, &x, 16);
-            } else {
-                for (int j = 0; j < width - e; ++j) to[j] = from[j];
-            }
+        for (int j = 0; j < kAhead; ++j) {
+            const uint32_t i = i0 + j * kAttnThreads < all ? i0 + j * kAttnThreads : i0;
+            const T* from;
+            place(i / chunks, i % chunks * kE, &from, &to[j]);
+            __builtin_memcpy(&x[j], from, 16);
         }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) asm volatile("" : "+v"(x[j]));  // all on their way before the first store
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (i0 + j * kAttnThreads < all) __builtin_memcpy(to[j], &x[j], 16);
+    }
+    const int rest = width - chunks * kE;
+    for (int i = threadIdx.x; i < 2 * (c.r1 - c.r0) * rest; i += kAttnThreads) {
+        const T* from;
+        T* to;
+        place(i / rest, chunks * kE + i % rest, &from, &to);
+        *to = *from;
     }
 }
 

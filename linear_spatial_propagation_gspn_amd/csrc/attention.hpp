@@ -27,7 +27,7 @@ constexpr int kAttnRows = 1 << kAttnShift;
 constexpr int kAttnThreads = 256;
 constexpr int kKeyShift = 6;     // keys of a workgroup of their gradients
 constexpr int kKeyRows = 1 << kKeyShift;
-constexpr int kAppendShift = 5;  // 32 rows a workgroup go into their entries
+constexpr int kAppendShift = 3;  // 8 rows a workgroup go into their entries
 
 struct AttnK {
     SeqK seq, kv;
