@@ -99,72 +99,73 @@ def _call(name: str, args: ctypes.Structure, dtype: int, index: int) -> None:
         G._raise(st, name)
 
 
-def _need_heads(x, name: str) -> int:
+def _need_heads(x, name: str) -> tuple:
+    """A [.., heads, d] tensor's shape, device index and storage type."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if x.dim() not in (3, 4):
-        raise ValueError("%s must be [rows, heads, d] or [batch, length, heads, d], got %s" % (name, tuple(x.shape)))
-    if x.get_device() < 0:
+    shape, dev = x.shape, x.get_device()
+    if len(shape) not in (3, 4):
+        raise ValueError("%s must be [rows, heads, d] or [batch, length, heads, d], got %s" % (name, tuple(shape)))
+    if dev < 0:
         raise ValueError("%s must live on a HIP device" % name)
-    if x.shape[-1] < 1 or x.shape[-2] < 1:
-        raise ValueError("%s must have at least one head of at least one element, got %s" % (name, tuple(x.shape)))
-    return G._dtype_code(x)
+    if shape[-1] < 1 or shape[-2] < 1:
+        raise ValueError("%s must have at least one head of at least one element, got %s" % (name, tuple(shape)))
+    return shape, dev, G._dtype_code(x)
 
 
-def _shape_of(x, like, name: str) -> tuple:
-    """The shape of x's companion rows: like's rows, x's own heads."""
-    if not isinstance(x, torch.Tensor) or x.dim() != like.dim():
-        raise ValueError("%s must be a tensor of %d dimensions" % (name, like.dim()))
-    return (*like.shape[:-2], x.shape[-2], like.shape[-1])
+def _heads_beside(x, shape, name: str) -> int:
+    """The heads of a companion of rows of ``shape``."""
+    if not isinstance(x, torch.Tensor) or x.dim() != len(shape):
+        raise ValueError("%s must be a tensor of %d dimensions" % (name, len(shape)))
+    return x.shape[-2]
 
 
-def _new_rows(x) -> torch.Tensor:
-    return torch.empty_like(x, memory_format=torch.contiguous_format)
-
-
-def _out_rows(out, x, name: str) -> tuple:
+def _out_rows(out, x, shape, dev: int, name: str) -> tuple:
     """Rows of x's shape to write to, new ones if not given: the tensor, its pointer and row stride."""
     if out is None:
-        out = _new_rows(x)
-        return out, out.data_ptr(), x.shape[-1] * x.shape[-2]
-    return (out, *S._ptr_rows(out, name, x.shape, x.dtype, x.get_device(), 2))
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        return out, out.data_ptr(), shape[-1] * shape[-2]
+    return (out, *S._ptr_rows(out, name, shape, x.dtype, dev, 2))
 
 
 # ------------------------------------------------------------------------------------------------ head rotary
 
-def _rotary_args(q, positions, freqs, k, q_weight, k_weight, sections, interleaved, eps, read: bool = True) -> RotaryArgs:
-    dev, d = q.get_device(), q.shape[-1]
-    a = RotaryArgs()
-    a.heads, a.d = q.shape[-2], d
-    a.rows = q.numel() // (a.heads * d)
-    a.interleaved, a.eps = 1 if interleaved else 0, float(eps)
-    S._tensor(freqs, "freqs", torch.float64, dev)
-    a.freqs, a.pairs = S._flat(freqs, "freqs", (freqs.numel(),), torch.float64, dev), freqs.numel()
-    sections = (a.pairs,) if sections is None else tuple(int(n) for n in sections)
-    if not 1 <= len(sections) <= GSPN_ROTARY_MAX_AXES or sum(sections) != a.pairs or min(sections) < 0:
-        raise ValueError("sections %s must share out %d pairs among 1 to %d axes" % (sections, a.pairs,
+_Sections = _i64 * GSPN_ROTARY_MAX_AXES
+
+
+def _rotary_args(shape, dev, q, positions, freqs, k, q_weight, k_weight, sections, interleaved, eps,
+                 read: bool = True) -> RotaryArgs:
+    """The arguments up to the outputs."""
+    d, heads, lead, dtype = shape[-1], shape[-2], shape[:-2], q.dtype
+    rows = lead[0] if len(lead) == 1 else lead[0] * lead[1]
+    pairs = freqs.numel() if isinstance(freqs, torch.Tensor) else 0
+    pfreqs = S._flat(freqs, "freqs", (pairs,), torch.float64, dev)
+    if freqs is None:
+        raise TypeError("freqs must be a torch.Tensor")
+    sections = (pairs,) if sections is None else tuple(sections)
+    axes = len(sections)
+    if not 1 <= axes <= GSPN_ROTARY_MAX_AXES or sum(sections) != pairs or min(sections) < 0:
+        raise ValueError("sections %s must share out %d pairs among 1 to %d axes" % (sections, pairs,
                                                                                       GSPN_ROTARY_MAX_AXES))
-    if 2 * a.pairs > d:
-        raise ValueError("%d pairs do not fit into heads of %d elements" % (a.pairs, d))
-    a.axes = len(sections)
-    a.section[:len(sections)] = sections
-    S._tensor(positions, "positions", torch.int32, dev)
-    lead = tuple(q.shape[:-2])
-    if a.axes == 1 and positions.dim() == len(lead):
+    if 2 * pairs > d:
+        raise ValueError("%d pairs do not fit into heads of %d elements" % (pairs, d))
+    if axes == 1 and isinstance(positions, torch.Tensor) and positions.dim() == len(lead):
         positions = positions.unsqueeze(-1)
-    a.positions, a.ldpos = S._ptr_rows(positions, "positions", (*lead, a.axes), torch.int32, dev)
-    a.q_weight = S._flat(q_weight, "q_weight", (d,), torch.float32, dev)
-    if read or q_weight is not None:
-        a.q, a.ldq = S._ptr_rows(q, "q", q.shape, q.dtype, dev, 2)
+    ppos, ldpos = S._ptr_rows(positions, "positions", (*lead, axes), torch.int32, dev)
+    pqw = S._flat(q_weight, "q_weight", (d,), torch.float32, dev)
+    pq = ldq = pk = ldk = kv_heads = 0
+    pkw = None
+    if read or pqw is not None:
+        pq, ldq = S._ptr_rows(q, "q", shape, dtype, dev, 2)
     if k is not None:
-        shape = _shape_of(k, q, "k")
-        a.kv_heads = shape[-2]
-        a.k_weight = S._flat(k_weight, "k_weight", (d,), torch.float32, dev)
-        if read or k_weight is not None:
-            a.k, a.ldk = S._ptr_rows(k, "k", shape, q.dtype, dev, 2)
+        kv_heads = _heads_beside(k, shape, "k")
+        pkw = S._flat(k_weight, "k_weight", (d,), torch.float32, dev)
+        if read or pkw is not None:
+            pk, ldk = S._ptr_rows(k, "k", (*lead, kv_heads, d), dtype, dev, 2)
     elif k_weight is not None:
         raise ValueError("k_weight needs k")
-    return a
+    return RotaryArgs(rows, heads, kv_heads, d, pairs, axes, 1 if interleaved else 0, _Sections(*sections), eps, pq, ldq, pk,
+                      ldk, pqw, pkw, ppos, ldpos, pfreqs)
 
 
 def gspn_head_rotary_fwd(q, positions, freqs, k=None, q_weight=None, k_weight=None, sections=None,
@@ -176,14 +177,14 @@ def gspn_head_rotary_fwd(q, positions, freqs, k=None, q_weight=None, k_weight=No
     elements behind the pairs are not turned.  ``positions``: int32 [rows, axes]
     ([rows] for one axis); ``sections``: how many pairs, in order, turn by each
     axis (default: all by one).  Returns (q, k) turned, k None without k."""
-    dt = _need_heads(q, "q")
-    a = _rotary_args(q, positions, freqs, k, q_weight, k_weight, sections, interleaved, eps)
-    out, a.q_out, a.ldqo = _out_rows(out, q, "out")
+    shape, dev, dt = _need_heads(q, "q")
+    a = _rotary_args(shape, dev, q, positions, freqs, k, q_weight, k_weight, sections, interleaved, eps)
+    out, a.q_out, a.ldqo = _out_rows(out, q, shape, dev, "out")
     if k is not None:
-        out_k, a.k_out, a.ldko = _out_rows(out_k, k, "out_k")
+        out_k, a.k_out, a.ldko = _out_rows(out_k, k, k.shape, dev, "out_k")
     elif out_k is not None:
         raise ValueError("out_k needs k")
-    _call("gspn_head_rotary_fwd", a, dt, q.get_device())
+    _call("gspn_head_rotary_fwd", a, dt, dev)
     return out, out_k
 
 
@@ -192,15 +193,14 @@ def gspn_head_rotary_bwd(q, positions, freqs, gq, k=None, gk=None, q_weight=None
     """Gradients of gspn_head_rotary_fwd for dL/dq_out = gq, dL/dk_out = gk:
     (dq, dk, dq_weight, dk_weight), None for what was not given.  q and k are
     read where they are normalised."""
-    dt = _need_heads(q, "q")
-    dev = q.get_device()
-    a = _rotary_args(q, positions, freqs, k, q_weight, k_weight, sections, interleaved, eps, read=False)
-    a.gq, a.ldgq = S._ptr_rows(gq, "gq", q.shape, q.dtype, dev, 2)
-    dq, a.dq, a.lddq = _out_rows(None, q, "dq")
+    shape, dev, dt = _need_heads(q, "q")
+    a = _rotary_args(shape, dev, q, positions, freqs, k, q_weight, k_weight, sections, interleaved, eps, read=False)
+    a.gq, a.ldgq = S._ptr_rows(gq, "gq", shape, q.dtype, dev, 2)
+    dq, a.dq, a.lddq = _out_rows(None, q, shape, dev, "dq")
     dk = None
     if k is not None:
         a.gk, a.ldgk = S._ptr_rows(gk, "gk", k.shape, q.dtype, dev, 2)
-        dk, a.dk, a.lddk = _out_rows(None, k, "dk")
+        dk, a.dk, a.lddk = _out_rows(None, k, k.shape, dev, "dk")
     elif gk is not None:
         raise ValueError("gk needs k")
     dqw, dkw = (None if w is None else S._new_like(w) for w in (q_weight, k_weight))
@@ -214,38 +214,32 @@ def gspn_head_rotary_bwd(q, positions, freqs, gq, k=None, gk=None, q_weight=None
 
 # -------------------------------------------------------------------------------------------------- attention
 
-def _rows_of(x):
-    """A stand-in of x's rows for the sequences' checks: [rows, heads] or [batch, length, heads]."""
-    return x[..., 0]
-
-
-def _attn_args(q, k, v, causal, scale, cu, nseq, cu_k, state=None, slots=None) -> AttnArgs:
-    dev, dtype, d = q.get_device(), q.dtype, q.shape[-1]
-    if not isinstance(k, torch.Tensor) or k.dim() != q.dim():
-        raise ValueError("k must be a tensor of %d dimensions" % q.dim())
-    a = AttnArgs()
-    a.seq = S._sequences(_rows_of(q), cu, nseq, None if state is None else state[0], slots)
-    a.heads, a.kv_heads, a.d, a.causal = q.shape[-2], k.shape[-2], d, 1 if causal else 0
-    a.scale = d ** -0.5 if scale is None else float(scale)
-    if a.kv_heads < 1 or a.heads % a.kv_heads:
-        raise ValueError("%d heads are not equal groups for %d of keys" % (a.heads, a.kv_heads))
-    lead = tuple(k.shape[:-2])
-    a.kv_rows = math.prod(lead)
+def _attn_args(shape, dev, q, k, v, causal, scale, cu, nseq, cu_k, state=None, slots=None) -> AttnArgs:
+    """The arguments up to the output."""
+    dtype, d, heads = q.dtype, shape[-1], shape[-2]
+    kv_heads = _heads_beside(k, shape, "k")
+    seq = S._sequences_of(shape[:-2], dev, cu, nseq, None if state is None else state[0], slots)
+    scale = d ** -0.5 if scale is None else float(scale)
+    if kv_heads < 1 or heads % kv_heads:
+        raise ValueError("%d heads are not equal groups for %d of keys" % (heads, kv_heads))
+    lead = k.shape[:-2]
+    kv_rows = lead[0] if len(lead) == 1 else lead[0] * lead[1]
+    kv_cu = None
     if cu_k is not None:
-        if q.dim() != 3:
+        if len(shape) != 3:
             raise ValueError("cu_k goes with [rows, heads, d] tensors")
-        S._tensor(cu_k, "cu_k", torch.int32, dev)
-        a.kv_cu = S._flat(cu_k, "cu_k", (a.seq.nseq + 1,), torch.int32, dev)
-    elif q.dim() == 4 and lead[0] != q.shape[0]:
-        raise ValueError("q holds %d sequences, k %d" % (q.shape[0], lead[0]))
-    elif cu is not None and a.kv_rows != a.seq.rows:
-        raise ValueError("keys of other lengths than the queries' need cu_k")
-    elif cu is None and a.seq.nseq and a.kv_rows % a.seq.nseq:
-        raise ValueError("%d rows of keys are not %d equal sequences" % (a.kv_rows, a.seq.nseq))
-    a.q, a.ldq = S._ptr_rows(q, "q", q.shape, dtype, dev, 2)
-    a.k, a.ldk = S._ptr_rows(k, "k", (*lead, a.kv_heads, d), dtype, dev, 2)
-    a.v, a.ldv = S._ptr_rows(v, "v", (*lead, a.kv_heads, d), dtype, dev, 2)
-    return a
+        kv_cu = S._flat(cu_k, "cu_k", (seq.nseq + 1,), torch.int32, dev)
+    elif len(lead) == 2 and lead[0] != shape[0]:
+        raise ValueError("q holds %d sequences, k %d" % (shape[0], lead[0]))
+    elif cu is not None:
+        if kv_rows != seq.rows:
+            raise ValueError("keys of other lengths than the queries' need cu_k")
+    elif seq.nseq and kv_rows % seq.nseq:
+        raise ValueError("%d rows of keys are not %d equal sequences" % (kv_rows, seq.nseq))
+    kshape = (*lead, kv_heads, d)
+    return AttnArgs(seq, kv_rows, kv_cu, heads, kv_heads, d, 1 if causal else 0, scale,
+                    *S._ptr_rows(q, "q", shape, dtype, dev, 2), *S._ptr_rows(k, "k", kshape, dtype, dev, 2),
+                    *S._ptr_rows(v, "v", kshape, dtype, dev, 2))
 
 
 def _cache(a: AttnArgs, q, state, held) -> None:
@@ -282,15 +276,14 @@ def gspn_attention_fwd(q, k, v, causal: bool = True, scale=None, cu=None, nseq=N
     or an fp32 [heads, rows] tensor): also the logarithms of the softmax's sums
     for gspn_attention_bwd; the call then returns (out, lse).  Rows outside the
     sequences of ``cu`` are left as they are in ``out``."""
-    dt = _need_heads(q, "q")
-    dev = q.get_device()
+    shape, dev, dt = _need_heads(q, "q")
     state = _pools(state)
-    a = _attn_args(q, k, v, causal, scale, cu, nseq, cu_k, state, slots)
+    a = _attn_args(shape, dev, q, k, v, causal, scale, cu, nseq, cu_k, state, slots)
     if state is not None:
         _cache(a, q, state, held)
     elif held is not None:
         raise ValueError("held counts rows of a cache: pass state")
-    out, a.out, a.ldo = _out_rows(out, q, "out")
+    out, a.out, a.ldo = _out_rows(out, q, shape, dev, "out")
     keep = lse is not None and lse is not False
     if keep:
         if lse is True:
@@ -305,17 +298,17 @@ def gspn_attention_step(q, k, v, state, held, slots=None, scale=None, out=None, 
     the new key and value go behind the ``held`` rows of the sequence's cache
     entry, and the row attends to all of them.  Padding rows (negative slot) are
     left as they are in ``out``."""
-    dt = _need_heads(q, "q")
-    if q.dim() != 3:
+    shape, dev, dt = _need_heads(q, "q")
+    if len(shape) != 3:
         raise ValueError("a step takes one row per sequence: q [nseq, heads, d]")
     state = _pools(state)
     if state is None or held is None:
         raise ValueError("a step continues a cache: pass state and held")
-    dev = q.get_device()
-    a = _attn_args(q, k, v, True, scale, None, q.shape[0] if q.shape[0] else None, None, state, slots)
+    n = shape[0]
+    a = _attn_args(shape, dev, q, k, v, True, scale, None, n if n else None, None, state, slots)
     _cache(a, q, state, held)
-    out, a.out, a.ldo = _out_rows(out, q, "out")
-    if q.shape[0]:
+    out, a.out, a.ldo = _out_rows(out, q, shape, dev, "out")
+    if n:
         need = _bytes("gspn_attention_step_workspace_bytes", a.seq.nseq, a.heads, a.kv_heads, a.d, a.capacity)
         ws = S._workspace(a, workspace, need, q) if need > 0 else None
         _call("gspn_attention_step", a, dt, dev)
@@ -327,17 +320,16 @@ def gspn_attention_bwd(q, k, v, out, lse, gout, causal: bool = True, scale=None,
     """Gradients of gspn_attention_fwd without a cache, for dL/dout = gout, from
     its ``out`` and ``lse``: (dq, dk, dv).  Rows outside the sequences have zero
     gradients."""
-    dt = _need_heads(q, "q")
-    dev = q.get_device()
-    a = _attn_args(q, k, v, causal, scale, cu, nseq, cu_k)
-    a.out, a.ldo = S._ptr_rows(out, "out", q.shape, q.dtype, dev, 2)
-    a.gout, a.ldgo = S._ptr_rows(gout, "gout", q.shape, q.dtype, dev, 2)
+    shape, dev, dt = _need_heads(q, "q")
+    a = _attn_args(shape, dev, q, k, v, causal, scale, cu, nseq, cu_k)
+    a.out, a.ldo = S._ptr_rows(out, "out", shape, q.dtype, dev, 2)
+    a.gout, a.ldgo = S._ptr_rows(gout, "gout", shape, q.dtype, dev, 2)
     if lse is None:
         raise ValueError("the backward needs the forward's lse")
     a.lse = S._flat(lse, "lse", (a.heads, a.seq.rows), torch.float32, dev)
-    dq, a.dq, a.lddq = _out_rows(None, q, "dq")
-    dk, a.dk, a.lddk = _out_rows(None, k, "dk")
-    dv, a.dv, a.lddv = _out_rows(None, v, "dv")
+    dq, a.dq, a.lddq = _out_rows(None, q, shape, dev, "dq")
+    dk, a.dk, a.lddk = _out_rows(None, k, k.shape, dev, "dk")
+    dv, a.dv, a.lddv = _out_rows(None, v, k.shape, dev, "dv")
     need = 0
     if a.seq.nseq:
         need = _bytes("gspn_attention_bwd_workspace_bytes", a.seq.rows, a.seq.nseq, a.heads, a.kv_rows, a.kv_heads, a.d)

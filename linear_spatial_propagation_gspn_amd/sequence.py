@@ -213,14 +213,18 @@ def _need_rows(x, name: str) -> int:
 
 def _sequences(x, cu, nseq, state=None, slots=None, resume=None) -> Sequences:
     """The sequences of rows x, and their pool's entries."""
-    dev = x.get_device()
+    return _sequences_of(x.shape[:-1], x.get_device(), cu, nseq, state, slots, resume)
+
+
+def _sequences_of(lead, dev: int, cu, nseq, state=None, slots=None, resume=None) -> Sequences:
+    """The sequences of rows whose leading dimensions are ``lead`` ([rows] or [batch, length])."""
     s = Sequences()
-    if x.dim() == 3:
-        if cu is not None or nseq not in (None, x.shape[0]):
-            raise ValueError("cu / nseq go with [rows, channels] tensors: a 3-D tensor's batch entries are its sequences")
-        s.rows, s.nseq = x.shape[0] * x.shape[1], x.shape[0]
+    if len(lead) == 2:
+        if cu is not None or nseq not in (None, lead[0]):
+            raise ValueError("cu / nseq go with tensors of rows: a batch's entries are its sequences")
+        s.rows, s.nseq = lead[0] * lead[1], lead[0]
     else:
-        s.rows = x.shape[0]
+        s.rows = lead[0]
         if cu is not None:
             _tensor(cu, "cu", torch.int32, dev)
             if cu.dim() != 1 or cu.numel() < 1 or not cu.is_contiguous():
