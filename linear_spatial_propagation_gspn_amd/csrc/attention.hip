@@ -54,51 +54,178 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnK a
     const T* const kp = static_cast<const T*>(keys.k);
     const T* const vp = static_cast<const T*>(keys.v);
     clear_tiles<kDirect>(tid, kAttnThreads, lds[0][0], sizeof lds, a.d == D);
-    if (tiles > 0) {
-        sk.fetch(tid, kp, keys.ldk, 0, keys.count - 1, a.d, lds[0][0]);
-        sv.fetch(tid, vp, keys.ldv, 0, keys.count - 1, a.d, lds[0][1]);
-        sk.commit(tid, lds[0][0]);
-        sv.commit(tid, lds[0][1]);
-    }
-    __syncthreads();
-    for (int t = 0; t < tiles; ++t) {
-        const bool more = t + 1 < tiles;
-        if (more) {
-            sk.fetch(tid, kp, keys.ldk, (t + 1) * BN, keys.count - 1, a.d, lds[(t + 1) & 1][0]);
-            sv.fetch(tid, vp, keys.ldv, (t + 1) * BN, keys.count - 1, a.d, lds[(t + 1) & 1][1]);
+    const int wave_tiles = (wave_keys + BN - 1) / BN;
+    const auto fetch_k = [&](int t) { sk.fetch(tid, kp, keys.ldk, t * BN, keys.count - 1, a.d, lds[t & 1][0]); };
+    const auto fetch_v = [&](int t) { sv.fetch(tid, vp, keys.ldv, t * BN, keys.count - 1, a.d, lds[t & 1][1]); };
+    const auto scores = [&](int buf, f32x16(&s)[BN / 32]) {
+        const uint32_t kt = Tl::rows_at(lds_at(lds[buf][0]));
+#pragma unroll
+        for (int n = 0; n < BN / 32; ++n) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[n][r] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < Tl::kSteps; ++i) s[n] = mma<T>(Tl::rows(kt, 32 * n, i), q[i], s[n]);
         }
-        const int key0 = t * BN;
-        if (key0 < wave_keys) {
-            const uint32_t kt = Tl::rows_at(lds_at(lds[t & 1][0]));
-            const uint32_t vt = Tl::columns_at(lds_at(lds[t & 1][1]));
-            f32x16 s[BN / 32];
+    };
+    const auto hide = [&](int t, f32x16(&s)[BN / 32]) {
+        if ((t + 1) * BN > wave_all) {
+            int most = my_keys;
+            asm volatile("" : "+v"(most));  // (or the comparisons would be made in every tile)
 #pragma unroll
-            for (int n = 0; n < BN / 32; ++n) {
+            for (int n = 0; n < BN / 32; ++n)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) s[n][r] = 0.0f;
+                for (int r = 0; r < 16; ++r)
+                    if (t * BN + 32 * n + result_row(r) >= most) s[n][r] = -INFINITY;
+        }
+    };
+    const auto values = [&](int buf, const f32x16(&s)[BN / 32]) {
+        const uint32_t vt = Tl::columns_at(lds_at(lds[buf][1]));
 #pragma unroll
-                for (int i = 0; i < Tl::kSteps; ++i) s[n] = mma<T>(Tl::rows(kt, 32 * n, i), q[i], s[n]);
+        for (int n = 0; n < BN / 32; ++n) {
+            const Factor<T> p(s[n]);
+#pragma unroll
+            for (int b = 0; b < D / 32; ++b) sm.o[b] = Tl::columns(vt, 32 * n, b, p.p, sm.o[b]);
+        }
+    };
+    if constexpr (!kIsBf16<T>) {
+        // fp32 products take so long that nothing else counts
+        if (tiles > 0) {
+            fetch_k(0);
+            sk.commit(tid, lds[0][0]);
+            fetch_v(0);
+            sv.commit(tid, lds[0][1]);
+        }
+        __syncthreads();
+        for (int t = 0; t < tiles; ++t) {
+            if (t + 1 < tiles) {
+                fetch_k(t + 1);
+                fetch_v(t + 1);
             }
-            if (key0 + BN > wave_all) {
+            if (t < wave_tiles) {
+                f32x16 s[BN / 32];
+                scores(t & 1, s);
+                hide(t, s);
+                sm.meet(s, a.scale_log2);
+                sm.weigh(s, a.scale_log2);
+                values(t & 1, s);
+                sm.add(s);
+            }
+            if (t + 1 < tiles) {
+                sk.commit(tid, lds[(t + 1) & 1][0]);
+                sv.commit(tid, lds[(t + 1) & 1][1]);
+            }
+            __syncthreads();
+        }
+    } else {
+        // A tile's scores are formed while those before it become weights, and its
+        // maximum while those weigh their values: keys run two tiles ahead of the
+        // walk, values one.  Each product is followed by its share of the softmax,
+        // which the vector unit does meanwhile; the compiler, left to itself, does the
+        // one after the other.
+        f32x16 even[BN / 32], odd[BN / 32];
+        if (tiles > 0) {
+            fetch_k(0);
+            sk.commit(tid, lds[0][0]);
+            fetch_v(0);
+            sv.commit(tid, lds[0][1]);
+            if (tiles > 1) {
+                fetch_k(1);
+                sk.commit(tid, lds[1][0]);
+            }
+        }
+        __syncthreads();
+        if (wave_tiles > 0) {
+            scores(0, even);
+            hide(0, even);
+            sm.meet(even, a.scale_log2);
+        }
+        __syncthreads();
+        const auto step = [&](int t, auto buffer, f32x16(&s)[BN / 32], f32x16(&next)[BN / 32]) {
+            constexpr int buf = decltype(buffer)::value;
+            constexpr int kElems = BN / 2;  // of a lane's scores
+            if (t + 2 < tiles) fetch_k(t + 2);
+            if (t + 1 < tiles) fetch_v(t + 1);
+            {
+                uint32_t kt = Tl::rows_at(lds_at(lds[buf ^ 1][0]));
+                uint32_t vt = Tl::columns_at(lds_at(lds[buf][1]));
+                asm volatile("" : "+v"(kt), "+v"(vt));  // (every address held over the loop would be spilled)
+                const float base = sm.m == -INFINITY ? 0.0f : sm.m * a.scale_log2;
+                constexpr int kScores = BN / 32 * Tl::kSteps, kAhead = 3;
+                Quad kf[kAhead + 1];
+                Quad p[kElems / 8];
+                float sum[2] = {0.0f, 0.0f};
 #pragma unroll
                 for (int n = 0; n < BN / 32; ++n)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (key0 + 32 * n + result_row(r) >= my_keys) s[n][r] = -INFINITY;
-            }
-            sm.template tile<BN / 32>(s, a.scale_log2);
+                    for (int r = 0; r < 16; ++r) next[n][r] = 0.0f;
 #pragma unroll
-            for (int n = 0; n < BN / 32; ++n) {
-                const Factor<T> p(s[n]);
+                for (int i = 0; i < kAhead; ++i) kf[i] = Tl::rows(kt, i % (BN / 32) * 32, i / (BN / 32));
 #pragma unroll
-                for (int b = 0; b < D / 32; ++b) sm.o[b] = Tl::columns(vt, 32 * n, b, p.p, sm.o[b]);
+                for (int i = 0; i < kScores; ++i) {
+                    const int j = i + kAhead;
+                    if (j < kScores) kf[j % (kAhead + 1)] = Tl::rows(kt, j % (BN / 32) * 32, j / (BN / 32));
+                    next[i % (BN / 32)] = mma<T>(kf[i % (kAhead + 1)], q[i / (BN / 32)], next[i % (BN / 32)]);
+#pragma unroll
+                    for (int e = kElems * i / kScores; e < kElems * (i + 1) / kScores; ++e) {
+                        s[e / 16][e % 16] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e / 16][e % 16], a.scale_log2, -base));
+                        sum[e % 2] += s[e / 16][e % 16];
+                        if (e % 2) p[e / 8][e / 2 % 4] = pack_bf16x2(s[e / 16][e % 16 - 1], s[e / 16][e % 16]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                sm.l += sum[0] + sum[1];
+                asm volatile("" : "+v"(sm.l));  // (here, not after the next products)
+                constexpr int kBlocks = D / 32, kValues = BN / 16 * kBlocks;
+                const auto vf_at = [&](int i) { return Tl::column(vt, i / (2 * kBlocks) * 32, i % kBlocks, i / kBlocks % 2); };
+                Quad vf[kAhead + 1];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) vf[i] = vf_at(i);
+                float top = next[0][0];
+#pragma unroll
+                for (int i = 0; i < kValues; ++i) {
+                    const int j = i + kAhead;
+                    if (j < kValues) vf[j % (kAhead + 1)] = vf_at(j);
+                    sm.o[i % kBlocks] = mma<T>(vf[i % (kAhead + 1)], p[i / kBlocks], sm.o[i % kBlocks]);
+#pragma unroll
+                    for (int e = kElems * i / kValues; e < kElems * (i + 1) / kValues; ++e)
+                        top = __builtin_fmaxf(top, next[e / 16][e % 16]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                asm volatile("" : "+v"(top));
+                if ((t + 2) * BN > wave_all) {
+                    hide(t + 1, next);
+                    top = sm.most(next);
+                }
+                sm.meet(top, a.scale_log2);
             }
+            if (t + 2 < tiles) sk.commit(tid, lds[buf][0]);
+            if (t + 1 < tiles) sv.commit(tid, lds[buf ^ 1][1]);
+            __syncthreads();
+        };
+        int t = 0;
+        for (; t + 2 < wave_tiles; t += 2) {
+            step(t, std::integral_constant<int, 0>{}, even, odd);
+            step(t + 1, std::integral_constant<int, 1>{}, odd, even);
         }
-        if (more) {
-            sk.commit(tid, lds[(t + 1) & 1][0]);
-            sv.commit(tid, lds[(t + 1) & 1][1]);
+        if (t + 1 < wave_tiles) {
+            step(t, std::integral_constant<int, 0>{}, even, odd);
+            ++t;
+#pragma unroll
+            for (int n = 0; n < BN / 32; ++n) even[n] = odd[n];
         }
-        __syncthreads();
+        // the wave's last tile, and those that only other waves walk
+        for (; t < tiles; ++t) {
+            if (t + 2 < tiles) fetch_k(t + 2);
+            if (t + 1 < tiles) fetch_v(t + 1);
+            if (t < wave_tiles) {
+                sm.weigh(even, a.scale_log2);
+                values(t & 1, even);
+                sm.add(even);
+            }
+            if (t + 2 < tiles) sk.commit(tid, lds[t & 1][0]);
+            if (t + 1 < tiles) sv.commit(tid, lds[(t + 1) & 1][1]);
+            __syncthreads();
+        }
     }
     const float l = both_sum(sm.l);
     if (mine) {
@@ -227,7 +354,7 @@ hipError_t launch_attn_fwd(const gspn_attn_args& a, int dtype, hipStream_t strea
     }
     const dim3 grid(static_cast<unsigned>(chunk_ids(ragged, a.seq.rows, a.seq.nseq, kAttnShift) * a.heads));
     replay_fwd("attn_fwd_kernel", a, es);
-    const bool direct = a.k_pool ? attn_direct(a.k_pool, 0, a.d, es) && attn_direct(a.v_pool, 0, a.d, es)
+    const bool direct = a.k_pool ? attn_direct(a.k_pool, a.kv_heads * a.d, a.d, es) && attn_direct(a.v_pool, a.kv_heads * a.d, a.d, es)
                                  : attn_direct(a.k, a.ldk, a.d, es) && attn_direct(a.v, a.ldv, a.d, es);
     attn_dispatch(dtype, a.d, direct, [&](auto t, auto width, auto straight) {
         using T = decltype(t);

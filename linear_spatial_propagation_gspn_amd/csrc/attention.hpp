@@ -174,21 +174,23 @@ struct Tile {
             return tile + row * kRow + (flip(row) ^ ((lane & 31) >> 2)) * 16 + 4 * (lane & 3);
         }
     }
-    // c + (columns 32 b .. of rows row0 .. row0 + 31, transposed) p: a first
-    // factor whose rows are the tile's columns, summed over the tile's rows in
-    // the order in which a result's registers p hold them.
+    // Columns 32 b .. of rows row0 + 16 i .. + 15, transposed: a first factor whose
+    // rows are the tile's columns, summed over the tile's rows in the order in
+    // which a result's registers 8 i .. hold them.
+    static __device__ __forceinline__ Quad column(uint32_t x, int row0, int b, int i) {
+        s16x4 v[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            v[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_s16x4*)(at(x, (4 * b) ^ flip(8 * j)) + (row0 + 16 * i + 8 * j) * kRow));
+        Quad a;
+        __builtin_memcpy(&a, v, 16);
+        return a;
+    }
+    // c + (columns 32 b .. of rows row0 .. row0 + 31, transposed) p.
     static __device__ __forceinline__ f32x16 columns(uint32_t x, int row0, int b, const Quad (&p)[2], f32x16 c) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            s16x4 v[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                v[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (lds_s16x4*)(at(x, (4 * b) ^ flip(8 * j)) + (row0 + 16 * i + 8 * j) * kRow));
-            Quad a;
-            __builtin_memcpy(&a, v, 16);
-            c = mma<T>(a, p[i], c);
-        }
+        for (int i = 0; i < 2; ++i) c = mma<T>(column(x, row0, b, i), p[i], c);
         return c;
     }
     static __device__ __forceinline__ f32x16 columns(uint32_t x, int row0, int b, const float (&p)[16], f32x16 c) {
@@ -236,20 +238,27 @@ struct Stage {
 
     // Rows row0 .., those behind `last` as the last again.
     __device__ __forceinline__ void fetch(int tid, const T* base, int64_t ld, int row0, int last, int d, char* tile) {
+        if constexpr (kDirect) {
+            const T* const from = base + row0 * ld;  // the same for the wave, as the tile's address is
+            const uint32_t pitch = static_cast<uint32_t>(ld) * sizeof(T);
+            const uint32_t to = lds_at(tile) + __builtin_amdgcn_readfirstlane(tid >> 6) * 1024;
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const int at = i * kThreads + tid;
-            const int r = at / Tl::kChunks;
-            const int row = row0 + r < last ? row0 + r : last;
-            if constexpr (kDirect) {
-                const int c = Tl::swizzle(r, at % Tl::kChunks) * Tl::kE;
-                const uint32_t to = __builtin_amdgcn_readfirstlane(lds_at(tile) + (at - (tid & 63)) * 16);
-                const T* const from = base + row * ld + c;
-                if (c < d)
-                    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
-            } else {
-                const int c = at % Tl::kChunks * Tl::kE;
-                v[i] = ld16(base + row * ld + c, d - c);
+            for (int i = 0; i < kN; ++i) {
+                const int at = i * kThreads + tid;
+                const int r = at / Tl::kChunks;
+                const int c = Tl::swizzle(r, at % Tl::kChunks);
+                const uint32_t off = static_cast<uint32_t>(r < last - row0 ? r : last - row0) * pitch + c * 16;
+                if (c * Tl::kE < d)
+                    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to + i * kThreads * 16), "v"(off),
+                                 "s"(from)
+                                 : "memory");
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                const int at = i * kThreads + tid;
+                const int row = row0 + at / Tl::kChunks, c = at % Tl::kChunks * Tl::kE;
+                v[i] = ld16(base + (row < last ? row : last) * ld + c, d - c);
             }
         }
     }
@@ -330,14 +339,21 @@ struct Softmax {
 #pragma unroll
             for (int r = 0; r < 16; ++r) o[b][r] = 0.0f;
     }
-    // s: scores, -Inf where hidden; on return the numerators.
+    // The maximum goes on over scores s, -Inf where hidden.
     template <int N>
-    __device__ __forceinline__ void tile(f32x16 (&s)[N], float scale_log2) {
+    __device__ __forceinline__ void meet(const f32x16 (&s)[N], float scale_log2) {
+        meet(most(s), scale_log2);
+    }
+    template <int N>
+    static __device__ __forceinline__ float most(const f32x16 (&s)[N]) {
         float t = s[0][0];
 #pragma unroll
         for (int n = 0; n < N; ++n)
 #pragma unroll
             for (int r = 0; r < 16; ++r) t = __builtin_fmaxf(t, s[n][r]);
+        return t;
+    }
+    __device__ __forceinline__ void meet(float t, float scale_log2) {
         t = both_max(t);
         if (__any((t - m) * scale_log2 > 8.0f || t != t)) {
             const float top = __builtin_fmaxf(m, t);
@@ -349,16 +365,25 @@ struct Softmax {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) o[b][r] *= a;
         }
+    }
+    // Scores into numerators.
+    template <int N>
+    __device__ __forceinline__ void weigh(f32x16 (&s)[N], float scale_log2) {
         const float base = m == -INFINITY ? 0.0f : m * scale_log2;
-        float sum = 0.0f;
 #pragma unroll
         for (int n = 0; n < N; ++n)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                s[n][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][r], scale_log2, -base));
-                sum += s[n][r];
-            }
-        l += sum;
+            for (int r = 0; r < 16; ++r) s[n][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][r], scale_log2, -base));
+    }
+    // Numerators into their sum.
+    template <int N>
+    __device__ __forceinline__ void add(const f32x16 (&s)[N]) {
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) sum[r % 4] += s[n][r];
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
 };
 
@@ -473,9 +498,9 @@ void attn_dispatch(int dtype, int64_t d, bool direct, F&& f) {
         way(bf16_t{});
 }
 
-// Whether rows are whole 16-byte chunks.
+// Whether rows are whole 16-byte chunks, and a tile's within 2^31 bytes.
 inline bool attn_direct(const void* p, int64_t ld, int64_t d, int64_t es) {
-    return d * es % 16 == 0 && aligned_rows(p, ld, static_cast<int>(es), 16);
+    return d * es % 16 == 0 && ld * es <= (int64_t{1} << 25) && aligned_rows(p, ld, static_cast<int>(es), 16);
 }
 
 }  // namespace gspn

@@ -110,7 +110,9 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_step_kernel(const AttnK 
             for (int r = 0; r < 16; ++r)
                 if (key0 + result_row(r) >= end) s[0][r] = -INFINITY;
         }
-        sm.template tile<1>(s, a.scale_log2);
+        sm.meet(s, a.scale_log2);
+        sm.weigh(s, a.scale_log2);
+        sm.add(s);
         const Factor<T> p(s[0]);
 #pragma unroll
         for (int b = 0; b < D / 32; ++b) sm.o[b] = Tl::columns(vc, 0, b, p.p, sm.o[b]);
