@@ -64,7 +64,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnK a
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[n][r] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < Tl::kSteps; ++i) s[n] = mma<T>(Tl::rows(kt, 32 * n, i), q[i], s[n]);
+            for (int i = 0; i < Tl::kSteps; ++i)
+                if (Tl::holds(i, a.d)) s[n] = mma<T>(Tl::rows(kt, 32 * n, i), q[i], s[n]);
         }
     };
     const auto hide = [&](int t, f32x16(&s)[BN / 32]) {

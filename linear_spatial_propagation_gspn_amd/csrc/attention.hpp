@@ -139,6 +139,11 @@ struct Tile {
     static constexpr int kSpan = kRow % 256 == 0 ? 16 : kRow % 256 == 128 ? 8 : 4;
     static_assert(kRow % (kSpan * 16) == 0);
 
+    // Whether step i of a product over a row holds any of the head's d elements.
+    // (Only fp32 products take long enough for the question: 2003 rows over 539
+    // keys, 6 heads of 40, 77 us in the three kernels of a training step, 72 so.)
+    static __device__ __forceinline__ bool holds(int i, int d) { return kIsBf16<T> || 2 * i * kE < d; }
+
     static __device__ __forceinline__ constexpr int flip(int row) {
         return kSpan == 16  ? (row & 3) << 2 | ((row >> 2) & 3)
                : kSpan == 8 ? (row & 2) << 1 | ((row >> 2) & 3)
@@ -251,7 +256,7 @@ struct Stage {
                 if (c * Tl::kE < d)
                     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to + i * kThreads * 16), "v"(off),
                                  "s"(from)
-                                 : "memory");
+                                 : "memory", "m0");
             }
         } else {
 #pragma unroll

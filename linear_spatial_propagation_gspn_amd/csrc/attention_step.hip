@@ -104,7 +104,8 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_step_kernel(const AttnK 
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[0][r] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < Tl::kSteps; ++i) s[0] = mma<T>(Tl::rows(kr, 0, i), q[i], s[0]);
+        for (int i = 0; i < Tl::kSteps; ++i)
+            if (Tl::holds(i, a.d)) s[0] = mma<T>(Tl::rows(kr, 0, i), q[i], s[0]);
         if (key0 + kStepKeys > end) {
 #pragma unroll
             for (int r = 0; r < 16; ++r)

@@ -219,6 +219,44 @@ def test_attention(dtype, heads, kv_heads, d, view, causal, lengths, keys, first
     assert all(torch.equal(a, b) for a, b in zip((dq, dk, dv), again))
 
 
+@pytest.mark.parametrize("dtype,heads,kv_heads,d", [(BF16, 2, 1, 128), (BF16, 1, 1, 72), (BF16, 3, 1, 64), (BF16, 1, 1, 90),
+                                                    (F32, 1, 1, 96)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_long(dtype, heads, kv_heads, d, causal):
+    """Many tiles, and keys enough that rows are not cut into parts."""
+    g = gen(d)
+    lengths = [1500, 64, 701]
+    seqs = R.spans(lengths)
+    rows = sum(lengths)
+    q, go = rnd(g, rows, heads, d, dtype=dtype), rnd(g, rows, heads, d, dtype=dtype)
+    k, v = rnd(g, rows, kv_heads, d, dtype=dtype), rnd(g, rows, kv_heads, d, dtype=dtype)
+    ref = R.attention(*map(wide, (q, k, v)), seqs, seqs, d ** -0.5, causal, dtype == BF16, wide(go))
+    cu = cu_of(lengths)
+    out, lse = A.gspn_attention_fwd(dev(q), dev(k), dev(v), causal=causal, cu=cu, lse=True)
+    check(out, ref["out"], "out")
+    check_lse(lse, ref["lse"], list(range(rows)))
+    for n, t in zip(("dq", "dk", "dv"), A.gspn_attention_bwd(dev(q), dev(k), dev(v), out, lse, dev(go), causal=causal, cu=cu)):
+        check(t, ref[n], n)
+
+
+@pytest.mark.parametrize("d", [72, 128])
+def test_attention_many_workgroups(d):
+    """More rows of keys than two workgroups a CU hold: sums of their own, no parts.  Every sequence is the same, and so
+    must its results be."""
+    g = gen(d)
+    n, t, h = 24, 200, 8
+    one = [rnd(g, t, h, d, dtype=BF16) for _ in range(4)]
+    q, k, v, go = (x.to(DEV).repeat(n, 1, 1) for x in one)
+    out, lse = A.gspn_attention_fwd(q, k, v, nseq=n, lse=True)
+    res = (out, *A.gspn_attention_bwd(q, k, v, out, lse, go, nseq=n))
+    seqs = [(0, t)]
+    ref = R.attention(*map(wide, one[:3]), seqs, seqs, d ** -0.5, True, True, wide(one[3]))
+    for name, x in zip(("out", "dq", "dk", "dv"), res):
+        x = x.view(n, t, h, d)
+        assert (x == x[:1]).all(), name
+        check(x[0], ref[name], name)
+
+
 @pytest.mark.parametrize("scale", [-0.3, 0.0, 1e-30, 3.0])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_attention_scales(dtype, scale):
