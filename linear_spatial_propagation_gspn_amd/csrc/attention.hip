@@ -92,8 +92,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnK a
         // fp32 products take so long that nothing else counts
         if (tiles > 0) {
             fetch_k(0);
-            sk.commit(tid, lds[0][0]);
             fetch_v(0);
+            sk.commit(tid, lds[0][0]);
             sv.commit(tid, lds[0][1]);
         }
         __syncthreads();
@@ -126,10 +126,11 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnK a
         f32x16 even[BN / 32], odd[BN / 32];
         if (tiles > 0) {
             fetch_k(0);
-            sk.commit(tid, lds[0][0]);
             fetch_v(0);
+            if (kDirect && tiles > 1) fetch_k(1);
+            sk.commit(tid, lds[0][0]);
             sv.commit(tid, lds[0][1]);
-            if (tiles > 1) {
+            if (!kDirect && tiles > 1) {
                 fetch_k(1);
                 sk.commit(tid, lds[1][0]);
             }
