@@ -356,8 +356,11 @@ hipError_t launch_attn_fwd(const gspn_attn_args& a, int dtype, hipStream_t strea
     }
     const dim3 grid(static_cast<unsigned>(chunk_ids(ragged, a.seq.rows, a.seq.nseq, kAttnShift) * a.heads));
     replay_fwd("attn_fwd_kernel", a, es);
-    const bool direct = a.k_pool ? attn_direct(a.k_pool, a.kv_heads * a.d, a.d, es) && attn_direct(a.v_pool, a.kv_heads * a.d, a.d, es)
-                                 : attn_direct(a.k, a.ldk, a.d, es) && attn_direct(a.v, a.ldv, a.d, es);
+    // entries, and the rows themselves where no entry holds them: without a cache and for padding
+    const int64_t ck = a.kv_heads * a.d;
+    const bool entries = !a.k_pool || (attn_direct(a.k_pool, ck, a.d, es) && attn_direct(a.v_pool, ck, a.d, es));
+    const bool apart = a.k_pool && !a.seq.slots;
+    const bool direct = entries && (apart || (attn_direct(a.k, a.ldk, a.d, es) && attn_direct(a.v, a.ldv, a.d, es)));
     attn_dispatch(dtype, a.d, direct, [&](auto t, auto width, auto straight) {
         using T = decltype(t);
         constexpr int D = decltype(width)::value;

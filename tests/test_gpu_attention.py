@@ -367,6 +367,27 @@ def test_attention_cache(dtype, heads, kv_heads, d, causal):
         assert torch.equal(torch.nan_to_num(p.cpu().float(), 12345.0), torch.nan_to_num(w.float(), 12345.0))
 
 
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (F32, 32)])
+@pytest.mark.parametrize("slots", [None, [1, -1, 0]])
+def test_attention_cache_unaligned_rows(dtype, d, slots):
+    """New rows at odd addresses beside whole chunks in the entries: those of padding are read where they are."""
+    g = gen(77 + d)
+    n, length, heads, kv_heads = 3, 150, 4, 2
+    wide_rows = rnd(g, n * length, 2 * kv_heads * d + 3, dtype=dtype)
+    rows = dev(wide_rows)
+    at = lambda t, i: t[:, 1 + i * kv_heads * d:1 + (i + 1) * kv_heads * d].unflatten(-1, (kv_heads, d))
+    q = rnd(g, n * length, heads, d, dtype=dtype)
+    state = tuple(torch.full((n, length + 5, kv_heads, d), math.nan, dtype=dtype, device=DEV) for _ in range(2))
+    out = A.gspn_attention_fwd(dev(q), at(rows, 0), at(rows, 1), nseq=n, state=state, slots=slots and ints(slots))
+    spans = [(i * length, (i + 1) * length) for i in range(n)]
+    ref = R.attention(wide(q), wide(at(wide_rows, 0)), wide(at(wide_rows, 1)), spans, spans, d ** -0.5, True, dtype == BF16)
+    check(out, ref["out"], "out")
+    for i, p in enumerate(state):
+        for b, e in enumerate(range(n) if slots is None else slots):
+            if e >= 0:
+                assert torch.equal(p[e, :length], at(rows, i)[spans[b][0]:spans[b][1]])
+
+
 @pytest.mark.parametrize("dtype,heads,kv_heads,d", [(F32, 4, 2, 20), (F32, 3, 1, 128), (BF16, 8, 2, 72), (BF16, 40, 1, 128),
                                                     (BF16, 2, 2, 33), (F32, 2, 2, 96)])
 @pytest.mark.parametrize("cap", [1, 40, 2500])
