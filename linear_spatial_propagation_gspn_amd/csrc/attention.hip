@@ -26,8 +26,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnK a
     T* const out = static_cast<T*>(a.out) + at * a.ldo + static_cast<int64_t>(w.head) * a.d;
     float* const lse = a.lse ? a.lse + static_cast<int64_t>(w.head) * a.seq.rows + at : nullptr;
     if (keys.state == kBadSlot) {
-        f32x16 o[D / 32];
-        for (int b = 0; b < D / 32; ++b)
+        f32x16 o[kBlocks<D>];
+        for (int b = 0; b < kBlocks<D>; ++b)
             for (int r = 0; r < 16; ++r) o[b][r] = NAN;
         if (mine) {
             st_result<T, D>(out, o, 1.0f, a.d);
@@ -85,7 +85,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnK a
         for (int n = 0; n < BN / 32; ++n) {
             const Factor<T> p(s[n]);
 #pragma unroll
-            for (int b = 0; b < D / 32; ++b) sm.o[b] = Tl::columns(vt, 32 * n, b, p.p, sm.o[b]);
+            for (int b = 0; b < kBlocks<D>; ++b) sm.o[b] = Tl::columns(vt, 32 * n, b, p.p, sm.o[b]);
         }
     };
     if constexpr (!kIsBf16<T>) {
@@ -177,8 +177,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnK a
                 }
                 sm.l += sum[0] + sum[1];
                 asm volatile("" : "+v"(sm.l));  // (here, not after the next products)
-                constexpr int kBlocks = D / 32, kValues = BN / 16 * kBlocks;
-                const auto vf_at = [&](int i) { return Tl::column(vt, i / (2 * kBlocks) * 32, i % kBlocks, i / kBlocks % 2); };
+                constexpr int kN = kBlocks<D>, kValues = BN / 16 * kN;
+                const auto vf_at = [&](int i) { return Tl::column(vt, i / (2 * kN) * 32, i % kN, i / kN % 2); };
                 Quad vf[kAhead + 1];
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) vf[i] = vf_at(i);
@@ -187,7 +187,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnK a
                 for (int i = 0; i < kValues; ++i) {
                     const int j = i + kAhead;
                     if (j < kValues) vf[j % (kAhead + 1)] = vf_at(j);
-                    sm.o[i % kBlocks] = mma<T>(vf[i % (kAhead + 1)], p[i / kBlocks], sm.o[i % kBlocks]);
+                    sm.o[i % kN] = mma<T>(vf[i % (kAhead + 1)], p[i / kN], sm.o[i % kN]);
 #pragma unroll
                     for (int e = kElems * i / kValues; e < kElems * (i + 1) / kValues; ++e)
                         top = __builtin_fmaxf(top, next[e / 16][e % 16]);
@@ -365,7 +365,7 @@ hipError_t launch_attn_fwd(const gspn_attn_args& a, int dtype, hipStream_t strea
         using T = decltype(t);
         constexpr int D = decltype(width)::value;
         constexpr bool kDirect = decltype(straight)::value;
-        GSPN_REPLAYED("attn_fwd_kernel", kAttnThreads, 4 * kTileRows<T> * D * static_cast<int64_t>(sizeof(T)));
+        GSPN_REPLAYED("attn_fwd_kernel", kAttnThreads, int64_t{4} * kTileRows<T> * Tile<T, D>::kRow);
         hipLaunchKernelGGL((attn_fwd_kernel<T, D, kDirect>), grid, dim3(kAttnThreads), 0, stream, k);
     });
     return hipGetLastError();

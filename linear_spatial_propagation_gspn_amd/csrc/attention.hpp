@@ -62,6 +62,10 @@ template <typename T>
 constexpr int kTileRows = kIsBf16<T> ? 64 : 32;
 
 
+// Blocks of 32 columns that heads of up to D elements take as columns of a result.
+template <int D>
+constexpr int kBlocks = (D + 31) / 32;
+
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -132,9 +136,9 @@ __device__ __forceinline__ f32x16 mma(Quad a, Quad b, f32x16 c) {
 // one register a tile.
 template <typename T, int D>
 struct Tile {
-    static constexpr int kRow = D * static_cast<int>(sizeof(T));  // bytes
+    static constexpr int kRow = 32 * kBlocks<D> * static_cast<int>(sizeof(T));  // bytes
     static constexpr int kChunks = kRow / 16;
-    static constexpr int kSteps = kRow / 32;  // products over a whole row
+    static constexpr int kSteps = D * static_cast<int>(sizeof(T)) / 32;  // products over a whole row
     static constexpr int kE = 16 / static_cast<int>(sizeof(T));
     static constexpr int kSpan = kRow % 256 == 0 ? 16 : kRow % 256 == 128 ? 8 : 4;
     static_assert(kRow % (kSpan * 16) == 0);
@@ -318,9 +322,9 @@ __device__ __forceinline__ int result_row(int r) { return 8 * (r / 4) + 4 * ((th
 // One row of the result (transposed: this lane's column, blocks of 32 rows),
 // times f.
 template <typename T, int D>
-__device__ __forceinline__ void st_result(T* row, const f32x16 (&o)[D / 32], float f, int d) {
+__device__ __forceinline__ void st_result(T* row, const f32x16 (&o)[kBlocks<D>], float f, int d) {
 #pragma unroll
-    for (int b = 0; b < D / 32; ++b)
+    for (int b = 0; b < kBlocks<D>; ++b)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
             const int c = 32 * b + result_row(4 * g);
@@ -336,11 +340,11 @@ __device__ __forceinline__ void st_result(T* row, const f32x16 (&o)[D / 32], flo
 template <int D>
 struct Softmax {
     float m = -INFINITY, l = 0.0f;
-    f32x16 o[D / 32];
+    f32x16 o[kBlocks<D>];
 
     __device__ __forceinline__ Softmax() {
 #pragma unroll
-        for (int b = 0; b < D / 32; ++b)
+        for (int b = 0; b < kBlocks<D>; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) o[b][r] = 0.0f;
     }
@@ -366,7 +370,7 @@ struct Softmax {
             m = top;
             l *= a;
 #pragma unroll
-            for (int b = 0; b < D / 32; ++b)
+            for (int b = 0; b < kBlocks<D>; ++b)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) o[b][r] *= a;
         }
@@ -484,8 +488,11 @@ int64_t rotary_bwd_parts(int64_t rows);
 template <typename F>
 void attn_dispatch(int dtype, int64_t d, bool direct, F&& f) {
     auto width = [&](auto t, auto straight) {
+        constexpr int kOver64 = kIsBf16<decltype(t)> ? 80 : 96;
         if (d <= 64)
             f(t, std::integral_constant<int, 64>{}, straight);
+        else if (d <= kOver64)
+            f(t, std::integral_constant<int, kOver64>{}, straight);
         else if (d <= 96)
             f(t, std::integral_constant<int, 96>{}, straight);
         else

@@ -72,9 +72,9 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_dq_kernel(const AttnK a)
     const int wave_all = wave0 < rows ? seen(wave0) : 0;
     const int my_keys = mine ? seen(row) : 0;
 
-    f32x16 dq[D / 32];
+    f32x16 dq[kBlocks<D>];
 #pragma unroll
-    for (int b = 0; b < D / 32; ++b)
+    for (int b = 0; b < kBlocks<D>; ++b)
 #pragma unroll
         for (int r = 0; r < 16; ++r) dq[b][r] = 0.0f;
     Stage<T, D, BN, kAttnThreads, kDirect> sk, sv;
@@ -140,7 +140,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_dq_kernel(const AttnK a)
                 }
                 const Factor<T> ds(s);
 #pragma unroll
-                for (int b = 0; b < D / 32; ++b) dq[b] = Tl::columns(kc, 32 * n, b, ds.p, dq[b]);
+                for (int b = 0; b < kBlocks<D>; ++b) dq[b] = Tl::columns(kc, 32 * n, b, ds.p, dq[b]);
             }
         }
         if (more) {
@@ -222,9 +222,9 @@ __global__ __launch_bounds__(kAttnThreads, kIsBf16<T> ? 2 : 1) void attn_dkv_ker
     const int first = static_cast<int>(all * part / a.splits);
     const int tiles = static_cast<int>(all * (part + 1) / a.splits);
 
-    f32x16 dk[D / 32], dv[D / 32];
+    f32x16 dk[kBlocks<D>], dv[kBlocks<D>];
 #pragma unroll
-    for (int b = 0; b < D / 32; ++b)
+    for (int b = 0; b < kBlocks<D>; ++b)
 #pragma unroll
         for (int r = 0; r < 16; ++r) dk[b][r] = dv[b][r] = 0.0f;
 
@@ -295,7 +295,7 @@ __global__ __launch_bounds__(kAttnThreads, kIsBf16<T> ? 2 : 1) void attn_dkv_ker
             {
                 const Factor<T> p(s);
 #pragma unroll
-                for (int b = 0; b < D / 32; ++b) dv[b] = Tl::columns(gc, 0, b, p.p, dv[b]);
+                for (int b = 0; b < kBlocks<D>; ++b) dv[b] = Tl::columns(gc, 0, b, p.p, dv[b]);
             }
             if constexpr (kInLds) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -321,7 +321,7 @@ __global__ __launch_bounds__(kAttnThreads, kIsBf16<T> ? 2 : 1) void attn_dkv_ker
             {
                 const Factor<T> ds(s);
 #pragma unroll
-                for (int b = 0; b < D / 32; ++b) dk[b] = Tl::columns(qc, 0, b, ds.p, dk[b]);
+                for (int b = 0; b < kBlocks<D>; ++b) dk[b] = Tl::columns(qc, 0, b, ds.p, dk[b]);
             }
             if constexpr (kInLds) __builtin_amdgcn_sched_barrier(0);
         }
@@ -334,11 +334,12 @@ __global__ __launch_bounds__(kAttnThreads, kIsBf16<T> ? 2 : 1) void attn_dkv_ker
     }
 
     // the second half of the waves hands its sums to the first
-    f32x4* const join = reinterpret_cast<f32x4*>(lds[0][0]) + (wave & 1) * (D / 4) * 64 + lane;
-    static_assert(sizeof lds >= 2 * (D / 4) * 64 * 16);
+    constexpr int kJoin = 8 * kBlocks<D>;  // f32x4 of a lane
+    f32x4* const join = reinterpret_cast<f32x4*>(lds[0][0]) + (wave & 1) * kJoin * 64 + lane;
+    static_assert(sizeof lds >= 2 * kJoin * 64 * 16);
     if (half == 1) {
 #pragma unroll
-        for (int b = 0; b < D / 32; ++b)
+        for (int b = 0; b < kBlocks<D>; ++b)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 join[(8 * b + g) * 64] = f32x4{dk[b][4 * g], dk[b][4 * g + 1], dk[b][4 * g + 2], dk[b][4 * g + 3]};
@@ -348,7 +349,7 @@ __global__ __launch_bounds__(kAttnThreads, kIsBf16<T> ? 2 : 1) void attn_dkv_ker
     __syncthreads();
     if (half == 1 || !mine) return;
 #pragma unroll
-    for (int b = 0; b < D / 32; ++b)
+    for (int b = 0; b < kBlocks<D>; ++b)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
             const f32x4 x = join[(8 * b + g) * 64], y = join[(8 * b + 4 + g) * 64];
@@ -453,7 +454,7 @@ hipError_t launch_attn_bwd(const gspn_attn_args& a, int dtype, hipStream_t strea
             using T = decltype(t);
             constexpr int D = decltype(width)::value;
             constexpr bool kDirect = decltype(straight)::value;
-            GSPN_REPLAYED("attn_dq_kernel", kAttnThreads, 4 * kTileRows<T> * D * static_cast<int64_t>(sizeof(T)));
+            GSPN_REPLAYED("attn_dq_kernel", kAttnThreads, int64_t{4} * kTileRows<T> * Tile<T, D>::kRow);
             hipLaunchKernelGGL((attn_dq_kernel<T, D, kDirect>), grid, dim3(kAttnThreads), 0, stream, k);
         });
         e = hipGetLastError();
@@ -474,7 +475,7 @@ hipError_t launch_attn_bwd(const gspn_attn_args& a, int dtype, hipStream_t strea
             constexpr int D = decltype(width)::value;
             constexpr bool kDirect = decltype(straight)::value;
             GSPN_REPLAYED("attn_dkv_kernel", kAttnThreads,
-                          kBwdRows * (4 * D * static_cast<int64_t>(sizeof(T)) + 16) +
+                          kBwdRows * (int64_t{4} * Tile<T, D>::kRow + 16) +
                               (kValuesInLds<T, D> ? kKeyRows * kValueRow : 16));
             hipLaunchKernelGGL((attn_dkv_kernel<T, D, kDirect>), grid, dim3(kAttnThreads), 0, stream, k);
         });

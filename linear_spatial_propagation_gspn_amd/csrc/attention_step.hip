@@ -20,7 +20,8 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_step_kernel(const AttnK 
     using Tl = Tile<T, D>;
     // the waves' tiles, and where they are joined afterwards
     constexpr int kTiles = 2 * kStepKeys * Tl::kRow;
-    constexpr int kJoin = 32 * (D + 2) * 4;
+    constexpr int kJoin = 32 * (32 * kBlocks<D> + 2) * 4;
+    constexpr int kSum = 32 * 32 * kBlocks<D>, kMost = kSum + 32;
     constexpr int kWave = kTiles > kJoin ? kTiles : kJoin;
     __shared__ __attribute__((aligned(16))) char lds[kStepWaves][kWave];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -116,7 +117,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_step_kernel(const AttnK 
         sm.add(s);
         const Factor<T> p(s[0]);
 #pragma unroll
-        for (int b = 0; b < D / 32; ++b) sm.o[b] = Tl::columns(vc, 0, b, p.p, sm.o[b]);
+        for (int b = 0; b < kBlocks<D>; ++b) sm.o[b] = Tl::columns(vc, 0, b, p.p, sm.o[b]);
     }
 
     // the waves' results: [32][d values, sum, maximum], each on the others' scale
@@ -124,25 +125,25 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_step_kernel(const AttnK 
     float* const join = reinterpret_cast<float*>(lds[wave]);
     const float l = both_sum(sm.l);
 #pragma unroll
-    for (int b = 0; b < D / 32; ++b)
+    for (int b = 0; b < kBlocks<D>; ++b)
 #pragma unroll
         for (int r = 0; r < 16; ++r) join[(32 * b + result_row(r)) * 32 + (lane & 31)] = sm.o[b][r];
     if (lane < 32) {
-        join[D * 32 + lane] = l;
-        join[(D + 1) * 32 + lane] = sm.m;
+        join[kSum + lane] = l;
+        join[kMost + lane] = sm.m;
     }
     __syncthreads();
     float f[kStepWaves], top = -INFINITY, sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < kStepWaves; ++j) {
-        f[j] = reinterpret_cast<const float*>(lds[j])[(D + 1) * 32 + (lane & 31)];
+        f[j] = reinterpret_cast<const float*>(lds[j])[kMost + (lane & 31)];
         top = __builtin_fmaxf(top, f[j]);
     }
     if (top == -INFINITY) top = 0.0f;  // no key, or every score -Inf
 #pragma unroll
     for (int j = 0; j < kStepWaves; ++j) {
         f[j] = __builtin_amdgcn_exp2f((f[j] - top) * a.scale_log2);
-        sum = __builtin_fmaf(f[j], reinterpret_cast<const float*>(lds[j])[D * 32 + (lane & 31)], sum);
+        sum = __builtin_fmaf(f[j], reinterpret_cast<const float*>(lds[j])[kSum + (lane & 31)], sum);
     }
     if (!mine) return;
     const float inv = part ? 1.0f : 1.0f / sum;
@@ -256,8 +257,8 @@ hipError_t launch_attn_step(const gspn_attn_args& a, int dtype, hipStream_t stre
         using T = decltype(t);
         constexpr int D = decltype(width)::value;
         GSPN_REPLAYED("attn_step_kernel", kAttnThreads,
-                      4 * kStepKeys * (2 * D * static_cast<int64_t>(sizeof(T)) > (D + 2) * 4
-                                           ? 2 * D * static_cast<int64_t>(sizeof(T)) : (D + 2) * 4));
+                      4 * kStepKeys * (2 * Tile<T, D>::kRow > (32 * kBlocks<D> + 2) * 4 ? 2 * Tile<T, D>::kRow
+                                                                                    : (32 * kBlocks<D> + 2) * 4));
         hipLaunchKernelGGL((attn_step_kernel<T, D>), dim3(static_cast<unsigned>(blocks)), dim3(kAttnThreads), 0, stream,
                            k);
     });
