@@ -7,16 +7,65 @@
 namespace gspn {
 namespace {
 
-template <typename T, int D, bool kDirect>
+// New rows of keys and values into their entries.
+template <typename T>
+__device__ __forceinline__ void append_rows(const AttnK& a, uint32_t id) {
+    const Chunk c = find_chunk(a.seq, id, kAppendShift);
+    if (c.seq < 0 || c.r0 >= c.r1) return;
+    const Keys<T> keys = find_keys<T>(a, c.seq, c.begin, c.end - c.begin, 0);
+    if (keys.state != 0) return;
+    constexpr int kE = 16 / sizeof(T);
+    const int width = a.kv_heads * a.d;
+    const int64_t at = keys.k.held + (c.r0 - c.begin);
+    const uint32_t chunks = width / kE;  // whole ones of a row; keys' and values' rows in turn
+    const uint32_t all = 2 * (c.r1 - c.r0) * chunks;
+    const auto place = [&](uint32_t row, int e, const T** from, T** to) {
+        const int r = row >> 1, value = row & 1;
+        *from = static_cast<const T*>(value ? a.v : a.k) + (c.r0 + r) * (value ? a.ldv : a.ldk) + e;
+        *to = const_cast<T*>((value ? keys.v : keys.k).entry) + (at + r) * width + e;
+    };
+    constexpr int kAhead = 4;
+    for (uint32_t i0 = threadIdx.x; i0 < all; i0 += kAhead * kAttnThreads) {
+        Quad x[kAhead];
+        T* to[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const uint32_t i = i0 + j * kAttnThreads < all ? i0 + j * kAttnThreads : i0;
+            const T* from;
+            place(i / chunks, i % chunks * kE, &from, &to[j]);
+            __builtin_memcpy(&x[j], from, 16);
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) asm volatile("" : "+v"(x[j]));  // all on their way before the first store
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (i0 + j * kAttnThreads < all) __builtin_memcpy(to[j], &x[j], 16);
+    }
+    const int rest = width - chunks * kE;
+    for (int i = threadIdx.x; i < 2 * (c.r1 - c.r0) * rest; i += kAttnThreads) {
+        const T* from;
+        T* to;
+        place(i / rest, chunks * kE + i % rest, &from, &to);
+        *to = *from;
+    }
+}
+
+template <typename T, int D, bool kDirect, bool kCache>
 __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnK a) {
     using Tl = Tile<T, D>;
     constexpr int BN = kTileRows<T>;
     __shared__ __attribute__((aligned(16))) char lds[2][2][BN * Tl::kRow];
+    if constexpr (kCache) {
+        if (blockIdx.x >= static_cast<uint32_t>(a.walks)) {
+            append_rows<T>(a, blockIdx.x - a.walks);
+            return;
+        }
+    }
     const AttnItem w = find_item(a.seq, a.heads, a.causal != 0, kAttnShift, blockIdx.x);
     if (w.c.seq < 0 || w.c.r0 >= w.c.r1) return;
     const int tid = threadIdx.x, lane = tid & 63;
     const int rows = w.c.end - w.c.begin;
-    const Keys keys = find_keys<T>(a, w.c.seq, w.c.begin, rows, w.head / a.group);
+    const Keys<T> keys = find_keys<T>(a, w.c.seq, w.c.begin, rows, w.head / a.group);
     const int off = keys.count - rows;  // row i sees i + off + 1 keys where later ones are hidden
 
     const int wave0 = w.c.r0 - w.c.begin + __builtin_amdgcn_readfirstlane(tid >> 6) * 32;  // the wave's first row
@@ -51,12 +100,16 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnK a
 
     Softmax<D> sm;
     Stage<T, D, BN, kAttnThreads, kDirect> sk, sv;
-    const T* const kp = static_cast<const T*>(keys.k);
-    const T* const vp = static_cast<const T*>(keys.v);
     clear_tiles<kDirect>(tid, kAttnThreads, lds[0][0], sizeof lds, a.d == D);
     const int wave_tiles = (wave_keys + BN - 1) / BN;
-    const auto fetch_k = [&](int t) { sk.fetch(tid, kp, keys.ldk, t * BN, keys.count - 1, a.d, lds[t & 1][0]); };
-    const auto fetch_v = [&](int t) { sv.fetch(tid, vp, keys.ldv, t * BN, keys.count - 1, a.d, lds[t & 1][1]); };
+    const auto fetch = [&](auto& stage, const Rows<T>& from, int t, char* tile) {
+        if constexpr (kCache)
+            stage.fetch(tid, from, t * BN, keys.count - 1, a.d, tile);
+        else
+            stage.fetch(tid, from.fresh, from.ld, t * BN, keys.count - 1, a.d, tile);
+    };
+    const auto fetch_k = [&](int t) { fetch(sk, keys.k, t, lds[t & 1][0]); };
+    const auto fetch_v = [&](int t) { fetch(sv, keys.v, t, lds[t & 1][1]); };
     const auto scores = [&](int buf, f32x16(&s)[BN / 32]) {
         const uint32_t kt = Tl::rows_at(lds_at(lds[buf][0]));
 #pragma unroll
@@ -237,49 +290,6 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnK a
     }
 }
 
-// New rows of keys and values into their entries.
-template <typename T>
-__global__ __launch_bounds__(kAttnThreads) void attn_append_kernel(const AttnK a) {
-    const Chunk c = find_chunk(a.seq, blockIdx.x, kAppendShift);
-    if (c.seq < 0 || c.r0 >= c.r1) return;
-    const Keys keys = find_keys<T>(a, c.seq, c.begin, c.end - c.begin, 0);
-    if (keys.state != 0) return;
-    constexpr int kE = 16 / sizeof(T);
-    const int width = a.kv_heads * a.d;
-    const int64_t at = keys.count - (c.end - c.begin) + (c.r0 - c.begin);
-    const uint32_t chunks = width / kE;  // whole ones of a row; keys' and values' rows in turn
-    const uint32_t all = 2 * (c.r1 - c.r0) * chunks;
-    const auto place = [&](uint32_t row, int e, const T** from, T** to) {
-        const int r = row >> 1, value = row & 1;
-        *from = static_cast<const T*>(value ? a.v : a.k) + (c.r0 + r) * (value ? a.ldv : a.ldk) + e;
-        *to = const_cast<T*>(static_cast<const T*>(value ? keys.v : keys.k)) + (at + r) * width + e;
-    };
-    constexpr int kAhead = 4;
-    for (uint32_t i0 = threadIdx.x; i0 < all; i0 += kAhead * kAttnThreads) {
-        Quad x[kAhead];
-        T* to[kAhead];
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const uint32_t i = i0 + j * kAttnThreads < all ? i0 + j * kAttnThreads : i0;
-            const T* from;
-            place(i / chunks, i % chunks * kE, &from, &to[j]);
-            __builtin_memcpy(&x[j], from, 16);
-        }
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) asm volatile("" : "+v"(x[j]));  // all on their way before the first store
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            if (i0 + j * kAttnThreads < all) __builtin_memcpy(to[j], &x[j], 16);
-    }
-    const int rest = width - chunks * kE;
-    for (int i = threadIdx.x; i < 2 * (c.r1 - c.r0) * rest; i += kAttnThreads) {
-        const T* from;
-        T* to;
-        place(i / rest, chunks * kE + i % rest, &from, &to);
-        *to = *from;
-    }
-}
-
 void replay_fwd(const char* kn, const gspn_attn_args& a, int64_t es) {
     (void)kn;
     (void)a;
@@ -340,33 +350,25 @@ AttnK make_attn(const gspn_attn_args& a) {
 }
 
 hipError_t launch_attn_fwd(const gspn_attn_args& a, int dtype, hipStream_t stream) {
-    const AttnK k = make_attn(a);
+    AttnK k = make_attn(a);
     const int64_t es = dtype == GSPN_F32 ? 4 : 2;
     const bool ragged = a.seq.cu != nullptr;
-    if (a.k_pool) {
-        const dim3 grid(static_cast<unsigned>(chunk_ids(ragged, a.seq.rows, a.seq.nseq, kAppendShift)));
-        replay_fwd("attn_append_kernel", a, es);
-        GSPN_REPLAYED("attn_append_kernel", kAttnThreads, 0);
-        if (dtype == GSPN_F32)
-            hipLaunchKernelGGL((attn_append_kernel<float>), grid, dim3(kAttnThreads), 0, stream, k);
-        else
-            hipLaunchKernelGGL((attn_append_kernel<bf16_t>), grid, dim3(kAttnThreads), 0, stream, k);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    const dim3 grid(static_cast<unsigned>(chunk_ids(ragged, a.seq.rows, a.seq.nseq, kAttnShift) * a.heads));
+    k.walks = static_cast<int32_t>(chunk_ids(ragged, a.seq.rows, a.seq.nseq, kAttnShift) * a.heads);
+    const int64_t copies = a.k_pool ? chunk_ids(ragged, a.seq.rows, a.seq.nseq, kAppendShift) : 0;
+    const dim3 grid(static_cast<unsigned>(k.walks + copies));
     replay_fwd("attn_fwd_kernel", a, es);
-    // entries, and the rows themselves where no entry holds them: without a cache and for padding
     const int64_t ck = a.kv_heads * a.d;
-    const bool entries = !a.k_pool || (attn_direct(a.k_pool, ck, a.d, es) && attn_direct(a.v_pool, ck, a.d, es));
-    const bool apart = a.k_pool && !a.seq.slots;
-    const bool direct = entries && (apart || (attn_direct(a.k, a.ldk, a.d, es) && attn_direct(a.v, a.ldv, a.d, es)));
+    const bool direct = attn_direct(a.k, a.ldk, a.d, es) && attn_direct(a.v, a.ldv, a.d, es) &&
+                        (!a.k_pool || (attn_direct(a.k_pool, ck, a.d, es) && attn_direct(a.v_pool, ck, a.d, es)));
     attn_dispatch(dtype, a.d, direct, [&](auto t, auto width, auto straight) {
         using T = decltype(t);
         constexpr int D = decltype(width)::value;
         constexpr bool kDirect = decltype(straight)::value;
         GSPN_REPLAYED("attn_fwd_kernel", kAttnThreads, int64_t{4} * kTileRows<T> * Tile<T, D>::kRow);
-        hipLaunchKernelGGL((attn_fwd_kernel<T, D, kDirect>), grid, dim3(kAttnThreads), 0, stream, k);
+        if (a.k_pool)
+            hipLaunchKernelGGL((attn_fwd_kernel<T, D, kDirect, true>), grid, dim3(kAttnThreads), 0, stream, k);
+        else
+            hipLaunchKernelGGL((attn_fwd_kernel<T, D, kDirect, false>), grid, dim3(kAttnThreads), 0, stream, k);
     });
     return hipGetLastError();
 }

@@ -52,6 +52,7 @@ struct AttnK {
     float* part;   // of the step's splits
     int64_t ldq, ldk, ldv, ldo, ldgo, lddq, lddk, lddv;
     int32_t splits;
+    int32_t walks;  // workgroups before those that copy new rows into their entries
 };
 
 template <typename T>
@@ -232,6 +233,28 @@ struct Factor<float> {
     }
 };
 
+// A sequence's rows of keys or values: those that its cache entry holds, then
+// the new ones.
+template <typename T>
+struct Rows {
+    const T* fresh;
+    const T* entry;
+    int64_t ld, ld_held;
+    int32_t held;
+    __device__ __forceinline__ const T* at(int row) const {
+        return row < held ? entry + row * ld_held : fresh + (row - held) * ld;
+    }
+};
+
+// A pointer that is the same for the wave, in scalar registers.
+template <typename T>
+__device__ __forceinline__ const T* same(const T* p) {
+    const uint64_t x = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x >> 32));
+    return reinterpret_cast<const T*>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
 // ROWS rows on their way from memory to a tile, over kThreads threads.
 // kDirect: straight to LDS, 1 KB a wave and instruction, which the wave only
 // waits for before the barrier that hands the tile over (the prompt of 16384
@@ -248,18 +271,27 @@ struct Stage {
     // Rows row0 .., those behind `last` as the last again.
     __device__ __forceinline__ void fetch(int tid, const T* base, int64_t ld, int row0, int last, int d, char* tile) {
         if constexpr (kDirect) {
-            const T* const from = base + row0 * ld;  // the same for the wave, as the tile's address is
-            const uint32_t pitch = static_cast<uint32_t>(ld) * sizeof(T);
+            fetch_run(tid, base + row0 * ld, ld, last - row0, d, tile);
+        } else {
+            fetch(tid, Rows<T>{base, nullptr, ld, 0, 0}, row0, last, d, tile);
+        }
+    }
+    __device__ __forceinline__ void fetch(int tid, const Rows<T>& rows, int row0, int last, int d, char* tile) {
+        if constexpr (kDirect) {
+            if (rows.held <= row0 || rows.held > last || rows.held >= row0 + ROWS) {
+                fetch_run(tid, same(rows.at(row0)), rows.held <= row0 ? rows.ld : rows.ld_held, last - row0, d, tile);
+                return;
+            }
             const uint32_t to = lds_at(tile) + __builtin_amdgcn_readfirstlane(tid >> 6) * 1024;
 #pragma unroll
             for (int i = 0; i < kN; ++i) {
                 const int at = i * kThreads + tid;
                 const int r = at / Tl::kChunks;
                 const int c = Tl::swizzle(r, at % Tl::kChunks);
-                const uint32_t off = static_cast<uint32_t>(r < last - row0 ? r : last - row0) * pitch + c * 16;
+                const T* const from = rows.at(row0 + r < last ? row0 + r : last) + c * Tl::kE;
                 if (c * Tl::kE < d)
-                    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to + i * kThreads * 16), "v"(off),
-                                 "s"(from)
+                    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to + i * kThreads * 16),
+                                 "v"(from)
                                  : "memory", "m0");
             }
         } else {
@@ -267,8 +299,24 @@ struct Stage {
             for (int i = 0; i < kN; ++i) {
                 const int at = i * kThreads + tid;
                 const int row = row0 + at / Tl::kChunks, c = at % Tl::kChunks * Tl::kE;
-                v[i] = ld16(base + (row < last ? row : last) * ld + c, d - c);
+                v[i] = ld16(rows.at(row < last ? row : last) + c, d - c);
             }
+        }
+    }
+    // Straight to LDS, rows `from` .. of one pitch; `from` is the same for the wave, as the tile's address is.
+    __device__ __forceinline__ void fetch_run(int tid, const T* from, int64_t ld, int last, int d, char* tile) {
+        const uint32_t pitch = static_cast<uint32_t>(ld) * sizeof(T);
+        const uint32_t to = lds_at(tile) + __builtin_amdgcn_readfirstlane(tid >> 6) * 1024;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int at = i * kThreads + tid;
+            const int r = at / Tl::kChunks;
+            const int c = Tl::swizzle(r, at % Tl::kChunks);
+            const uint32_t off = static_cast<uint32_t>(r < last ? r : last) * pitch + c * 16;
+            if (c * Tl::kE < d)
+                asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to + i * kThreads * 16), "v"(off),
+                             "s"(from)
+                             : "memory", "m0");
         }
     }
     __device__ __forceinline__ void commit(int tid, char* tile) const {
@@ -398,24 +446,21 @@ struct Softmax {
 
 // Where a sequence's keys lie, and how many there are.  state: 0 as they are,
 // kNoSlot (padding), kBadSlot (an error).
+template <typename T>
 struct Keys {
-    const void* k;
-    const void* v;
-    int64_t ldk, ldv;
-    int32_t count, state, first;  // first: the row of kv that holds the first (without a cache)
+    Rows<T> k, v;
+    int32_t count, state;
 };
 
 template <typename T>
-__device__ __forceinline__ Keys find_keys(const AttnK& a, int seq, int begin, int rows, int kv_head) {
-    Keys w;
-    w.state = 0;
-    w.ldk = a.ldk;
-    w.ldv = a.ldv;
-    w.first = begin;
+__device__ __forceinline__ Keys<T> find_keys(const AttnK& a, int seq, int begin, int rows, int kv_head) {
+    Keys<T> w = {};
+    w.k.ld = a.ldk;
+    w.v.ld = a.ldv;
     w.count = rows;
-    int slot = kNoSlot;
+    int first = begin;
     if (a.k_pool) {
-        slot = slot_of(a.seq, seq);
+        const int slot = slot_of(a.seq, seq);
         if (slot < 0) w.state = slot;
         if (slot >= 0) {
             const int held = a.held ? __builtin_amdgcn_readfirstlane(a.held[seq]) : 0;
@@ -423,19 +468,19 @@ __device__ __forceinline__ Keys find_keys(const AttnK& a, int seq, int begin, in
                 w.state = kBadSlot;
             } else {
                 const int64_t at = (slot * a.capacity * a.kv_heads + kv_head) * a.d;
-                w.k = static_cast<const T*>(a.k_pool) + at;
-                w.v = static_cast<const T*>(a.v_pool) + at;
-                w.ldk = w.ldv = static_cast<int64_t>(a.kv_heads) * a.d;
+                w.k.entry = static_cast<const T*>(a.k_pool) + at;
+                w.v.entry = static_cast<const T*>(a.v_pool) + at;
+                w.k.ld_held = w.v.ld_held = static_cast<int64_t>(a.kv_heads) * a.d;
+                w.k.held = w.v.held = held;
                 w.count = held + rows;
-                return w;
             }
         }
     } else {
-        w.first = seq_begin(a.kv, seq);
-        w.count = seq_end(a.kv, seq, w.first) - w.first;
+        first = seq_begin(a.kv, seq);
+        w.count = seq_end(a.kv, seq, first) - first;
     }
-    w.k = static_cast<const T*>(a.k) + w.first * a.ldk + static_cast<int64_t>(kv_head) * a.d;
-    w.v = static_cast<const T*>(a.v) + w.first * a.ldv + static_cast<int64_t>(kv_head) * a.d;
+    w.k.fresh = static_cast<const T*>(a.k) + first * a.ldk + static_cast<int64_t>(kv_head) * a.d;
+    w.v.fresh = static_cast<const T*>(a.v) + first * a.ldv + static_cast<int64_t>(kv_head) * a.d;
     return w;
 }
 

@@ -96,7 +96,7 @@ gspn_status check_attn(const gspn_attn_args* a, int dtype, Which which, bool* em
         const int64_t ids = gspn::chunk_ids(true, rows, nseq, gspn::kAttnShift) * a->heads;
         const int64_t kv_ids = gspn::chunk_ids(true, kv, nseq, gspn::kKeyShift) * a->kv_heads;
         const int64_t copies = pool ? gspn::chunk_ids(true, rows, nseq, gspn::kAppendShift) : 0;
-        if (ids > kMaxGrid || kv_ids > kMaxGrid || copies > kMaxGrid) return GSPN_ERR_UNSUPPORTED;
+        if (ids + copies > kMaxGrid || kv_ids > kMaxGrid) return GSPN_ERR_UNSUPPORTED;
     }
     const int64_t cq = a->heads * a->d, ck = a->kv_heads * a->d;
     b.rows(a->q, rows, a->ldq, cq, es, false);

@@ -33,7 +33,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_dq_kernel(const AttnK a)
     if (w.c.seq < 0 || w.c.r0 >= w.c.r1) return;
     const int tid = threadIdx.x, lane = tid & 63;
     const int rows = w.c.end - w.c.begin;
-    const Keys keys = find_keys<T>(a, w.c.seq, w.c.begin, rows, w.head / a.group);
+    const Keys<T> keys = find_keys<T>(a, w.c.seq, w.c.begin, rows, w.head / a.group);
     const int off = keys.count - rows;
 
     const int wave0 = w.c.r0 - w.c.begin + __builtin_amdgcn_readfirstlane(tid >> 6) * 32;
@@ -78,12 +78,12 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_dq_kernel(const AttnK a)
 #pragma unroll
         for (int r = 0; r < 16; ++r) dq[b][r] = 0.0f;
     Stage<T, D, BN, kAttnThreads, kDirect> sk, sv;
-    const T* const kp = static_cast<const T*>(keys.k);
-    const T* const vp = static_cast<const T*>(keys.v);
+    const T* const kp = keys.k.fresh;
+    const T* const vp = keys.v.fresh;
     clear_tiles<kDirect>(tid, kAttnThreads, lds[0][0], sizeof lds, a.d == D);
     if (tiles > 0) {
-        sk.fetch(tid, kp, keys.ldk, 0, keys.count - 1, a.d, lds[0][0]);
-        sv.fetch(tid, vp, keys.ldv, 0, keys.count - 1, a.d, lds[0][1]);
+        sk.fetch(tid, kp, a.ldk, 0, keys.count - 1, a.d, lds[0][0]);
+        sv.fetch(tid, vp, a.ldv, 0, keys.count - 1, a.d, lds[0][1]);
         sk.commit(tid, lds[0][0]);
         sv.commit(tid, lds[0][1]);
     }
@@ -91,8 +91,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_dq_kernel(const AttnK a)
     for (int t = 0; t < tiles; ++t) {
         const bool more = t + 1 < tiles;
         if (more) {
-            sk.fetch(tid, kp, keys.ldk, (t + 1) * BN, keys.count - 1, a.d, lds[(t + 1) & 1][0]);
-            sv.fetch(tid, vp, keys.ldv, (t + 1) * BN, keys.count - 1, a.d, lds[(t + 1) & 1][1]);
+            sk.fetch(tid, kp, a.ldk, (t + 1) * BN, keys.count - 1, a.d, lds[(t + 1) & 1][0]);
+            sv.fetch(tid, vp, a.ldv, (t + 1) * BN, keys.count - 1, a.d, lds[(t + 1) & 1][1]);
         }
         const int key0 = t * BN;
         if (key0 < wave_keys) {

@@ -37,7 +37,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_step_kernel(const AttnK 
     const int column = block * 32 + (lane & 31);
     const int head = kv_head * a.group + column;
     const bool mine = column < a.group;
-    const Keys keys = find_keys<T>(a, seq, seq, 1, kv_head);
+    const Keys<T> keys = find_keys<T>(a, seq, seq, 1, kv_head);
     T* const out = static_cast<T*>(a.out) + seq * a.ldo + static_cast<int64_t>(head) * a.d;
     // a split's results: numerators' sum and maximum behind the d values
     float* const part = a.splits > 1
@@ -62,14 +62,14 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_step_kernel(const AttnK 
     const int64_t most = static_cast<int64_t>(begin) + static_cast<int64_t>(each) * kStepRound;
     const int end = most < keys.count ? static_cast<int>(most) : keys.count;
 
-    const T* const kp = static_cast<const T*>(keys.k);
-    const T* const vp = static_cast<const T*>(keys.v);
-    const T* const knew = static_cast<const T*>(a.k) + seq * a.ldk + static_cast<int64_t>(kv_head) * a.d;
-    const T* const vnew = static_cast<const T*>(a.v) + seq * a.ldv + static_cast<int64_t>(kv_head) * a.d;
+    const T* const kp = keys.k.entry;
+    const T* const vp = keys.v.entry;
+    const T* const knew = keys.k.fresh;
+    const T* const vnew = keys.v.fresh;
     if (begin <= held && held < end && block == 0 && wave == 0) {  // nobody reads this row of the pool
         for (int i = lane; i < a.d; i += 64) {
-            const_cast<T*>(kp)[held * keys.ldk + i] = knew[i];
-            const_cast<T*>(vp)[held * keys.ldv + i] = vnew[i];
+            const_cast<T*>(kp)[held * keys.k.ld_held + i] = knew[i];
+            const_cast<T*>(vp)[held * keys.v.ld_held + i] = vnew[i];
         }
     }
 
@@ -80,8 +80,8 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_step_kernel(const AttnK 
         for (int i = 0; i < kN; ++i) {
             const int at = i * 64 + lane;
             const int r = key0 + at / Tl::kChunks, c = at % Tl::kChunks * Tl::kE;
-            sk[i] = ld16((r < held ? kp + r * keys.ldk : knew) + c, a.d - c);
-            sv[i] = ld16((r < held ? vp + r * keys.ldv : vnew) + c, a.d - c);
+            sk[i] = ld16((r < held ? kp + r * keys.k.ld_held : knew) + c, a.d - c);
+            sv[i] = ld16((r < held ? vp + r * keys.v.ld_held : vnew) + c, a.d - c);
         }
     };
     char* const kt = lds[wave];

@@ -340,8 +340,7 @@ def test_launches_stay_in_their_buffers(chk, lib, dt, d, ld):
         for rows, nseq in ((40, 2), (1, 1), (1200, 3)):
             kw = dict(d=d, ld=ld, rows=rows, nseq=nseq, cu=cu)
             assert replay(chk, lib, "attn", "fwd", dt, **kw) == ["attn_fwd_kernel"]
-            assert replay(chk, lib, "attn", "fwd", dt, capacity=1300, slots=5, **kw) == ["attn_append_kernel",
-                                                                                         "attn_fwd_kernel"]
+            assert replay(chk, lib, "attn", "fwd", dt, capacity=1300, slots=5, **kw) == ["attn_fwd_kernel"]
             clear = ["reduce_parts_kernel"] * (2 if cu else 0)
             parts = ["attn_parts_kernel"] * (rows == 1200)  # rows enough to be cut
             assert replay(chk, lib, "attn", "bwd", dt, **kw) == clear + ["attn_dq_kernel", "attn_dkv_kernel"] + parts
