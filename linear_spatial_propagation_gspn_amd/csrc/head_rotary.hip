@@ -453,12 +453,16 @@ int slices_for(int64_t rows, int64_t heads, int group) {
     return static_cast<int>(want < most ? want : most);
 }
 
-// Calls f with the storage type, the pairs a lane takes (16 bytes of them, or 8
-// where only those come out even: heads of 72 bf16 elements), the lanes of a head,
-// and the two flags.
+// Calls f with the storage type, the pairs a lane takes, the lanes of a head, and
+// the two flags.  A lane takes 16 bytes of pairs, or where they come out even 12 or
+// 8, whichever leaves fewest lanes idle.
 template <typename F>
 void rotary_dispatch(int dtype, const RotaryK& k, F&& f) {
     const int rest = k.d - 2 * k.pairs;
+    const auto lanes_of = [&](int v) {
+        const int units = (k.pairs + v - 1) / v + (rest + 2 * v - 1) / (2 * v);
+        return units <= 8 ? 8 : units <= 16 ? 16 : units <= 32 ? 32 : 64;
+    };
     const auto flags = [&](auto t, auto v, auto g, auto even) {
         if (k.interleaved)
             f(t, v, g, std::true_type{}, even);
@@ -467,12 +471,12 @@ void rotary_dispatch(int dtype, const RotaryK& k, F&& f) {
     };
     const auto lanes = [&](auto t, auto v, auto even) {
         constexpr int V = decltype(v)::value;
-        const int units = (k.pairs + V - 1) / V + (rest + 2 * V - 1) / (2 * V);
-        if (units <= 8)
+        const int g = lanes_of(V);
+        if (g == 8)
             flags(t, v, std::integral_constant<int, 8>{}, even);
-        else if (units <= 16)
+        else if (g == 16)
             flags(t, v, std::integral_constant<int, 16>{}, even);
-        else if (decltype(even)::value || units <= 32)
+        else if (decltype(even)::value || g == 32)
             flags(t, v, std::integral_constant<int, 32>{}, even);
         else if constexpr (!decltype(even)::value)
             flags(t, v, std::integral_constant<int, 64>{}, even);
@@ -483,13 +487,19 @@ void rotary_dispatch(int dtype, const RotaryK& k, F&& f) {
             lanes(float{}, std::integral_constant<int, 4>{}, std::true_type{});
         else
             lanes(float{}, std::integral_constant<int, 4>{}, std::false_type{});
-    } else if (even(8)) {
-        lanes(bf16_t{}, std::integral_constant<int, 8>{}, std::true_type{});
-    } else if (even(4)) {
-        lanes(bf16_t{}, std::integral_constant<int, 4>{}, std::true_type{});
-    } else {
-        lanes(bf16_t{}, std::integral_constant<int, 8>{}, std::false_type{});
+        return;
     }
+    int best = 0;
+    for (const int v : {8, 6, 4})
+        if (even(v) && (best == 0 || lanes_of(v) * v < lanes_of(best) * best)) best = v;
+    if (best == 8)
+        lanes(bf16_t{}, std::integral_constant<int, 8>{}, std::true_type{});
+    else if (best == 6)
+        lanes(bf16_t{}, std::integral_constant<int, 6>{}, std::true_type{});
+    else if (best == 4)
+        lanes(bf16_t{}, std::integral_constant<int, 4>{}, std::true_type{});
+    else
+        lanes(bf16_t{}, std::integral_constant<int, 8>{}, std::false_type{});
 }
 
 void replay(const char* kn, const gspn_rotary_args& a, bool bwd, int64_t es) {

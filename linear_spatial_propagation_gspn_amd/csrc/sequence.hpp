@@ -128,8 +128,9 @@ __device__ __forceinline__ int slot_of(const SeqK& s, int i) {
 
 // V consecutive elements of the storage type, widened to fp32, in 16-byte
 // accesses (or one shorter access) that the pointer is aligned to.
+constexpr int pack_align(int bytes) { return (bytes & -bytes) < 16 ? bytes & -bytes : 16; }
 template <typename T, int V>
-struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V : 16) Pack {
+struct alignas(pack_align(sizeof(T) * V)) Pack {
     T e[V];
 };
 

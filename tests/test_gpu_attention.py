@@ -96,7 +96,8 @@ def check_lse(got, ref, rows):
 @pytest.mark.parametrize("rows,heads,kv_heads,d,sections,view", [
     (1, 1, 1, 2, (1,), False), (7, 3, 2, 16, (8,), True), (65, 5, 1, 80, (6, 14, 14), False), (33, 2, 2, 27, (3, 4), True),
     (130, 4, 0, 128, (64,), False), (9, 2, 1, 256, (30, 0, 60, 38), True), (21, 17, 3, 1, (0,), False),
-    (40, 9, 2, 62, (31,), False), (5, 2, 2, 200, (11,), False)])
+    (40, 9, 2, 62, (31,), False), (5, 2, 2, 200, (11,), False), (11, 5, 2, 72, (36,), True), (6, 3, 1, 96, (18, 6), False),
+    (4, 2, 2, 64, (32,), True), (3, 1, 1, 252, (126,), False), (70, 6, 6, 24, (6,), True)])
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("norm", [True, False])
 def test_rotary(dtype, rows, heads, kv_heads, d, sections, view, interleaved, norm):
