@@ -58,7 +58,7 @@ __device__ __forceinline__ void sincos_turn(double t, float* s, float* c) {
 }
 
 // A lane's place in a head: V pairs (a[i], b[i]), their elements from these on, or
-// 2 V elements in a row behind the pairs (as a, then b).  Where units do not come
+// 2 V elements in a row behind the pairs (as a, then b, or as pairs of neighbours).  Where units do not come
 // out even (kEven: they do), the last of either kind ends where its kind does and
 // so begins within the one before: its first `skip` values are that one's too,
 // count for nothing in sums, and are stored twice, the same bits; where there are
@@ -99,13 +99,14 @@ __device__ __forceinline__ Place place_of(const RotaryK& k, int unit) {
 }
 
 // Which of a place's values are its own, in range and not another unit's too.
-template <int V, bool kEven>
+template <int V, bool kInter, bool kEven>
 __device__ __forceinline__ bool own_a(const Place& p, int i) {
-    return kEven || (i >= p.skip && i < p.left);
+    const int j = p.turns || !kInter ? i : 2 * i;
+    return kEven || (j >= p.skip && j < p.left);
 }
-template <int V, bool kEven>
+template <int V, bool kInter, bool kEven>
 __device__ __forceinline__ bool own_b(const Place& p, int i) {
-    const int j = p.turns ? i : V + i;
+    const int j = p.turns ? i : kInter ? 2 * i + 1 : V + i;
     return kEven || (j >= p.skip && j < p.left);
 }
 
@@ -136,7 +137,7 @@ __device__ __forceinline__ Raw<T, V> ld_raw(const Place& p, const T* head) {
 }
 
 template <typename T, int V, bool kInter>
-__device__ __forceinline__ void pairs_of(const Place& p, const Raw<T, V>& r, float (&a)[V], float (&b)[V]) {
+__device__ __forceinline__ void pairs_of(const Raw<T, V>& r, float (&a)[V], float (&b)[V]) {
     widen<T, V>(r.a, a);
     widen<T, V>(r.b, b);
     if constexpr (kInter) {
@@ -148,8 +149,8 @@ __device__ __forceinline__ void pairs_of(const Place& p, const Raw<T, V>& r, flo
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            a[i] = p.turns ? f[2 * i] : f[i];
-            b[i] = p.turns ? f[2 * i + 1] : f[V + i];
+            a[i] = f[2 * i];
+            b[i] = f[2 * i + 1];
         }
     }
 }
@@ -165,8 +166,8 @@ __device__ __forceinline__ void st_pairs(const Place& p, T* head, float (&a)[V],
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            a[i] = p.turns ? f[i] : a[i];
-            b[i] = p.turns ? f[V + i] : b[i];
+            a[i] = f[i];
+            b[i] = f[V + i];
         }
     }
     if (p.idle) return;
@@ -197,7 +198,7 @@ struct Weight {
     __device__ __forceinline__ void load(const Place& p, const float* w, bool key) {
         if (of == key) return;
         of = key;
-        pairs_of<float, V, kInter>(p, ld_raw<float, V, kInter, kEven>(p, w), u, v);
+        pairs_of<float, V, kInter>(ld_raw<float, V, kInter, kEven>(p, w), u, v);
     }
 };
 
@@ -280,7 +281,7 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_fwd_kernel(const Rotary
         for (; h < total; h += step) {
             const HeadAt w = head_at(k, h);
             float a[V], b[V];
-            pairs_of<T, V, kInter>(p, x, a, b);
+            pairs_of<T, V, kInter>(x, a, b);
             x = next;
             if (h + 2 * step < total) next = load(h + 2 * step);
             const float* const weight = w.key ? k.kw : k.qw;
@@ -289,8 +290,8 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_fwd_kernel(const Rotary
                 wt.template load<kInter, kEven>(p, weight, w.key);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    sum = __builtin_fmaf(own_a<V, kEven>(p, i) ? a[i] : 0.0f, a[i], sum);
-                    sum = __builtin_fmaf(own_b<V, kEven>(p, i) ? b[i] : 0.0f, b[i], sum);
+                    sum = __builtin_fmaf(own_a<V, kInter, kEven>(p, i) ? a[i] : 0.0f, a[i], sum);
+                    sum = __builtin_fmaf(own_b<V, kInter, kEven>(p, i) ? b[i] : 0.0f, b[i], sum);
                 }
                 const float r = 1.0f / __builtin_sqrtf(group_sum<G>(sum) / static_cast<float>(k.d) + k.eps);
 #pragma unroll
@@ -351,8 +352,8 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_bwd_kernel(const Rotary
             const HeadAt w = head_at(k, h);
             const float* const weight = w.key ? k.kw : k.qw;
             float ga[V], gb[V], a[V], b[V];
-            pairs_of<T, V, kInter>(p, now.g, ga, gb);
-            if (weight) pairs_of<T, V, kInter>(p, now.x, a, b);
+            pairs_of<T, V, kInter>(now.g, ga, gb);
+            if (weight) pairs_of<T, V, kInter>(now.x, a, b);
             now = next;
             if (h + 2 * step < total) next = load(h + 2 * step);
             if (p.turns) {
@@ -368,8 +369,8 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_bwd_kernel(const Rotary
                 wt.template load<kInter, kEven>(p, weight, w.key);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    sum = __builtin_fmaf(own_a<V, kEven>(p, i) ? a[i] : 0.0f, a[i], sum);
-                    sum = __builtin_fmaf(own_b<V, kEven>(p, i) ? b[i] : 0.0f, b[i], sum);
+                    sum = __builtin_fmaf(own_a<V, kInter, kEven>(p, i) ? a[i] : 0.0f, a[i], sum);
+                    sum = __builtin_fmaf(own_b<V, kInter, kEven>(p, i) ? b[i] : 0.0f, b[i], sum);
                 }
                 const float r = 1.0f / __builtin_sqrtf(group_sum<G>(sum) / static_cast<float>(k.d) + k.eps);
 #pragma unroll
@@ -383,8 +384,8 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_bwd_kernel(const Rotary
                     wb[1][i] += w.key ? y : 0.0f;
                     ga[i] *= wt.u[i];
                     gb[i] *= wt.v[i];
-                    dot = __builtin_fmaf(own_a<V, kEven>(p, i) ? ga[i] : 0.0f, a[i], dot);
-                    dot = __builtin_fmaf(own_b<V, kEven>(p, i) ? gb[i] : 0.0f, b[i], dot);
+                    dot = __builtin_fmaf(own_a<V, kInter, kEven>(p, i) ? ga[i] : 0.0f, a[i], dot);
+                    dot = __builtin_fmaf(own_b<V, kInter, kEven>(p, i) ? gb[i] : 0.0f, b[i], dot);
                 }
                 dot = group_sum<G>(dot) / static_cast<float>(k.d);
 #pragma unroll
@@ -413,11 +414,11 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_bwd_kernel(const Rotary
         const int u = at / (4 * V), i = at % (4 * V), e = i % V;
         const bool second = i / V % 2;
         const Place z = place_of<V, kInter, kEven>(k, u);
-        if (z.idle || !(second ? own_b<V, kEven>(z, e) : own_a<V, kEven>(z, e))) continue;
+        if (z.idle || !(second ? own_b<V, kInter, kEven>(z, e) : own_a<V, kInter, kEven>(z, e))) continue;
         float t = 0.0f;
         for (int w = 0; w < kRotaryWaves; ++w)
             for (int g = 0; g < 64 / G; ++g) t += reinterpret_cast<float(*)[4 * V]>(lds[w])[g * G + u][i];
-        const int col = z.turns && kInter ? z.a + 2 * e + second : (second ? z.b : z.a) + e;
+        const int col = kInter ? z.a + 2 * e + second : (second ? z.b : z.a) + e;
         k.part[(static_cast<int64_t>(blockIdx.x) * 2 + i / (2 * V)) * k.d + col] = t;
     }
 }
