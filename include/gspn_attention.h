@@ -101,7 +101,8 @@ gspn_status gspn_head_rotary_bwd(const gspn_rotary_args* args, int dtype, void* 
  * that sees no key has out = 0 and lse = -Inf.  Keys that a row does not see
  * count for nothing, whatever they hold, if they lie in another sequence,
  * outside all of them or behind an entry's rows; of the row's own sequence,
- * a later key's v must be finite (a product with weight 0).
+ * a later key's v must be finite (a product with weight 0), in the backward
+ * also its k, and q and gout of the rows that do not see a key.
  *   q, out  [rows][heads][d];  k, v [kv_rows][kv_heads][d]; d 1 to 128 (else
  *           GSPN_ERR_UNSUPPORTED); kv_heads divides heads
  *   lse     [heads][rows] fp32 or NULL (the backward needs it)

@@ -257,8 +257,8 @@ __device__ __forceinline__ const T* same(const T* p) {
 
 // ROWS rows on their way from memory to a tile, over kThreads threads.
 // kDirect: straight to LDS, 1 KB a wave and instruction, which the wave only
-// waits for before the barrier that hands the tile over (the prompt of 16384
-// rows: 2.9 ms through registers, 2.2 so).  It takes rows of whole, aligned
+// waits for before the barrier that hands the tile over (when it was chosen, a
+// prompt of 16384 rows, 32 heads of 128: 2.9 ms through registers, 2.2 so).  It takes rows of whole, aligned
 // 16-byte chunks; the swizzle is in the chunk that a lane asks for, and chunks
 // behind the head's end keep the zeros that clear() left.
 template <typename T, int D, int ROWS, int kThreads, bool kDirect>
@@ -529,7 +529,10 @@ hipError_t launch_rotary_bwd(const gspn_rotary_args& a, int dtype, hipStream_t s
 int64_t rotary_bwd_parts(int64_t rows);
 
 // Calls f with the storage type, the width of the tiles that heads of d
-// elements take, and whether their rows go straight to LDS.
+// elements take, and whether their rows go straight to LDS.  Widths are whole
+// blocks of 32 columns, but for bf16 heads of 65 to 80 elements, whose scores
+// take five steps of 16, not six (four maps of 3136 tokens, 16 heads of 72, a
+// training step: 1180 us at 96, 1130 so).  fp32 leaves such steps out anyway.
 template <typename F>
 void attn_dispatch(int dtype, int64_t d, bool direct, F&& f) {
     auto width = [&](auto t, auto straight) {

@@ -24,6 +24,11 @@ __device__ __forceinline__ float log2_sum(float lse) {
     return lse == -INFINITY ? INFINITY : lse * 1.44269504088896340736f;
 }
 
+// Queries at rest, keys and values in tiles as in the forward.  8 x 1024 rows, 18
+// heads, 6 of keys, of 128: 100 us; four maps of 3136 tokens, 16 heads of 72: 370,
+// the matrix unit busy in 53% of the cycles.  Products one after the other, as
+// the compiler orders them: interleaved by hand as in the forward they took 16%
+// longer.
 template <typename T, int D, bool kDirect>
 __global__ __launch_bounds__(kAttnThreads, 2) void attn_dq_kernel(const AttnK a) {
     using Tl = Tile<T, D>;
@@ -158,7 +163,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_dq_kernel(const AttnK a)
 // Values of a workgroup's keys for the keys' gradients.  Two waves a SIMD have
 // 256 registers each: heads of 128 bf16 elements leave no room there for both
 // keys and values beside the gradients' sums, and spilled every reload waits for
-// the tiles on their way (301 us where values in LDS took 211).  All but the last
+// the tiles on their way (8 x 1024 rows, 18 heads, 6 of keys, when it was chosen:
+// 301 us, 211 with values in LDS).  All but the last
 // of the products' steps lie in LDS then, the last in registers, so that two
 // workgroups share a CU.  Rows of 240 bytes need no swizzle.
 template <typename T, int D>
@@ -172,7 +178,9 @@ constexpr int kBwdRows = 64;
 // Keys at rest: two waves of 32 of them, twice, each pair for one half of every
 // tile of rows (joined in LDS at the end).  Long walks are half as long so, which
 // counts where later rows see more keys: 8 x 1024 rows, 18 heads, 6 of keys, 211
-// us with 128 keys a workgroup.
+// us with 128 keys a workgroup, 114 so and in parts.  Four maps of 3136 tokens,
+// 16 heads of 72: 580 us; what bounds both is the matrix unit (busy in 37 and 41%
+// of the cycles) behind LDS, which gives two fragments a product.
 template <typename T, int D, bool kDirect>
 __global__ __launch_bounds__(kAttnThreads, kIsBf16<T> ? 2 : 1) void attn_dkv_kernel(const AttnK a) {
     using Tl = Tile<T, D>;
@@ -328,7 +336,7 @@ __global__ __launch_bounds__(kAttnThreads, kIsBf16<T> ? 2 : 1) void attn_dkv_ker
         if (more) commit(buf ^ 1);
         // (used here whatever happened: a load that may be under way still would be waited
         // for wherever its register is next written, among the fetches, and they with it:
-        // 750 us for four maps of 3136 tokens, 16 heads of 72, where this takes 626)
+        // four maps of 3136 tokens, 16 heads of 72, 750 us, 626 so)
         asm volatile("" ::"v"(stat));
         __syncthreads();
     }
@@ -413,7 +421,8 @@ hipError_t clear_rows(const SeqK& s, bool all, int es, std::initializer_list<std
 
 // Parts that the rows which a workgroup of keys walks are cut into: as many as
 // fill two workgroups a CU, none of fewer than two tiles on average.  Their sums
-// pass through memory in fp32, little where there are few keys.
+// pass through memory in fp32, little where there are few keys (the sum of the
+// parts takes 4 us of the 27 + 4 for 2003 rows over 539 keys, 6 heads of 40).
 int attn_bwd_parts(int64_t rows, int64_t nseq, int64_t heads, int64_t kv_rows, int64_t kv_heads) {
     const int64_t groups = chunk_ids(true, kv_rows, nseq, kKeyShift) * kv_heads;
     const int64_t tiles = (rows / nseq + kBwdRows - 1) / kBwdRows * (heads / kv_heads);

