@@ -184,7 +184,8 @@ SHAPES = [  # lengths of queries, of keys (None: the same), rows before the firs
     ([1], None, 0), ([31], None, 0), ([128], None, 0), ([129], None, 0), ([65, 0, 1, 200], None, 3),
     ([40, 7, 0, 130], [9, 30, 20, 131], 0), ([300], [64], 0), ([5, 3, 0], [0, 4, 0], 2), ([1] * 70, None, 0)]
 HEADS = [(F32, 2, 1, 64, True), (F32, 1, 1, 1, False), (F32, 4, 2, 100, False), (BF16, 3, 3, 128, True),
-         (BF16, 6, 2, 72, False), (BF16, 2, 1, 33, True), (BF16, 4, 4, 64, False), (F32, 2, 2, 80, True)]
+         (BF16, 6, 2, 72, False), (BF16, 2, 1, 33, True), (BF16, 4, 4, 64, False), (F32, 2, 2, 80, True),
+         (BF16, 2, 1, 80, False), (BF16, 2, 2, 79, True), (BF16, 1, 1, 90, False), (BF16, 2, 2, 112, False)]
 
 
 @pytest.mark.parametrize("lengths,keys,first", SHAPES)
@@ -387,6 +388,30 @@ def test_attention_cache_unaligned_rows(dtype, d, slots):
         for b, e in enumerate(range(n) if slots is None else slots):
             if e >= 0:
                 assert torch.equal(p[e, :length], at(rows, i)[spans[b][0]:spans[b][1]])
+
+
+@pytest.mark.parametrize("dtype,heads,kv_heads,d", [(BF16, 4, 2, 128), (BF16, 2, 2, 80), (F32, 3, 1, 32), (BF16, 2, 1, 30)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_cache_seams(dtype, heads, kv_heads, d, causal):
+    """Entries that end before, at and behind a tile's end, and new rows that begin there."""
+    g = gen(78 + d)
+    held = [0, 1, 31, 32, 33, 63, 64, 65, 127, 128, 129, 200]
+    lengths = [1, 64, 33, 1, 130, 1, 65, 2, 1, 64, 128, 57]
+    n, cap, rows = len(held), 330, sum(lengths)
+    q, k, v = (rnd(g, rows, h, d, dtype=dtype) for h in (heads, kv_heads, kv_heads))
+    pools = [torch.full((n, cap, kv_heads, d), math.nan, dtype=dtype) for _ in range(2)]
+    for i in range(n):
+        for p in pools:
+            p[i, :held[i]] = rnd(g, held[i], kv_heads, d, dtype=dtype)
+    state = tuple(dev(p) for p in pools)
+    out = A.gspn_attention_fwd(dev(q), dev(k), dev(v), causal=causal, cu=cu_of(lengths), state=state, held=ints(held))
+    for i, (a, b) in enumerate(R.spans(lengths)):
+        for p, t, s in zip(pools, (k, v), state):
+            p[i, held[i]:held[i] + b - a] = t[a:b]
+            assert torch.equal(torch.nan_to_num(s[i].cpu().float(), 12345.0), torch.nan_to_num(p[i].float(), 12345.0)), i
+        kk, vv = (wide(p[i, :held[i] + b - a]) for p in pools)
+        ref = R.attention(wide(q[a:b]), kk, vv, [(0, b - a)], [(0, len(kk))], d ** -0.5, causal, dtype == BF16)
+        check(out[a:b], ref["out"], "out %d" % i)
 
 
 @pytest.mark.parametrize("dtype,heads,kv_heads,d", [(F32, 4, 2, 20), (F32, 3, 1, 128), (BF16, 8, 2, 72), (BF16, 40, 1, 128),
