@@ -17,8 +17,9 @@
  *    `held` says how many rows an entry holds.
  *  - Sums, softmax statistics and norms are fp32.  The kernels for GSPN_BF16
  *    round the softmax's numerators, and in the backward the scores'
- *    gradients, to bf16 as factors of matrix products that add up in fp32;
- *    those for GSPN_F32 round nothing below fp32.
+ *    gradients, to bf16 as factors of matrix products that add up in fp32 (a
+ *    step's numerators keep 16 bits); those for GSPN_F32 round nothing below
+ *    fp32.
  */
 #ifndef GSPN_ATTENTION_H_
 #define GSPN_ATTENTION_H_

@@ -213,7 +213,8 @@ struct Tile {
     }
 };
 
-// A result's registers as a second factor of Tile::columns.
+// A result's registers as a second factor of Tile::columns.  For bf16 tiles they are
+// rounded to bf16, since a product of fp32 factors takes 16 times as long.
 template <typename T>
 struct Factor;
 template <>
@@ -222,6 +223,16 @@ struct Factor<bf16_t> {
     __device__ __forceinline__ explicit Factor(const f32x16& f) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) p[i / 4][i % 4] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+    }
+    // What its rounding took from f: the two together hold f to 2^-16.
+    __device__ __forceinline__ Factor left_of(const f32x16& f) const {
+        f32x16 r;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            r[2 * i] = f[2 * i] - __uint_as_float(p[i / 4][i % 4] << 16);
+            r[2 * i + 1] = f[2 * i + 1] - __uint_as_float(p[i / 4][i % 4] & 0xffff0000u);
+        }
+        return Factor(r);
     }
 };
 template <>

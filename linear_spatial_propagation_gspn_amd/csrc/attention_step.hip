@@ -6,8 +6,11 @@
 // a workgroup each; its four waves walk every fourth tile of 32 keys through LDS
 // of their own, without a barrier, and are joined at the end, as the runs are
 // by a second launch.  64 tokens over entries of 2048 to 4096 rows, 8 heads of keys
-// of 128: 159 us, 4980 GB/s, 96% of what a copy reaches.  Two entries of 46000
+// of 128: 162 us, 4870 GB/s, 94% of what a copy reaches.  Two entries of 46000
 // rows, 2 heads of keys: 64 runs each, 22 us and 4.3 to join them.
+// bf16 numerators go into their product as two factors, themselves rounded and
+// what that lost: one factor alone took 160 us, and the results lay 0.0023 (root
+// mean square, of their size) from the exact ones, 0.0017 so, their own rounding.
 #include "attention.hpp"
 
 namespace gspn {
@@ -120,6 +123,11 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_step_kernel(const AttnK 
         const Factor<T> p(s[0]);
 #pragma unroll
         for (int b = 0; b < kBlocks<D>; ++b) sm.o[b] = Tl::columns(vc, 0, b, p.p, sm.o[b]);
+        if constexpr (kIsBf16<T>) {
+            const Factor<T> rest = p.left_of(s[0]);
+#pragma unroll
+            for (int b = 0; b < kBlocks<D>; ++b) sm.o[b] = Tl::columns(vc, 0, b, rest.p, sm.o[b]);
+        }
     }
 
     // the waves' results: [32][d values, sum, maximum], each on the others' scale

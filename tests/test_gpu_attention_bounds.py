@@ -1,0 +1,73 @@
+"""The attention operators on the GPU where their bounds are closer than attention_reference's, and where a call takes a
+way of its own that test_gpu_attention.py does not: against the same 64-bit definitions, element by element."""
+import math
+import sys
+
+import pytest
+import torch
+
+import attention_bounds as B
+import attention_reference as R
+from linear_spatial_propagation_gspn_amd import attention as A
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    A.lib()
+    yield
+    torch.cuda.synchronize()
+
+
+@pytest.fixture(autouse=True)
+def _say(request):
+    print("case:", request.node.name, flush=True)
+    sys.stdout.flush()
+    yield
+    torch.cuda.synchronize()
+
+
+def rnd(g, *shape, dtype=F32, by=1.0):
+    return (torch.randn(shape, generator=g) * by).to(dtype)
+
+
+def wide(t):
+    return None if t is None else t.detach().cpu().double()
+
+
+def dev(t):
+    return None if t is None else t.to(DEV)
+
+
+def ints(values):
+    return torch.tensor(values, dtype=torch.int32, device=DEV)
+
+
+def check(got, value, bound, what):
+    """|got - value| <= half a step of got's type + the bound, element by element."""
+    off = (wide(got) - value).abs()
+    most = R.half_step(got.dtype) * value.abs() * (1 + 2.0 ** -7) + 1.01 * R.U * bound + 1e-37
+    assert torch.isfinite(off).all(), what
+    assert (off <= most).all(), "%s: worst %.3g of its bound" % (what, float((off / most).max()))
+
+
+@pytest.mark.parametrize("heads,kv_heads,d,cap", [(8, 2, 128, 300), (4, 4, 72, 40), (40, 1, 64, 200), (6, 2, 33, 2500),
+                                                  (8, 1, 96, 2500), (2, 1, 80, 700), (1, 1, 1, 9)])
+def test_step_adds_no_error_of_bf16(heads, kv_heads, d, cap):
+    """The numerators' rounding to bf16 does not reach a single token's result."""
+    g = torch.Generator().manual_seed(cap + d)
+    held = [cap - 1, cap // 2, 0, min(cap - 1, 33)]
+    n = len(held)
+    q, k, v = (rnd(g, n, h, d, dtype=BF16) for h in (heads, kv_heads, kv_heads))
+    pools = [rnd(g, n, cap, kv_heads, d, dtype=BF16) for _ in range(2)]
+    out = A.gspn_attention_step(dev(q), dev(k), dev(v), tuple(dev(p) for p in pools), ints(held))
+    for i, m in enumerate(held):
+        for h in range(heads):
+            j = h // (heads // kv_heads)
+            kk, vv = (torch.cat([wide(p[i, :m, j]), wide(t[i:i + 1, j])]) for p, t in zip(pools, (k, v)))
+            check(out[i:i + 1, h], *B.step(wide(q[i:i + 1, h]), kk, vv, d ** -0.5), "out %d %d" % (i, h))
