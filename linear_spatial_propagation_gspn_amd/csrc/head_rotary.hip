@@ -38,11 +38,13 @@ struct RotaryK {
 
 
 // sin and cos of 2 pi t for a 64-bit t: reduced to an eighth of a turn either
-// way, then the first terms of their series (the next are below 2^-28).
+// way, an angle that is rounded once (in 64 bits up to here: a product in fp32 would
+// leave 1.26 2^-24 of it, not 2^-25), then the first terms of their series (the next are
+// below 2^-28).
 __device__ __forceinline__ void sincos_turn(double t, float* s, float* c) {
     t -= __builtin_rint(t);
     const double quarter = __builtin_rint(4.0 * t);
-    const float x = static_cast<float>(t - 0.25 * quarter) * 6.28318530717958647692f;
+    const float x = static_cast<float>((t - 0.25 * quarter) * 6.28318530717958647692);
     const float y = x * x;
     float a = __builtin_fmaf(y, 2.75573192e-6f, -1.98412698e-4f);  // 1/9!, -1/7!
     a = __builtin_fmaf(a, y, 8.33333333e-3f);                      // 1/5!
