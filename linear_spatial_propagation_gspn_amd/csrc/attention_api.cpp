@@ -28,7 +28,7 @@ gspn_status check_rotary(const gspn_rotary_args* a, int dtype, bool bwd, bool* e
     if (a->d > GSPN_ROTARY_MAX_HEAD || a->axes > GSPN_ROTARY_MAX_AXES || a->heads > kMaxHeads ||
         a->kv_heads > kMaxHeads)
         return GSPN_ERR_UNSUPPORTED;
-    if (a->axes < 1 || a->pairs < 0 || 2 * a->pairs > a->d) return GSPN_ERR_BAD_SHAPE;
+    if (a->axes < 1 || a->pairs < 0 || a->pairs > a->d / 2) return GSPN_ERR_BAD_SHAPE;
     int64_t sum = 0;
     for (int i = 0; i < a->axes; ++i) {
         if (a->section[i] < 0 || a->section[i] > a->pairs) return GSPN_ERR_BAD_SHAPE;

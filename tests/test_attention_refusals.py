@@ -1,0 +1,18 @@
+"""CPU tests of refusals at the ends of the attention operators' argument types: sums and products of sizes that would pass
+64 bits, scales that pass fp32.  Nothing is launched."""
+import pytest
+
+from linear_spatial_propagation_gspn_amd import attention as A
+from test_attention_abi import BF16, F32, SHAPE, UNSUP, refuse
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return A.lib()
+
+
+@pytest.mark.parametrize("kind", ["fwd", "bwd"])
+@pytest.mark.parametrize("pairs", [1 << 62, (1 << 62) + 3, (1 << 63) - 1, 1 << 61])
+def test_pairs_whose_double_passes_64_bits(lib, kind, pairs):
+    refuse(lib, "rotary", kind, SHAPE, pairs=pairs, axes=1, section0=pairs, section1=0)
+    refuse(lib, "rotary", kind, SHAPE, dtype=BF16, pairs=pairs, section0=pairs, section1=0)
