@@ -86,7 +86,7 @@ gspn_status check_attn(const gspn_attn_args* a, int dtype, Which which, bool* em
     gspn_status s = check_seq(a->seq, pool, which == kStep, empty, &b);
     if (s != GSPN_OK) return s;
     if (a->seq.resume) return GSPN_ERR_BAD_SHAPE;
-    if (kv < 0 || kv + nseq > kMaxRows) return GSPN_ERR_BAD_SHAPE;
+    if (kv < 0 || kv > kMaxRows || kv + nseq > kMaxRows) return GSPN_ERR_BAD_SHAPE;
     const bool none = *empty;  // a backward has rows to clear, also where there is no sequence
     *empty = which == kBwd ? rows == 0 && kv == 0 : none || rows == 0;
     if (*empty) return GSPN_OK;

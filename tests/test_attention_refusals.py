@@ -16,3 +16,15 @@ def lib():
 def test_pairs_whose_double_passes_64_bits(lib, kind, pairs):
     refuse(lib, "rotary", kind, SHAPE, pairs=pairs, axes=1, section0=pairs, section1=0)
     refuse(lib, "rotary", kind, SHAPE, dtype=BF16, pairs=pairs, section0=pairs, section1=0)
+
+
+@pytest.mark.parametrize("kind", ["fwd", "step", "bwd"])
+@pytest.mark.parametrize("kv_rows", [(1 << 63) - 1, (1 << 63) - 2, 1 << 62, (1 << 30) + 2])
+def test_keys_whose_number_with_the_sequences_passes_64_bits(lib, kind, kv_rows):
+    # (128 heads of keys: a count of their workgroups would come round to a small one)
+    for heads in (128, 2):
+        build = dict(heads=heads, kv_heads=heads, d=2, lse=True)
+        refuse(lib, "attn", kind, SHAPE, build=build, kv_rows=kv_rows)
+        if kind != "step":
+            refuse(lib, "attn", kind, SHAPE, build=dict(build, kv_cu=True), kv_rows=kv_rows)
+            refuse(lib, "attn", kind, SHAPE, build=dict(build, cu=True, nseq=1), kv_rows=kv_rows)
