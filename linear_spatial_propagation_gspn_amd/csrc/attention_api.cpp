@@ -69,7 +69,7 @@ gspn_status check_rotary(const gspn_rotary_args* a, int dtype, bool bwd, bool* e
 }
 
 bool attn_sizes_ok(int64_t rows, int64_t nseq, int64_t heads, int64_t kv_heads, int64_t d) {
-    return rows >= 0 && nseq >= 0 && rows <= kMaxRows && rows + nseq <= kMaxRows && kv_heads >= 1 && heads >= 1 &&
+    return rows >= 0 && nseq >= 0 && rows <= kMaxRows && nseq <= kMaxRows - rows && kv_heads >= 1 && heads >= 1 &&
            heads <= kMaxHeads && heads % kv_heads == 0 && d >= 1 && d <= GSPN_ATTENTION_MAX_HEAD;
 }
 

@@ -28,3 +28,11 @@ def test_keys_whose_number_with_the_sequences_passes_64_bits(lib, kind, kv_rows)
         if kind != "step":
             refuse(lib, "attn", kind, SHAPE, build=dict(build, kv_cu=True), kv_rows=kv_rows)
             refuse(lib, "attn", kind, SHAPE, build=dict(build, cu=True, nseq=1), kv_rows=kv_rows)
+
+
+@pytest.mark.parametrize("nseq", [(1 << 63) - 1, (1 << 63) - 30, 1 << 62, 1 << 30])
+def test_workspaces_of_too_many_sequences(lib, nseq):
+    assert lib.gspn_attention_bwd_workspace_bytes(40, nseq, 6, 40, 2, 20) == -1
+    assert lib.gspn_attention_bwd_workspace_bytes(1 << 30, nseq, 6, 40, 2, 20) == -1
+    if nseq > 1 << 30:
+        assert lib.gspn_attention_step_workspace_bytes(nseq, 6, 2, 20, 50) == -1
