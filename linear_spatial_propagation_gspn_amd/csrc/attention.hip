@@ -66,7 +66,7 @@ template <typename T, int D, bool kDirect, bool kCache>
 __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnK a) {
     using Tl = Tile<T, D>;
     constexpr int BN = kTileRows<T>;
-    __shared__ __attribute__((aligned(16))) char lds[2][2][BN * Tl::kRow];
+    __shared__ __attribute__((aligned(kTileAlign))) char lds[2][2][BN * Tl::kRow];
     if constexpr (kCache) {
         if (blockIdx.x >= static_cast<uint32_t>(a.walks)) {
             append_rows<T>(a, blockIdx.x - a.walks);

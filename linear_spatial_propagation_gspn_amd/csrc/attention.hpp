@@ -128,6 +128,9 @@ __device__ __forceinline__ f32x16 mma(Quad a, Quad b, f32x16 c) {
     }
 }
 
+// The alignment of arrays of tiles.
+constexpr int kTileAlign = 256;
+
 // A tile of rows of D elements in LDS, by its byte address there.  LDS gives 256
 // bytes a cycle, in banks: its 16-byte chunks are swizzled so that 16 rows'
 // chunks of one column (row fragments) and four rows' four of them (transposed
@@ -142,7 +145,9 @@ struct Tile {
     static constexpr int kSteps = D * static_cast<int>(sizeof(T)) / 32;  // products over a whole row
     static constexpr int kE = 16 / static_cast<int>(sizeof(T));
     static constexpr int kSpan = kRow % 256 == 0 ? 16 : kRow % 256 == 128 ? 8 : 4;
-    static_assert(kRow % (kSpan * 16) == 0);
+    // What a tile's address must be a multiple of: at() changes the address' bits below.
+    static constexpr int kAlign = kSpan * 16;
+    static_assert(kRow % kAlign == 0 && kAlign <= kTileAlign);
 
     // Whether step i of a product over a row holds any of the head's d elements.
     // (Only fp32 products take long enough for the question: 2003 rows over 539

@@ -33,7 +33,7 @@ template <typename T, int D, bool kDirect>
 __global__ __launch_bounds__(kAttnThreads, 2) void attn_dq_kernel(const AttnK a) {
     using Tl = Tile<T, D>;
     constexpr int BN = kTileRows<T>;
-    __shared__ __attribute__((aligned(16))) char lds[2][2][BN * Tl::kRow];
+    __shared__ __attribute__((aligned(kTileAlign))) char lds[2][2][BN * Tl::kRow];
     const AttnItem w = find_item(a.seq, a.heads, a.causal != 0, kAttnShift, blockIdx.x);
     if (w.c.seq < 0 || w.c.r0 >= w.c.r1) return;
     const int tid = threadIdx.x, lane = tid & 63;
@@ -186,7 +186,7 @@ __global__ __launch_bounds__(kAttnThreads, kIsBf16<T> ? 2 : 1) void attn_dkv_ker
     using Tl = Tile<T, D>;
     constexpr int BM = kBwdRows;
     constexpr bool kInLds = kValuesInLds<T, D>;
-    __shared__ __attribute__((aligned(16))) char lds[2][2][BM * Tl::kRow];
+    __shared__ __attribute__((aligned(kTileAlign))) char lds[2][2][BM * Tl::kRow];
     __shared__ __attribute__((aligned(16))) char values[kInLds ? kKeyRows * kValueRow : 16];
     __shared__ __attribute__((aligned(16))) float stats[2][2][BM];
     const int part = static_cast<int>(blockIdx.x % a.splits);

@@ -28,7 +28,8 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_step_kernel(const AttnK 
     constexpr int kJoin = 32 * (32 * kBlocks<D> + 2) * 4;
     constexpr int kSum = 32 * 32 * kBlocks<D>, kMost = kSum + 32;
     constexpr int kWave = kTiles > kJoin ? kTiles : kJoin;
-    __shared__ __attribute__((aligned(16))) char lds[kStepWaves][kWave];
+    static_assert(kWave % Tl::kAlign == 0);  // each wave's tiles lie as the first one's do
+    __shared__ __attribute__((aligned(kTileAlign))) char lds[kStepWaves][kWave];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int blocks = (a.group + 31) / 32;  // of 32 heads of a group
     int64_t id = blockIdx.x;
