@@ -107,7 +107,7 @@ gspn_status gspn_head_rotary_bwd(const gspn_rotary_args* args, int dtype, void* 
  *   q, out  [rows][heads][d];  k, v [kv_rows][kv_heads][d]; d 1 to 128 (else
  *           GSPN_ERR_UNSUPPORTED); kv_heads divides heads
  *   lse     [heads][rows] fp32 or NULL (the backward needs it)
- *   scale   finite
+ *   scale   finite, also times log2 e in fp32: |scale| < 2.35e38
  * Keys' sequences: kv_cu is a device array of nseq + 1 offsets into the
  *   kv_rows rows; NULL: as the queries' (kv_rows == rows with seq.cu; without,
  *   equal lengths kv_rows / nseq).  A sequence may have no key.

@@ -2,8 +2,6 @@
 // packed sequences and prompts that continue a cache entry.
 #include "attention.hpp"
 
-#include <cmath>
-
 namespace gspn {
 namespace {
 
@@ -335,8 +333,9 @@ AttnK make_attn(const gspn_attn_args& a) {
     k.causal = a.causal != 0;
     k.flip = a.scale < 0.0;
     k.scale = static_cast<float>(a.scale);
-    k.scale_log2 = static_cast<float>(std::fabs(a.scale) * 1.4426950408889634);
-    if (!(k.scale_log2 >= 1e-37f)) k.scale_log2 = 1e-37f;  // so that a hidden score, -Inf, stays one when it is scaled
+    k.scale_log2 = scale_log2(a.scale);
+    // (so that a hidden score, -Inf, stays one when it is scaled; the largest other becomes 2^-21)
+    if (k.scale_log2 == 0.0f) k.scale_log2 = 0x1p-149f;
     k.q = a.q;
     k.k = a.k;
     k.v = a.v;

@@ -14,6 +14,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
 #include <type_traits>
 
 #include "../../include/gspn_attention.h"
@@ -34,7 +35,7 @@ struct AttnK {
     int32_t heads, kv_heads, group, d, causal;
     int32_t flip;      // scale < 0: queries (keys) enter the scores negated
     float scale;       // as given
-    float scale_log2;  // |scale| log2 e, at least 1e-37
+    float scale_log2;  // |scale| log2 e, at least 2^-149
     const void* q;
     const void* k;
     const void* v;
@@ -530,6 +531,8 @@ __device__ __forceinline__ AttnItem find_item(const SeqK& s, int heads, bool bac
 // Host side ---------------------------------------------------------------
 
 AttnK make_attn(const gspn_attn_args& a);
+// |scale| log2 e, which a call needs to be finite.
+inline float scale_log2(double scale) { return static_cast<float>(std::fabs(scale) * 1.4426950408889634); }
 int attn_splits(int64_t nseq, int64_t heads, int64_t kv_heads, int64_t capacity);
 constexpr int kAttnMaxSplits = 64;
 int attn_bwd_parts(int64_t rows, int64_t nseq, int64_t heads, int64_t kv_rows, int64_t kv_heads);

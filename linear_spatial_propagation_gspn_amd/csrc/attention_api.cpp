@@ -77,7 +77,7 @@ gspn_status check_attn(const gspn_attn_args* a, int dtype, Which which, bool* em
     if (!a) return GSPN_ERR_NULL_POINTER;
     if (!valid_dtype(dtype)) return GSPN_ERR_BAD_DTYPE;
     if (a->heads < 1 || a->kv_heads < 1 || a->heads % a->kv_heads != 0 || a->d < 1) return GSPN_ERR_BAD_SHAPE;
-    if (!std::isfinite(a->scale) || !std::isfinite(static_cast<float>(a->scale))) return GSPN_ERR_BAD_SHAPE;
+    if (!std::isfinite(gspn::scale_log2(a->scale))) return GSPN_ERR_BAD_SHAPE;
     if (a->d > GSPN_ATTENTION_MAX_HEAD || a->heads > kMaxHeads) return GSPN_ERR_UNSUPPORTED;
     const int64_t es = elem_size(dtype), rows = a->seq.rows, nseq = a->seq.nseq, kv = a->kv_rows;
     const bool pool = a->k_pool || a->v_pool || which == kStep;

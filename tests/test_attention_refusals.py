@@ -36,3 +36,11 @@ def test_workspaces_of_too_many_sequences(lib, nseq):
     assert lib.gspn_attention_bwd_workspace_bytes(1 << 30, nseq, 6, 40, 2, 20) == -1
     if nseq > 1 << 30:
         assert lib.gspn_attention_step_workspace_bytes(nseq, 6, 2, 20, 50) == -1
+
+
+@pytest.mark.parametrize("kind", ["fwd", "step", "bwd"])
+def test_scales_whose_powers_of_two_pass_fp32(lib, kind):
+    for scale in (2.4e38, -3.4e38):
+        refuse(lib, "attn", kind, SHAPE, scale=scale)
+        refuse(lib, "attn", kind, SHAPE, dtype=BF16, scale=scale)
+    refuse(lib, "attn", kind, UNSUP, scale=2.3e38, d=129)  # (the scale alone is no reason)

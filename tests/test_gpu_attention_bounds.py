@@ -89,3 +89,31 @@ def test_rotation_of_a_unit_is_its_sine_and_cosine():
     t = pos.double()[:, None] * freqs
     for name, got, want in (("cos", y[:, :pairs], torch.cos(t)), ("sin", y[:, pairs:], torch.sin(t))):
         assert float((got - want).abs().max()) <= 1.35 * R.U, name
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("scale", [0.0, 1e-42, -1e-40])
+def test_scales_near_zero_weigh_alike(dtype, scale):
+    """Scores of 1e36 and more times (next to) nothing: every key that a row sees has the same weight, but for
+    exponents up to 3.4e38 1e-40 = 0.034."""
+    g = torch.Generator().manual_seed(6)
+    n, d = 70, 8
+    q, k = (rnd(g, n, 1, d).to(dtype) * 2.0 ** 60 for _ in range(2))
+    v, go = rnd(g, n, 1, d, dtype=dtype), rnd(g, n, 1, d, dtype=dtype)
+    out, lse = A.gspn_attention_fwd(dev(q), dev(k), dev(v), scale=scale, lse=True)
+    # the scale itself, rounded to a multiple of 2^-149, is off by 2^-150: times |score| log2 e, and the same in lse
+    mag = wide(q[:, 0]).abs() @ wide(k[:, 0]).abs().t()
+    assert float(mag.max()) < 3e38
+    off = float(mag.max()) * 2.0 ** -149 * 2 / R.U
+    ref = R.attend(wide(q[:, 0]), wide(k[:, 0]), wide(v[:, 0]), scale, True, dtype == BF16)
+    p = R.attend(wide(q[:, 0]), wide(k[:, 0]), wide(v[:, 0].abs()), scale, True, dtype == BF16)["out"][0]
+    check(out[:, 0], ref["out"][0], ref["out"][1] + off * p, "out")
+    assert float((wide(lse[0]) - ref["lse"][0]).abs().max()) <= R.U * float(ref["lse"][1].max() + off + 4)
+    step = A.gspn_attention_step(dev(q[-1:]), dev(k[-1:]), dev(v[-1:]), (dev(k[None]).contiguous(), dev(v[None]).contiguous()),
+                                 ints([n - 1]), scale=scale)
+    check(step[:, 0], ref["out"][0][-1:], (ref["out"][1] + off * p)[-1:], "step")
+    grads = A.gspn_attention_bwd(dev(q), dev(k), dev(v), out, lse, dev(go), scale=scale)
+    assert all(torch.isfinite(t).all() for t in grads)
+    back = R.attend(wide(q[:, 0]), wide(k[:, 0]), wide(v[:, 0]), scale, True, dtype == BF16, wide(go[:, 0]))["dv"]
+    pg = R.attend(wide(q[:, 0]), wide(k[:, 0]), wide(v[:, 0]), scale, True, dtype == BF16, wide(go[:, 0].abs()))["dv"][0]
+    check(grads[2][:, 0], back[0], back[1] + 2 * off * pg, "dv")
