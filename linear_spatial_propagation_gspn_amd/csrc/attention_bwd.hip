@@ -8,9 +8,10 @@
 // twice, seven products instead of five, and nothing is added through memory.
 //
 // D from a bf16 out carries its rounding, as large against ds as one over the
-// root of the keys: rows that see one tile of keys or less get theirs from the
-// weights, sum_j p_ij <gout_i, v_j>.  A row that sees one key has p = 1 whatever
-// the score: its ds is 0, not the rounding that is left of the difference.
+// root of the keys: rows that see one tile of keys or less (64; fp32: 32) get theirs
+// from the weights, sum_j p_ij <gout_i, v_j>, whatever the others of their wave see.
+// A row that sees one key has p = 1 whatever the score: its ds is 0, not the rounding
+// that is left of the difference.
 #include "attention.hpp"
 
 #include <array>
@@ -93,50 +94,49 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_dq_kernel(const AttnK a)
         sv.commit(tid, lds[0][1]);
     }
     __syncthreads();
+    // the weights of 32 keys of tile t and their gradients
+    const auto weights = [&](int t, int n, f32x16& s, f32x16& dp) {
+        const uint32_t kt = Tl::rows_at(lds_at(lds[t & 1][0])), vt = Tl::rows_at(lds_at(lds[t & 1][1]));
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < Tl::kSteps; ++i) {
+            if (!Tl::holds(i, a.d)) continue;
+            s = mma<T>(Tl::rows(kt, 32 * n, i), q[i], s);
+            dp = mma<T>(Tl::rows(vt, 32 * n, i), g[i], dp);
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], a.scale_log2, -lse2));
+        if ((t + 1) * BN > wave_all) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (t * BN + 32 * n + result_row(r) >= my_keys) s[r] = dp[r] = 0.0f;
+        }
+    };
+    if (wave_keys > 0 && wave_all <= BN) {  // some row's keys are all in the first tile
+        float sum = 0.0f;
+#pragma unroll 1
+        for (int n = 0; n < BN / 32; ++n) {
+            f32x16 s, dp;
+            weights(0, n, s, dp);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) sum = __builtin_fmaf(s[r], dp[r], sum);
+        }
+        sum = both_sum(sum);
+        delta = my_keys <= BN ? sum : delta;
+    }
     for (int t = 0; t < tiles; ++t) {
         const bool more = t + 1 < tiles;
         if (more) {
             sk.fetch(tid, kp, a.ldk, (t + 1) * BN, keys.count - 1, a.d, lds[(t + 1) & 1][0]);
             sv.fetch(tid, vp, a.ldv, (t + 1) * BN, keys.count - 1, a.d, lds[(t + 1) & 1][1]);
         }
-        const int key0 = t * BN;
-        if (key0 < wave_keys) {
-            const uint32_t kt = Tl::rows_at(lds_at(lds[t & 1][0])), kc = Tl::columns_at(lds_at(lds[t & 1][0]));
-            const uint32_t vt = Tl::rows_at(lds_at(lds[t & 1][1]));
-            // the weights of 32 keys and their gradients
-            const auto weights = [&](int n, f32x16& s, f32x16& dp) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.0f;
-#pragma unroll
-                for (int i = 0; i < Tl::kSteps; ++i) {
-                    if (!Tl::holds(i, a.d)) continue;
-                    s = mma<T>(Tl::rows(kt, 32 * n, i), q[i], s);
-                    dp = mma<T>(Tl::rows(vt, 32 * n, i), g[i], dp);
-                }
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], a.scale_log2, -lse2));
-                if (key0 + BN > wave_all) {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (key0 + 32 * n + result_row(r) >= my_keys) s[r] = dp[r] = 0.0f;
-                }
-            };
-            if (wave_keys <= BN) {
-                delta = 0.0f;
-#pragma unroll 1
-                for (int n = 0; n < BN / 32; ++n) {
-                    f32x16 s, dp;
-                    weights(n, s, dp);
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) delta = __builtin_fmaf(s[r], dp[r], delta);
-                }
-                delta = both_sum(delta);
-            }
+        if (t * BN < wave_keys) {
+            const uint32_t kc = Tl::columns_at(lds_at(lds[t & 1][0]));
 #pragma unroll
             for (int n = 0; n < BN / 32; ++n) {
                 f32x16 s, dp;
-                weights(n, s, dp);
+                weights(t, n, s, dp);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[r] *= dp[r] - delta;
                 if (my_keys < 2) {

@@ -117,3 +117,34 @@ def test_scales_near_zero_weigh_alike(dtype, scale):
     back = R.attend(wide(q[:, 0]), wide(k[:, 0]), wide(v[:, 0]), scale, True, dtype == BF16, wide(go[:, 0]))["dv"]
     pg = R.attend(wide(q[:, 0]), wide(k[:, 0]), wide(v[:, 0]), scale, True, dtype == BF16, wide(go[:, 0].abs()))["dv"][0]
     check(grads[2][:, 0], back[0], back[1] + 2 * off * pg, "dv")
+
+
+def common(g, rows, heads, d, mean):
+    """Rows about a common vector: <gout, v_j> - D is then far smaller than either."""
+    sign = (torch.randint(0, 2, (heads, d), generator=g) * 2 - 1).float()
+    return (mean * sign + torch.randn(rows, heads, d, generator=g)).to(BF16)
+
+
+@pytest.mark.parametrize("nq,nk,causal", [(40, 40, True), (64, 64, True), (33, 50, False), (7, 64, False),
+                                          (30, 70, True), (100, 90, True), (130, 141, True), (1, 33, True)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_within_one_tile_take_their_sums_from_the_weights(nq, nk, causal, d):
+    """D of a row that sees 64 keys or less does not carry the rounding of its bf16 out, whatever its neighbours see."""
+    g = torch.Generator().manual_seed(nq * 7 + nk)
+    heads, kv_heads, scale = 4, 2, d ** -0.5
+    q, go = rnd(g, nq, heads, d, dtype=BF16), rnd(g, nq, heads, d, dtype=BF16)
+    k, v = common(g, nk, kv_heads, d, 4.0), common(g, nk, kv_heads, d, 32.0)
+    out, lse = A.gspn_attention_fwd(dev(q), dev(k), dev(v), causal=causal, scale=scale, cu=ints([0, nq]), cu_k=ints([0, nk]),
+                                    lse=True)
+    dq, dk, dv = A.gspn_attention_bwd(dev(q), dev(k), dev(v), out, lse, dev(go), causal=causal, scale=scale,
+                                      cu=ints([0, nq]), cu_k=ints([0, nk]))
+    near = R.visible(nq, nk, causal).sum(1) <= B.TILE
+    want = {"dk": [0.0, 0.0], "dv": [0.0, 0.0]}
+    for h in range(heads):
+        one = B.gradients(*(wide(t) for t in (q[:, h], k[:, h // 2], v[:, h // 2])), scale, causal, wide(go[:, h]))
+        check(dq[:, h][near], one["dq"][0][near], one["dq"][1][near], "dq %d" % h)
+        for n in want:
+            want[n] = [a + b for a, b in zip(want[n], one[n])]
+            if h % 2:
+                check({"dk": dk, "dv": dv}[n][:, h // 2], want[n][0], want[n][1] + 2 * want[n][0].abs(), n)
+                want[n] = [0.0, 0.0]
