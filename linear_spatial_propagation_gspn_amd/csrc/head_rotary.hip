@@ -452,10 +452,17 @@ RotaryK make_rotary(const gspn_rotary_args& a) {
 }
 
 // Waves that share a row's heads, so that few rows still fill the SIMDs: two a
-// SIMD; more would only form a row's sines more often.
-int slices_for(int64_t rows, int64_t heads, int group) {
-    const int64_t most = (heads + 64 / group - 1) / (64 / group);
-    const int64_t want = rows < 1 ? 1 : (2048 + rows - 1) / rows;
+// SIMD; more would only form a row's sines more often.  A backward's waves leave sums
+// of the weights' gradients too: it has no more than those two (2000 rows, 32 + 8 heads
+// of 128 bf16 elements: 19.8 us with one slice, 25.6 with two; 500 rows 17.7 with one
+// workgroup a four rows, 11.9 with four slices, 64 rows 15.6 and 8.9).
+int64_t most_slices(int64_t rows, bool bwd) {
+    const int64_t n = rows < 1 ? 1 : bwd ? 2048 / rows : (2048 + rows - 1) / rows;
+    return n < 1 ? 1 : n;
+}
+
+int slices_for(int64_t rows, int64_t heads, int group, bool bwd) {
+    const int64_t most = (heads + 64 / group - 1) / (64 / group), want = most_slices(rows, bwd);
     return static_cast<int>(want < most ? want : most);
 }
 
@@ -527,12 +534,15 @@ void replay(const char* kn, const gspn_rotary_args& a, bool bwd, int64_t es) {
 
 }  // namespace
 
-// Workgroups that walk the rows of a backward: four a CU, each with a wave for
-// at least one row.
-int64_t rotary_bwd_parts(int64_t rows) {
-    const int64_t n = (rows + kRotaryWaves - 1) / kRotaryWaves;
+// Workgroups that walk the rows of a backward: four a CU at most, each wave with at
+// least one row's slice of heads.
+int64_t rotary_bwd_groups(int64_t rows, int64_t slices) {
+    const int64_t n = (rows * slices + kRotaryWaves - 1) / kRotaryWaves;
     return n < 1 ? 1 : n < 1024 ? n : 1024;
 }
+
+// Their partial sums, whatever the heads.
+int64_t rotary_bwd_parts(int64_t rows) { return rotary_bwd_groups(rows, most_slices(rows, true)); }
 
 hipError_t launch_rotary_fwd(const gspn_rotary_args& a, int dtype, hipStream_t stream) {
     RotaryK k = make_rotary(a);
@@ -548,7 +558,7 @@ hipError_t launch_rotary_fwd(const gspn_rotary_args& a, int dtype, hipStream_t s
         using T = decltype(t);
         constexpr int V = decltype(v)::value, G = decltype(g)::value;
         constexpr bool kInter = decltype(inter)::value, kEven = decltype(even)::value;
-        k.slices = slices_for(a.rows, a.heads + a.kv_heads, G);
+        k.slices = slices_for(a.rows, a.heads + a.kv_heads, G, false);
         const int64_t blocks = (a.rows * k.slices + kRotaryWaves - 1) / kRotaryWaves;
         const dim3 grid(static_cast<unsigned>(blocks < kRotaryBlocks ? blocks : kRotaryBlocks));
         GSPN_REPLAYED("rotary_fwd_kernel", kRotaryThreads, 0);
@@ -569,19 +579,21 @@ hipError_t launch_rotary_bwd(const gspn_rotary_args& a, int dtype, hipStream_t s
     k.ldgk = a.ldgk;
     const bool sums = a.dq_weight || a.dk_weight;
     k.part = sums ? static_cast<float*>(a.workspace) : nullptr;
-    const int64_t es = dtype == GSPN_F32 ? 4 : 2, parts = rotary_bwd_parts(a.rows);
+    const int64_t es = dtype == GSPN_F32 ? 4 : 2;
+    int64_t parts = 0;
     if (a.rows > 0) {
         replay("rotary_bwd_kernel", a, true, es);
         GSPN_REPLAY_ROWS("rotary_bwd_kernel", "gq", a.gq, a.rows, a.ldgq, a.heads * a.d, es);
         GSPN_REPLAY_ROWS("rotary_bwd_kernel", "dq", a.dq, a.rows, a.lddq, a.heads * a.d, es);
         GSPN_REPLAY_ROWS("rotary_bwd_kernel", "gk", a.gk, a.rows, a.ldgk, a.kv_heads * a.d, es);
         GSPN_REPLAY_ROWS("rotary_bwd_kernel", "dk", a.dk, a.rows, a.lddk, a.kv_heads * a.d, es);
-        if (sums) GSPN_REPLAY_ROWS("rotary_bwd_kernel", "partial sums", a.workspace, parts, 2 * a.d, 2 * a.d, 4);
         rotary_dispatch(dtype, k, [&](auto t, auto v, auto g, auto inter, auto even) {
             using T = decltype(t);
             constexpr int V = decltype(v)::value, G = decltype(g)::value;
-        constexpr bool kInter = decltype(inter)::value, kEven = decltype(even)::value;
-            k.slices = slices_for(a.rows, a.heads + a.kv_heads, G);
+            constexpr bool kInter = decltype(inter)::value, kEven = decltype(even)::value;
+            k.slices = slices_for(a.rows, a.heads + a.kv_heads, G, true);
+            parts = rotary_bwd_groups(a.rows, k.slices);
+            if (sums) GSPN_REPLAY_ROWS("rotary_bwd_kernel", "partial sums", a.workspace, parts, 2 * a.d, 2 * a.d, 4);
             GSPN_REPLAYED("rotary_bwd_kernel", kRotaryThreads, kRotaryThreads * 4 * V * 4);
             hipLaunchKernelGGL((rotary_bwd_kernel<T, V, G, kInter, kEven>), dim3(static_cast<unsigned>(parts)), dim3(kRotaryThreads), 0,
                                stream, k);
@@ -592,7 +604,7 @@ hipError_t launch_rotary_bwd(const gspn_rotary_args& a, int dtype, hipStream_t s
     if (!sums) return hipSuccess;
     ReduceK r = {};
     r.part = k.part;
-    r.parts = a.rows > 0 ? parts : 0;
+    r.parts = parts;
     r.ld = r.cols = 2 * a.d;
     r.c = a.d;
     r.o[0] = {a.dq_weight, 1, 1, 0};
