@@ -148,3 +148,35 @@ def test_rows_within_one_tile_take_their_sums_from_the_weights(nq, nk, causal, d
             if h % 2:
                 check({"dk": dk, "dv": dv}[n][:, h // 2], want[n][0], want[n][1] + 2 * want[n][0].abs(), n)
                 want[n] = [0.0, 0.0]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,heads,kv_heads,d,sections", [(1, 2, 1, 64, (32,)), (70, 5, 3, 72, (18, 18)), (33, 2, 2, 27, (4,)),
+                                                            (9, 1, 9, 128, (20, 12)), (600, 6, 2, 48, (24,))])
+@pytest.mark.parametrize("which", ["q", "k"])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_norm_of_queries_or_keys_alone(dtype, rows, heads, kv_heads, d, sections, which, interleaved):
+    g = torch.Generator().manual_seed(rows + d)
+    pairs = sum(sections)
+    freqs = 10000.0 ** -torch.rand(pairs, generator=g, dtype=torch.float64)
+    pos = torch.randint(-3000, 100000, (rows, len(sections)), generator=g, dtype=torch.int32)
+    x = {n: rnd(g, rows, h, d, dtype=dtype) for n, h in (("q", heads), ("k", kv_heads))}
+    go = {n: rnd(g, rows, h, d, dtype=dtype) for n, h in (("q", heads), ("k", kv_heads))}
+    w = 1 + rnd(g, d, by=0.2)
+    kw = {which + "_weight": dev(w), "sections": sections, "interleaved": interleaved}
+    y = A.gspn_head_rotary_fwd(dev(x["q"]), dev(pos), dev(freqs), dev(x["k"]), **kw)
+    dq, dk, dqw, dkw = A.gspn_head_rotary_bwd(dev(x["q"]), dev(pos), dev(freqs), dev(go["q"]), dev(x["k"]), dev(go["k"]), **kw)
+    leaves = {n: x[n].to(DEV).requires_grad_() for n in x}
+    lw = w.to(DEV).requires_grad_()
+    z = A.head_rotary(leaves["q"], dev(pos), dev(freqs), leaves["k"], **dict(kw, **{which + "_weight": lw}))
+    auto = torch.autograd.grad(z, [leaves["q"], leaves["k"], lw], [dev(go["q"]), dev(go["k"])])
+    got = {"q": (y[0], dq, dqw), "k": (y[1], dk, dkw)}
+    for n in "qk":
+        ref = R.rotary(wide(x[n]), wide(w) if n == which else None, pos, freqs, sections, interleaved, 1e-6, wide(go[n]))
+        for part, t in zip(("y", "dx", "dw"), got[n]):
+            if part in ref:
+                check(t, *ref[part], n + part)
+            else:
+                assert t is None
+    assert torch.equal(auto[0], dq) and torch.equal(auto[1], dk) and torch.equal(auto[2], dqw if which == "q" else dkw)
+    assert torch.equal(z[0], y[0]) and torch.equal(z[1], y[1])
