@@ -50,6 +50,7 @@ ROOT = os.path.dirname(os.path.abspath(__file__))
 if ROOT not in sys.path:
     sys.path.insert(0, ROOT)
 
+from linear_spatial_propagation_gspn_amd import build as hipbuild  # noqa: E402
 from linear_spatial_propagation_gspn_amd import gspn as G  # noqa: E402
 from linear_spatial_propagation_gspn_amd.workloads import WORKLOADS, make_inputs  # noqa: E402
 
@@ -283,23 +284,28 @@ KERNEL_SOURCES = {
     "wgrad_mfma": ["wgrad.hip"],
 }
 _COMMON = ["device.hpp", "check.hpp"]
+# The sources of the operators over token rows, which no step launches.
+TOKEN_ROW_SOURCES = ["sequence.hpp", "sequence_api.cpp", "buffers.hpp", "causal_conv.hip", "selscan.hpp", "selscan.hip",
+                     "selscan_bwd.hip", "block_join.hip", "attention.hpp", "attention_api.cpp", "attention.hip",
+                     "attention_bwd.hip", "attention_step.hip", "head_rotary.hip"]
 
 
 def kernel_sources_digest(kernel: str | None = None) -> str:
     """sha256 over the sources of one kernel (KERNEL_SOURCES, plus the shared
-    device helpers and build.py), or over every kernel source of the library
-    for an unlisted kernel."""
+    device helpers), or for an unlisted kernel over every source that a step
+    may be built from; and over the flags that they are compiled with."""
     if kernel in KERNEL_SOURCES:
         names = sorted(set(KERNEL_SOURCES[kernel] + _COMMON))
     else:
-        names = sorted(n for n in os.listdir(CSRC) if n.endswith((".hip", ".hpp", ".cpp", ".h")))
+        names = sorted(n for n in os.listdir(CSRC)
+                       if n.endswith((".hip", ".hpp", ".cpp", ".h")) and n not in TOKEN_ROW_SOURCES)
     h = hashlib.sha256()
     for name in names:
         h.update(name.encode())
         with open(os.path.join(CSRC, name), "rb") as f:
             h.update(f.read())
-    with open(os.path.join(os.path.dirname(CSRC), "build.py"), "rb") as f:
-        h.update(f.read())
+    flags = [f for f in hipbuild.COMMON + hipbuild.DEVICE if not f.startswith("-I")]
+    h.update(" ".join(flags).encode())
     return h.hexdigest()
 
 
