@@ -570,7 +570,7 @@ def _no_tangents(*tensors) -> None:
     be taken for one whose derivative is zero."""
     for t in tensors:
         if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
-            raise NotImplementedError("the sequence operators have no forward-mode derivative")
+            raise NotImplementedError("the operators over token rows have no forward-mode derivative")
 
 
 def _clear(x, cu):

@@ -1,6 +1,9 @@
 """CPU tests of refusals at the ends of the attention operators' argument types: sums and products of sizes that would pass
-64 bits, scales that pass fp32.  Nothing is launched."""
+64 bits, scales that pass fp32.  And the words of
+one.  Nothing is launched."""
 import pytest
+import torch
+from torch.autograd import forward_ad
 
 from linear_spatial_propagation_gspn_amd import attention as A
 from test_attention_abi import BF16, F32, SHAPE, UNSUP, refuse
@@ -44,3 +47,12 @@ def test_scales_whose_powers_of_two_pass_fp32(lib, kind):
         refuse(lib, "attn", kind, SHAPE, scale=scale)
         refuse(lib, "attn", kind, SHAPE, dtype=BF16, scale=scale)
     refuse(lib, "attn", kind, UNSUP, scale=2.3e38, d=129)  # (the scale alone is no reason)
+
+
+def test_forward_mode_is_not_refused_in_another_operators_name():
+    x, pos, freqs = torch.zeros(4, 2, 8), torch.zeros(4, 1, dtype=torch.int32), torch.zeros(4, dtype=torch.float64)
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(x, torch.ones_like(x))
+        for call in (lambda: A.attention(x, dual, x), lambda: A.head_rotary(dual, pos, freqs)):
+            with pytest.raises(NotImplementedError, match="over token rows"):
+                call()
