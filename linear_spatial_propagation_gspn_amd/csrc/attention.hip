@@ -52,10 +52,15 @@ __device__ __forceinline__ void append_rows(const AttnK& a, uint32_t id) {
 // Attention of 128 rows, 32 a wave, over their keys in tiles of 64 (fp32: 32) that
 // the waves share: one pass with a running maximum and sum (Softmax), keys and
 // values twice in LDS.  Bound by the matrix unit, and by the power that it takes:
-// a prompt of 16384 rows, 32 heads of 128, takes 2060 us, 1070 TFLOP/s, with
+// a prompt of 16384 rows, 32 heads of 128, takes 2070 us, 1060 TFLOP/s, with
 // the unit busy in 59% of the cycles at a clock of 1.6 GHz; a large plain product
 // reaches 1160 to 1220.  Short walks pay for their start, which takes as long as
 // two to four tiles: 16 ragged prompts of 8192 rows in all 140 us, 595 TFLOP/s.
+// bf16 numerators are rounded to bf16 for their product: what that loses, as a
+// second factor, would bring the results from 0.0020 of their size (root mean
+// square) to 0.0018 of the exact ones, for 2810 us and 168 in place of those.
+// A walk is never cut along its keys: eight rows behind 32768 held ones, 32 heads on
+// 8 of keys, take 660 us where the entry's bytes take 26.
 // kCache: the rows that an entry holds are read there, the new ones where they
 // are (any other way the copies would have to be done first: 12 us of 147), and
 // workgroups behind the others copy them over while the last walks end (before

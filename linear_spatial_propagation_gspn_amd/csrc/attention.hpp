@@ -400,8 +400,9 @@ __device__ __forceinline__ void st_result(T* row, const f32x16 (&o)[kBlocks<D>],
 // The softmax of the rows that a wave's lanes hold, over tiles: the running
 // maximum of the scores (unscaled), the sum of this lane's half of the
 // numerators and their products with the values.  The maximum that the
-// numerators are taken from follows the true one only once it is 2^8 behind,
-// so that the products are rarely scaled anew; no numerator exceeds 2^8.
+// numerators are taken from follows the true one only once it is 2^8 behind (a
+// published idea), so that the products are rarely scaled anew; no numerator
+// exceeds 2^8.
 template <int D>
 struct Softmax {
     float m = -INFINITY, l = 0.0f;

@@ -11,7 +11,8 @@
 // root of the keys: rows that see one tile of keys or less (64; fp32: 32) get theirs
 // from the weights, sum_j p_ij <gout_i, v_j>, whatever the others of their wave see.
 // A row that sees one key has p = 1 whatever the score: its ds is 0, not the rounding
-// that is left of the difference.
+// that is left of the difference.  For bf16, p and ds are rounded to bf16 as factors,
+// for the forward's reason: a second factor each would take three more products.
 #include "attention.hpp"
 
 #include <array>
@@ -26,8 +27,8 @@ __device__ __forceinline__ float log2_sum(float lse) {
 }
 
 // Queries at rest, keys and values in tiles as in the forward.  8 x 1024 rows, 18
-// heads, 6 of keys, of 128: 100 us; four maps of 3136 tokens, 16 heads of 72: 370,
-// the matrix unit busy in 53% of the cycles.  Products one after the other, as
+// heads, 6 of keys, of 128: 101 us; four maps of 3136 tokens, 16 heads of 72: 360,
+// the matrix unit busy in 55% of the cycles.  Products one after the other, as
 // the compiler orders them: interleaved by hand as in the forward they took 16%
 // longer.
 template <typename T, int D, bool kDirect>
@@ -178,8 +179,8 @@ constexpr int kBwdRows = 64;
 // Keys at rest: two waves of 32 of them, twice, each pair for one half of every
 // tile of rows (joined in LDS at the end).  Long walks are half as long so, which
 // counts where later rows see more keys: 8 x 1024 rows, 18 heads, 6 of keys, 211
-// us with 128 keys a workgroup, 114 so and in parts.  Four maps of 3136 tokens,
-// 16 heads of 72: 580 us; what bounds both is the matrix unit (busy in 37 and 41%
+// us with 128 keys a workgroup, 118 so.  Four maps of 3136 tokens,
+// 16 heads of 72: 584 us; what bounds both is the matrix unit (busy in 37 and 41%
 // of the cycles) behind LDS, which gives two fragments a product.
 template <typename T, int D, bool kDirect>
 __global__ __launch_bounds__(kAttnThreads, kIsBf16<T> ? 2 : 1) void attn_dkv_kernel(const AttnK a) {

@@ -7,7 +7,7 @@
 // of their own, without a barrier, and are joined at the end, as the runs are
 // by a second launch.  64 tokens over entries of 2048 to 4096 rows, 8 heads of keys
 // of 128: 162 us, 4870 GB/s, 94% of what a copy reaches.  Two entries of 46000
-// rows, 2 heads of keys: 64 runs each, 22 us and 4.3 to join them.
+// rows, 2 heads of keys: 64 runs each, 23 us and 4.3 to join them.
 // bf16 numerators go into their product as two factors, themselves rounded and
 // what that lost: one factor alone took 160 us, and the results lay 0.0023 (root
 // mean square, of their size) from the exact ones, 0.0017 so, their own rounding.
@@ -234,9 +234,12 @@ __global__ __launch_bounds__(kAttnThreads) void attn_step_join_kernel(const Attn
 
 }  // namespace
 
-// Runs of a sequence's keys: enough workgroups for two a CU, none shorter than
-// four rounds of its waves over a full entry, which take about as long as the
-// join's launch.
+// Runs of a sequence's keys: 512 workgroups or more, none shorter than four rounds
+// of its waves over a full entry, which take about as long as the join's launch.
+// (Two share a CU, but for heads past 96 bf16 or 64 fp32 elements, whose waves hold
+// more than 256 registers.)  The host knows the entries' capacity, not what they
+// hold: with 512 groups or more an entry is one run, and a long one among short ones
+// is waited for (one of 32768 rows among 63 of 512, 8 heads of keys: 486 us, 52 of bytes).
 int attn_splits(int64_t nseq, int64_t heads, int64_t kv_heads, int64_t capacity) {
     const int64_t groups = nseq * kv_heads * ((heads / kv_heads + 31) / 32);
     if (groups < 1) return 1;

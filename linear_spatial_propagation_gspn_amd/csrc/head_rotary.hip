@@ -5,9 +5,9 @@
 // (2 V elements) a lane: for pairs of halves V elements at j and V at pairs + j,
 // for neighbours 2 V in a row; elements behind the pairs are dealt out the same
 // way and turn by nothing.  A lane keeps its pairs' sines and cosines for all the
-// heads of a row.  16384 rows of 40 heads of 128 bf16 elements: 70 us, 4700 GB/s, 92%
-// of what a copy reaches; 12544 rows of 32 heads of 72, interleaved: 24 us forward,
-// 4800 GB/s, 41 backward, 4200.
+// heads of a row.  16384 rows of 40 heads of 128 bf16 elements: 71 us, 4700 GB/s, 91%
+// of what a copy reaches; 12544 rows of 32 heads of 72, interleaved: 26 us forward,
+// 4400 GB/s, 41 backward, 4250.
 #include "attention.hpp"
 
 namespace gspn {
