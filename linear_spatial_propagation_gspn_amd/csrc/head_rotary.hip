@@ -454,8 +454,8 @@ RotaryK make_rotary(const gspn_rotary_args& a) {
 // Waves that share a row's heads, so that few rows still fill the SIMDs: two a
 // SIMD; more would only form a row's sines more often.  A backward's waves leave sums
 // of the weights' gradients too: it has no more than those two (2000 rows, 32 + 8 heads
-// of 128 bf16 elements: 19.8 us with one slice, 25.6 with two; 500 rows 17.7 with one
-// workgroup a four rows, 11.9 with four slices, 64 rows 15.6 and 8.9).
+// of 128 bf16 elements: 19.7 us with one slice, 25.6 with two; 500 rows 17.6 with a
+// workgroup for every four rows, 12.1 with four slices, 64 rows 15.6 and 8.9).
 int64_t most_slices(int64_t rows, bool bwd) {
     const int64_t n = rows < 1 ? 1 : bwd ? 2048 / rows : (2048 + rows - 1) / rows;
     return n < 1 ? 1 : n;
